@@ -96,6 +96,18 @@ _SIGNATURES = {
     "gpt2_diag_wait_timeout": (_I, [ctypes.c_longlong, _P, _P]),
 }
 
+# the same for include/gpt2fwd_serve.h
+_SERVE_SIGNATURES = {
+    "paged_build_tables": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "gpt2_prefill_slots": (_I, [_CFG, _P, _P, _P, _I, _I, _P, _P, _PKV, _P, _P, _Z, _I, _P]),
+    "attention_shared_prefix_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
+    "attention_shared_prefix": (_I, [_P, _P, _PKV, _P, _I, _I, _I, _I, _I, _P, _Z, _P]),
+    "gpt2_shared_workspace_size": (_Z, [_CFG, _I, _I, _I]),
+    "gpt2_decode_step_shared": (_I, [_CFG, _P, _P, _PKV, _P, _P, _I, _I, _P, _P, _P, _Z, _I, _P]),
+    "logprobs_forward": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _P]),
+    "logprobs_backward": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
+}
+
 _handle = None
 
 
@@ -111,7 +123,7 @@ def _lib():
             raise ImportError(f"libgpt2fwd.so is not built ({path}); run "
                               "`python -m gpt_transformer_forward_gb300.build`")
         h = ctypes.CDLL(path)
-        for name, (res, args) in _SIGNATURES.items():
+        for name, (res, args) in {**_SIGNATURES, **_SERVE_SIGNATURES}.items():
             fn = getattr(h, name)
             fn.restype = res
             fn.argtypes = args
@@ -126,9 +138,9 @@ def load(build_if_missing: bool = True):
     return _lib()
 
 
-def header_functions() -> list:
-    """Function names declared in include/gpt2fwd.h."""
-    path = os.path.join(_build.INCLUDE, "gpt2fwd.h")
+def header_functions(header: str = "gpt2fwd.h") -> list:
+    """Function names declared in a header of include/."""
+    path = os.path.join(_build.INCLUDE, header)
     with open(path) as f:
         return re.findall(r"^GPT2_API [^(]*?\b([a-z_0-9]+)\(", f.read(), flags=re.M)
 
@@ -313,6 +325,71 @@ def gpt2_decode_step_paged(cfg, params, packed, kv, tok, pos, B, logits, probs, 
     _check("gpt2_decode_step_paged", _lib().gpt2_decode_step_paged(
         _cfg(cfg), _ptr(params), _ptr(packed), ctypes.byref(kv) if kv is not None else None, _ptr(tok), _ptr(pos), B,
         _ptr(logits), _ptr(probs), _ptr(workspace), ws_bytes, precision, _stream(stream)))
+
+
+# ------------------------------------------- gpt2fwd_serve.h
+LOGPROBS_MAX_TOP = 32
+
+
+def element_type(t) -> int:
+    """The GPT2ProbsType code of a tensor's dtype (fp32, fp16 or bf16)."""
+    import torch
+    codes = {torch.float32: GPT2_PROBS_F32, torch.float16: GPT2_PROBS_F16, torch.bfloat16: GPT2_PROBS_BF16}
+    if t.dtype not in codes:
+        raise TypeError(f"element type {t.dtype}: fp32, fp16 or bf16 expected")
+    return codes[t.dtype]
+
+
+def paged_build_tables(block_table, slots, next_len, taken_out, cached_len, new_len, free_blocks, num_free, taken_in,
+                       prefix_blocks, prefix_len, B, T, num_blocks, block_size, max_blocks_per_seq, stream=None):
+    _check("paged_build_tables", _lib().paged_build_tables(
+        _ptr(block_table), _ptr(slots), _ptr(next_len), _ptr(taken_out), _ptr(cached_len), _ptr(new_len),
+        _ptr(free_blocks), num_free, _ptr(taken_in), _ptr(prefix_blocks), prefix_len, B, T, num_blocks, block_size,
+        max_blocks_per_seq, _stream(stream)))
+
+
+def gpt2_prefill_slots(cfg, params, packed, tok, B, T, logits, probs, kv, slots, workspace, ws_bytes, precision,
+                       stream=None):
+    _check("gpt2_prefill_slots", _lib().gpt2_prefill_slots(
+        _cfg(cfg), _ptr(params), _ptr(packed), _ptr(tok), B, T, _ptr(logits), _ptr(probs),
+        ctypes.byref(kv) if kv is not None else None, _ptr(slots), _ptr(workspace), ws_bytes, precision,
+        _stream(stream)))
+
+
+def attention_shared_prefix_workspace_size(B, C, NH, prefix_len, precision) -> int:
+    return _lib().attention_shared_prefix_workspace_size(B, C, NH, prefix_len, precision)
+
+
+def attention_shared_prefix(out, qkv, kv, pos, B, C, NH, prefix_len, precision, workspace=None, ws_bytes=0,
+                            stream=None):
+    """kv: one layer's slab and the block table (paged_kv)."""
+    _check("attention_shared_prefix", _lib().attention_shared_prefix(
+        _ptr(out), _ptr(qkv), ctypes.byref(kv) if kv is not None else None, _ptr(pos), B, C, NH, prefix_len, precision,
+        _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def gpt2_shared_workspace_size(cfg, B, prefix_len, precision) -> int:
+    return _lib().gpt2_shared_workspace_size(_cfg(cfg), B, prefix_len, precision)
+
+
+def gpt2_decode_step_shared(cfg, params, packed, kv, tok, pos, B, prefix_len, logits, probs, workspace, ws_bytes,
+                            precision, stream=None):
+    _check("gpt2_decode_step_shared", _lib().gpt2_decode_step_shared(
+        _cfg(cfg), _ptr(params), _ptr(packed), ctypes.byref(kv) if kv is not None else None, _ptr(tok), _ptr(pos), B,
+        prefix_len, _ptr(logits), _ptr(probs), _ptr(workspace), ws_bytes, precision, _stream(stream)))
+
+
+def logprobs_forward(logprob, entropy, lse, top_ids, top_logprobs, logits, logits_type, targets, N, V, Vp, K,
+                     stream=None):
+    _check("logprobs_forward", _lib().logprobs_forward(
+        _ptr(logprob), _ptr(entropy), _ptr(lse), _ptr(top_ids), _ptr(top_logprobs), _ptr(logits), logits_type,
+        _ptr(targets), N, V, Vp, K, _stream(stream)))
+
+
+def logprobs_backward(dlogits, logits, logits_type, targets, lse, entropy, dlogprob, dentropy, N, V, Vp, stream=None):
+    _check("logprobs_backward", _lib().logprobs_backward(
+        _ptr(dlogits), _ptr(logits), logits_type, _ptr(targets), _ptr(lse), _ptr(entropy), _ptr(dlogprob),
+        _ptr(dentropy), N, V, Vp, _stream(stream)))
 
 
 def gpt2_forward_profile(cfg, params, packed, tok, B, T, logits, probs, workspace, ws_bytes, precision,

@@ -20,7 +20,7 @@
 #include <string>
 #include <vector>
 
-#include "kernels.cuh"
+#include "serve.cuh"
 
 namespace gpt2 {
 
@@ -562,15 +562,31 @@ size_t gpt2_kvcache_size(const GPT2Config* cfg, int B, int precision) {
   return static_cast<size_t>(cfg->num_layers) * kv_layer_elems(cfg, B) * kv_elem_bytes(precision);
 }
 
+// Decode attention of a batch that shares its first p.prefix_len positions:
+// the prefix's partial results for all queries, then each sequence's own
+// positions and the join.
+static int shared_attention(void* out, const void* qkv, void* kc, void* vc, int precision, int B, int C, int NH,
+                            const int* pos, const KVRows& rows, const PrefixPartials& p, cudaStream_t s) {
+  const int op = is16(precision) ? op_of(precision) : kOpTF32;  // an fp32 cache in the other modes
+  if (p.splits > 0) TRY(launch_shared_prefix(p, qkv, kc, vc, op, B, C, NH, rows, s));
+  // the kernel waits for the prefix's results itself
+  PdlScope pdl(pdl_on() || p.splits > 0);
+  launch_shared_decode_attention(out, qkv, kc, vc, op, B, C, NH, pos, rows, p, s);
+  return check_launch();
+}
+
 // The body shared by the full forward pass and the decode step.  decode
 // false: rows are B sequences x T tokens at positions 0..T-1 (their keys and
 // values written into kv when it is given: a prefill); decode true: rows are
 // the B sequences' tokens at position decode_pos, or pos_arr[b] when pos_arr
 // is given (T == 1), attending over and appending to kv.
+// slots (a prefill): tokens go to slots[b*T + t] of kv's pool instead.
+// shared (a decode step): kv's sequences share their first positions.
 static int run_forward(const GPT2Config* cfg, const float* params, const void* packed, const int* tok, int B, int T,
                        bool decode, int decode_pos, const int* pos_arr, float* logits, void* probs,
                        const KVLayout* kv, void* workspace, size_t ws_bytes, int precision, cudaStream_t s,
-                       StageProfiler* prof = nullptr, int probs_type = GPT2_PROBS_F32) {
+                       StageProfiler* prof = nullptr, int probs_type = GPT2_PROBS_F32, const int* slots = nullptr,
+                       const PrefixPartials* shared = nullptr) {
   auto mark = [&](int stage) { return prof ? prof->record(stage) : GPT2_OK; };
   const int C = cfg->channels, L = cfg->num_layers, NH = cfg->num_heads, V = cfg->vocab_size;
   const int Vp = cfg->padded_vocab_size, maxT = cfg->max_seq_len;
@@ -635,7 +651,12 @@ static int run_forward(const GPT2Config* cfg, const float* params, const void* p
     TRY(mark(GPT2_STAGE_LN1));
     TRY(gemm(precision, qkv, ln, wmat(po.qkvw, ko.qkvw, 3 * CC, l), params + po.qkvb + static_cast<size_t>(l) * 3 * C,
              N, 3 * C, C, bf16 ? kEpiOut16 : kEpiF32, s));
-    if (kv != nullptr && !decode) {  // a decode step appends in its attention kernel
+    if (slots != nullptr) {
+      const size_t e = kv_elem_bytes(precision);
+      uint8_t* kc = static_cast<uint8_t*>(kv->base) + l * kv_slab * e;
+      launch_kv_store_slots(kc, kc + kv_half * e, qkv, slots, static_cast<int>(e), B, T, C, NH, kv->rows.lbs,
+                            kv->rows.num_blocks, s);
+    } else if (kv != nullptr && !decode) {  // a decode step appends in its attention kernel
       if (bf16) {
         uint16_t* kc = static_cast<uint16_t*>(kv->base) + l * kv_slab;
         launch_kv_store_16(kc, kc + kv_half, static_cast<const uint16_t*>(qkv), B, T, C, NH, kv->rows, s);
@@ -655,6 +676,10 @@ static int run_forward(const GPT2Config* cfg, const float* params, const void* p
       } else {
         TRY(launch_attention_16(att, true, qkv, op, B, T, C, NH, s));
       }
+    } else if (shared != nullptr) {
+      const size_t e = kv_elem_bytes(precision);
+      uint8_t* kc = static_cast<uint8_t*>(kv->base) + l * kv_slab * e;
+      TRY(shared_attention(att, qkv, kc, kc + kv_half * e, precision, B, C, NH, pos_arr, kv->rows, *shared, s));
     } else {
       if (bf16) {
         uint16_t* kc = static_cast<uint16_t*>(kv->base) + l * kv_slab;
@@ -821,6 +846,177 @@ int gpt2_decode_step_paged(const GPT2Config* cfg, const float* params, const voi
   PdlScope pdl(is16(precision));
   return run_forward(cfg, params, packed, tok, B, 1, true, 0, pos, logits, probs, &kv, workspace, ws_bytes, precision,
                      as_stream(stream));
+}
+
+// -------------------------------------------------- gpt2fwd_serve.h
+int paged_build_tables(int* block_table, int* slots, int* next_len, int* taken_out, const int* cached_len,
+                       const int* new_len, const int* free_blocks, int num_free, const int* taken_in,
+                       const int* prefix_blocks, int prefix_len, int B, int T, int num_blocks, int block_size,
+                       int max_blocks_per_seq, void* stream) {
+  RETURN_IF(!block_table || !cached_len, GPT2_ERR_ARG);
+  RETURN_IF(B < 0 || T < 0 || num_free < 0 || prefix_len < 0 || num_blocks <= 0 || max_blocks_per_seq <= 0,
+            GPT2_ERR_ARG);
+  const int lbs = log2_exact(block_size);
+  RETURN_IF(lbs < 0 || (num_free > 0 && !free_blocks) || (prefix_len > 0) != (prefix_blocks != nullptr),
+            GPT2_ERR_ARG);
+  RETURN_IF(taken_out != nullptr && taken_out == taken_in, GPT2_ERR_ARG);
+  RETURN_IF(next_len != nullptr && (next_len == cached_len || next_len == new_len), GPT2_ERR_ARG);
+  const long long cap = static_cast<long long>(max_blocks_per_seq) << lbs;
+  RETURN_IF(B > kMaxTableRequests || max_blocks_per_seq > kMaxBlocksPerSeq ||
+                (static_cast<long long>(num_blocks) << lbs) > 0x7fffffffLL || prefix_len % block_size != 0 ||
+                prefix_len > cap,
+            GPT2_ERR_SHAPE);
+  for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(slots),
+                        static_cast<const void*>(next_len), static_cast<const void*>(taken_out),
+                        static_cast<const void*>(cached_len), static_cast<const void*>(new_len),
+                        static_cast<const void*>(free_blocks), static_cast<const void*>(taken_in),
+                        static_cast<const void*>(prefix_blocks)})
+    RETURN_IF((reinterpret_cast<uintptr_t>(p) & 3u) != 0, GPT2_ERR_ALIGN);
+  if (B == 0) {  // nobody takes a block
+    if (taken_out == nullptr) return GPT2_OK;
+    const cudaError_t e = taken_in != nullptr ? cudaMemcpyAsync(taken_out, taken_in, sizeof(int),
+                                                                cudaMemcpyDeviceToDevice, as_stream(stream))
+                                              : cudaMemsetAsync(taken_out, 0, sizeof(int), as_stream(stream));
+    return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
+  }
+  TableArgs a{block_table, slots, next_len, taken_out, cached_len, new_len, free_blocks, taken_in, prefix_blocks,
+              num_free, prefix_len >> lbs, B, T, num_blocks, lbs, max_blocks_per_seq,
+              static_cast<int>(std::min<long long>(cap, 0x7fffffffLL))};
+  launch_build_tables(a, as_stream(stream));
+  return check_launch();
+}
+
+int gpt2_prefill_slots(const GPT2Config* cfg, const float* params, const void* packed, const int* tok, int B, int T,
+                       float* logits, float* probs, const GPT2PagedKVCache* kvc, const int* slots, void* workspace,
+                       size_t ws_bytes, int precision, void* stream) {
+  TRY(check_config(cfg));
+  RETURN_IF(!params || !tok || !logits || !workspace || !slots || !valid_precision(precision), GPT2_ERR_ARG);
+  RETURN_IF(B <= 0 || T <= 0 || kvc == nullptr || kvc->pool == nullptr || kvc->num_blocks <= 0, GPT2_ERR_ARG);
+  const int lbs = log2_exact(kvc->block_size);
+  RETURN_IF(lbs < 0, GPT2_ERR_ARG);
+  RETURN_IF(T > cfg->max_seq_len || (static_cast<long long>(kvc->num_blocks) << lbs) > 0x7fffffffLL, GPT2_ERR_SHAPE);
+  TRY(check_attention_shape(cfg->channels, cfg->num_heads));
+  RETURN_IF(is16(precision) && packed == nullptr, GPT2_ERR_ARG);
+  RETURN_IF(!aligned16(params) || !aligned16(logits) || (probs && !aligned16(probs)) || !aligned16(kvc->pool) ||
+                (reinterpret_cast<uintptr_t>(slots) & 3u) != 0 || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+                (packed && (reinterpret_cast<uintptr_t>(packed) & 255u) != 0),
+            GPT2_ERR_ALIGN);
+  KVLayout kv;
+  kv.base = kvc->pool;
+  kv.rows = KVRows{nullptr, lbs, 0, kvc->num_blocks, cfg->max_seq_len, 0};
+  kv.layer_elems = paged_layer_elems(cfg, kvc->num_blocks, kvc->block_size);
+  PdlScope pdl(is16(precision));
+  return run_forward(cfg, params, packed, tok, B, T, false, 0, nullptr, logits, probs, &kv, workspace, ws_bytes,
+                     precision, as_stream(stream), nullptr, GPT2_PROBS_F32, slots);
+}
+
+// grid limits of the attention kernels: sequences and heads
+constexpr int kMaxSharedBatch = 65535;
+
+size_t attention_shared_prefix_workspace_size(int B, int C, int NH, int prefix_len, int precision) {
+  if (B <= 0 || B > kMaxSharedBatch || C <= 0 || NH <= 0 || NH > kMaxSharedBatch || C % NH != 0 || prefix_len <= 0 ||
+      !valid_precision(precision) || check_attention_shape(C, NH) != GPT2_OK)
+    return 0;
+  return shared_prefix_bytes(B, NH, C / NH, prefix_len, is16(precision));
+}
+
+int attention_shared_prefix(void* out, const void* qkv, const GPT2PagedKVCache* kvc, const int* pos, int B, int C,
+                            int NH, int prefix_len, int precision, void* workspace, size_t ws_bytes, void* stream) {
+  RETURN_IF(!out || !qkv || !pos || kvc == nullptr || kvc->pool == nullptr || kvc->block_table == nullptr,
+            GPT2_ERR_ARG);
+  RETURN_IF(B < 0 || C <= 0 || NH <= 0 || prefix_len < 0 || !valid_precision(precision) || out == qkv, GPT2_ERR_ARG);
+  const int lbs = log2_exact(kvc->block_size);
+  RETURN_IF(lbs < 0 || kvc->num_blocks <= 0 || kvc->max_blocks_per_seq <= 0, GPT2_ERR_ARG);
+  RETURN_IF(C % NH != 0 || kvc->max_blocks_per_seq > kMaxBlocksPerSeq || B > kMaxSharedBatch || NH > kMaxSharedBatch,
+            GPT2_ERR_SHAPE);
+  const long long cap =
+      std::min<long long>(0x7fffffffLL, static_cast<long long>(kvc->max_blocks_per_seq) << lbs);
+  RETURN_IF(prefix_len >= cap, GPT2_ERR_SHAPE);  // the new token's position lies behind the prefix
+  TRY(check_attention_shape(C, NH));
+  if (B == 0) return GPT2_OK;
+  const size_t need = attention_shared_prefix_workspace_size(B, C, NH, prefix_len, precision);
+  RETURN_IF(need > 0 && (workspace == nullptr || ws_bytes < need), GPT2_ERR_WORKSPACE);
+  RETURN_IF(!aligned16(out) || !aligned16(qkv) || !aligned16(kvc->pool) || !aligned16(workspace) ||
+                (reinterpret_cast<uintptr_t>(kvc->block_table) & 3u) != 0 ||
+                (reinterpret_cast<uintptr_t>(pos) & 3u) != 0,
+            GPT2_ERR_ALIGN);
+  const size_t e = kv_elem_bytes(precision);
+  const size_t half = static_cast<size_t>(kvc->num_blocks) * kvc->block_size * C;
+  uint8_t* kc = static_cast<uint8_t*>(kvc->pool);
+  const KVRows rows{kvc->block_table, lbs, kvc->max_blocks_per_seq, kvc->num_blocks, static_cast<int>(cap),
+                    static_cast<int>(cap)};
+  const PrefixPartials p = shared_prefix_layout(workspace, B, NH, C / NH, prefix_len, is16(precision));
+  return shared_attention(out, qkv, kc, kc + half * e, precision, B, C, NH, pos, rows, p, as_stream(stream));
+}
+
+size_t gpt2_shared_workspace_size(const GPT2Config* cfg, int B, int prefix_len, int precision) {
+  const size_t base = gpt2_workspace_size(cfg, B, 1, precision);
+  if (base == 0 || B > kMaxSharedBatch || prefix_len < 0 ||
+      check_attention_shape(cfg->channels, cfg->num_heads) != GPT2_OK)
+    return 0;
+  return base + attention_shared_prefix_workspace_size(B, cfg->channels, cfg->num_heads, prefix_len, precision);
+}
+
+int gpt2_decode_step_shared(const GPT2Config* cfg, const float* params, const void* packed,
+                            const GPT2PagedKVCache* kvc, const int* tok, const int* pos, int B, int prefix_len,
+                            float* logits, float* probs, void* workspace, size_t ws_bytes, int precision,
+                            void* stream) {
+  TRY(check_config(cfg));
+  RETURN_IF(!params || !tok || !pos || !logits || !workspace || !valid_precision(precision), GPT2_ERR_ARG);
+  RETURN_IF(B <= 0 || prefix_len < 0, GPT2_ERR_ARG);
+  TRY(check_attention_shape(cfg->channels, cfg->num_heads));
+  RETURN_IF(is16(precision) && packed == nullptr, GPT2_ERR_ARG);
+  KVLayout kv;
+  TRY(paged_kv(cfg, kvc, 0, &kv));
+  RETURN_IF(B > kMaxSharedBatch || prefix_len >= kv.rows.capacity, GPT2_ERR_SHAPE);
+  RETURN_IF(!aligned16(params) || !aligned16(logits) || (probs && !aligned16(probs)) ||
+                (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+                (packed && (reinterpret_cast<uintptr_t>(packed) & 255u) != 0),
+            GPT2_ERR_ALIGN);
+  RETURN_IF(ws_bytes < gpt2_shared_workspace_size(cfg, B, prefix_len, precision), GPT2_ERR_WORKSPACE);
+  const size_t base = gpt2_workspace_size(cfg, B, 1, precision);
+  const PrefixPartials p = shared_prefix_layout(static_cast<uint8_t*>(workspace) + base, B, cfg->num_heads,
+                                                cfg->channels / cfg->num_heads, prefix_len, is16(precision));
+  PdlScope pdl(is16(precision));
+  return run_forward(cfg, params, packed, tok, B, 1, true, 0, pos, logits, probs, &kv, workspace, base, precision,
+                     as_stream(stream), nullptr, GPT2_PROBS_F32, nullptr, &p);
+}
+
+// rows of a whole number of 16-byte vectors
+static bool logit_rows_ok(int Vp, int logits_type) { return Vp % (logits_type == GPT2_PROBS_F32 ? 4 : 8) == 0; }
+
+int logprobs_forward(float* logprob, float* entropy, float* lse, int* top_ids, float* top_logprobs, const void* logits,
+                     int logits_type, const int* targets, int N, int V, int Vp, int K, void* stream) {
+  RETURN_IF(!logits || N < 0 || V <= 0 || Vp < V || K < 0 || !valid_probs_type(logits_type), GPT2_ERR_ARG);
+  RETURN_IF(logprob != nullptr && targets == nullptr, GPT2_ERR_ARG);
+  RETURN_IF(!logit_rows_ok(Vp, logits_type) || K > GPT2_LOGPROBS_MAX_TOP, GPT2_ERR_SHAPE);
+  RETURN_IF(!aligned16(logits), GPT2_ERR_ALIGN);
+  for (const void* p : {static_cast<const void*>(logprob), static_cast<const void*>(entropy),
+                        static_cast<const void*>(lse), static_cast<const void*>(top_ids),
+                        static_cast<const void*>(top_logprobs), static_cast<const void*>(targets)})
+    RETURN_IF((reinterpret_cast<uintptr_t>(p) & 3u) != 0, GPT2_ERR_ALIGN);
+  if (K == 0) top_ids = nullptr, top_logprobs = nullptr;
+  if (N == 0 || (!logprob && !entropy && !lse && !top_ids && !top_logprobs)) return GPT2_OK;
+  launch_logprobs(logprob, entropy, lse, top_ids, top_logprobs, logits, logits_type, targets, N, V, Vp, K,
+                  as_stream(stream));
+  return check_launch();
+}
+
+int logprobs_backward(void* dlogits, const void* logits, int logits_type, const int* targets, const float* lse,
+                      const float* entropy, const float* dlogprob, const float* dentropy, int N, int V, int Vp,
+                      void* stream) {
+  RETURN_IF(!dlogits || !logits || !lse || N < 0 || V <= 0 || Vp < V || !valid_probs_type(logits_type), GPT2_ERR_ARG);
+  RETURN_IF((dlogprob != nullptr && targets == nullptr) || (dentropy != nullptr && entropy == nullptr), GPT2_ERR_ARG);
+  RETURN_IF(!logit_rows_ok(Vp, logits_type), GPT2_ERR_SHAPE);
+  RETURN_IF(!aligned16(dlogits) || !aligned16(logits), GPT2_ERR_ALIGN);
+  for (const void* p : {static_cast<const void*>(targets), static_cast<const void*>(lse),
+                        static_cast<const void*>(entropy), static_cast<const void*>(dlogprob),
+                        static_cast<const void*>(dentropy)})
+    RETURN_IF((reinterpret_cast<uintptr_t>(p) & 3u) != 0, GPT2_ERR_ALIGN);
+  if (N == 0) return GPT2_OK;
+  launch_logprobs_backward(dlogits, logits, logits_type, targets, lse, entropy, dlogprob, dentropy, N, V, Vp,
+                           as_stream(stream));
+  return check_launch();
 }
 
 int gpt2_get_error(void* stream) {

@@ -90,3 +90,38 @@ class GPT2Model:
         B = tok.shape[0]
         ab.gpt2_decode_step_paged(self.cfg, self.params, self.packed, kv, tok, pos, B, logits, probs, self.workspace,
                                   self.ws_bytes, self.precision, stream)
+
+    # ------------------------------------- many continuations of one prompt
+    def prefill_slots(self, tok, logits, kv, slots, probs=None, stream=None):
+        """gpt2_forward storing token (b, t) at slot slots[b, t] of kv's pool
+        (none where it is -1)."""
+        B, T = tok.shape
+        ab.gpt2_prefill_slots(self.cfg, self.params, self.packed, tok, B, T, logits, probs, kv, slots, self.workspace,
+                              self.ws_bytes, self.precision, stream)
+
+    def new_shared_workspace(self, B: int, prefix_len: int):
+        """A workspace for decode_step_shared with up to B sequences and this prefix."""
+        nbytes = ab.gpt2_shared_workspace_size(self.cfg, B, prefix_len, self.precision)
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+
+    def decode_step_shared(self, kv, tok, pos, prefix_len: int, logits, workspace, probs=None, stream=None):
+        """decode_step_paged for sequences that share their first prefix_len
+        positions; workspace from new_shared_workspace."""
+        B = tok.shape[0]
+        ab.gpt2_decode_step_shared(self.cfg, self.params, self.packed, kv, tok, pos, B, prefix_len, logits, probs,
+                                   workspace, workspace.numel(), self.precision, stream)
+
+    def logprobs(self, logits, targets=None, top: int = 0, stream=None) -> dict:
+        """The log probability of each row's target (targets: int32, -1 for
+        none), its entropy, log-sum-exp and `top` alternatives, of logits
+        [..., Vp]; results have the logits' leading shape."""
+        shape, Vp = logits.shape[:-1], logits.shape[-1]
+        new = lambda *more, dtype=torch.float32: torch.empty(*shape, *more, dtype=dtype, device=logits.device)  # noqa: E731
+        r = {"entropy": new(), "lse": new()}
+        if targets is not None:
+            r["logprob"] = new()
+        if top:
+            r["top_ids"], r["top_logprobs"] = new(top, dtype=torch.int32), new(top)
+        ab.logprobs_forward(r.get("logprob"), r["entropy"], r["lse"], r.get("top_ids"), r.get("top_logprobs"), logits,
+                            ab.element_type(logits), targets, r["lse"].numel(), self.cfg.vocab_size, Vp, top, stream)
+        return r

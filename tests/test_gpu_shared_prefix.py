@@ -1,0 +1,368 @@
+"""Decode attention over a shared prefix [NTU "KV Caching"; FlashAttention
+Algorithm 0], against a 64-bit form on the CPU that walks each sequence's
+positions.
+
+Tolerances: u = 2^-24, w the half step of the element type (relative 2^-8 for
+bf16, 2^-11 for fp16; u for fp32).  A score of hs products is off by at most
+(hs + 4) u sum|q k| / sqrt(hs) (products, sums, scale and the log2 units), a
+probability relative to the row's sum by twice that, the exponential's 8 u and
+the sums' (n / 16 + 64) u over n positions; an output by that times max|v|,
+plus w max|v| for probabilities rounded to the 16-bit type and w |out| for the
+output's own rounding."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gpt_transformer_forward_gb300 import binding as ab
+from gpt_transformer_forward_gb300 import inputs
+from gpt_transformer_forward_gb300.runner import GPT2Model
+
+from gpu_helpers import assert_close, dev, host, need_gpu, no_device_error
+from serve_reference import shared_attention
+
+pytestmark = pytest.mark.gpu
+u = 2.0 ** -24
+DT = {ab.GPT2_FP32: torch.float32, ab.GPT2_TF32: torch.float32, ab.GPT2_BF16: torch.bfloat16,
+      ab.GPT2_FP16: torch.float16}
+HALF = {torch.float32: u, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+ALL = [ab.GPT2_FP32, ab.GPT2_TF32, ab.GPT2_BF16, ab.GPT2_FP16]
+NAMES = {v: k for k, v in ab.PRECISIONS.items()}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def make(precision, B, NH, hs, P, own, bs, seed, qscale=2.0):
+    """Inputs as CPU tensors; `own`: each sequence's own cached positions."""
+    g = torch.Generator().manual_seed(seed)
+    dt = DT[precision]
+    own = torch.as_tensor(own)
+    n_own = (P + int(own.max())) // bs + 1 - P // bs
+    num_blocks = P // bs + B * n_own + 3
+    ids = torch.randperm(num_blocks, generator=g).to(torch.int32)
+    table = torch.empty(B, P // bs + n_own + 1, dtype=torch.int32)
+    table[:] = -5  # entries no call reaches
+    table[:, :P // bs] = ids[:P // bs]
+    table[:, P // bs:P // bs + n_own] = ids[P // bs:P // bs + B * n_own].view(B, n_own)
+    pool = torch.randn(2, num_blocks, NH, bs, hs, generator=g).to(dt)
+    if P % bs:
+        mine = table[:, P // bs].long()
+        pool[:, mine, :, :P % bs] = pool[:, mine[:1], :, :P % bs].clone()
+    pos = (P + own).to(torch.int32)
+    qkv = torch.randn(B, 3, NH, hs, generator=g)
+    qkv[:, 0] *= qscale
+    return dict(precision=precision, NH=NH, hs=hs, P=P, bs=bs, pool=pool, table=table, pos=pos,
+                qkv=qkv.reshape(B, -1).to(dt))
+
+
+def call(c, pool, qkv, table, pos, out, ws=None, P=None):
+    B, C = qkv.shape[0], c["NH"] * c["hs"]
+    P = c["P"] if P is None else P
+    n = ab.attention_shared_prefix_workspace_size(B, C, c["NH"], P, c["precision"])
+    if ws is None:
+        ws = torch.full((max(n, 1),), 255, dtype=torch.uint8, device="cuda")  # NaN bytes
+    kv = ab.paged_kv(pool, table, c["pool"].shape[1], c["bs"], c["table"].shape[1])
+    ab.attention_shared_prefix(out, qkv, kv, pos, B, C, c["NH"], P, c["precision"], ws, n)
+    return ws
+
+
+def run(c, **kw):
+    g = {k: c[k].cuda() for k in ("pool", "qkv", "table", "pos")}
+    out = torch.full((c["qkv"].shape[0], c["NH"] * c["hs"]), 9.0, dtype=DT[c["precision"]], device="cuda")
+    call(c, g["pool"], g["qkv"], g["table"], g["pos"], out, **kw)
+    torch.cuda.synchronize()
+    return out.cpu(), g["pool"].cpu()
+
+
+def reference(c):
+    B = c["qkv"].shape[0]
+    q, k, v = c["qkv"].double().numpy().reshape(B, 3, c["NH"], c["hs"]).transpose(1, 0, 2, 3)
+    out, sabs, vmax = shared_attention(q, k, v, c["pool"].double().numpy(), c["table"].numpy(), c["pos"].numpy(),
+                                       c["P"], c["bs"])
+    w = HALF[DT[c["precision"]]]
+    n = c["pos"].numpy()[:, None] + 1
+    part = 2 * (c["hs"] + 4) * u * sabs + 8 * u + (n / 16 + 64) * u
+    tol = (part + (w if w > u else 0)) * vmax
+    return out, tol[..., None] + w * np.abs(out)
+
+
+def check(c, **kw):
+    out, pool = run(c, **kw)
+    no_device_error()
+    B = out.shape[0]
+    ref, tol = reference(c)
+    err = np.abs(out.double().numpy().reshape(ref.shape) - ref)
+    assert (err <= tol).all(), f"{(err > tol).sum()} off, worst {(err / tol).max():.3f} of the tolerance"
+    want = c["pool"].clone()
+    k, v = c["qkv"].view(B, 3, c["NH"], c["hs"])[:, 1:].unbind(1)
+    blk = c["table"].gather(1, (c["pos"].long() // c["bs"])[:, None])[:, 0].long()
+    want[0, blk, :, c["pos"].long() % c["bs"]] = k
+    want[1, blk, :, c["pos"].long() % c["bs"]] = v
+    assert torch.equal(pool, want), "the cache"
+    return out
+
+
+def own_of(B, most, seed):
+    own = np.random.default_rng(seed).integers(0, most + 1, B)
+    own[0] = most
+    own[-1] = 0
+    return own
+
+
+@pytest.mark.parametrize("precision", ALL, ids=[NAMES[p] for p in ALL])
+@pytest.mark.parametrize("hs", [16, 32, 64])
+@pytest.mark.parametrize("B,NH,P,most,bs", [
+    (1, 1, 1, 0, 1), (1, 2, 64, 5, 16), (2, 3, 63, 1, 16), (3, 1, 65, 40, 2), (5, 2, 128, 3, 128), (16, 2, 127, 9, 8),
+    (17, 2, 129, 9, 4), (31, 3, 500, 17, 16), (33, 2, 1001, 33, 32), (65, 1, 257, 300, 64), (4, 12, 960, 63, 16),
+    (130, 2, 777, 20, 16), (1, 1, 5000, 2, 64),
+])
+def test_against_64_bits(precision, hs, B, NH, P, most, bs):
+    check(make(precision, B, NH, hs, P, own_of(B, most, P), bs, seed=B + P))
+
+
+@pytest.mark.parametrize("precision", ALL, ids=[NAMES[p] for p in ALL])
+def test_no_prefix(precision):
+    check(make(precision, 6, 3, 64, 0, own_of(6, 200, 1), 16, seed=2))
+
+
+@pytest.mark.parametrize("precision", [ab.GPT2_FP16, ab.GPT2_BF16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("B", [1, 8, 40, 128, 200, 257])
+def test_many_sequences(precision, B):
+    check(make(precision, B, 2, 64, 2085, own_of(B, 70, B), 32, seed=B))
+
+
+@pytest.mark.parametrize("precision", ALL, ids=[NAMES[p] for p in ALL])
+@pytest.mark.parametrize("B", [3, 70])
+def test_peaked_and_rising_scores(precision, B):
+    """Scores that grow along the prefix (every step raises the running
+    maximum), and one that dominates late."""
+    c = make(precision, B, 2, 64, 900, own_of(B, 30, 3), 16, seed=4, qscale=1.0)
+    rise = torch.linspace(0.2, 8.0, 900)
+    for j in range(900):
+        c["pool"][0, c["table"][0, j // 16].long(), 0, j % 16] = (rise[j] * torch.ones(64)).to(c["pool"].dtype)
+    if 900 % 16:
+        mine = c["table"][:, 900 // 16].long()
+        c["pool"][:, mine, :, :900 % 16] = c["pool"][:, mine[:1], :, :900 % 16].clone()
+    c["qkv"].view(B, 3, 2, 64)[:, 0, 0] = 1.0
+    c["pool"][0, c["table"][0, 850 // 16].long(), 1, 850 % 16] *= 6
+    check(c)
+
+
+def test_extreme_values_stay_in_their_rows():
+    """Huge values and NaN in cache slots that no position reaches."""
+    for precision in ALL:
+        c = make(precision, 5, 2, 32, 100, [0, 3, 10, 1, 7], 16, seed=7)
+        used = torch.zeros(c["pool"].shape[1], 16, dtype=torch.bool)
+        for b in range(5):
+            for j in range(int(c["pos"][b]) + 1):
+                used[c["table"][b if j >= 100 else 0, j // 16].long(), j % 16] = True
+        for b in range(1, 5):  # the other rows' copies of the prefix's tail are not read
+            assert not used[c["table"][b, 100 // 16].long(), 0]
+        bad = ~used
+        c["pool"].permute(1, 3, 0, 2, 4)[bad] = float("nan")
+        out, pool = run(c)
+        ref, tol = reference(c)
+        assert (np.abs(out.double().numpy().reshape(ref.shape) - ref) <= tol).all(), NAMES[precision]
+        no_device_error()
+
+
+@pytest.mark.parametrize("precision", [ab.GPT2_FP32, ab.GPT2_FP16], ids=["fp32", "fp16"])
+def test_bad_positions(precision):
+    c = make(precision, 6, 2, 64, 100, [0, 5, 9, 3, 2, 8], 16, seed=3)
+    good = run(c)[0]
+    cap = c["table"].shape[1] * 16
+    bad = dict(c, pos=c["pos"].clone())
+    bad["pos"][1], bad["pos"][2], bad["pos"][4], bad["pos"][5] = -1, 99, cap, 2**31 - 1
+    out, pool = run(bad)
+    assert ab.gpt2_get_error() == ab.DEVERR_POSITION
+    assert (out[[1, 2, 4, 5]] == 0).all() and torch.equal(out[[0, 3]], good[[0, 3]])
+    changed = (pool.view(torch.uint8) != c["pool"].view(torch.uint8)).flatten(2).any(2).any(0)
+    mine = {int(c["table"][b, int(c["pos"][b]) // 16]) for b in (0, 3)}
+    assert set(changed.nonzero()[:, 0].tolist()) <= mine
+
+
+@pytest.mark.parametrize("precision", [ab.GPT2_FP32, ab.GPT2_FP16], ids=["fp32", "fp16"])
+@pytest.mark.parametrize("where", [(0, 2), (3, 7)])
+def test_bad_blocks(precision, where):
+    """A block id outside the pool, in the prefix (row 0) or in a sequence's
+    own positions: flagged and read as block 0."""
+    for value in (-1, 10**6):
+        c = make(precision, 4, 2, 64, 100, [20, 20, 20, 20], 16, seed=3)
+        c["table"][where] = value
+        run(c)
+        assert ab.gpt2_get_error() == ab.DEVERR_BLOCK
+
+
+def test_entries_that_are_not_reached_may_hold_anything():
+    # rows other than 0 over the prefix's whole blocks
+    c = make(ab.GPT2_FP16, 5, 2, 64, 96, [4, 0, 30, 2, 9], 16, seed=3)
+    good = run(c)[0]
+    c["table"][1:, :6] = 10**8
+    assert torch.equal(run(c)[0], good)
+    no_device_error()
+
+
+@pytest.mark.parametrize("precision", ALL, ids=[NAMES[p] for p in ALL])
+def test_repeats_streams_and_graphs(precision):
+    """Two captured graphs with workspaces of their own and one that both
+    replay in turn; the same values again, on another stream, and with more
+    workspace than needed."""
+    c = make(precision, 12, 4, 64, 1500, own_of(12, 90, 5), 16, seed=6)
+    first, pool1 = run(c)
+    big = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    assert torch.equal(run(c, ws=big)[0], first)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        assert torch.equal(run(c)[0], first)
+    d = make(precision, 12, 4, 64, 1500, own_of(12, 90, 6), 16, seed=7)
+    second = run(d)[0]
+    graphs = []
+    for x in (c, d):
+        g = {k: x[k].cuda() for k in ("pool", "qkv", "table", "pos")}
+        out = torch.zeros(12, 256, dtype=DT[precision], device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(x, g["pool"], g["qkv"], g["table"], g["pos"], out, ws=big)
+        graphs.append((graph, out, g))
+    for k in (0, 1, 0, 1, 1, 0):
+        graph, out, _ = graphs[k]
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), (first, second)[k])
+    no_device_error()
+
+
+def test_cache_past_32_bits():
+    """Blocks whose offset passes 2^31 elements (bf16, 8.6 GB)."""
+    NH, hs, bs, P = 16, 64, 64, 300
+    num_blocks = 2 ** 31 // (NH * bs * hs) + 64
+    pool = torch.zeros(2, num_blocks, NH, bs, hs, dtype=torch.bfloat16, device="cuda")
+    c = make(ab.GPT2_BF16, 3, NH, hs, P, [70, 0, 5], bs, seed=2)
+    n = c["pool"].shape[1]
+    pool[:, num_blocks - n:] = c["pool"].cuda()
+    table = c["table"] + (num_blocks - n)
+    out = torch.empty(3, NH * hs, dtype=torch.bfloat16, device="cuda")
+    kv = ab.paged_kv(pool, table.cuda(), num_blocks, bs, table.shape[1])
+    nb = ab.attention_shared_prefix_workspace_size(3, NH * hs, NH, P, ab.GPT2_BF16)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    tbl = table.cuda()
+    kv = ab.paged_kv(pool, tbl, num_blocks, bs, table.shape[1])
+    ab.attention_shared_prefix(out, c["qkv"].cuda(), kv, c["pos"].cuda(), 3, NH * hs, NH, P, ab.GPT2_BF16, ws, nb)
+    ref, tol = reference(c)
+    assert (np.abs(out.double().cpu().numpy().reshape(ref.shape) - ref) <= tol).all()
+    no_device_error()
+
+
+# ------------------------------------------------------------- the model
+LOGIT_TOL = {ab.GPT2_BF16: 2e-2, ab.GPT2_FP16: 2e-2, ab.GPT2_TF32: 2e-2, ab.GPT2_FP32: 1e-4}
+
+
+@pytest.mark.parametrize("precision", [ab.GPT2_FP32, ab.GPT2_TF32, ab.GPT2_FP16], ids=["fp32", "tf32", "fp16"])
+@pytest.mark.parametrize("B", [3, 70])
+def test_continuations_of_one_prompt(precision, B):
+    """The operators together: a prompt is prefilled once by a slot map, every
+    continuation's tables are built on the GPU, decode steps read the prompt's
+    blocks once for all, and each step's log probabilities rank the drawn
+    tokens.  Against the oracle's forward pass over each whole sequence."""
+    w = inputs.WORKLOADS["tiny"]
+    cfg = w.cfg
+    params, _ = inputs.workload_inputs(w, "perturbed")
+    bs, prompt, steps, top = 4, 22, 9, 5
+    shared = prompt // bs * bs  # whole blocks; the prompt's last 2 tokens are fed to every continuation
+    rng = np.random.default_rng(B)
+    seq = np.empty((B, prompt + steps), np.int32)
+    seq[:, :prompt] = rng.integers(0, cfg.vocab_size, prompt)
+    seq[:, prompt:] = rng.integers(0, cfg.vocab_size, (B, steps))
+    ref_logits, _ = oracle.forward(cfg, params, seq[:min(B, 6)])
+    m = GPT2Model(cfg, params, B, prompt, precision)
+    maxb = -(-(prompt + steps) // bs)
+    num_blocks = shared // bs + B * (maxb - shared // bs) + 2
+    pool = m.new_paged_kvcache(num_blocks, bs)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    free = dev(rng.permutation(num_blocks).astype(np.int32))
+    # the prompt: one request of `shared` new positions
+    table1, slots1, len1, taken = i32(1, maxb), i32(1, shared), i32(1), [i32(1), i32(1)]
+    ab.paged_build_tables(table1, slots1, len1, taken[1], i32(1), dev(np.array([shared], np.int32)), free, num_blocks,
+                          taken[0], None, 0, 1, shared, num_blocks, bs, maxb)
+    kv1 = ab.paged_kv(pool, table1, num_blocks, bs, maxb)
+    lg, _ = m.new_outputs(1, shared, probs=False)
+    m.prefill_slots(dev(seq[:1, :shared]), lg, kv1, slots1)
+    assert_close(host(lg)[0][:, :cfg.vocab_size], ref_logits[0, :shared, :cfg.vocab_size], atol=LOGIT_TOL[precision],
+                 what="prompt")
+    prefix_blocks = table1[0, :shared // bs].clone()
+    # the continuations: one position a step, all buffers on the GPU
+    table, lens = i32(B, maxb), [torch.full((B,), shared, dtype=torch.int32, device="cuda"), i32(B)]
+    kv = ab.paged_kv(pool, table, num_blocks, bs, maxb)
+    ws = m.new_shared_workspace(B, shared)
+    logits, _ = m.new_outputs(B, None, probs=False)
+    plain, _ = m.new_outputs(B, None, probs=False)
+    toks = dev(seq)
+    cur = 1
+    for i, t in enumerate(range(shared, prompt + steps - 1)):
+        a, b = i % 2, 1 - i % 2
+        ab.paged_build_tables(table, None, lens[b], taken[1 - cur], lens[a], None, free, num_blocks, taken[cur],
+                              prefix_blocks, shared, B, 1, num_blocks, bs, maxb)
+        cur = 1 - cur
+        tok = toks[:, t].contiguous()
+        m.decode_step_shared(kv, tok, lens[a], shared, logits, ws)
+        got = host(logits)[:, :cfg.vocab_size]
+        assert_close(got[:len(ref_logits)], ref_logits[:, t, :cfg.vocab_size], atol=LOGIT_TOL[precision],
+                     what=f"step {t}")
+        # the unshared step over the same cache agrees to the precision's rounding
+        m.decode_step_paged(kv, tok, lens[a], plain)
+        assert_close(host(plain)[:, :cfg.vocab_size], got, atol=LOGIT_TOL[precision], what="unshared")
+        nxt = toks[:, t + 1].contiguous()
+        r = m.logprobs(logits, nxt, top=top)
+        lp = torch.log_softmax(logits[:, :cfg.vocab_size].double(), 1)
+        assert (r["logprob"] - lp.gather(1, nxt.long()[:, None])[:, 0]).abs().max() < 1e-5
+        best = torch.topk(lp, top, 1)
+        assert (r["top_logprobs"] - best.values).abs().max() < 1e-5
+        assert torch.equal(lens[b], lens[a] + 1)
+    no_device_error()
+
+
+def test_prefill_slots_leaves_padding_out():
+    """A padded batch of prompts of different lengths: the outputs are the
+    forward pass's, the cache holds what gpt2_prefill_paged writes at the
+    stored positions, and nothing else of the pool changes; a slot past the
+    pool is flagged."""
+    w = inputs.WORKLOADS["tiny"]
+    cfg = w.cfg
+    params, tok = inputs.workload_inputs(w, "perturbed")
+    B, T = tok.shape
+    for precision in ALL:
+        m = GPT2Model(cfg, params, B, T, precision)
+        bs, maxb = 8, 8
+        num_blocks = B * maxb + 5
+        table = torch.arange(B * maxb, dtype=torch.int32).view(B, maxb).cuda()
+        kv = ab.paged_kv(None, table, num_blocks, bs, maxb)
+        lens = torch.tensor([T, 13][:B])
+        t = torch.arange(T)
+        slots = torch.where(t < lens[:, None], table.cpu()[:, t // bs] * bs + t % bs, -1).int().cuda()
+        ref_pool, pool = m.new_paged_kvcache(num_blocks, bs), m.new_paged_kvcache(num_blocks, bs)
+        lg0, _ = m.new_outputs(B, T, probs=False)
+        lg1, _ = m.new_outputs(B, T, probs=False)
+        tg = dev(tok)
+        kv.pool = ref_pool.data_ptr()
+        m.prefill_paged(tg, lg0, kv)
+        kv.pool = pool.data_ptr()
+        m.prefill_slots(tg, lg1, kv, slots)
+        assert torch.equal(lg0, lg1)
+        e = 2 if precision in (ab.GPT2_BF16, ab.GPT2_FP16) else 4
+        view = lambda p: p.view(cfg.num_layers, 2, num_blocks, cfg.num_heads, bs, -1)  # noqa: E731
+        a, b = view(ref_pool), view(pool)
+        assert a.shape[-1] == cfg.head_size * e
+        want = torch.zeros_like(a)
+        for s in range(B):
+            for p in range(int(lens[s])):
+                want[:, :, table[s, p // bs], :, p % bs] = a[:, :, table[s, p // bs], :, p % bs]
+        assert torch.equal(b, want)
+        no_device_error()
+        slots[0, 3] = num_blocks * bs
+        m.prefill_slots(tg, lg1, kv, slots)
+        assert ab.gpt2_get_error() == ab.DEVERR_BLOCK
+        assert torch.equal(view(pool), want)

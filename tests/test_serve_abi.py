@@ -1,0 +1,183 @@
+"""The calls of include/gpt2fwd_serve.h on the host: every one is exported and
+bound, sizes answer without a GPU, and invalid arguments are refused before
+anything is launched (the addresses here are aligned and never read)."""
+import ctypes
+
+import pytest
+
+from gpt_transformer_forward_gb300 import binding as ab
+from gpt_transformer_forward_gb300 import build, inputs
+
+FAKE = 1 << 20
+A, S, AL, W, U = -1, -2, -3, -4, -7  # GPT2_ERR_ARG, _SHAPE, _ALIGN, _WORKSPACE, _UNSUPPORTED
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return ab.load(build_if_missing=False)
+
+
+def refused(code, call, *args, **kw):
+    with pytest.raises(ab.GPT2Error) as e:
+        call(*args, **kw, stream=0)
+    assert e.value.code == code, (e.value.code, code)
+
+
+def test_every_declared_function_is_bound(lib):
+    names = ab.header_functions("gpt2fwd_serve.h")
+    assert sorted(names) == sorted(ab._SERVE_SIGNATURES)
+    for n in names:
+        assert hasattr(lib, n), n
+    assert not set(names) & set(ab.header_functions())
+
+
+TABLES = dict(block_table=FAKE, slots=FAKE, next_len=FAKE + 64, taken_out=FAKE + 128, cached_len=FAKE + 192,
+              new_len=FAKE + 256, free_blocks=FAKE, num_free=4, taken_in=FAKE + 320, prefix_blocks=None, prefix_len=0,
+              B=2, T=3, num_blocks=10, block_size=16, max_blocks_per_seq=8)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(block_table=None), A), (dict(cached_len=None), A), (dict(B=-1), A), (dict(T=-1), A), (dict(num_free=-1), A),
+    (dict(free_blocks=None), A), (dict(num_blocks=0), A), (dict(block_size=0), A), (dict(block_size=24), A),
+    (dict(max_blocks_per_seq=0), A), (dict(prefix_len=16), A), (dict(prefix_blocks=FAKE), A),
+    (dict(prefix_len=-16, prefix_blocks=FAKE), A), (dict(taken_out=FAKE + 320), A), (dict(next_len=FAKE + 192), A),
+    (dict(next_len=FAKE + 256), A),
+    (dict(prefix_len=8, prefix_blocks=FAKE), S), (dict(prefix_len=160, prefix_blocks=FAKE), S),
+    (dict(B=65537), S), (dict(max_blocks_per_seq=1025), S), (dict(num_blocks=1 << 27), S),
+    (dict(slots=FAKE + 2), AL), (dict(taken_out=FAKE + 1), AL), (dict(cached_len=FAKE + 3), AL),
+])
+def test_tables_refuse(change, code):
+    refused(code, ab.paged_build_tables, **{**TABLES, **change})
+
+
+def shared_args(**kw):
+    d = dict(out=FAKE, qkv=2 * FAKE, kv=ab.paged_kv(FAKE, FAKE, 64, 16, 32), pos=FAKE, B=4, C=256, NH=4, prefix_len=100,
+             precision=ab.GPT2_FP16, workspace=FAKE, ws_bytes=1 << 30)
+    d.update(kw)
+    return d
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(out=None), A), (dict(qkv=None), A), (dict(kv=None), A), (dict(pos=None), A), (dict(B=-1), A),
+    (dict(C=0), A), (dict(NH=0), A), (dict(prefix_len=-1), A), (dict(precision=4), A), (dict(qkv=FAKE), A),
+    (dict(kv=ab.paged_kv(None, FAKE, 64, 16, 32)), A), (dict(kv=ab.paged_kv(FAKE, None, 64, 16, 32)), A),
+    (dict(kv=ab.paged_kv(FAKE, FAKE, 0, 16, 32)), A), (dict(kv=ab.paged_kv(FAKE, FAKE, 64, 12, 32)), A),
+    (dict(kv=ab.paged_kv(FAKE, FAKE, 64, 16, 0)), A),
+    (dict(NH=3), S), (dict(kv=ab.paged_kv(FAKE, FAKE, 64, 16, 1025)), S), (dict(prefix_len=512), S),
+    (dict(B=65536), S), (dict(C=512), U), (dict(C=96), U),
+    (dict(workspace=None), W), (dict(ws_bytes=16), W),
+    (dict(out=FAKE + 8), AL), (dict(qkv=FAKE + 8), AL), (dict(workspace=FAKE + 8), AL), (dict(pos=FAKE + 2), AL),
+    (dict(kv=ab.paged_kv(FAKE + 8, FAKE, 64, 16, 32)), AL),
+])
+def test_shared_prefix_refuses(change, code):
+    refused(code, ab.attention_shared_prefix, **shared_args(**change))
+
+
+def test_shared_prefix_sizes():
+    size = ab.attention_shared_prefix_workspace_size
+    assert size(4, 256, 4, 0, ab.GPT2_FP16) == 0
+    for bad in [(0, 256, 4, 10, 3), (4, 256, 3, 10, 3), (4, 512, 4, 10, 3), (4, 256, 4, -1, 3), (4, 256, 4, 10, 9),
+                (65536, 256, 4, 10, 3)]:
+        assert size(*bad) == 0, bad
+    # a workspace for a batch serves smaller ones and shorter prefixes
+    for precision in (ab.GPT2_FP32, ab.GPT2_FP16):
+        for P in (1, 64, 65, 1000, 3328, 3329, 20000):
+            for B in (1, 16, 17, 32, 33, 64, 65, 128, 129, 300):
+                most = size(B, 768, 12, P, precision)
+                assert most > 0
+                for b in (1, B // 2 + 1, B - 1):
+                    assert b < 1 or size(b, 768, 12, P, precision) <= most, (precision, P, B, b)
+                for q in (1, P // 2 + 1, P - 1):
+                    assert q < 1 or size(B, 768, 12, q, precision) <= most, (precision, P, B, q)
+    cfg = inputs.TINY
+    base = ab.gpt2_workspace_size(cfg, 3, 1, ab.GPT2_FP16)
+    assert ab.gpt2_shared_workspace_size(cfg, 3, 0, ab.GPT2_FP16) == base
+    assert ab.gpt2_shared_workspace_size(cfg, 3, 40, ab.GPT2_FP16) == base + size(3, 64, 4, 40, ab.GPT2_FP16)
+    assert ab.gpt2_shared_workspace_size(cfg, 3, -1, ab.GPT2_FP16) == 0
+
+
+def step_args(**kw):
+    d = dict(cfg=inputs.TINY, params=FAKE, packed=FAKE, kv=ab.paged_kv(FAKE, FAKE, 64, 16, 4), tok=FAKE, pos=FAKE, B=4,
+             prefix_len=32, logits=FAKE, probs=None, workspace=FAKE, ws_bytes=1 << 30, precision=ab.GPT2_FP16)
+    d.update(kw)
+    return d
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(params=None), A), (dict(tok=None), A), (dict(pos=None), A), (dict(logits=None), A), (dict(workspace=None), A),
+    (dict(kv=None), A), (dict(packed=None), A), (dict(B=0), A), (dict(prefix_len=-1), A), (dict(precision=7), A),
+    (dict(prefix_len=64), S), (dict(kv=ab.paged_kv(FAKE, FAKE, 64, 16, 2)), S), (dict(B=65536), S),
+    (dict(ws_bytes=100), W), (dict(logits=FAKE + 4), AL), (dict(workspace=FAKE + 16), AL),
+])
+def test_shared_step_refuses(change, code):
+    refused(code, ab.gpt2_decode_step_shared, **step_args(**change))
+
+
+def slots_args(**kw):
+    d = dict(cfg=inputs.TINY, params=FAKE, packed=FAKE, tok=FAKE, B=4, T=8, logits=FAKE, probs=None,
+             kv=ab.paged_kv(FAKE, None, 64, 16, 0), slots=FAKE, workspace=FAKE, ws_bytes=1 << 30,
+             precision=ab.GPT2_FP16)
+    d.update(kw)
+    return d
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(slots=None), A), (dict(kv=None), A), (dict(tok=None), A), (dict(T=0), A), (dict(packed=None), A),
+    (dict(kv=ab.paged_kv(None, None, 64, 16, 0)), A), (dict(kv=ab.paged_kv(FAKE, None, 64, 20, 0)), A),
+    (dict(kv=ab.paged_kv(FAKE, None, 0, 16, 0)), A), (dict(kv=ab.paged_kv(FAKE, None, 1 << 27, 16, 0)), S),
+    (dict(T=65), S), (dict(ws_bytes=64), W), (dict(slots=FAKE + 1), AL),
+    (dict(kv=ab.paged_kv(FAKE + 8, None, 64, 16, 0)), AL),
+])
+def test_prefill_slots_refuses(change, code):
+    refused(code, ab.gpt2_prefill_slots, **slots_args(**change))
+
+
+def lp_args(**kw):
+    d = dict(logprob=FAKE, entropy=FAKE, lse=FAKE, top_ids=FAKE, top_logprobs=FAKE, logits=FAKE,
+             logits_type=ab.GPT2_PROBS_F32, targets=FAKE, N=2, V=10, Vp=12, K=3)
+    d.update(kw)
+    return d
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(logits=None), A), (dict(targets=None), A), (dict(N=-1), A), (dict(V=0), A), (dict(V=13), A), (dict(K=-1), A),
+    (dict(logits_type=3), A), (dict(logits_type=-1), A), (dict(Vp=14), S), (dict(K=33), S),
+    (dict(logits_type=ab.GPT2_PROBS_F16), S), (dict(logits_type=ab.GPT2_PROBS_BF16), S),
+    (dict(logits=FAKE + 8), AL), (dict(lse=FAKE + 2), AL), (dict(targets=FAKE + 1), AL),
+])
+def test_logprobs_refuse(change, code):
+    refused(code, ab.logprobs_forward, **lp_args(**change))
+
+
+def test_nothing_to_do_is_no_launch(lib):
+    # no rows, or no output asked for: an answer without a GPU
+    ab.logprobs_forward(**lp_args(N=0), stream=0)
+    ab.logprobs_forward(**lp_args(logprob=None, entropy=None, lse=None, K=0), stream=0)
+    ab.attention_shared_prefix(**shared_args(B=0), stream=0)
+    ab.paged_build_tables(**{**TABLES, "B": 0, "taken_out": None}, stream=0)
+
+
+def lb_args(**kw):
+    d = dict(dlogits=FAKE, logits=FAKE, logits_type=ab.GPT2_PROBS_F32, targets=FAKE, lse=FAKE, entropy=FAKE,
+             dlogprob=FAKE, dentropy=FAKE, N=2, V=10, Vp=12)
+    d.update(kw)
+    return d
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(dlogits=None), A), (dict(logits=None), A), (dict(lse=None), A), (dict(targets=None), A),
+    (dict(entropy=None), A), (dict(V=0), A), (dict(Vp=9), A), (dict(logits_type=5), A), (dict(Vp=14), S),
+    (dict(logits_type=ab.GPT2_PROBS_F16), S), (dict(dlogits=FAKE + 4), AL), (dict(dentropy=FAKE + 2), AL),
+])
+def test_logprobs_backward_refuses(change, code):
+    refused(code, ab.logprobs_backward, **lb_args(**change))
+
+
+def test_element_types():
+    import torch
+    assert ab.element_type(torch.empty(1)) == ab.GPT2_PROBS_F32
+    assert ab.element_type(torch.empty(1, dtype=torch.bfloat16)) == ab.GPT2_PROBS_BF16
+    with pytest.raises(TypeError):
+        ab.element_type(torch.empty(1, dtype=torch.float64))
+    assert ctypes.sizeof(ab.GPT2PagedKVCache) == 32
