@@ -997,8 +997,9 @@ int logprobs_forward(float* logprob, float* entropy, float* lse, int* top_ids, f
     RETURN_IF((reinterpret_cast<uintptr_t>(p) & 3u) != 0, GPT2_ERR_ALIGN);
   if (K == 0) top_ids = nullptr, top_logprobs = nullptr;
   if (N == 0 || (!logprob && !entropy && !lse && !top_ids && !top_logprobs)) return GPT2_OK;
-  launch_logprobs(logprob, entropy, lse, top_ids, top_logprobs, logits, logits_type, targets, N, V, Vp, K,
-                  as_stream(stream));
+  PdlScope pdl(true);  // the kernel waits for its predecessor itself
+  TRY(launch_logprobs(logprob, entropy, lse, top_ids, top_logprobs, logits, logits_type, targets, N, V, Vp, K,
+                      as_stream(stream)));
   return check_launch();
 }
 
@@ -1014,8 +1015,9 @@ int logprobs_backward(void* dlogits, const void* logits, int logits_type, const 
                         static_cast<const void*>(dentropy)})
     RETURN_IF((reinterpret_cast<uintptr_t>(p) & 3u) != 0, GPT2_ERR_ALIGN);
   if (N == 0) return GPT2_OK;
-  launch_logprobs_backward(dlogits, logits, logits_type, targets, lse, entropy, dlogprob, dentropy, N, V, Vp,
-                           as_stream(stream));
+  PdlScope pdl(true);  // the kernel waits for its predecessor itself
+  TRY(launch_logprobs_backward(dlogits, logits, logits_type, targets, lse, entropy, dlogprob, dentropy, N, V, Vp,
+                               as_stream(stream)));
   return check_launch();
 }
 

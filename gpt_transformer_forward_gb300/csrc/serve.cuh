@@ -51,10 +51,10 @@ void launch_shared_decode_attention(void* out, const void* qkv, void* kcache, vo
                                     cudaStream_t s);
 
 // vocab.cu
-void launch_logprobs(float* logprob, float* entropy, float* lse, int* top_ids, float* top_logprobs, const void* logits,
-                     int logits_type, const int* targets, int N, int V, int Vp, int K, cudaStream_t s);
-void launch_logprobs_backward(void* dlogits, const void* logits, int logits_type, const int* targets, const float* lse,
-                              const float* entropy, const float* dlogprob, const float* dentropy, int N, int V, int Vp,
-                              cudaStream_t s);
+int launch_logprobs(float* logprob, float* entropy, float* lse, int* top_ids, float* top_logprobs, const void* logits,
+                    int logits_type, const int* targets, int N, int V, int Vp, int K, cudaStream_t s);
+int launch_logprobs_backward(void* dlogits, const void* logits, int logits_type, const int* targets, const float* lse,
+                             const float* entropy, const float* dlogprob, const float* dentropy, int N, int V, int Vp,
+                             cudaStream_t s);
 
 }  // namespace gpt2

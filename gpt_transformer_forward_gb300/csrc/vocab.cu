@@ -7,6 +7,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kVocThreads = 256;
+constexpr int kShortRow = 2048;  // vectors; below, blocks of 128 threads
 // From here on the backward takes a row's maximum and sum anew instead of its
 // lse, whose fp32 rounding |lse| 2^-24 is an error of every p (6e-5 here).
 constexpr float kLargeLse = 1024.f;
@@ -51,164 +52,519 @@ __device__ __forceinline__ float block_reduce(float v, float* red, F op, float n
   return v;
 }
 
-// a is listed before b: the larger value, then the lower id
-__device__ __forceinline__ bool before(float av, int ai, float bv, int bi) { return av > bv || (av == bv && ai < bi); }
+// ---------------------------------------------------------------- forward
+// One pass over a row.  A thread walks 16-byte vectors tid, tid + kT, ... with
+// its running maximum m, s = sum e^(x - m) and w = sum e^(x - m) (x - m); when m
+// grows to m', s' = s e^(m - m') and w' = (w + s (m - m')) e^(m - m').  Pairs
+// (m, s, w) of threads, warps and blocks join the same way, and
+//   lse = m + log s,  entropy = log s - w / s.
+// x - m is taken before the scaling to log2 units, so that logits near the
+// type's limits neither overflow nor lose their differences.
+struct Stat {
+  float m, s, w;
+};
+// (-inf, 0, 0) is the empty sum; NaN (or +inf - +inf) ends up in s
+__device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
+  const float m = fmaxf(a.m, b.m);
+  const float da = a.m == -INFINITY ? 0.f : a.m - m, db = b.m == -INFINITY ? 0.f : b.m - m;
+  const float fa = exp2_approx(da * kLog2e), fb = exp2_approx(db * kLog2e);
+  // a difference past fp32's range has the factor 0, not 0 * inf
+  return Stat{m, a.s * fa + b.s * fb, fmaf(a.s, fmaxf(da, -200.f), a.w) * fa + fmaf(b.s, fmaxf(db, -200.f), b.w) * fb};
+}
+__device__ __forceinline__ Stat warp_join(Stat v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = join(v, Stat{__shfl_xor_sync(0xffffffffu, v.m, o), __shfl_xor_sync(0xffffffffu, v.s, o),
+                     __shfl_xor_sync(0xffffffffu, v.w, o)});
+  return v;
+}
 
-// One block per row: the maximum, then the sums, then K searches for the next
-// alternative.
-template <typename T>
-__global__ void __launch_bounds__(kVocThreads) logprobs_kernel(float* __restrict__ logprob, float* __restrict__ entropy,
-                                                               float* __restrict__ lse_out, int* __restrict__ top_ids,
-                                                               float* __restrict__ top_logprobs,
-                                                               const T* __restrict__ logits,
-                                                               const int* __restrict__ targets, int V, int Vp, int K) {
-  __shared__ float red[32], sv[32];
-  __shared__ int si[32];
-  const size_t n = blockIdx.x;
-  const T* row = logits + n * Vp;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  auto fmx = [](float a, float b) { return fmaxf(a, b); };
-  auto add = [](float a, float b) { return a + b; };
-  float m = -INFINITY;
-  for (int v = threadIdx.x; v < V; v += blockDim.x) m = fmaxf(m, to_f32(row[v]));
-  m = block_reduce(m, red, fmx, -INFINITY);
-  const float m0 = m == -INFINITY ? 0.f : m;
-  float s = 0.f, w = 0.f;
-  for (int v = threadIdx.x; v < V; v += blockDim.x) {
-    const float d = to_f32(row[v]) - m0, e = exp2_approx(d * kLog2e);
-    s += e;
-    w = fmaf(e, fmaxf(d, -200.f), w);
+// max(a, b), NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Top alternatives are ordered by 64-bit keys: the value's bits in an order
+// that compares like the value (-0 as 0), then the lowest index first.
+typedef unsigned long long Key;
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return (b & 0x80000000u) != 0u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) != 0u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ Key key_of(float x, uint32_t index) {
+  return (static_cast<Key>(ordered(x)) << 32) | (0xffffffffu - index);
+}
+
+constexpr int kGroups = 128;         // groups of threads that propose a threshold
+constexpr int kMaxCandidates = 1024;
+
+template <int kT>
+struct TopSmem {
+  Key group[kGroups];
+  Key tau;                          // the K-th largest group's best vector (0: fewer than K)
+  int n_threads, n_cand;
+  uint16_t thread[kT];
+  Key cand[kMaxCandidates];
+};
+struct RowSmem {
+  Stat warp[32];
+  Stat block;
+  Key top[GPT2_LOGPROBS_MAX_TOP];   // this block's alternatives, largest first (0: none)
+};
+
+struct ForwardArgs {
+  float* logprob;
+  float* entropy;
+  float* lse;
+  int* top_ids;
+  float* top_logprobs;
+  const int* targets;
+  int V, Vp, K;
+};
+
+// The K largest elements of this block's vectors [lo, hi) into rs.top.  Each
+// thread brings its best vector (best, at vector index best_vec).  A group's
+// best is the largest of its threads', and tau, the K-th largest group's,
+// cannot exceed the K-th largest element: at least K elements are no less than
+// it in the order (value, lower vector first).  Those elements lie with
+// threads whose own best is >= tau, about K of them, whose vectors all threads
+// read again together (a few per cent of the row, from L2); the elements found
+// are ranked by counting.  Equal values do not add candidates, since vectors
+// are ordered by index; a row in which a few threads hold all the largest
+// elements may exceed the candidate buffer and is searched K times instead.
+template <typename T, int kT>
+__device__ __forceinline__ void select_top(RowSmem& rs, TopSmem<kT>& ts, const uint4* row, int lo, int hi, int V, int K,
+                                           float best, int best_vec) {
+  constexpr int kN = Vec<T>::n;
+  const int tid = threadIdx.x;
+  const Key mine = best > -INFINITY ? key_of(best, static_cast<uint32_t>(best_vec)) : 0ull;
+  Key g = mine;
+#pragma unroll
+  for (int o = kT / kGroups / 2; o > 0; o >>= 1) {
+    const Key other = __shfl_xor_sync(0xffffffffu, g, o);
+    g = other > g ? other : g;
   }
-  s = block_reduce(s, red, add, 0.f);
-  w = block_reduce(w, red, add, 0.f);
-  const bool nan = !(s >= 0.f) || m == INFINITY, none = s == 0.f;
-  const float ls = logf(s), lse = nan ? NAN : (none ? -INFINITY : m0 + ls);
-  if (threadIdx.x == 0) {
-    if (lse_out != nullptr) lse_out[n] = lse;
-    if (entropy != nullptr) entropy[n] = nan ? NAN : (none ? 0.f : ls - w / s);
-    if (logprob != nullptr) {
-      const int t = targets[n];
-      float lp = 0.f;
-      if (t < -1 || t >= V)
-        set_error(GPT2_DEVERR_TOKEN);
-      else if (t >= 0)
-        lp = nan ? NAN : (none ? -INFINITY : (to_f32(row[t]) - m0) - ls);
-      logprob[n] = lp;
+  if (tid % (kT / kGroups) == 0) ts.group[tid / (kT / kGroups)] = g;
+  if (tid == 0) {
+    ts.tau = 0ull;
+    ts.n_threads = 0;
+    ts.n_cand = 0;
+  }
+  if (tid < K) rs.top[tid] = 0ull;
+  __syncthreads();
+  if (tid < kGroups) {
+    const Key k = ts.group[tid];
+    int rank = 0;
+#pragma unroll 8
+    for (int i = 0; i < kGroups; ++i) rank += ts.group[i] > k ? 1 : 0;
+    if (rank == K - 1 && k != 0ull) ts.tau = k;  // keys other than 0 are distinct
+  }
+  __syncthreads();
+  const Key tau = ts.tau;
+  if (mine != 0ull && mine >= tau) ts.thread[atomicAdd(&ts.n_threads, 1)] = static_cast<uint16_t>(tid);
+  __syncthreads();
+  const int per = (hi - lo + kT - 1) / kT;  // vectors of a thread, at most
+  const uint32_t tau_value = static_cast<uint32_t>(tau >> 32);
+  const int tau_vec = static_cast<int>(0xffffffffu - static_cast<uint32_t>(tau));
+  const int total = ts.n_threads * per;
+  for (int i = tid; i < total; i += kT) {
+    const int vec = lo + ts.thread[i / per] + (i % per) * kT;
+    if (vec >= hi) continue;
+    const Vec<T> v = widen<T>(__ldg(row + vec));
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const uint32_t o = ordered(v.x[j]);
+      const int id = vec * kN + j;
+      if (id >= V || !(v.x[j] > -INFINITY)) continue;
+      if (tau != 0ull && (o < tau_value || (o == tau_value && vec > tau_vec))) continue;
+      const int at = atomicAdd(&ts.n_cand, 1);
+      if (at < kMaxCandidates) ts.cand[at] = (static_cast<Key>(o) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
     }
   }
-  if (top_ids == nullptr && top_logprobs == nullptr) return;
-  float pv = INFINITY;
-  int pi = -1;
-  for (int k = 0; k < K; ++k) {
-    float bv = -INFINITY;
-    int bi = 0x7fffffff;
-    for (int v = threadIdx.x; v < V; v += blockDim.x) {
-      const float x = to_f32(row[v]);
-      if (before(pv, pi, x, v) && before(x, v, bv, bi)) {
-        bv = x;
-        bi = v;
+  __syncthreads();
+  const int n = ts.n_cand;
+  if (n <= kMaxCandidates) {
+    for (int c = tid; c < n; c += kT) {
+      const Key k = ts.cand[c];
+      int rank = 0;
+      for (int i = 0; i < n; ++i) rank += ts.cand[i] > k ? 1 : 0;
+      if (rank < K) rs.top[rank] = k;
+    }
+  } else {
+    Key last = ~0ull;
+    for (int r = 0; r < K && last != 0ull; ++r) {
+      Key b = 0ull;
+      for (int vec = lo + tid; vec < hi; vec += kT) {
+        const Vec<T> v = widen<T>(__ldg(row + vec));
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+          if (vec * kN + j >= V || !(v.x[j] > -INFINITY)) continue;
+          const Key k = key_of(v.x[j], static_cast<uint32_t>(vec * kN + j));
+          if (k < last && k > b) b = k;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const Key other = __shfl_xor_sync(0xffffffffu, b, o);
+        b = other > b ? other : b;
+      }
+      if ((tid & 31) == 0) ts.group[tid >> 5] = b;
+      __syncthreads();
+      for (int i = 0; i < kT / 32; ++i) b = ts.group[i] > b ? ts.group[i] : b;
+      if (tid == 0) rs.top[r] = b;
+      last = b;
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+}
+
+// The blocks of a cluster share a row (one block: the whole row).  kU vectors
+// per thread in flight.
+template <typename T, int kT, bool kTop>
+__global__ void __launch_bounds__(kT) logprobs_kernel(const T* __restrict__ logits, ForwardArgs a, int parts) {
+  constexpr int kN = Vec<T>::n, kU = 4;
+  __shared__ RowSmem rs;
+  __shared__ TopSmem<kTop ? kT : 1> ts;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const size_t n = blockIdx.x / parts;
+  const int part = static_cast<int>(blockIdx.x % parts);
+  const uint4* row = reinterpret_cast<const uint4*>(logits + n * a.Vp);
+  const int vecs = (a.V + kN - 1) / kN, share = (vecs + parts - 1) / parts;
+  const int lo = min(vecs, part * share), hi = min(vecs, lo + share);
+  const int full = min(hi, a.V / kN);  // vectors of real tokens only
+  pdl_wait();
+  pdl_trigger();
+  // the target's logit is asked for ahead of the row
+  int target = -1;
+  float xt = 0.f;
+  if (tid == 0 && part == 0 && a.logprob != nullptr) {
+    target = a.targets[n];
+    if (target < -1 || target >= a.V) {
+      set_error(GPT2_DEVERR_TOKEN);
+      target = -1;
+    }
+    if (target >= 0) xt = to_f32(logits[n * a.Vp + target]);
+  }
+  Stat st{-INFINITY, 0.f, 0.f};
+  int best_vec = 0;
+  auto largest = [](const Vec<T>& v) {
+    float mx = fmax3(v.x[0], v.x[1], fmaxf(v.x[2], v.x[3]));
+    if constexpr (kN == 8) mx = fmax3(mx, fmax3(v.x[4], v.x[5], v.x[6]), v.x[7]);
+    return mx;
+  };
+  auto raise = [&](float to) {  // the maximum grows
+    if (st.m != -INFINITY) {
+      const float d = st.m - to, f = exp2_approx(d * kLog2e);
+      st.w = fmaf(st.s, fmaxf(d, -200.f), st.w) * f;
+      st.s *= f;
+    }
+    st.m = to;
+  };
+  auto add = [&](const Vec<T>& v) {
+    const float m0 = st.m == -INFINITY ? 0.f : st.m;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      // -inf as -200: its term is 0 in fp32, its product with x - m too
+      const float d = max_nan(v.x[j] - m0, -200.f), e = exp2_approx(d * kLog2e);
+      st.s += e;
+      st.w = fmaf(e, d, st.w);
+    }
+  };
+  int i = lo + tid;
+  for (; i + (kU - 1) * kT < full; i += kU * kT) {
+    uint4 raw[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k) raw[k] = __ldg(row + i + k * kT);
+    float mx = st.m;
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const float x = largest(widen<T>(raw[k]));
+      if (x > mx) {  // vectors in ascending order: the first of equal ones stays
+        mx = x;
+        if (kTop) best_vec = i + k * kT;
       }
     }
+    if (mx > st.m) raise(mx);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float v2 = __shfl_xor_sync(0xffffffffu, bv, o);
-      const int i2 = __shfl_xor_sync(0xffffffffu, bi, o);
-      if (before(v2, i2, bv, bi)) bv = v2, bi = i2;
-    }
-    __syncthreads();
-    if (lane == 0) sv[wid] = bv, si[wid] = bi;
-    __syncthreads();
-    for (int i = 0; i < kVocThreads / 32; ++i)
-      if (before(sv[i], si[i], bv, bi)) bv = sv[i], bi = si[i];
-    pv = bv;
-    pi = bi;
-    if (threadIdx.x == 0) {
-      const bool gone = nan || bv == -INFINITY;
-      if (top_ids != nullptr) top_ids[n * K + k] = gone ? -1 : bi;
-      if (top_logprobs != nullptr) top_logprobs[n * K + k] = nan ? NAN : (gone ? -INFINITY : (bv - m0) - ls);
+    for (int k = 0; k < kU; ++k) add(widen<T>(raw[k]));
+  }
+  {
+    uint4 raw[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k)
+      if (i + k * kT < hi) raw[k] = __ldg(row + i + k * kT);
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const int vec = i + k * kT;
+      if (vec >= hi) break;
+      Vec<T> v = widen<T>(raw[k]);
+      if (vec >= full) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          if (vec * kN + j >= a.V) v.x[j] = -INFINITY;
+      }
+      const float x = largest(v);
+      if (x > st.m) {
+        raise(x);
+        if (kTop) best_vec = vec;
+      }
+      add(v);
     }
   }
+  const float best = st.m;
+  st = warp_join(st);
+  if (lane == 0) rs.warp[wid] = st;
+  if constexpr (kTop) {
+    select_top<T, kT>(rs, ts, row, lo, hi, a.V, a.K, best, best_vec);
+  } else {
+    __syncthreads();
+  }
+  if (wid == 0) {
+    st = lane < kT / 32 ? rs.warp[lane] : Stat{-INFINITY, 0.f, 0.f};
+    st = warp_join(st);
+    if (lane == 0) rs.block = st;
+  }
+  if (parts > 1) {
+    cluster_sync();
+    if (part != 0) {
+      cluster_sync();  // block 0 has read this block's shared memory
+      return;
+    }
+  } else {
+    __syncthreads();
+  }
+  // block 0: the row's statistics, and its alternatives from those of all parts
+  if (parts > 1 && wid == 0) {
+    st = Stat{-INFINITY, 0.f, 0.f};
+    if (lane < parts) {
+      const uint32_t at = mapa_shared(smem_u32(&rs.block), lane);
+      st = Stat{ld_shared_cluster_f32(at), ld_shared_cluster_f32(at + 4), ld_shared_cluster_f32(at + 8)};
+    }
+    st = warp_join(st);
+    if (lane == 0) rs.warp[0] = st;
+  }
+  if constexpr (kTop) {
+    if (parts > 1) {
+      for (int c = tid; c < parts * a.K; c += kT)
+        ts.cand[c] = ld_shared_cluster_u64(mapa_shared(smem_u32(&rs.top[c % a.K]), c / a.K));
+    }
+  }
+  if (parts > 1) {
+    __syncthreads();
+    st = rs.warp[0];
+  } else {
+    st = rs.block;
+  }
+  const bool nan = !(st.s >= 0.f) || st.m == INFINITY, none = st.s == 0.f;
+  const float ls = logf(st.s);
+  if (tid == 0) {
+    if (a.lse != nullptr) a.lse[n] = nan ? NAN : (none ? -INFINITY : st.m + ls);
+    if (a.entropy != nullptr) a.entropy[n] = nan ? NAN : (none ? 0.f : ls - st.w / st.s);
+    if (a.logprob != nullptr)
+      a.logprob[n] = target < 0 ? 0.f : (nan ? NAN : (none ? -INFINITY : (xt - st.m) - ls));
+  }
+  if constexpr (kTop) {
+    auto put = [&](int r, Key k) {
+      const bool gone = nan || k == 0ull;
+      if (a.top_ids != nullptr)
+        a.top_ids[n * a.K + r] = gone ? -1 : static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
+      if (a.top_logprobs != nullptr)
+        a.top_logprobs[n * a.K + r] =
+            nan ? NAN : (gone ? -INFINITY : (value_of(static_cast<uint32_t>(k >> 32)) - st.m) - ls);
+    };
+    if (parts == 1) {
+      if (tid < a.K) put(tid, rs.top[tid]);
+    } else {
+      const int total = parts * a.K;
+      for (int c = tid; c < total; c += kT) {
+        const Key k = ts.cand[c];
+        int rank = 0;
+        for (int o = 0; o < total; ++o) rank += ts.cand[o] > k || (ts.cand[o] == k && o < c) ? 1 : 0;
+        if (rank < a.K) put(rank, k);
+      }
+    }
+  }
+  if (parts > 1) cluster_sync();
 }
 
-// One element per thread and step: p from the row's lse.
+// --------------------------------------------------------------- backward
+// d = g ([v = t] - p) - h p (log p + H) = -p (g + h (log p + H)) + g [v = t]:
+// one read and one write of the row, p from its lse.  The blocks of a cluster
+// share a row, as in the forward.
+struct BackwardArgs {
+  const int* targets;
+  const float* lse;
+  const float* entropy;
+  const float* dlogprob;
+  const float* dentropy;
+  int V, Vp;
+};
+
 template <typename T>
-__global__ void __launch_bounds__(kVocThreads) logprobs_backward_kernel(
-    T* dlogits, const T* logits, const int* __restrict__ targets, const float* __restrict__ lse,
-    const float* __restrict__ entropy, const float* __restrict__ dlogprob, const float* __restrict__ dentropy, int V,
-    int Vp) {
+__global__ void __launch_bounds__(kVocThreads) logprobs_backward_kernel(T* dlogits, const T* logits, BackwardArgs a,
+                                                                        int parts) {
+  constexpr int kN = Vec<T>::n, kU = 4, kT = kVocThreads;
   __shared__ float red[32];
-  const size_t n = blockIdx.x;
-  const T* row = logits + n * Vp;
-  T* out = dlogits + n * Vp;
-  // log p = (l - L) - c
-  float L = lse[n], c = 0.f;
-  const bool none = L == -INFINITY;
-  if (!none && fabsf(L) >= kLargeLse) {
-    auto fmx = [](float a, float b) { return fmaxf(a, b); };
-    auto add = [](float a, float b) { return a + b; };
-    float m = -INFINITY, s = 0.f;
-    for (int v = threadIdx.x; v < V; v += blockDim.x) m = fmaxf(m, to_f32(row[v]));
-    L = block_reduce(m, red, fmx, -INFINITY);
-    for (int v = threadIdx.x; v < V; v += blockDim.x) s += exp2_approx((to_f32(row[v]) - L) * kLog2e);
-    c = logf(block_reduce(s, red, add, 0.f));
-  }
+  const int tid = threadIdx.x;
+  const size_t n = blockIdx.x / parts;
+  const int part = static_cast<int>(blockIdx.x % parts);
+  const T* row = logits + n * a.Vp;
+  const int vecs = a.Vp / kN, share = (vecs + parts - 1) / parts;
+  const int lo = min(vecs, part * share), hi = min(vecs, lo + share);
+  const uint4* in = reinterpret_cast<const uint4*>(row);
+  uint4* out = reinterpret_cast<uint4*>(dlogits + n * a.Vp);
+  pdl_wait();
+  pdl_trigger();
+  float L = a.lse[n], c = 0.f;  // log p = (l - L) - c
   int t = -1;
   float g = 0.f, h = 0.f, H = 0.f;
-  if (dlogprob != nullptr) {
-    t = targets[n];
-    if (t < -1 || t >= V) {
-      if (threadIdx.x == 0) set_error(GPT2_DEVERR_TOKEN);
+  if (a.dlogprob != nullptr) {
+    t = a.targets[n];
+    if (t < -1 || t >= a.V) {
+      if (tid == 0 && part == 0) set_error(GPT2_DEVERR_TOKEN);
       t = -1;
     }
-    if (t >= 0) g = dlogprob[n];
+    if (t >= 0) g = a.dlogprob[n];
   }
-  if (dentropy != nullptr) {
-    h = dentropy[n];
-    H = entropy[n];
+  if (a.dentropy != nullptr) {
+    h = a.dentropy[n];
+    H = a.entropy[n];
   }
-  __syncthreads();  // (in place) the row has been read above
-  for (int v = threadIdx.x; v < Vp; v += blockDim.x) {
-    float d = 0.f;
-    if (v < V && !none) {
-      const float lp = (to_f32(row[v]) - L) - c, p = exp2_approx(lp * kLog2e);
-      d = -p * fmaf(h, fmaxf(lp, -200.f) + H, g);
-      if (v == t) d += g;
+  const bool none = L == -INFINITY;
+  if (!none && fabsf(L) >= kLargeLse) {
+    auto fmx = [](float x, float y) { return fmaxf(x, y); };
+    auto add = [](float x, float y) { return x + y; };
+    float m = -INFINITY, s = 0.f;
+    for (int v = tid; v < a.V; v += kT) m = fmaxf(m, to_f32(row[v]));
+    L = block_reduce(m, red, fmx, -INFINITY);
+    for (int v = tid; v < a.V; v += kT) s += exp2_approx((to_f32(row[v]) - L) * kLog2e);
+    c = logf(block_reduce(s, red, add, 0.f));
+    // (in place) every block of the row has read it before any writes
+    if (parts > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+  }
+  const float gH = fmaf(h, H, g);  // d = -p (h log p + (g + h H))
+  auto grad = [&](float x) {
+    const float lp = (x - L) - c, p = exp2_approx(lp * kLog2e);
+    return -p * fmaf(h, max_nan(lp, -200.f), gH);
+  };
+  auto one = [&](int vec, const uint4& raw) {
+    Vec<T> v = widen<T>(raw);
+    const int v0 = vec * kN;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v.x[j] = none ? 0.f : grad(v.x[j]);
+    if (v0 + kN > a.V || (t >= v0 && t < v0 + kN)) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        if (v0 + j == t && !none) v.x[j] += g;
+        if (v0 + j >= a.V) v.x[j] = 0.f;
+      }
     }
-    out[v] = from_f32<T>(d);
+    uint4 r;
+    if constexpr (kN == 4)
+      r = make_uint4(__float_as_uint(v.x[0]), __float_as_uint(v.x[1]), __float_as_uint(v.x[2]),
+                     __float_as_uint(v.x[3]));
+    else
+      r = make_uint4(pack2<T>(v.x[0], v.x[1]), pack2<T>(v.x[2], v.x[3]), pack2<T>(v.x[4], v.x[5]),
+                     pack2<T>(v.x[6], v.x[7]));
+    __stcs(out + vec, r);
+  };
+  int i = lo + tid;
+  for (; i + (kU - 1) * kT < hi; i += kU * kT) {
+    uint4 raw[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k) raw[k] = __ldcs(in + i + k * kT);
+#pragma unroll
+    for (int k = 0; k < kU; ++k) one(i + k * kT, raw[k]);
+  }
+  {
+    uint4 raw[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k)
+      if (i + k * kT < hi) raw[k] = __ldcs(in + i + k * kT);
+#pragma unroll
+    for (int k = 0; k < kU; ++k)
+      if (i + k * kT < hi) one(i + k * kT, raw[k]);
   }
 }
 
-template <typename T>
-void logprobs_typed(float* logprob, float* entropy, float* lse, int* top_ids, float* top_logprobs, const void* logits,
-                    const int* targets, int N, int V, int Vp, int K, cudaStream_t s) {
-  logprobs_kernel<T><<<N, kVocThreads, 0, s>>>(logprob, entropy, lse, top_ids, top_logprobs,
-                                               static_cast<const T*>(logits), targets, V, Vp, K);
+// Launches a kernel over N rows, `parts` blocks of a cluster to a row.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_rows(void (*kern)(KArgs...), int threads, int N, int parts, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(N) * parts);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(parts);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // the kernels wait for their predecessor
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_on() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+// Blocks that share a row: enough to cover the SMs twice when rows are few,
+// each with a vector for every thread at least (8: the largest portable
+// cluster).
+int row_parts(int N, int vecs, int threads) {
+  int parts = 1;
+  while (parts < 8 && static_cast<long long>(N) * parts < 2LL * num_sms() && vecs >= 2 * parts * threads) parts *= 2;
+  return parts;
 }
 
 template <typename T>
-void backward_typed(void* dlogits, const void* logits, const int* targets, const float* lse, const float* entropy,
-                    const float* dlogprob, const float* dentropy, int N, int V, int Vp, cudaStream_t s) {
-  logprobs_backward_kernel<T><<<N, kVocThreads, 0, s>>>(static_cast<T*>(dlogits), static_cast<const T*>(logits),
-                                                        targets, lse, entropy, dlogprob, dentropy, V, Vp);
+int logprobs_typed(const void* logits, const ForwardArgs& a, int N, cudaStream_t s) {
+  const int vecs = (a.V + Vec<T>::n - 1) / Vec<T>::n;
+  const bool top = a.top_ids != nullptr || a.top_logprobs != nullptr;
+  const T* l = static_cast<const T*>(logits);
+  cudaError_t e;
+  if (vecs < kShortRow) {
+    const int parts = row_parts(N, vecs, 128);
+    e = launch_rows(top ? logprobs_kernel<T, 128, true> : logprobs_kernel<T, 128, false>, 128, N, parts, s, l, a, parts);
+  } else {
+    const int parts = row_parts(N, vecs, 512);
+    e = launch_rows(top ? logprobs_kernel<T, 512, true> : logprobs_kernel<T, 512, false>, 512, N, parts, s, l, a, parts);
+  }
+  return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
+}
+
+template <typename T>
+int backward_typed(void* dlogits, const void* logits, const BackwardArgs& a, int N, cudaStream_t s) {
+  const int parts = row_parts(N, a.Vp / Vec<T>::n, kVocThreads);
+  const cudaError_t e = launch_rows(logprobs_backward_kernel<T>, kVocThreads, N, parts, s, static_cast<T*>(dlogits),
+                                    static_cast<const T*>(logits), a, parts);
+  return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
 }
 
 }  // namespace
 
-void launch_logprobs(float* logprob, float* entropy, float* lse, int* top_ids, float* top_logprobs, const void* logits,
-                     int logits_type, const int* targets, int N, int V, int Vp, int K, cudaStream_t s) {
-  auto go = logits_type == kProbsF16    ? logprobs_typed<__half>
-            : logits_type == kProbsBF16 ? logprobs_typed<__nv_bfloat16>
-                                        : logprobs_typed<float>;
-  go(logprob, entropy, lse, top_ids, top_logprobs, logits, targets, N, V, Vp, K, s);
+int launch_logprobs(float* logprob, float* entropy, float* lse, int* top_ids, float* top_logprobs, const void* logits,
+                    int logits_type, const int* targets, int N, int V, int Vp, int K, cudaStream_t s) {
+  const ForwardArgs a{logprob, entropy, lse, top_ids, top_logprobs, targets, V, Vp, K};
+  if (logits_type == kProbsF16) return logprobs_typed<__half>(logits, a, N, s);
+  if (logits_type == kProbsBF16) return logprobs_typed<__nv_bfloat16>(logits, a, N, s);
+  return logprobs_typed<float>(logits, a, N, s);
 }
 
-void launch_logprobs_backward(void* dlogits, const void* logits, int logits_type, const int* targets, const float* lse,
-                              const float* entropy, const float* dlogprob, const float* dentropy, int N, int V, int Vp,
-                              cudaStream_t s) {
-  auto go = logits_type == kProbsF16    ? backward_typed<__half>
-            : logits_type == kProbsBF16 ? backward_typed<__nv_bfloat16>
-                                        : backward_typed<float>;
-  go(dlogits, logits, targets, lse, entropy, dlogprob, dentropy, N, V, Vp, s);
+int launch_logprobs_backward(void* dlogits, const void* logits, int logits_type, const int* targets, const float* lse,
+                             const float* entropy, const float* dlogprob, const float* dentropy, int N, int V, int Vp,
+                             cudaStream_t s) {
+  const BackwardArgs a{targets, lse, entropy, dlogprob, dentropy, V, Vp};
+  if (logits_type == kProbsF16) return backward_typed<__half>(dlogits, logits, a, N, s);
+  if (logits_type == kProbsBF16) return backward_typed<__nv_bfloat16>(dlogits, logits, a, N, s);
+  return backward_typed<float>(dlogits, logits, a, N, s);
 }
 
 }  // namespace gpt2
