@@ -2,11 +2,14 @@
 // alternatives of each row of logits, and their gradient.
 #include "serve.cuh"
 
+#include <algorithm>
+
 namespace gpt2 {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kVocThreads = 256;
+constexpr int kRowThreads = 256;
 constexpr int kShortRow = 2048;  // vectors; below, blocks of 128 threads
 // From here on the backward takes a row's maximum and sum anew instead of its
 // lse, whose fp32 rounding |lse| 2^-24 is an error of every p (6e-5 here).
@@ -63,21 +66,6 @@ __device__ __forceinline__ float block_reduce(float v, float* red, F op, float n
 struct Stat {
   float m, s, w;
 };
-// (-inf, 0, 0) is the empty sum; NaN (or +inf - +inf) ends up in s
-__device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
-  const float m = fmaxf(a.m, b.m);
-  const float da = a.m == -INFINITY ? 0.f : a.m - m, db = b.m == -INFINITY ? 0.f : b.m - m;
-  const float fa = exp2_approx(da * kLog2e), fb = exp2_approx(db * kLog2e);
-  // a difference past fp32's range has the factor 0, not 0 * inf
-  return Stat{m, a.s * fa + b.s * fb, fmaf(a.s, fmaxf(da, -200.f), a.w) * fa + fmaf(b.s, fmaxf(db, -200.f), b.w) * fb};
-}
-__device__ __forceinline__ Stat warp_join(Stat v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    v = join(v, Stat{__shfl_xor_sync(0xffffffffu, v.m, o), __shfl_xor_sync(0xffffffffu, v.s, o),
-                     __shfl_xor_sync(0xffffffffu, v.w, o)});
-  return v;
-}
 
 // max(a, b), NaN if either is
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -86,9 +74,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Top alternatives are ordered by 64-bit keys: the value's bits in an order
-// that compares like the value (-0 as 0), then the lowest index first.
-typedef unsigned long long Key;
+// A float's bits in an order that compares like the value (-0 as 0).
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);
   return (b & 0x80000000u) != 0u ? ~b : b | 0x80000000u;
@@ -96,26 +82,59 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float value_of(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) != 0u ? o & 0x7fffffffu : ~o);
 }
+
+// The statistic with its maximum raised to m.  (-inf, 0, 0) is the empty sum;
+// NaN, or +inf - +inf, ends up in s.  A difference past fp32's range gives the
+// factor 0, not 0 * inf.
+__device__ __forceinline__ Stat raised(const Stat& a, float m) {
+  const float d = a.m == -INFINITY ? 0.f : a.m - m, f = exp2_approx(d * kLog2e);
+  return Stat{m, a.s * f, fmaf(a.s, fmaxf(d, -200.f), a.w) * f};
+}
+// over the lanes of a warp
+__device__ __forceinline__ Stat warp_join(Stat v) {
+  v = raised(v, value_of(__reduce_max_sync(0xffffffffu, ordered(v.m))));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.s += __shfl_xor_sync(0xffffffffu, v.s, o);
+    v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+  }
+  return v;
+}
+
+// Top alternatives are ordered by 64-bit keys: the value, then the lowest
+// index first.  0 is no element.
+typedef unsigned long long Key;
 __device__ __forceinline__ Key key_of(float x, uint32_t index) {
   return (static_cast<Key>(ordered(x)) << 32) | (0xffffffffu - index);
 }
+__device__ __forceinline__ Key larger(Key a, Key b) { return a > b ? a : b; }
 
 constexpr int kGroups = 128;         // groups of threads that propose a threshold
 constexpr int kMaxCandidates = 1024;
+constexpr int kU = 4;                // vectors of a thread in a chunk
+constexpr int kStages = 3;           // chunks of the row stream in shared memory
 
+// kT threads compute, one more warp issues the copies
 template <int kT>
-struct TopSmem {
+struct RowSmem {
+  uint4 ring[kStages][kT * kU];
+  uint64_t full[kStages], empty[kStages];
+  Stat warp[2][kT / 32];            // by the parity of the row: a late reader is at most a row behind
+  Stat block;
+  // alternatives
+  Key top[GPT2_LOGPROBS_MAX_TOP];   // this block's, largest first
   Key group[kGroups];
+  Key cand[kMaxCandidates];
   Key tau;                          // the K-th largest group's best vector (0: fewer than K)
   int n_threads, n_cand;
   uint16_t thread[kT];
-  Key cand[kMaxCandidates];
 };
-struct RowSmem {
-  Stat warp[32];
-  Stat block;
-  Key top[GPT2_LOGPROBS_MAX_TOP];   // this block's alternatives, largest first (0: none)
-};
+
+// the threads that compute
+template <int kT>
+__device__ __forceinline__ void bar() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+}
 
 struct ForwardArgs {
   float* logprob;
@@ -124,10 +143,28 @@ struct ForwardArgs {
   int* top_ids;
   float* top_logprobs;
   const int* targets;
-  int V, Vp, K;
+  int N, V, Vp, K;
 };
 
-// The K largest elements of this block's vectors [lo, hi) into rs.top.  Each
+// keys[0 .. n) ranked by counting, eight threads to a key; put(rank, key) for
+// the K largest.  Equal keys (only 0 occurs twice) rank by their place.
+template <int kT, typename Put>
+__device__ __forceinline__ void rank_keys(const Key* keys, int n, int K, Put put) {
+  const int sub = threadIdx.x & 7;
+  for (int c = threadIdx.x >> 3; c < (n + 3) / 4 * 4; c += kT / 8) {  // whole warps: four keys each
+    const Key k = c < n ? keys[c] : 0ull;
+    int rank = 0;
+    for (int i = sub; i < n; i += 8) {
+      const Key o = keys[i];
+      rank += o > k || (o == k && i < c) ? 1 : 0;
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (sub == 0 && c < n && rank < K) put(rank, k);
+  }
+}
+
+// The K largest elements of this block's vectors [lo, hi) into sm.top.  Each
 // thread brings its best vector (best, at vector index best_vec).  A group's
 // best is the largest of its threads', and tau, the K-th largest group's,
 // cannot exceed the K-th largest element: at least K elements are no less than
@@ -138,42 +175,40 @@ struct ForwardArgs {
 // are ordered by index; a row in which a few threads hold all the largest
 // elements may exceed the candidate buffer and is searched K times instead.
 template <typename T, int kT>
-__device__ __forceinline__ void select_top(RowSmem& rs, TopSmem<kT>& ts, const uint4* row, int lo, int hi, int V, int K,
-                                           float best, int best_vec) {
-  constexpr int kN = Vec<T>::n;
+__device__ __forceinline__ void select_top(RowSmem<kT>& sm, const uint4* row, int lo, int hi, int V, int K, float best,
+                                           int best_vec) {
+  constexpr int kN = Vec<T>::n, kPer = kT / kGroups;
   const int tid = threadIdx.x;
   const Key mine = best > -INFINITY ? key_of(best, static_cast<uint32_t>(best_vec)) : 0ull;
   Key g = mine;
 #pragma unroll
-  for (int o = kT / kGroups / 2; o > 0; o >>= 1) {
-    const Key other = __shfl_xor_sync(0xffffffffu, g, o);
-    g = other > g ? other : g;
-  }
-  if (tid % (kT / kGroups) == 0) ts.group[tid / (kT / kGroups)] = g;
+  for (int o = kPer / 2; o > 0; o >>= 1) g = larger(g, __shfl_xor_sync(0xffffffffu, g, o));
+  if (tid % kPer == 0) sm.group[tid / kPer] = g;
   if (tid == 0) {
-    ts.tau = 0ull;
-    ts.n_threads = 0;
-    ts.n_cand = 0;
+    sm.tau = 0ull;
+    sm.n_threads = 0;
+    sm.n_cand = 0;
   }
-  if (tid < K) rs.top[tid] = 0ull;
-  __syncthreads();
-  if (tid < kGroups) {
-    const Key k = ts.group[tid];
+  if (tid < K) sm.top[tid] = 0ull;
+  bar<kT>();
+  {
     int rank = 0;
 #pragma unroll 8
-    for (int i = 0; i < kGroups; ++i) rank += ts.group[i] > k ? 1 : 0;
-    if (rank == K - 1 && k != 0ull) ts.tau = k;  // keys other than 0 are distinct
+    for (int i = tid % kPer; i < kGroups; i += kPer) rank += sm.group[i] > g ? 1 : 0;
+#pragma unroll
+    for (int o = kPer / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (tid % kPer == 0 && rank == K - 1 && g != 0ull) sm.tau = g;  // keys other than 0 are distinct
   }
-  __syncthreads();
-  const Key tau = ts.tau;
-  if (mine != 0ull && mine >= tau) ts.thread[atomicAdd(&ts.n_threads, 1)] = static_cast<uint16_t>(tid);
-  __syncthreads();
+  bar<kT>();
+  const Key tau = sm.tau;
+  if (mine != 0ull && mine >= tau) sm.thread[atomicAdd(&sm.n_threads, 1)] = static_cast<uint16_t>(tid);
+  bar<kT>();
   const int per = (hi - lo + kT - 1) / kT;  // vectors of a thread, at most
   const uint32_t tau_value = static_cast<uint32_t>(tau >> 32);
   const int tau_vec = static_cast<int>(0xffffffffu - static_cast<uint32_t>(tau));
-  const int total = ts.n_threads * per;
+  const int total = sm.n_threads * per;
   for (int i = tid; i < total; i += kT) {
-    const int vec = lo + ts.thread[i / per] + (i % per) * kT;
+    const int vec = lo + sm.thread[i / per] + (i % per) * kT;
     if (vec >= hi) continue;
     const Vec<T> v = widen<T>(__ldg(row + vec));
 #pragma unroll
@@ -182,19 +217,14 @@ __device__ __forceinline__ void select_top(RowSmem& rs, TopSmem<kT>& ts, const u
       const int id = vec * kN + j;
       if (id >= V || !(v.x[j] > -INFINITY)) continue;
       if (tau != 0ull && (o < tau_value || (o == tau_value && vec > tau_vec))) continue;
-      const int at = atomicAdd(&ts.n_cand, 1);
-      if (at < kMaxCandidates) ts.cand[at] = (static_cast<Key>(o) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
+      const int at = atomicAdd(&sm.n_cand, 1);
+      if (at < kMaxCandidates) sm.cand[at] = (static_cast<Key>(o) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
     }
   }
-  __syncthreads();
-  const int n = ts.n_cand;
+  bar<kT>();
+  const int n = sm.n_cand;
   if (n <= kMaxCandidates) {
-    for (int c = tid; c < n; c += kT) {
-      const Key k = ts.cand[c];
-      int rank = 0;
-      for (int i = 0; i < n; ++i) rank += ts.cand[i] > k ? 1 : 0;
-      if (rank < K) rs.top[rank] = k;
-    }
+    rank_keys<kT>(sm.cand, n, K, [&](int r, Key k) { sm.top[r] = k; });
   } else {
     Key last = ~0ull;
     for (int r = 0; r < K && last != 0ull; ++r) {
@@ -209,188 +239,206 @@ __device__ __forceinline__ void select_top(RowSmem& rs, TopSmem<kT>& ts, const u
         }
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const Key other = __shfl_xor_sync(0xffffffffu, b, o);
-        b = other > b ? other : b;
-      }
-      if ((tid & 31) == 0) ts.group[tid >> 5] = b;
-      __syncthreads();
-      for (int i = 0; i < kT / 32; ++i) b = ts.group[i] > b ? ts.group[i] : b;
-      if (tid == 0) rs.top[r] = b;
+      for (int o = 16; o > 0; o >>= 1) b = larger(b, __shfl_xor_sync(0xffffffffu, b, o));
+      if ((tid & 31) == 0) sm.group[tid >> 5] = b;
+      bar<kT>();
+      for (int i = 0; i < kT / 32; ++i) b = larger(b, sm.group[i]);
+      if (tid == 0) sm.top[r] = b;
       last = b;
-      __syncthreads();
+      bar<kT>();
     }
   }
-  __syncthreads();
+  bar<kT>();
 }
 
-// The blocks of a cluster share a row (one block: the whole row).  kU vectors
-// per thread in flight.
+// Rows stream through a ring of chunks in shared memory, copied by a warp of
+// its own (bulk copies of kT * kU vectors): the loads in flight do not wait
+// for the arithmetic nor for the search of a row's alternatives, and the next
+// row's first chunks arrive during the latter.  parts == 1: a block walks rows
+// blockIdx.x, + gridDim.x, ...; else the `parts` blocks of a cluster share the
+// one row.
 template <typename T, int kT, bool kTop>
-__global__ void __launch_bounds__(kT) logprobs_kernel(const T* __restrict__ logits, ForwardArgs a, int parts) {
-  constexpr int kN = Vec<T>::n, kU = 4;
-  __shared__ RowSmem rs;
-  __shared__ TopSmem<kTop ? kT : 1> ts;
+__global__ void __launch_bounds__(kT + 32) logprobs_kernel(const T* __restrict__ logits, ForwardArgs a, int parts) {
+  constexpr int kN = Vec<T>::n, kChunk = kT * kU;
+  extern __shared__ __align__(128) uint8_t voc_smem[];
+  RowSmem<kT>& sm = *reinterpret_cast<RowSmem<kT>*>(voc_smem);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const size_t n = blockIdx.x / parts;
-  const int part = static_cast<int>(blockIdx.x % parts);
-  const uint4* row = reinterpret_cast<const uint4*>(logits + n * a.Vp);
+  const int part = static_cast<int>(blockIdx.x) % parts;
   const int vecs = (a.V + kN - 1) / kN, share = (vecs + parts - 1) / parts;
   const int lo = min(vecs, part * share), hi = min(vecs, lo + share);
-  const int full = min(hi, a.V / kN);  // vectors of real tokens only
+  const int chunks = (hi - lo + kChunk - 1) / kChunk;
+  const int full_vecs = a.V / kN;  // vectors of real tokens only
+  const int row0 = static_cast<int>(blockIdx.x) / parts, row_step = static_cast<int>(gridDim.x) / parts;
+  const size_t row_vecs = static_cast<size_t>(a.Vp) / kN;
+  const uint4* base = reinterpret_cast<const uint4*>(logits);
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full[i], 1u);
+      mbar_init(&sm.empty[i], kT / 32);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  // the target's logit is asked for ahead of the row
-  int target = -1;
-  float xt = 0.f;
-  if (tid == 0 && part == 0 && a.logprob != nullptr) {
-    target = a.targets[n];
-    if (target < -1 || target >= a.V) {
-      set_error(GPT2_DEVERR_TOKEN);
-      target = -1;
+  if (wid == kT / 32) {
+    if (lane == 0) {
+      int q = 0;  // chunks asked for
+      bool ok = true;
+      for (long long n = row0; n < a.N && ok; n += row_step) {
+        const uint4* row = base + n * row_vecs;
+        for (int c = 0; c < chunks; ++c, ++q) {
+          const int st = q % kStages;
+          if (q >= kStages && !(ok = mbar_wait(&sm.empty[st], (q / kStages - 1) & 1))) break;
+          const int v0 = lo + c * kChunk;
+          const uint32_t bytes = static_cast<uint32_t>(min(kChunk, hi - v0)) * 16u;
+          mbar_arrive_expect_tx(&sm.full[st], bytes);
+          bulk_load(sm.ring[st], row + v0, bytes, &sm.full[st]);
+        }
+      }
+      // the last copies have landed before the block may exit
+      for (int i = max(0, q - kStages); i < q; ++i) mbar_wait(&sm.full[i % kStages], (i / kStages) & 1);
     }
-    if (target >= 0) xt = to_f32(logits[n * a.Vp + target]);
+    __syncwarp();
+    if (parts > 1) {
+      cluster_sync();
+      cluster_sync();
+    }
+    return;
   }
-  Stat st{-INFINITY, 0.f, 0.f};
-  int best_vec = 0;
-  auto largest = [](const Vec<T>& v) {
-    float mx = fmax3(v.x[0], v.x[1], fmaxf(v.x[2], v.x[3]));
-    if constexpr (kN == 8) mx = fmax3(mx, fmax3(v.x[4], v.x[5], v.x[6]), v.x[7]);
-    return mx;
-  };
-  auto raise = [&](float to) {  // the maximum grows
-    if (st.m != -INFINITY) {
-      const float d = st.m - to, f = exp2_approx(d * kLog2e);
-      st.w = fmaf(st.s, fmaxf(d, -200.f), st.w) * f;
-      st.s *= f;
+  bool ok = true;  // no wait has given up
+  int q = 0;
+  int turn = 0;
+  for (long long n = row0; n < a.N; n += row_step, turn ^= 1) {
+    const uint4* row = base + n * row_vecs;
+    // the target's logit is asked for ahead of the row
+    int target = -1;
+    float xt = 0.f;
+    if (tid == 0 && part == 0 && a.logprob != nullptr) {
+      target = a.targets[n];
+      if (target < -1 || target >= a.V) {
+        set_error(GPT2_DEVERR_TOKEN);
+        target = -1;
+      }
+      if (target >= 0) xt = to_f32(reinterpret_cast<const T*>(row)[target]);
     }
-    st.m = to;
-  };
-  auto add = [&](const Vec<T>& v) {
-    const float m0 = st.m == -INFINITY ? 0.f : st.m;
+    Stat st{-INFINITY, 0.f, 0.f};
+    int best_vec = 0;
+    auto largest = [](const Vec<T>& v) {
+      float mx = fmax3(v.x[0], v.x[1], fmaxf(v.x[2], v.x[3]));
+      if constexpr (kN == 8) mx = fmax3(mx, fmax3(v.x[4], v.x[5], v.x[6]), v.x[7]);
+      return mx;
+    };
+    auto add = [&](const Vec<T>& v) {
+      const float m0 = st.m == -INFINITY ? 0.f : st.m;
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      // -inf as -200: its term is 0 in fp32, its product with x - m too
-      const float d = max_nan(v.x[j] - m0, -200.f), e = exp2_approx(d * kLog2e);
-      st.s += e;
-      st.w = fmaf(e, d, st.w);
-    }
-  };
-  int i = lo + tid;
-  for (; i + (kU - 1) * kT < full; i += kU * kT) {
-    uint4 raw[kU];
+      for (int j = 0; j < kN; ++j) {
+        // -inf as -200: its term is 0 in fp32, its product with x - m too
+        const float d = max_nan(v.x[j] - m0, -200.f), e = exp2_approx(d * kLog2e);
+        st.s += e;
+        st.w = fmaf(e, d, st.w);
+      }
+    };
+    for (int c = 0; c < chunks; ++c, ++q) {
+      const int stage = q % kStages, v0 = lo + c * kChunk + tid;
+      ok = ok && mbar_wait(&sm.full[stage], (q / kStages) & 1);
+      uint4 raw[kU];
 #pragma unroll
-    for (int k = 0; k < kU; ++k) raw[k] = __ldg(row + i + k * kT);
-    float mx = st.m;
+      for (int k = 0; k < kU; ++k) raw[k] = sm.ring[stage][tid + k * kT];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[stage]);
+      if (lo + (c + 1) * kChunk <= min(hi, full_vecs)) {
+        float mx = st.m;
 #pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      const float x = largest(widen<T>(raw[k]));
-      if (x > mx) {  // vectors in ascending order: the first of equal ones stays
-        mx = x;
-        if (kTop) best_vec = i + k * kT;
+        for (int k = 0; k < kU; ++k) {
+          const float x = largest(widen<T>(raw[k]));
+          if (x > mx) {  // vectors in ascending order: the first of equal ones stays
+            mx = x;
+            if (kTop) best_vec = v0 + k * kT;
+          }
+        }
+        if (mx > st.m) st = raised(st, mx);
+#pragma unroll
+        for (int k = 0; k < kU; ++k) add(widen<T>(raw[k]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+          const int vec = v0 + k * kT;
+          if (vec >= hi) break;
+          Vec<T> v = widen<T>(raw[k]);
+          if (vec >= full_vecs) {
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+              if (vec * kN + j >= a.V) v.x[j] = -INFINITY;
+          }
+          const float x = largest(v);
+          if (x > st.m) {
+            st = raised(st, x);
+            if (kTop) best_vec = vec;
+          }
+          add(v);
+        }
       }
     }
-    if (mx > st.m) raise(mx);
-#pragma unroll
-    for (int k = 0; k < kU; ++k) add(widen<T>(raw[k]));
-  }
-  {
-    uint4 raw[kU];
-#pragma unroll
-    for (int k = 0; k < kU; ++k)
-      if (i + k * kT < hi) raw[k] = __ldg(row + i + k * kT);
-#pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      const int vec = i + k * kT;
-      if (vec >= hi) break;
-      Vec<T> v = widen<T>(raw[k]);
-      if (vec >= full) {
-#pragma unroll
-        for (int j = 0; j < kN; ++j)
-          if (vec * kN + j >= a.V) v.x[j] = -INFINITY;
-      }
-      const float x = largest(v);
-      if (x > st.m) {
-        raise(x);
-        if (kTop) best_vec = vec;
-      }
-      add(v);
-    }
-  }
-  const float best = st.m;
-  st = warp_join(st);
-  if (lane == 0) rs.warp[wid] = st;
-  if constexpr (kTop) {
-    select_top<T, kT>(rs, ts, row, lo, hi, a.V, a.K, best, best_vec);
-  } else {
-    __syncthreads();
-  }
-  if (wid == 0) {
-    st = lane < kT / 32 ? rs.warp[lane] : Stat{-INFINITY, 0.f, 0.f};
+    const float best = st.m;
     st = warp_join(st);
-    if (lane == 0) rs.block = st;
-  }
-  if (parts > 1) {
-    cluster_sync();
-    if (part != 0) {
-      cluster_sync();  // block 0 has read this block's shared memory
+    if (lane == 0) sm.warp[turn][wid] = st;
+    if constexpr (kTop) {
+      select_top<T, kT>(sm, row, lo, hi, a.V, a.K, best, best_vec);
+    } else {
+      bar<kT>();
+    }
+    if (wid == 0) st = warp_join(lane < kT / 32 ? sm.warp[turn][lane] : Stat{-INFINITY, 0.f, 0.f});
+    if (parts > 1) {
+      if (tid == 0) sm.block = st;
+      cluster_sync();
+      if (part != 0) {
+        cluster_sync();  // block 0 has read this block's shared memory
+        return;
+      }
+      if (wid == 0) {
+        st = Stat{-INFINITY, 0.f, 0.f};
+        if (lane < parts) {
+          const uint32_t at = mapa_shared(smem_u32(&sm.block), lane);
+          st = Stat{ld_shared_cluster_f32(at), ld_shared_cluster_f32(at + 4), ld_shared_cluster_f32(at + 8)};
+        }
+        st = warp_join(st);
+      }
+      if constexpr (kTop) {
+        for (int c = tid; c < parts * a.K; c += kT)
+          sm.cand[c] = ld_shared_cluster_u64(mapa_shared(smem_u32(&sm.top[c % a.K]), c / a.K));
+        bar<kT>();
+        rank_keys<kT>(sm.cand, parts * a.K, a.K, [&](int r, Key k) { sm.group[r] = k; });
+        bar<kT>();
+      }
+    }
+    if (wid == 0) {
+      const bool nan = !(st.s >= 0.f) || st.m == INFINITY, none = st.s == 0.f;
+      const float ls = logf(st.s);
+      if (lane == 0) {
+        if (a.lse != nullptr) a.lse[n] = nan ? NAN : (none ? -INFINITY : st.m + ls);
+        if (a.entropy != nullptr) a.entropy[n] = nan ? NAN : (none ? 0.f : ls - st.w / st.s);
+        if (a.logprob != nullptr)
+          a.logprob[n] = target < 0 ? 0.f : (nan ? NAN : (none ? -INFINITY : (xt - st.m) - ls));
+      }
+      if constexpr (kTop) {
+        static_assert(GPT2_LOGPROBS_MAX_TOP <= 32, "a lane per alternative");
+        if (lane < a.K) {
+          const Key k = parts > 1 ? sm.group[lane] : sm.top[lane];
+          const bool gone = nan || k == 0ull;
+          const size_t at = static_cast<size_t>(n) * a.K + lane;
+          if (a.top_ids != nullptr) a.top_ids[at] = gone ? -1 : static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
+          if (a.top_logprobs != nullptr)
+            a.top_logprobs[at] =
+                nan ? NAN : (gone ? -INFINITY : (value_of(static_cast<uint32_t>(k >> 32)) - st.m) - ls);
+        }
+      }
+    }
+    if (parts > 1) {
+      cluster_sync();
       return;
     }
-  } else {
-    __syncthreads();
   }
-  // block 0: the row's statistics, and its alternatives from those of all parts
-  if (parts > 1 && wid == 0) {
-    st = Stat{-INFINITY, 0.f, 0.f};
-    if (lane < parts) {
-      const uint32_t at = mapa_shared(smem_u32(&rs.block), lane);
-      st = Stat{ld_shared_cluster_f32(at), ld_shared_cluster_f32(at + 4), ld_shared_cluster_f32(at + 8)};
-    }
-    st = warp_join(st);
-    if (lane == 0) rs.warp[0] = st;
-  }
-  if constexpr (kTop) {
-    if (parts > 1) {
-      for (int c = tid; c < parts * a.K; c += kT)
-        ts.cand[c] = ld_shared_cluster_u64(mapa_shared(smem_u32(&rs.top[c % a.K]), c / a.K));
-    }
-  }
-  if (parts > 1) {
-    __syncthreads();
-    st = rs.warp[0];
-  } else {
-    st = rs.block;
-  }
-  const bool nan = !(st.s >= 0.f) || st.m == INFINITY, none = st.s == 0.f;
-  const float ls = logf(st.s);
-  if (tid == 0) {
-    if (a.lse != nullptr) a.lse[n] = nan ? NAN : (none ? -INFINITY : st.m + ls);
-    if (a.entropy != nullptr) a.entropy[n] = nan ? NAN : (none ? 0.f : ls - st.w / st.s);
-    if (a.logprob != nullptr)
-      a.logprob[n] = target < 0 ? 0.f : (nan ? NAN : (none ? -INFINITY : (xt - st.m) - ls));
-  }
-  if constexpr (kTop) {
-    auto put = [&](int r, Key k) {
-      const bool gone = nan || k == 0ull;
-      if (a.top_ids != nullptr)
-        a.top_ids[n * a.K + r] = gone ? -1 : static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
-      if (a.top_logprobs != nullptr)
-        a.top_logprobs[n * a.K + r] =
-            nan ? NAN : (gone ? -INFINITY : (value_of(static_cast<uint32_t>(k >> 32)) - st.m) - ls);
-    };
-    if (parts == 1) {
-      if (tid < a.K) put(tid, rs.top[tid]);
-    } else {
-      const int total = parts * a.K;
-      for (int c = tid; c < total; c += kT) {
-        const Key k = ts.cand[c];
-        int rank = 0;
-        for (int o = 0; o < total; ++o) rank += ts.cand[o] > k || (ts.cand[o] == k && o < c) ? 1 : 0;
-        if (rank < a.K) put(rank, k);
-      }
-    }
-  }
-  if (parts > 1) cluster_sync();
 }
 
 // --------------------------------------------------------------- backward
@@ -409,7 +457,7 @@ struct BackwardArgs {
 template <typename T>
 __global__ void __launch_bounds__(kVocThreads) logprobs_backward_kernel(T* dlogits, const T* logits, BackwardArgs a,
                                                                         int parts) {
-  constexpr int kN = Vec<T>::n, kU = 4, kT = kVocThreads;
+  constexpr int kN = Vec<T>::n, kT = kVocThreads;
   __shared__ float red[32];
   const int tid = threadIdx.x;
   const size_t n = blockIdx.x / parts;
@@ -496,12 +544,14 @@ __global__ void __launch_bounds__(kVocThreads) logprobs_backward_kernel(T* dlogi
   }
 }
 
-// Launches a kernel over N rows, `parts` blocks of a cluster to a row.
+// Launches a kernel over rows, `parts` blocks of a cluster to each.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_rows(void (*kern)(KArgs...), int threads, int N, int parts, cudaStream_t s, Args... args) {
+cudaError_t launch_rows(void (*kern)(KArgs...), unsigned rows, int threads, size_t smem, int parts, cudaStream_t s,
+                        Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(N) * parts);
+  cfg.gridDim = dim3(rows * parts);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -524,27 +574,42 @@ int row_parts(int N, int vecs, int threads) {
   return parts;
 }
 
+template <typename T, int kT, bool kTop>
+cudaError_t forward_go(const T* logits, const ForwardArgs& a, cudaStream_t s) {
+  static int resident[kMaxDevices] = {};  // blocks per SM
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev >= kMaxDevices) return e == cudaSuccess ? cudaErrorInvalidDevice : e;
+  auto kern = logprobs_kernel<T, kT, kTop>;
+  if (resident[dev] == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(RowSmem<kT>)));
+    int per = 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, kT + 32, sizeof(RowSmem<kT>));
+    if (e != cudaSuccess) return e;
+    resident[dev] = per > 0 ? per : 1;
+  }
+  const int parts = row_parts(a.N, (a.V + Vec<T>::n - 1) / Vec<T>::n, kT);
+  const int most = resident[dev] * num_sms();
+  const unsigned rows = static_cast<unsigned>(parts > 1 ? a.N : std::min(a.N, most));
+  return launch_rows(kern, rows, kT + 32, sizeof(RowSmem<kT>), parts, s, logits, a, parts);
+}
+
 template <typename T>
-int logprobs_typed(const void* logits, const ForwardArgs& a, int N, cudaStream_t s) {
-  const int vecs = (a.V + Vec<T>::n - 1) / Vec<T>::n;
+int forward_typed(const void* logits, const ForwardArgs& a, cudaStream_t s) {
   const bool top = a.top_ids != nullptr || a.top_logprobs != nullptr;
   const T* l = static_cast<const T*>(logits);
-  cudaError_t e;
-  if (vecs < kShortRow) {
-    const int parts = row_parts(N, vecs, 128);
-    e = launch_rows(top ? logprobs_kernel<T, 128, true> : logprobs_kernel<T, 128, false>, 128, N, parts, s, l, a, parts);
-  } else {
-    const int parts = row_parts(N, vecs, 512);
-    e = launch_rows(top ? logprobs_kernel<T, 512, true> : logprobs_kernel<T, 512, false>, 512, N, parts, s, l, a, parts);
-  }
+  const bool small = (a.V + Vec<T>::n - 1) / Vec<T>::n < kShortRow;
+  const cudaError_t e = small ? (top ? forward_go<T, 128, true>(l, a, s) : forward_go<T, 128, false>(l, a, s))
+                              : (top ? forward_go<T, kRowThreads, true>(l, a, s)
+                                     : forward_go<T, kRowThreads, false>(l, a, s));
   return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
 }
 
 template <typename T>
 int backward_typed(void* dlogits, const void* logits, const BackwardArgs& a, int N, cudaStream_t s) {
   const int parts = row_parts(N, a.Vp / Vec<T>::n, kVocThreads);
-  const cudaError_t e = launch_rows(logprobs_backward_kernel<T>, kVocThreads, N, parts, s, static_cast<T*>(dlogits),
-                                    static_cast<const T*>(logits), a, parts);
+  const cudaError_t e = launch_rows(logprobs_backward_kernel<T>, static_cast<unsigned>(N), kVocThreads, 0, parts, s,
+                                    static_cast<T*>(dlogits), static_cast<const T*>(logits), a, parts);
   return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
 }
 
@@ -552,10 +617,10 @@ int backward_typed(void* dlogits, const void* logits, const BackwardArgs& a, int
 
 int launch_logprobs(float* logprob, float* entropy, float* lse, int* top_ids, float* top_logprobs, const void* logits,
                     int logits_type, const int* targets, int N, int V, int Vp, int K, cudaStream_t s) {
-  const ForwardArgs a{logprob, entropy, lse, top_ids, top_logprobs, targets, V, Vp, K};
-  if (logits_type == kProbsF16) return logprobs_typed<__half>(logits, a, N, s);
-  if (logits_type == kProbsBF16) return logprobs_typed<__nv_bfloat16>(logits, a, N, s);
-  return logprobs_typed<float>(logits, a, N, s);
+  const ForwardArgs a{logprob, entropy, lse, top_ids, top_logprobs, targets, N, V, Vp, K};
+  if (logits_type == kProbsF16) return forward_typed<__half>(logits, a, s);
+  if (logits_type == kProbsBF16) return forward_typed<__nv_bfloat16>(logits, a, s);
+  return forward_typed<float>(logits, a, s);
 }
 
 int launch_logprobs_backward(void* dlogits, const void* logits, int logits_type, const int* targets, const float* lse,
