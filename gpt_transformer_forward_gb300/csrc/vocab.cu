@@ -10,6 +10,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kVocThreads = 256;
 constexpr int kRowThreads = 256;
+constexpr int kMaxParts = 8;  // blocks of a cluster that share a row
 constexpr int kShortRow = 2048;  // vectors; below, blocks of 128 threads
 // From here on the backward takes a row's maximum and sum anew instead of its
 // lse, whose fp32 rounding |lse| 2^-24 is an error of every p (6e-5 here).
@@ -39,6 +40,14 @@ __device__ __forceinline__ Vec<T> widen(const uint4& raw) {
     }
   }
   return v;
+}
+
+// ignoring NaN
+template <typename T>
+__device__ __forceinline__ float largest(const Vec<T>& v) {
+  float mx = fmax3(v.x[0], v.x[1], fmaxf(v.x[2], v.x[3]));
+  if constexpr (Vec<T>::n == 8) mx = fmax3(mx, fmax3(v.x[4], v.x[5], v.x[6]), v.x[7]);
+  return mx;
 }
 
 template <typename F>
@@ -109,7 +118,7 @@ __device__ __forceinline__ Key key_of(float x, uint32_t index) {
 }
 __device__ __forceinline__ Key larger(Key a, Key b) { return a > b ? a : b; }
 
-constexpr int kGroups = 128;         // groups of threads that propose a threshold
+constexpr int kGroups = 64;          // groups of threads that propose a threshold
 constexpr int kMaxCandidates = 1024;
 constexpr int kU = 4;                // vectors of a thread in a chunk
 constexpr int kStages = 3;           // chunks of the row stream in shared memory
@@ -125,8 +134,10 @@ struct RowSmem {
   Key top[GPT2_LOGPROBS_MAX_TOP];   // this block's, largest first
   Key group[kGroups];
   Key cand[kMaxCandidates];
+  uint4 vec[kT];                    // vectors that hold a candidate, and their indexes
+  int vec_at[kT];
   Key tau;                          // the K-th largest group's best vector (0: fewer than K)
-  int n_threads, n_cand;
+  int n_threads, n_vecs, n_cand;
   uint16_t thread[kT];
 };
 
@@ -134,6 +145,19 @@ struct RowSmem {
 template <int kT>
 __device__ __forceinline__ void bar() {
   asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+}
+
+// Two lists of 32, one key a lane, largest first: the 32 largest of both.  The
+// larger of a[i] and b[31 - i] are these 32, in an order that rises and falls
+// at most once, which five exchange steps sort.
+__device__ __forceinline__ Key merge_top(Key a, Key b, int lane) {
+  a = larger(a, __shfl_sync(0xffffffffu, b, 31 - lane));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Key x = __shfl_xor_sync(0xffffffffu, a, o);
+    a = ((lane & o) == 0) == (a > x) ? a : x;
+  }
+  return a;
 }
 
 struct ForwardArgs {
@@ -146,20 +170,17 @@ struct ForwardArgs {
   int N, V, Vp, K;
 };
 
-// keys[0 .. n) ranked by counting, eight threads to a key; put(rank, key) for
-// the K largest.  Equal keys (only 0 occurs twice) rank by their place.
+// keys[0 .. n), distinct, ranked by counting, two threads to a key; put(rank,
+// key) for the K largest
 template <int kT, typename Put>
 __device__ __forceinline__ void rank_keys(const Key* keys, int n, int K, Put put) {
-  const int sub = threadIdx.x & 7;
-  for (int c = threadIdx.x >> 3; c < (n + 3) / 4 * 4; c += kT / 8) {  // whole warps: four keys each
+  const int sub = threadIdx.x & 1;
+  for (int c = threadIdx.x >> 1; c < (n + 15) / 16 * 16; c += kT / 2) {  // whole warps: 16 keys each
     const Key k = c < n ? keys[c] : 0ull;
     int rank = 0;
-    for (int i = sub; i < n; i += 8) {
-      const Key o = keys[i];
-      rank += o > k || (o == k && i < c) ? 1 : 0;
-    }
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+#pragma unroll 4
+    for (int i = sub; i < n; i += 2) rank += keys[i] > k ? 1 : 0;
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
     if (sub == 0 && c < n && rank < K) put(rank, k);
   }
 }
@@ -169,14 +190,18 @@ __device__ __forceinline__ void rank_keys(const Key* keys, int n, int K, Put put
 // best is the largest of its threads', and tau, the K-th largest group's,
 // cannot exceed the K-th largest element: at least K elements are no less than
 // it in the order (value, lower vector first).  Those elements lie with
-// threads whose own best is >= tau, about K of them, whose vectors all threads
-// read again together (a few per cent of the row, from L2); the elements found
-// are ranked by counting.  Equal values do not add candidates, since vectors
-// are ordered by index; a row in which a few threads hold all the largest
-// elements may exceed the candidate buffer and is searched K times instead.
+// threads whose own best is >= tau, about K of them.  Where only the best can
+// reach tau (`second`, the largest of the thread's other vectors, does not),
+// that vector is read again; the few other threads' vectors are all read
+// again, by all threads together.  The vectors that reach tau are listed, then
+// their elements, which are ranked by counting.
+// Equal values do not add candidates, since vectors are ordered by index; a
+// row in which a few threads hold all the largest elements may exceed the
+// lists and is searched K times instead.  64 groups: with K = 32 about 44
+// elements reach tau (64 ln 2), and ranking 64 keys costs a quarter of 128.
 template <typename T, int kT>
 __device__ __forceinline__ void select_top(RowSmem<kT>& sm, const uint4* row, int lo, int hi, int V, int K, float best,
-                                           int best_vec) {
+                                           float second, int best_vec) {
   constexpr int kN = Vec<T>::n, kPer = kT / kGroups;
   const int tid = threadIdx.x;
   const Key mine = best > -INFINITY ? key_of(best, static_cast<uint32_t>(best_vec)) : 0ull;
@@ -187,6 +212,7 @@ __device__ __forceinline__ void select_top(RowSmem<kT>& sm, const uint4* row, in
   if (tid == 0) {
     sm.tau = 0ull;
     sm.n_threads = 0;
+    sm.n_vecs = 0;
     sm.n_cand = 0;
   }
   if (tid < K) sm.top[tid] = 0ull;
@@ -201,29 +227,70 @@ __device__ __forceinline__ void select_top(RowSmem<kT>& sm, const uint4* row, in
   }
   bar<kT>();
   const Key tau = sm.tau;
-  if (mine != 0ull && mine >= tau) sm.thread[atomicAdd(&sm.n_threads, 1)] = static_cast<uint16_t>(tid);
-  bar<kT>();
-  const int per = (hi - lo + kT - 1) / kT;  // vectors of a thread, at most
+  // lists are filled by one atomic a warp (their order does not matter: the
+  // elements are ranked), not one an element: serialised on one address, those
+  // took longer than the search itself
+  const int lane = tid & 31;
+  auto place = [&](int* counter, bool in) -> int {  // this thread's place if `in`
+    const uint32_t who = __ballot_sync(0xffffffffu, in);
+    if (who == 0u) return 0;
+    int at = 0;
+    if (lane == 0) at = atomicAdd(counter, __popc(who));
+    return __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
+  };
   const uint32_t tau_value = static_cast<uint32_t>(tau >> 32);
   const int tau_vec = static_cast<int>(0xffffffffu - static_cast<uint32_t>(tau));
+  {
+    const bool in = mine != 0ull && mine >= tau;
+    const bool more = in && second > -INFINITY && ordered(second) >= tau_value;
+    const int at = place(&sm.n_threads, more);
+    if (more) sm.thread[at] = static_cast<uint16_t>(tid);
+    const int to = place(&sm.n_vecs, in && !more);
+    if (in && !more) {  // at most kT of these
+      sm.vec[to] = __ldg(row + best_vec);
+      sm.vec_at[to] = best_vec;
+    }
+  }
+  bar<kT>();
+  const int per = (hi - lo + kT - 1) / kT;  // vectors of a thread, at most
   const int total = sm.n_threads * per;
-  for (int i = tid; i < total; i += kT) {
-    const int vec = lo + sm.thread[i / per] + (i % per) * kT;
-    if (vec >= hi) continue;
-    const Vec<T> v = widen<T>(__ldg(row + vec));
+  auto reaches = [&](float x, int vec) {
+    const uint32_t o = ordered(x);
+    return x > -INFINITY && (tau == 0ull || o > tau_value || (o == tau_value && vec <= tau_vec));
+  };
+  for (int i0 = 0; i0 < total; i0 += kT) {  // whole warps
+    const int i = i0 + tid;
+    const int vec = i < total ? lo + sm.thread[i / per] + (i % per) * kT : hi;
+    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+    if (vec < hi) raw = __ldg(row + vec);
+    Vec<T> v = widen<T>(raw);
+    if (vec * kN + kN > V) {  // (also where there is no vector)
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const uint32_t o = ordered(v.x[j]);
-      const int id = vec * kN + j;
-      if (id >= V || !(v.x[j] > -INFINITY)) continue;
-      if (tau != 0ull && (o < tau_value || (o == tau_value && vec > tau_vec))) continue;
-      const int at = atomicAdd(&sm.n_cand, 1);
-      if (at < kMaxCandidates) sm.cand[at] = (static_cast<Key>(o) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
+      for (int j = 0; j < kN; ++j)
+        if (vec >= hi || vec * kN + j >= V) v.x[j] = -INFINITY;
+    }
+    const bool in = vec < hi && reaches(largest(v), vec);
+    const int at = place(&sm.n_vecs, in);
+    if (in && at < kT) {
+      sm.vec[at] = raw;
+      sm.vec_at[at] = vec;
+    }
+  }
+  if (total > 0) bar<kT>();
+  const int n_vecs = sm.n_vecs;
+  if (n_vecs <= kT) {
+    for (int i0 = 0; i0 < n_vecs * kN; i0 += kT) {
+      const int i = i0 + tid, vec = i < n_vecs * kN ? sm.vec_at[i / kN] : 0, id = vec * kN + i % kN;
+      float x = -INFINITY;
+      if (i < n_vecs * kN && id < V) x = to_f32(reinterpret_cast<const T*>(sm.vec)[i]);
+      const bool in = reaches(x, vec);
+      const int at = place(&sm.n_cand, in);
+      if (in && at < kMaxCandidates) sm.cand[at] = key_of(x, static_cast<uint32_t>(id));
     }
   }
   bar<kT>();
   const int n = sm.n_cand;
-  if (n <= kMaxCandidates) {
+  if (n_vecs <= kT && n <= kMaxCandidates) {
     rank_keys<kT>(sm.cand, n, K, [&](int r, Key k) { sm.top[r] = k; });
   } else {
     Key last = ~0ull;
@@ -258,7 +325,7 @@ __device__ __forceinline__ void select_top(RowSmem<kT>& sm, const uint4* row, in
 // blockIdx.x, + gridDim.x, ...; else the `parts` blocks of a cluster share the
 // one row.
 template <typename T, int kT, bool kTop>
-__global__ void __launch_bounds__(kT + 32) logprobs_kernel(const T* __restrict__ logits, ForwardArgs a, int parts) {
+__global__ void __launch_bounds__(kT + 32, kT >= 256 ? 3 : 6) logprobs_kernel(const T* __restrict__ logits, ForwardArgs a, int parts) {
   constexpr int kN = Vec<T>::n, kChunk = kT * kU;
   extern __shared__ __align__(128) uint8_t voc_smem[];
   RowSmem<kT>& sm = *reinterpret_cast<RowSmem<kT>*>(voc_smem);
@@ -324,20 +391,27 @@ __global__ void __launch_bounds__(kT + 32) logprobs_kernel(const T* __restrict__
     }
     Stat st{-INFINITY, 0.f, 0.f};
     int best_vec = 0;
-    auto largest = [](const Vec<T>& v) {
-      float mx = fmax3(v.x[0], v.x[1], fmaxf(v.x[2], v.x[3]));
-      if constexpr (kN == 8) mx = fmax3(mx, fmax3(v.x[4], v.x[5], v.x[6]), v.x[7]);
-      return mx;
-    };
+    float second = -INFINITY;
+    // the sums in two halves, for packed fp32 instructions
+    float2 s2 = make_float2(0.f, 0.f), w2 = s2;
     auto add = [&](const Vec<T>& v) {
       const float m0 = st.m == -INFINITY ? 0.f : st.m;
+      const float2 neg = make_float2(-m0, -m0), lg = make_float2(kLog2e, kLog2e);
 #pragma unroll
-      for (int j = 0; j < kN; ++j) {
+      for (int j = 0; j < kN; j += 2) {
         // -inf as -200: its term is 0 in fp32, its product with x - m too
-        const float d = max_nan(v.x[j] - m0, -200.f), e = exp2_approx(d * kLog2e);
-        st.s += e;
-        st.w = fmaf(e, d, st.w);
+        float2 d = __fadd2_rn(make_float2(v.x[j], v.x[j + 1]), neg);
+        d = make_float2(max_nan(d.x, -200.f), max_nan(d.y, -200.f));
+        const float2 t = __fmul2_rn(d, lg), e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
+        s2 = __fadd2_rn(s2, e);
+        w2 = __ffma2_rn(e, d, w2);
       }
+    };
+    auto raise = [&](float m) {
+      const float d = st.m == -INFINITY ? 0.f : st.m - m, f = exp2_approx(d * kLog2e), dc = fmaxf(d, -200.f);
+      w2 = make_float2(fmaf(s2.x, dc, w2.x) * f, fmaf(s2.y, dc, w2.y) * f);
+      s2 = make_float2(s2.x * f, s2.y * f);
+      st.m = m;
     };
     for (int c = 0; c < chunks; ++c, ++q) {
       const int stage = q % kStages, v0 = lo + c * kChunk + tid;
@@ -352,12 +426,13 @@ __global__ void __launch_bounds__(kT + 32) logprobs_kernel(const T* __restrict__
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
           const float x = largest(widen<T>(raw[k]));
+          if (kTop) second = fmaxf(second, fminf(x, mx));
           if (x > mx) {  // vectors in ascending order: the first of equal ones stays
             mx = x;
             if (kTop) best_vec = v0 + k * kT;
           }
         }
-        if (mx > st.m) st = raised(st, mx);
+        if (mx > st.m) raise(mx);
 #pragma unroll
         for (int k = 0; k < kU; ++k) add(widen<T>(raw[k]));
       } else {
@@ -372,8 +447,9 @@ __global__ void __launch_bounds__(kT + 32) logprobs_kernel(const T* __restrict__
               if (vec * kN + j >= a.V) v.x[j] = -INFINITY;
           }
           const float x = largest(v);
+          if (kTop) second = fmaxf(second, fminf(x, st.m));
           if (x > st.m) {
-            st = raised(st, x);
+            raise(x);
             if (kTop) best_vec = vec;
           }
           add(v);
@@ -381,10 +457,10 @@ __global__ void __launch_bounds__(kT + 32) logprobs_kernel(const T* __restrict__
       }
     }
     const float best = st.m;
-    st = warp_join(st);
+    st = warp_join(Stat{st.m, s2.x + s2.y, w2.x + w2.y});
     if (lane == 0) sm.warp[turn][wid] = st;
     if constexpr (kTop) {
-      select_top<T, kT>(sm, row, lo, hi, a.V, a.K, best, best_vec);
+      select_top<T, kT>(sm, row, lo, hi, a.V, a.K, best, second, best_vec);
     } else {
       bar<kT>();
     }
@@ -404,12 +480,24 @@ __global__ void __launch_bounds__(kT + 32) logprobs_kernel(const T* __restrict__
         }
         st = warp_join(st);
       }
-      if constexpr (kTop) {
-        for (int c = tid; c < parts * a.K; c += kT)
-          sm.cand[c] = ld_shared_cluster_u64(mapa_shared(smem_u32(&sm.top[c % a.K]), c / a.K));
-        bar<kT>();
-        rank_keys<kT>(sm.cand, parts * a.K, a.K, [&](int r, Key k) { sm.group[r] = k; });
-        bar<kT>();
+    }
+    Key top = 0ull;  // lane r of warp 0: the row's alternative r
+    if constexpr (kTop) {
+      static_assert(GPT2_LOGPROBS_MAX_TOP <= 32, "a lane per alternative");
+      if (wid == 0) {
+        if (parts == 1) {
+          if (lane < a.K) top = sm.top[lane];
+        } else {
+          Key list[kMaxParts];
+#pragma unroll
+          for (int p = 0; p < kMaxParts; ++p)
+            list[p] = p < parts && lane < a.K ? ld_shared_cluster_u64(mapa_shared(smem_u32(&sm.top[lane]), p)) : 0ull;
+#pragma unroll
+          for (int w = kMaxParts / 2; w > 0; w >>= 1)
+#pragma unroll
+            for (int p = 0; p < w; ++p) list[p] = merge_top(list[p], list[p + w], lane);
+          top = list[0];
+        }
       }
     }
     if (wid == 0) {
@@ -422,9 +510,8 @@ __global__ void __launch_bounds__(kT + 32) logprobs_kernel(const T* __restrict__
           a.logprob[n] = target < 0 ? 0.f : (nan ? NAN : (none ? -INFINITY : (xt - st.m) - ls));
       }
       if constexpr (kTop) {
-        static_assert(GPT2_LOGPROBS_MAX_TOP <= 32, "a lane per alternative");
         if (lane < a.K) {
-          const Key k = parts > 1 ? sm.group[lane] : sm.top[lane];
+          const Key k = top;
           const bool gone = nan || k == 0ull;
           const size_t at = static_cast<size_t>(n) * a.K + lane;
           if (a.top_ids != nullptr) a.top_ids[at] = gone ? -1 : static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
@@ -565,13 +652,12 @@ cudaError_t launch_rows(void (*kern)(KArgs...), unsigned rows, int threads, size
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-// Blocks that share a row: enough to cover the SMs twice when rows are few,
-// each with a vector for every thread at least (8: the largest portable
-// cluster).
-int row_parts(int N, int vecs, int threads) {
-  int parts = 1;
-  while (parts < 8 && static_cast<long long>(N) * parts < 2LL * num_sms() && vecs >= 2 * parts * threads) parts *= 2;
-  return parts;
+// Blocks that share a row: as many as fit the GPU at once when rows are few
+// (`resident`: blocks that it holds), each with a vector for every thread at
+// least.  Clusters of up to eight blocks launch everywhere.
+int row_parts(int N, int vecs, int threads, int resident) {
+  const int most = std::min(kMaxParts, std::max(1, vecs / threads));
+  return std::max(1, std::min(most, resident / N));
 }
 
 template <typename T, int kT, bool kTop>
@@ -588,8 +674,8 @@ cudaError_t forward_go(const T* logits, const ForwardArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     resident[dev] = per > 0 ? per : 1;
   }
-  const int parts = row_parts(a.N, (a.V + Vec<T>::n - 1) / Vec<T>::n, kT);
   const int most = resident[dev] * num_sms();
+  const int parts = row_parts(a.N, (a.V + Vec<T>::n - 1) / Vec<T>::n, kT, most);
   const unsigned rows = static_cast<unsigned>(parts > 1 ? a.N : std::min(a.N, most));
   return launch_rows(kern, rows, kT + 32, sizeof(RowSmem<kT>), parts, s, logits, a, parts);
 }
@@ -607,7 +693,7 @@ int forward_typed(const void* logits, const ForwardArgs& a, cudaStream_t s) {
 
 template <typename T>
 int backward_typed(void* dlogits, const void* logits, const BackwardArgs& a, int N, cudaStream_t s) {
-  const int parts = row_parts(N, a.Vp / Vec<T>::n, kVocThreads);
+  const int parts = row_parts(N, a.Vp / Vec<T>::n, kVocThreads, 4 * num_sms());
   const cudaError_t e = launch_rows(logprobs_backward_kernel<T>, static_cast<unsigned>(N), kVocThreads, 0, parts, s,
                                     static_cast<T*>(dlogits), static_cast<const T*>(logits), a, parts);
   return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
