@@ -537,12 +537,61 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
   }
+  if constexpr (kShared) {
+    // the prefix's splits s = warp, warp + kDecWarps, ... join this warp's
+    // result: lane i holds dimensions i, i + 32 of each, four splits' loads in
+    // flight
+    if (!producer && pos_ok) {
+      if (g == 0) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) o_s[warp][dg * kPer + k] = acc[k];
+      }
+      __syncwarp();
+      constexpr int kD = (HS + 31) / 32, kB = 4;
+      float ox[kD];
+#pragma unroll
+      for (int d = 0; d < kD; ++d) ox[d] = lane + 32 * d < HS ? o_s[warp][lane + 32 * d] : 0.f;
+      const size_t step = static_cast<size_t>(NH) * gridDim.y;  // a split's rows
+      const size_t row0 = static_cast<size_t>(h) * gridDim.y + b;
+      for (int s0 = warp; s0 < prefix.splits; s0 += kDecWarps * kB) {
+        float2 ml[kB];
+        float po[kB][kD];
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+          const int s = s0 + i * kDecWarps;
+          const size_t at = (s < prefix.splits ? s : s0) * step + row0;
+          ml[i] = prefix.ml[at];
+          if (s >= prefix.splits) ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int d = 0; d < kD; ++d) po[i][d] = lane + 32 * d < HS ? prefix.o[at * HS + lane + 32 * d] : 0.f;
+        }
+        float m_new = m;
+#pragma unroll
+        for (int i = 0; i < kB; ++i) m_new = fmaxf(m_new, ml[i].x);
+        const float alpha = exp2_approx(m - m_new);  // 0 for a warp that had no chunk
+        l *= alpha;
+#pragma unroll
+        for (int d = 0; d < kD; ++d) ox[d] *= alpha;
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+          const float f = exp2_approx(ml[i].x - m_new);
+          l = fmaf(ml[i].y, f, l);
+#pragma unroll
+          for (int d = 0; d < kD; ++d) ox[d] = fmaf(po[i][d], f, ox[d]);
+        }
+        m = m_new;
+      }
+#pragma unroll
+      for (int d = 0; d < kD; ++d)
+        if (lane + 32 * d < HS) o_s[warp][lane + 32 * d] = ox[d];
+    }
+  }
   if (!producer) {
     if (lane == 0) {
       m_s[warp] = m;
       l_s[warp] = l;
     }
-    if (g == 0) {
+    if (!kShared && g == 0) {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) o_s[warp][dg * kPer + k] = acc[k];
     }
@@ -553,20 +602,7 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, m_s[w]);
-    const size_t pstep = static_cast<size_t>(NH) * gridDim.y;  // a split's rows
-    const size_t prow = static_cast<size_t>(h) * gridDim.y + b;
-    if constexpr (kShared) {
-      for (int s = 0; s < prefix.splits; ++s) M = fmaxf(M, prefix.ml[s * pstep + prow].x);
-    }
     float L = 0.f, O = 0.f;
-    if constexpr (kShared) {
-      for (int s = 0; s < prefix.splits; ++s) {
-        const float2 ml = prefix.ml[s * pstep + prow];
-        const float f = exp2_approx(ml.x - M);
-        L = fmaf(ml.y, f, L);
-        O = fmaf(prefix.o[(s * pstep + prow) * HS + d], f, O);
-      }
-    }
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
       if (m_s[w] == -INFINITY) continue;  // a warp that had no chunk

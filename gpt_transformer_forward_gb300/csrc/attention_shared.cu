@@ -17,9 +17,36 @@
 namespace gpt2 {
 namespace {
 
-constexpr int kTileQ = 32;    // queries per CTA
-constexpr int kTileK = 64;    // keys per step
+constexpr int kTileQ = 32;    // queries per CTA of the CUDA-core kernel
+constexpr int kTileK = 64;    // keys per step of a warp group
 constexpr int kThreads = 128;
+
+// How a shape is cut: queries per CTA, keys per step of a CTA, splits of the
+// prefix and positions per split (a multiple of the step).
+struct Plan {
+  int tile_q, step_k, splits, per;
+};
+
+// Tensor-core kernel: the four warps of a CTA are arranged over 16-row query
+// groups first and over keys with what is left.
+int row_groups(int B) { return B <= 16 ? 1 : B <= 32 ? 2 : 4; }
+
+// Enough splits that the CTAs cover the SMs about twice, each at least a step
+// long.  The count goes by the shape alone, not by the device: it sizes the
+// caller's workspace.
+Plan plan_of(int B, int NH, int prefix_len, bool is16, int* wanted = nullptr) {
+  Plan p;
+  p.tile_q = is16 ? 16 * row_groups(B) : kTileQ;
+  p.step_k = is16 ? kTileK * (4 / row_groups(B)) : kTileK;
+  const long long tiles = static_cast<long long>((B + p.tile_q - 1) / p.tile_q) * NH;
+  const long long want = std::max<long long>(1, (2 * 152 + tiles - 1) / tiles);
+  const long long most = (prefix_len + p.step_k - 1) / p.step_k;
+  const int n = static_cast<int>(std::max<long long>(1, std::min(want, most)));
+  if (wanted != nullptr) *wanted = n;
+  p.per = ((prefix_len + n - 1) / n + p.step_k - 1) / p.step_k * p.step_k;
+  p.splits = (prefix_len + p.per - 1) / p.per;  // at most n
+  return p;
+}
 
 // Copies the block ids of positions [k0, k1) (row 0 of the table) to shared
 // memory; an id outside the pool is flagged and read as block 0.
@@ -178,82 +205,349 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(float* __restrict
   }
 }
 
+// ------------------------------------------------------ tensor-core kernel
+// mma.sync m16n8k16 on the 16-bit type, fp32 accumulators.  Four warps: WM
+// groups of 16 query rows times WK = 4 / WM groups of 64 keys a step (few rows
+// leave a warp's rows for more keys in flight).  K and V tiles come by cp.async
+// into two buffers, rows of HS * 2 bytes with 16-byte chunk c of row r at chunk
+// c ^ (r mod chunks), as in attn_tc_kernel; any block size, since every chunk
+// finds its own block.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;  // 0 source bytes: zero-filled
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
+}
+template <typename T>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+
+template <int HS>
+__device__ __forceinline__ uint32_t swz(int row, int chunk) {
+  constexpr int kChunks = HS / 8;
+  return static_cast<uint32_t>(row * (HS * 2) + ((chunk ^ (row & (kChunks - 1))) << 4));
+}
+
+template <int HS, int WM>
+struct MmaSmem {
+  static constexpr int WK = 4 / WM;
+  static constexpr int kTile = kTileK * HS * 2;  // bytes of a K (or V) tile
+  uint8_t q[WM * 16 * HS * 2];
+  uint8_t k[2][WK][kTile];
+  uint8_t v[2][WK][kTile];
+  float2 ml[4][16];
+  int tbl[kMaxBlocksPerSeq];
+};
+
+template <int HS, typename T16, int WM>
+__global__ void __launch_bounds__(kThreads) prefix_mma_kernel(float* __restrict__ po, float2* __restrict__ pml,
+                                                              const uint16_t* __restrict__ qkv,
+                                                              const uint16_t* __restrict__ kcache,
+                                                              const uint16_t* __restrict__ vcache, int B, int C, int NH,
+                                                              int prefix_len, int per_split, KVRows rows,
+                                                              float scale_log2) {
+  constexpr int WK = 4 / WM, kStep = kTileK * WK;
+  constexpr int kKS = HS / 16;  // k-steps of Q K^T
+  constexpr int kDT = HS / 8;   // 8-wide output column tiles
+  constexpr int kChunks = HS / 8;
+  extern __shared__ __align__(128) uint8_t shared_raw[];
+  auto& sm = *reinterpret_cast<MmaSmem<HS, WM>*>(shared_raw);
+  const int b0 = static_cast<int>(blockIdx.x) * (16 * WM), h = blockIdx.y, split = blockIdx.z;
+  const int k_lo = split * per_split, k_hi = min(prefix_len, k_lo + per_split);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wm = warp % WM, wk = warp / WM;
+  const int g = lane >> 2, tig = lane & 3;
+  pdl_wait();  // the QKV projection ahead has finished
+  pdl_trigger();
+  stage_blocks(sm.tbl, rows, k_lo, k_hi, h == 0 && blockIdx.x == 0);
+  for (int i = threadIdx.x; i < WM * 16 * kChunks; i += kThreads) {
+    const int r = i / kChunks, c = i % kChunks;
+    const bool valid = b0 + r < B;
+    cp_async16(sm.q + swz<HS>(r, c), qkv + static_cast<size_t>(valid ? b0 + r : 0) * 3 * C + h * HS + c * 8, valid);
+  }
+  __syncthreads();  // the block ids
+  const int blk0 = k_lo >> rows.lbs, bs1 = (1 << rows.lbs) - 1;
+  auto load = [&](int buf, int j0) {  // keys [j0, j0 + kStep): group i's tile is keys j0 + 64 i ..
+    for (int i = threadIdx.x; i < kStep * kChunks; i += kThreads) {
+      const int r = i / kChunks, c = i % kChunks, j = j0 + r;
+      const bool valid = j < k_hi;
+      const int jj = valid ? j : k_lo;
+      const size_t row = ((static_cast<size_t>(sm.tbl[(jj >> rows.lbs) - blk0]) * NH + h) << rows.lbs) + (jj & bs1);
+      const uint32_t at = swz<HS>(r % kTileK, c);
+      cp_async16(sm.k[buf][r / kTileK] + at, kcache + row * HS + c * 8, valid);
+      cp_async16(sm.v[buf][r / kTileK] + at, vcache + row * HS + c * 8, valid);
+    }
+  };
+  load(0, k_lo);
+  cp_async_commit();
+  float o[kDT][4];
+#pragma unroll
+  for (int i = 0; i < kDT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.f, 0.f};
+  uint32_t qf[kKS][4];
+  for (int j0 = k_lo, buf = 0; j0 < k_hi; j0 += kStep, buf ^= 1) {
+    if (j0 + kStep < k_hi) load(buf ^ 1, j0 + kStep);
+    cp_async_commit();
+    cp_async_wait<1>();
+    __syncthreads();
+    if (j0 == k_lo) {
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks)
+        ldsm_x4(smem_u32(sm.q) + swz<HS>(wm * 16 + (lane & 15), ks * 2 + (lane >> 4)), qf[ks][0], qf[ks][1], qf[ks][2],
+                qf[ks][3]);
+    }
+    const int valid = k_hi - j0 - wk * kTileK;  // keys of this warp's tile
+    if (valid > 0) {
+      float s[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+      const uint32_t kb = smem_u32(sm.k[buf][wk]), vb = smem_u32(sm.v[buf][wk]);
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks) {
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+          uint32_t r0, r1, r2, r3;
+          ldsm_x4(kb + swz<HS>(np * 16 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)), r0, r1, r2, r3);
+          mma16<T16>(s[2 * np], qf[ks], r0, r1);
+          mma16<T16>(s[2 * np + 1], qf[ks], r2, r3);
+        }
+      }
+      if (valid < kTileK) {
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (nt * 8 + 2 * tig + (e & 1) >= valid) s[nt][e] = -INFINITY;
+      }
+      // online softmax in log2 units: rows g (e = 0, 1) and g + 8 (e = 2, 3)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) mx = fmax3(mx, s[nt][2 * r], s[nt][2 * r + 1]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float m_new = fmaxf(m_r[r], mx * scale_log2);
+        const float alpha = exp2_approx(m_r[r] - m_new);  // 0 on the first tile
+        m_r[r] = m_new;
+        float sum = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+          s[nt][2 * r] = exp2_approx(fmaf(s[nt][2 * r], scale_log2, -m_new));
+          s[nt][2 * r + 1] = exp2_approx(fmaf(s[nt][2 * r + 1], scale_log2, -m_new));
+          sum += s[nt][2 * r] + s[nt][2 * r + 1];
+        }
+        l_r[r] = l_r[r] * alpha + sum;
+#pragma unroll
+        for (int dt = 0; dt < kDT; ++dt) {
+          o[dt][2 * r] *= alpha;
+          o[dt][2 * r + 1] *= alpha;
+        }
+      }
+      // O += P V: P's accumulator layout is the A-operand layout of k-steps.
+      // Its values, at most 1, are rounded to the operands' type
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        uint32_t pa[4];
+        pa[0] = pack2<T16>(s[2 * ks][0], s[2 * ks][1]);
+        pa[1] = pack2<T16>(s[2 * ks][2], s[2 * ks][3]);
+        pa[2] = pack2<T16>(s[2 * ks + 1][0], s[2 * ks + 1][1]);
+        pa[3] = pack2<T16>(s[2 * ks + 1][2], s[2 * ks + 1][3]);
+#pragma unroll
+        for (int dp = 0; dp < kDT / 2; ++dp) {
+          uint32_t r0, r1, r2, r3;
+          ldsm_x4_t(vb + swz<HS>(ks * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), dp * 2 + (lane >> 4)), r0, r1, r2, r3);
+          mma16<T16>(o[2 * dp], pa, r0, r1);
+          mma16<T16>(o[2 * dp + 1], pa, r2, r3);
+        }
+      }
+    }
+    __syncthreads();  // this buffer is refilled by the next step's load
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l_r[r] += __shfl_xor_sync(0xffffffffu, l_r[r], 1);
+    l_r[r] += __shfl_xor_sync(0xffffffffu, l_r[r], 2);
+  }
+  // the key groups' results join in shared memory (over the K tiles), group 0
+  // writes the rows
+  float f[2] = {1.f, 1.f}, L[2] = {l_r[0], l_r[1]}, M[2] = {m_r[0], m_r[1]};
+  if constexpr (WK > 1) {
+    float* os = reinterpret_cast<float*>(sm.k);  // [4][16][HS + 4]
+    constexpr int kRow = HS + 4;
+    static_assert(4 * 16 * kRow * 4 <= sizeof(sm.k) + sizeof(sm.v), "the join's rows fit over the tiles");
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      if (tig == 0) sm.ml[warp][g + 8 * r] = make_float2(m_r[r], l_r[r]);
+    if (wk > 0) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int dt = 0; dt < kDT; ++dt)
+          *reinterpret_cast<float2*>(os + (warp * 16 + g + 8 * r) * kRow + dt * 8 + 2 * tig) =
+              make_float2(o[dt][2 * r], o[dt][2 * r + 1]);
+    }
+    __syncthreads();
+    if (wk > 0) return;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int w = 1; w < WK; ++w) M[r] = fmaxf(M[r], sm.ml[wm + w * WM][g + 8 * r].x);
+      f[r] = exp2_approx(m_r[r] - M[r]);  // group 0 has keys: M is finite
+      L[r] *= f[r];
+#pragma unroll
+      for (int dt = 0; dt < kDT; ++dt) {
+        o[dt][2 * r] *= f[r];
+        o[dt][2 * r + 1] *= f[r];
+      }
+#pragma unroll
+      for (int w = 1; w < WK; ++w) {
+        const float2 ml = sm.ml[wm + w * WM][g + 8 * r];
+        const float fw = exp2_approx(ml.x - M[r]);  // 0 for a group without keys
+        L[r] = fmaf(ml.y, fw, L[r]);
+#pragma unroll
+        for (int dt = 0; dt < kDT; ++dt) {
+          const float2 ow =
+              *reinterpret_cast<const float2*>(os + ((wm + w * WM) * 16 + g + 8 * r) * kRow + dt * 8 + 2 * tig);
+          o[dt][2 * r] = fmaf(ow.x, fw, o[dt][2 * r]);
+          o[dt][2 * r + 1] = fmaf(ow.y, fw, o[dt][2 * r + 1]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int b = b0 + wm * 16 + g + 8 * r;
+    if (b >= B) continue;
+    const size_t at = (static_cast<size_t>(split) * NH + h) * B + b;
+    if (tig == 0) pml[at] = make_float2(M[r], L[r]);
+#pragma unroll
+    for (int dt = 0; dt < kDT; ++dt)
+      *reinterpret_cast<float2*>(po + at * HS + dt * 8 + 2 * tig) = make_float2(o[dt][2 * r], o[dt][2 * r + 1]);
+  }
+}
+
+// Allows a prefix kernel its shared memory, once per instance and device.
+template <typename Smem, typename Kernel>
+cudaError_t allow_smem(bool (&allowed)[kMaxDevices], Kernel kern) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < kMaxDevices && !allowed[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Smem)));
+    allowed[dev] = e == cudaSuccess;
+  }
+  return e;
+}
+
+dim3 prefix_grid(const Plan& pl, int B, int NH) { return dim3((B + pl.tile_q - 1) / pl.tile_q, NH, pl.splits); }
+
 template <typename E, int HS>
 int simt_typed(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc, int B, int C, int NH,
                const KVRows& rows, cudaStream_t s) {
-  const int per = ((p.prefix_len + p.splits - 1) / p.splits + kTileK - 1) / kTileK * kTileK;
-  const dim3 grid((B + kTileQ - 1) / kTileQ, NH, (p.prefix_len + per - 1) / per);
-  const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(HS));
-  static_assert(sizeof(SimtSmem<E, HS>) <= 227 * 1024, "shared memory");
-  static bool attr_set[kMaxDevices] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && dev < kMaxDevices && !attr_set[dev]) {
-    e = cudaFuncSetAttribute(prefix_simt_kernel<E, HS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(sizeof(SimtSmem<E, HS>)));
-    attr_set[dev] = e == cudaSuccess;
-  }
+  static bool allowed[kMaxDevices] = {};
+  const Plan pl = plan_of(B, NH, p.prefix_len, false);
+  using Smem = SimtSmem<E, HS>;
+  cudaError_t e = allow_smem<Smem>(allowed, prefix_simt_kernel<E, HS>);
   if (e == cudaSuccess)
-    e = launch_pdl(prefix_simt_kernel<E, HS>, grid, dim3(kThreads), sizeof(SimtSmem<E, HS>), s, p.o, p.ml,
+    e = launch_pdl(prefix_simt_kernel<E, HS>, prefix_grid(pl, B, NH), dim3(kThreads), sizeof(Smem), s, p.o, p.ml,
                    static_cast<const E*>(qkv), static_cast<const E*>(kc), static_cast<const E*>(vc), B, C, NH,
-                   p.prefix_len, per, rows, scale_log2);
+                   p.prefix_len, pl.per, rows, 1.4426950408889634f / sqrtf(static_cast<float>(HS)));
   return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
 }
 
-template <typename E>
-int simt(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc, int B, int C, int NH,
-         const KVRows& rows, cudaStream_t s) {
+template <int HS, typename T16, int WM>
+int mma_typed(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc, int B, int C, int NH,
+              const KVRows& rows, cudaStream_t s) {
+  static bool allowed[kMaxDevices] = {};
+  const Plan pl = plan_of(B, NH, p.prefix_len, true);
+  using Smem = MmaSmem<HS, WM>;
+  static_assert(sizeof(Smem) <= 227 * 1024, "shared memory");
+  cudaError_t e = allow_smem<Smem>(allowed, prefix_mma_kernel<HS, T16, WM>);
+  if (e == cudaSuccess)
+    e = launch_pdl(prefix_mma_kernel<HS, T16, WM>, prefix_grid(pl, B, NH), dim3(kThreads), sizeof(Smem), s, p.o, p.ml,
+                   static_cast<const uint16_t*>(qkv), static_cast<const uint16_t*>(kc),
+                   static_cast<const uint16_t*>(vc), B, C, NH, p.prefix_len, pl.per, rows,
+                   1.4426950408889634f / sqrtf(static_cast<float>(HS)));
+  return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
+}
+
+template <int HS, typename T16>
+int mma_rows(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc, int B, int C, int NH,
+             const KVRows& rows, cudaStream_t s) {
+  switch (row_groups(B)) {
+    case 1: return mma_typed<HS, T16, 1>(p, qkv, kc, vc, B, C, NH, rows, s);
+    case 2: return mma_typed<HS, T16, 2>(p, qkv, kc, vc, B, C, NH, rows, s);
+    default: return mma_typed<HS, T16, 4>(p, qkv, kc, vc, B, C, NH, rows, s);
+  }
+}
+
+template <typename T16>
+int mma(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc, int B, int C, int NH,
+        const KVRows& rows, cudaStream_t s) {
   switch (C / NH) {
-    case 16: return simt_typed<E, 16>(p, qkv, kc, vc, B, C, NH, rows, s);
-    case 32: return simt_typed<E, 32>(p, qkv, kc, vc, B, C, NH, rows, s);
-    case 64: return simt_typed<E, 64>(p, qkv, kc, vc, B, C, NH, rows, s);
+    case 16: return mma_rows<16, T16>(p, qkv, kc, vc, B, C, NH, rows, s);
+    case 32: return mma_rows<32, T16>(p, qkv, kc, vc, B, C, NH, rows, s);
+    case 64: return mma_rows<64, T16>(p, qkv, kc, vc, B, C, NH, rows, s);
   }
   return GPT2_ERR_UNSUPPORTED;
 }
 
+// Partial rows a workspace holds: those of the worst batch of at most B
+// sequences, so that one workspace serves smaller batches and, as the wanted
+// splits grow with it, shorter prefixes too.  The worst of the batches with
+// the same query tiles is the one with full tiles.
+size_t partial_rows(int B, int NH, int prefix_len, bool is16) {
+  if (prefix_len <= 0) return 0;
+  size_t most = 0;
+  for (int b = 16;; b += b < 64 ? 16 : 32) {
+    const int c = std::min(b, B);
+    int n = 0;
+    plan_of(c, NH, prefix_len, is16, &n);
+    most = std::max(most, static_cast<size_t>(n) * c);
+    if (b >= B) return most * NH;
+  }
+}
+
 }  // namespace
 
-// Enough splits that the prefix's CTAs cover the SMs about twice, each at
-// least two steps long.  The count goes by the shape alone, not by the device:
-// it sizes the caller's workspace.
-static int splits_wanted(int B, int NH, int prefix_len) {
-  const long long tiles = static_cast<long long>((B + kTileQ - 1) / kTileQ) * NH;
-  const long long want = std::max<long long>(1, (2 * 152 + tiles - 1) / tiles);
-  const long long most = std::max(1, prefix_len / (2 * kTileK));
-  return static_cast<int>(std::min(want, most));
-}
-
-// The number of splits after rounding each to whole steps (never above the
-// number wanted).
-int shared_prefix_splits(int B, int NH, int hs, int prefix_len, bool is16) {
-  (void)hs;
-  (void)is16;
-  if (prefix_len <= 0) return 0;
-  const int n = splits_wanted(B, NH, prefix_len);
-  const int per = ((prefix_len + n - 1) / n + kTileK - 1) / kTileK * kTileK;
-  return (prefix_len + per - 1) / per;
-}
-
-// Partial rows a workspace holds: those of the worst batch of at most B
-// sequences (a full last query tile), so that one workspace serves smaller
-// batches and, as splits_wanted grows with it, shorter prefixes too.
-static size_t partial_rows(int B, int NH, int prefix_len) {
-  if (prefix_len <= 0) return 0;
-  size_t rows = static_cast<size_t>(splits_wanted(B, NH, prefix_len)) * B;
-  for (int b = kTileQ; b < B; b += kTileQ)
-    rows = std::max(rows, static_cast<size_t>(splits_wanted(b, NH, prefix_len)) * b);
-  return rows * NH;
+int shared_prefix_splits(int B, int NH, int prefix_len, bool is16) {
+  return prefix_len > 0 ? plan_of(B, NH, prefix_len, is16).splits : 0;
 }
 
 size_t shared_prefix_bytes(int B, int NH, int hs, int prefix_len, bool is16) {
-  (void)is16;
-  const size_t rows = partial_rows(B, NH, prefix_len);
+  const size_t rows = partial_rows(B, NH, prefix_len, is16);
   return (rows * hs * sizeof(float) + 255) / 256 * 256 + (rows * sizeof(float2) + 255) / 256 * 256;
 }
 
 PrefixPartials shared_prefix_layout(void* workspace, int B, int NH, int hs, int prefix_len, bool is16) {
   PrefixPartials p;
-  p.splits = shared_prefix_splits(B, NH, hs, prefix_len, is16);
+  p.splits = shared_prefix_splits(B, NH, prefix_len, is16);
   p.prefix_len = prefix_len;
   const size_t rows = static_cast<size_t>(p.splits) * NH * B;
   p.o = static_cast<float*>(workspace);
@@ -263,9 +557,14 @@ PrefixPartials shared_prefix_layout(void* workspace, int B, int NH, int hs, int 
 
 int launch_shared_prefix(const PrefixPartials& p, const void* qkv, const void* kcache, const void* vcache, int op,
                          int B, int C, int NH, const KVRows& rows, cudaStream_t s) {
-  if (op == kOpF16) return simt<__half>(p, qkv, kcache, vcache, B, C, NH, rows, s);
-  if (op == kOpBF16) return simt<__nv_bfloat16>(p, qkv, kcache, vcache, B, C, NH, rows, s);
-  return simt<float>(p, qkv, kcache, vcache, B, C, NH, rows, s);
+  if (op == kOpF16) return mma<__half>(p, qkv, kcache, vcache, B, C, NH, rows, s);
+  if (op == kOpBF16) return mma<__nv_bfloat16>(p, qkv, kcache, vcache, B, C, NH, rows, s);
+  switch (C / NH) {
+    case 16: return simt_typed<float, 16>(p, qkv, kcache, vcache, B, C, NH, rows, s);
+    case 32: return simt_typed<float, 32>(p, qkv, kcache, vcache, B, C, NH, rows, s);
+    case 64: return simt_typed<float, 64>(p, qkv, kcache, vcache, B, C, NH, rows, s);
+  }
+  return GPT2_ERR_UNSUPPORTED;
 }
 
 }  // namespace gpt2

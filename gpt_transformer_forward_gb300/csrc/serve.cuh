@@ -29,7 +29,7 @@ void launch_kv_store_slots(void* kc, void* vc, const void* qkv, const int* slots
 
 // attention_shared.cu
 // Splits of the prefix and the bytes of their partial results.
-int shared_prefix_splits(int B, int NH, int hs, int prefix_len, bool is16);
+int shared_prefix_splits(int B, int NH, int prefix_len, bool is16);
 size_t shared_prefix_bytes(int B, int NH, int hs, int prefix_len, bool is16);
 // The partial results over positions [0, prefix_len) for all B queries:
 // per split s, head h and sequence b the unnormalised output [hs], the running

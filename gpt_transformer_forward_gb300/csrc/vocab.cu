@@ -654,10 +654,14 @@ cudaError_t launch_rows(void (*kern)(KArgs...), unsigned rows, int threads, size
 
 // Blocks that share a row: as many as fit the GPU at once when rows are few
 // (`resident`: blocks that it holds), each with a vector for every thread at
-// least.  Clusters of up to eight blocks launch everywhere.
+// least, and a power of two: clusters of other sizes pack badly (64 rows of
+// 50257 fp32 logits: 7.2 us in clusters of seven, 5.3 us of four).  Clusters of
+// up to eight blocks launch everywhere.
 int row_parts(int N, int vecs, int threads, int resident) {
-  const int most = std::min(kMaxParts, std::max(1, vecs / threads));
-  return std::max(1, std::min(most, resident / N));
+  const int most = std::min(std::min(kMaxParts, vecs / threads), resident / N);
+  int parts = 1;
+  while (2 * parts <= most) parts *= 2;
+  return parts;
 }
 
 template <typename T, int kT, bool kTop>
