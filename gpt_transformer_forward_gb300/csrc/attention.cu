@@ -424,8 +424,15 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
   bool prod_ok = true;
   if (producer && lane == 0)
     for (int c = 0; c < min(n_cached, kDecStages) && prod_ok; ++c) prod_ok = issue(c);
-  pdl_wait();  // q and this token's key and value come from the QKV projection
-  pdl_trigger();
+  // kShared, behind a prefix kernel: that kernel began only once the QKV
+  // projection had finished, and this one once the prefix kernel had begun, so
+  // q may be read now and the own positions run beside the prefix; its results
+  // are waited for below
+  const bool late = kShared && prefix.splits > 0;
+  if (!late) {
+    pdl_wait();  // q and this token's key and value come from the QKV projection
+    pdl_trigger();
+  }
   float m = -INFINITY, l = 0.f, acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
@@ -536,6 +543,10 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
     l += __shfl_xor_sync(0xffffffffu, l, o);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+  }
+  if (late) {
+    pdl_wait();
+    pdl_trigger();
   }
   if constexpr (kShared) {
     // the prefix's splits s = warp, warp + kDecWarps, ... join this warp's

@@ -20,29 +20,41 @@ namespace {
 constexpr int kTileQ = 32;    // queries per CTA of the CUDA-core kernel
 constexpr int kTileK = 64;    // keys per step of a warp group
 constexpr int kThreads = 128;
+constexpr int kTcMinBatch = 65;  // sequences from which the tcgen05 kernel takes over (head size 64)
 
-// How a shape is cut: queries per CTA, keys per step of a CTA, splits of the
-// prefix and positions per split (a multiple of the step).
+// How a shape is cut: the kernel, queries per CTA, keys per step of a CTA,
+// splits of the prefix over CTAs, positions per split (a multiple of the step)
+// and partial results per split.
+enum Kernel { kSimt, kMma, kTc05 };
 struct Plan {
-  int tile_q, step_k, splits, per;
+  Kernel kernel;
+  int tile_q, step_k, splits, per, parts;
 };
 
-// Tensor-core kernel: the four warps of a CTA are arranged over 16-row query
-// groups first and over keys with what is left.
+// Tensor-core kernel of few sequences: the four warps of a CTA are arranged
+// over 16-row query groups first and over keys with what is left.
 int row_groups(int B) { return B <= 16 ? 1 : B <= 32 ? 2 : 4; }
 
-// Enough splits that the CTAs cover the SMs about twice, each at least a step
-// long.  The count goes by the shape alone, not by the device: it sizes the
-// caller's workspace.
-Plan plan_of(int B, int NH, int prefix_len, bool is16, int* wanted = nullptr) {
+// Enough splits that the CTAs cover the SMs (twice, where two fit an SM), each
+// at least a step long.  The count goes by the shape alone, not by the device:
+// it sizes the caller's workspace.
+Plan plan_of(int B, int NH, int hs, int prefix_len, bool is16, int* wanted = nullptr) {
   Plan p;
-  p.tile_q = is16 ? 16 * row_groups(B) : kTileQ;
-  p.step_k = is16 ? kTileK * (4 / row_groups(B)) : kTileK;
+  p.kernel = !is16 ? kSimt : hs == 64 && B >= kTcMinBatch ? kTc05 : kMma;
+  p.parts = 1;
+  if (p.kernel == kTc05) {
+    p.tile_q = 256;
+    p.step_k = 128;
+    p.parts = B <= 128 ? 2 : 1;  // its softmax groups split the keys
+  } else {
+    p.tile_q = is16 ? 16 * row_groups(B) : kTileQ;
+    p.step_k = is16 ? kTileK * (4 / row_groups(B)) : kTileK;
+  }
   const long long tiles = static_cast<long long>((B + p.tile_q - 1) / p.tile_q) * NH;
-  const long long want = std::max<long long>(1, (2 * 152 + tiles - 1) / tiles);
+  const long long want = p.kernel == kTc05 ? 152 / tiles : (2 * 152 + tiles - 1) / tiles;
   const long long most = (prefix_len + p.step_k - 1) / p.step_k;
   const int n = static_cast<int>(std::max<long long>(1, std::min(want, most)));
-  if (wanted != nullptr) *wanted = n;
+  if (wanted != nullptr) *wanted = n * p.parts;
   p.per = ((prefix_len + n - 1) / n + p.step_k - 1) / p.step_k * p.step_k;
   p.splits = (prefix_len + p.per - 1) / p.per;  // at most n
   return p;
@@ -471,7 +483,7 @@ template <typename E, int HS>
 int simt_typed(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc, int B, int C, int NH,
                const KVRows& rows, cudaStream_t s) {
   static bool allowed[kMaxDevices] = {};
-  const Plan pl = plan_of(B, NH, p.prefix_len, false);
+  const Plan pl = plan_of(B, NH, HS, p.prefix_len, false);
   using Smem = SimtSmem<E, HS>;
   cudaError_t e = allow_smem<Smem>(allowed, prefix_simt_kernel<E, HS>);
   if (e == cudaSuccess)
@@ -485,7 +497,7 @@ template <int HS, typename T16, int WM>
 int mma_typed(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc, int B, int C, int NH,
               const KVRows& rows, cudaStream_t s) {
   static bool allowed[kMaxDevices] = {};
-  const Plan pl = plan_of(B, NH, p.prefix_len, true);
+  const Plan pl = plan_of(B, NH, HS, p.prefix_len, true);
   using Smem = MmaSmem<HS, WM>;
   static_assert(sizeof(Smem) <= 227 * 1024, "shared memory");
   cudaError_t e = allow_smem<Smem>(allowed, prefix_mma_kernel<HS, T16, WM>);
@@ -522,13 +534,13 @@ int mma(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc
 // sequences, so that one workspace serves smaller batches and, as the wanted
 // splits grow with it, shorter prefixes too.  The worst of the batches with
 // the same query tiles is the one with full tiles.
-size_t partial_rows(int B, int NH, int prefix_len, bool is16) {
+size_t partial_rows(int B, int NH, int hs, int prefix_len, bool is16) {
   if (prefix_len <= 0) return 0;
   size_t most = 0;
   for (int b = 16;; b += b < 64 ? 16 : 32) {
     const int c = std::min(b, B);
     int n = 0;
-    plan_of(c, NH, prefix_len, is16, &n);
+    plan_of(c, NH, hs, prefix_len, is16, &n);
     most = std::max(most, static_cast<size_t>(n) * c);
     if (b >= B) return most * NH;
   }
@@ -536,18 +548,18 @@ size_t partial_rows(int B, int NH, int prefix_len, bool is16) {
 
 }  // namespace
 
-int shared_prefix_splits(int B, int NH, int prefix_len, bool is16) {
-  return prefix_len > 0 ? plan_of(B, NH, prefix_len, is16).splits : 0;
-}
-
 size_t shared_prefix_bytes(int B, int NH, int hs, int prefix_len, bool is16) {
-  const size_t rows = partial_rows(B, NH, prefix_len, is16);
+  const size_t rows = partial_rows(B, NH, hs, prefix_len, is16);
   return (rows * hs * sizeof(float) + 255) / 256 * 256 + (rows * sizeof(float2) + 255) / 256 * 256;
 }
 
 PrefixPartials shared_prefix_layout(void* workspace, int B, int NH, int hs, int prefix_len, bool is16) {
   PrefixPartials p;
-  p.splits = shared_prefix_splits(B, NH, prefix_len, is16);
+  p.splits = 0;
+  if (prefix_len > 0) {
+    const Plan pl = plan_of(B, NH, hs, prefix_len, is16);
+    p.splits = pl.splits * pl.parts;
+  }
   p.prefix_len = prefix_len;
   const size_t rows = static_cast<size_t>(p.splits) * NH * B;
   p.o = static_cast<float*>(workspace);
@@ -557,6 +569,11 @@ PrefixPartials shared_prefix_layout(void* workspace, int B, int NH, int hs, int 
 
 int launch_shared_prefix(const PrefixPartials& p, const void* qkv, const void* kcache, const void* vcache, int op,
                          int B, int C, int NH, const KVRows& rows, cudaStream_t s) {
+  if (op != kOpTF32) {
+    const Plan pl = plan_of(B, NH, C / NH, p.prefix_len, true);
+    if (pl.kernel == kTc05)
+      return launch_shared_prefix_tc05(p, qkv, kcache, vcache, op, B, C, NH, pl.per / pl.step_k, rows, s);
+  }
   if (op == kOpF16) return mma<__half>(p, qkv, kcache, vcache, B, C, NH, rows, s);
   if (op == kOpBF16) return mma<__nv_bfloat16>(p, qkv, kcache, vcache, B, C, NH, rows, s);
   switch (C / NH) {

@@ -28,8 +28,7 @@ void launch_kv_store_slots(void* kc, void* vc, const void* qkv, const int* slots
                            int lbs, int num_blocks, cudaStream_t s);
 
 // attention_shared.cu
-// Splits of the prefix and the bytes of their partial results.
-int shared_prefix_splits(int B, int NH, int prefix_len, bool is16);
+// Bytes of the prefix's partial results.
 size_t shared_prefix_bytes(int B, int NH, int hs, int prefix_len, bool is16);
 // The partial results over positions [0, prefix_len) for all B queries:
 // per split s, head h and sequence b the unnormalised output [hs], the running
@@ -44,6 +43,10 @@ PrefixPartials shared_prefix_layout(void* workspace, int B, int NH, int hs, int 
 // op: kOpBF16 or kOpF16 for a 16-bit cache, kOpTF32 for an fp32 one
 int launch_shared_prefix(const PrefixPartials& p, const void* qkv, const void* kcache, const void* vcache, int op,
                          int B, int C, int NH, const KVRows& rows, cudaStream_t s);
+// attention_shared_tc.cu: the tcgen05 kernel of launch_shared_prefix (head size
+// 64, 16-bit types)
+int launch_shared_prefix_tc05(const PrefixPartials& p, const void* qkv, const void* kcache, const void* vcache, int op,
+                              int B, int C, int NH, int tiles_per_split, const KVRows& rows, cudaStream_t s);
 // attention.cu: the sequences' own positions [prefix_len, pos] and the join
 // with the prefix's partial results; the token's key and value are appended
 void launch_shared_decode_attention(void* out, const void* qkv, void* kcache, void* vcache, int op, int B, int C,
