@@ -571,7 +571,7 @@ static int shared_attention(void* out, const void* qkv, void* kc, void* vc, int 
   if (p.splits > 0) TRY(launch_shared_prefix(p, qkv, kc, vc, op, B, C, NH, rows, s));
   // the kernel waits for the prefix's results itself
   PdlScope pdl(pdl_on() || p.splits > 0);
-  launch_shared_decode_attention(out, qkv, kc, vc, op, B, C, NH, pos, rows, p, s);
+  TRY(launch_own_join(out, qkv, kc, vc, op, B, C, NH, pos, rows, p, s));
   return check_launch();
 }
 
@@ -927,7 +927,8 @@ int attention_shared_prefix(void* out, const void* qkv, const GPT2PagedKVCache* 
   RETURN_IF(B < 0 || C <= 0 || NH <= 0 || prefix_len < 0 || !valid_precision(precision) || out == qkv, GPT2_ERR_ARG);
   const int lbs = log2_exact(kvc->block_size);
   RETURN_IF(lbs < 0 || kvc->num_blocks <= 0 || kvc->max_blocks_per_seq <= 0, GPT2_ERR_ARG);
-  RETURN_IF(C % NH != 0 || kvc->max_blocks_per_seq > kMaxBlocksPerSeq || B > kMaxSharedBatch || NH > kMaxSharedBatch,
+  RETURN_IF(C % NH != 0 || kvc->max_blocks_per_seq > kMaxBlocksPerSeq || B > kMaxSharedBatch || NH > kMaxSharedBatch ||
+                static_cast<long long>(B) * NH > 0x7fffffffLL,
             GPT2_ERR_SHAPE);
   const long long cap =
       std::min<long long>(0x7fffffffLL, static_cast<long long>(kvc->max_blocks_per_seq) << lbs);

@@ -17,7 +17,7 @@
 //   attn_f32_kernel     fp32 CUDA cores, reference-grade (GPT2_FP32 mode);
 //   decode_attn_kernel  one query per sequence against the KV cache, one
 //                       block per (head, sequence).
-#include "serve.cuh"
+#include "kernels.cuh"
 
 namespace gpt2 {
 namespace {
@@ -324,11 +324,6 @@ __global__ void __launch_bounds__(64) attn_f32_kernel(float* __restrict__ out, c
 // block of position p of sequence b is table[b][p / block] (the block-table
 // layout of a paged KV cache).  Positions come from `pos` (all sequences
 // at one position) or, when pos_arr is given, per sequence from it.
-//
-// kShared: the batch's first prefix.prefix_len positions are shared, and
-// another kernel ahead has left their partial results (attention_shared.cu).
-// The block then walks positions [prefix_len, pos] only and its merge takes
-// in, beside its warps' results, those of the prefix's splits.
 constexpr int kDecWarps = 4;       // warps computing; one more issues the copies
 constexpr int kDecStages = 8;      // chunks of the cache in shared memory
 constexpr int kDecStageBytes = 8192;  // a chunk's K rows, then its V rows (4 KB each)
@@ -339,11 +334,11 @@ constexpr int kDecSmem = kDecStages * kDecStageBytes + 2 * kDecStages * 8;
 // of the fill it needs (a waiter two phases ahead would pass at once)
 static_assert(kDecStages % kDecWarps == 0, "stages per warp");
 
-template <typename E, typename OutT, int HS, bool kShared>
+template <typename E, typename OutT, int HS>
 __global__ void __launch_bounds__(32 * (kDecWarps + 1))
     decode_attn_kernel(OutT* __restrict__ out, const E* __restrict__ qkv, E* __restrict__ kcache,
                        E* __restrict__ vcache, int C, int NH, int pos_all, const int* __restrict__ pos_arr,
-                       KVRows rows, float scale_log2, PrefixPartials prefix) {
+                       KVRows rows, float scale_log2) {
   constexpr int kPer = 16 / static_cast<int>(sizeof(E));  // elements per 16-byte load
   constexpr int kLPR = HS / kPer;                          // lanes per K or V row
   constexpr int kRPI = 32 / kLPR;                          // rows per warp instruction
@@ -365,8 +360,7 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
   // the caller's positions and block table are inputs of the step, written
   // before its first kernel: they may be read before the wait below
   const int pos = pos_arr != nullptr ? __ldg(pos_arr + b) : pos_all;
-  const int first = kShared ? prefix.prefix_len : 0;  // positions before it are another kernel's
-  const bool pos_ok = pos >= first && pos < rows.capacity;
+  const bool pos_ok = pos >= 0 && pos < rows.capacity;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDecStages; ++i) {
       mbar_init(&full[i], 1u);
@@ -375,7 +369,7 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
     fence_barrier_init();
   }
   if (rows.table != nullptr && pos_ok) {
-    for (int i = (first >> rows.lbs) + threadIdx.x; i <= (pos >> rows.lbs); i += blockDim.x) {
+    for (int i = threadIdx.x; i <= (pos >> rows.lbs); i += blockDim.x) {
       int blk = __ldg(rows.table + static_cast<size_t>(b) * rows.max_blocks + i);
       if (blk < 0 || blk >= rows.num_blocks) {
         if (h == 0) set_error(GPT2_DEVERR_BLOCK);
@@ -398,13 +392,13 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
   // leaves HBM mostly idle.  (With each warp loading its chunk into
   // registers and waiting for it in turn, the kernel kept one chunk per warp
   // in flight: measured, about 12 us per layer inside a decode step.)
-  const int n_cached = pos_ok ? (pos - first + kChunk - 1) / kChunk : 0;  // chunks with cache rows
+  const int n_cached = pos_ok ? (pos + kChunk - 1) / kChunk : 0;  // chunks with cache rows
   uint32_t filled = 0, fill_par = 0;  // producer: stages ever filled, parity of their last fill
   int issued = 0;
   auto issue = [&](int c) -> bool {  // producer lane: chunk c into stage c % kDecStages
     const int st = c % kDecStages;
     if (c >= kDecStages && !mbar_wait(&empty[st], ((c / kDecStages) - 1) & 1)) return false;
-    const int j0 = first + c * kChunk, j1 = min(j0 + kChunk, pos);
+    const int j0 = c * kChunk, j1 = min(j0 + kChunk, pos);
     uint8_t* kdst = dec_smem + st * kDecStageBytes;
     mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>((j1 - j0) * kRowBytes * 2));
     for (int j = j0; j < j1;) {
@@ -424,15 +418,8 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
   bool prod_ok = true;
   if (producer && lane == 0)
     for (int c = 0; c < min(n_cached, kDecStages) && prod_ok; ++c) prod_ok = issue(c);
-  // kShared, behind a prefix kernel: that kernel began only once the QKV
-  // projection had finished, and this one once the prefix kernel had begun, so
-  // q may be read now and the own positions run beside the prefix; its results
-  // are waited for below
-  const bool late = kShared && prefix.splits > 0;
-  if (!late) {
-    pdl_wait();  // q and this token's key and value come from the QKV projection
-    pdl_trigger();
-  }
+  pdl_wait();  // q and this token's key and value come from the QKV projection
+  pdl_trigger();
   float m = -INFINITY, l = 0.f, acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
@@ -463,12 +450,12 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
       reinterpret_cast<uint4*>(kcache + row(pos) * HS)[dg] = __ldg(kq);
       reinterpret_cast<uint4*>(vcache + row(pos) * HS)[dg] = __ldg(vq);
     }
-    const int nchunk = (pos - first) / kChunk + 1;  // chunks covering positions first .. pos
+    const int nchunk = pos / kChunk + 1;  // chunks covering positions 0 .. pos
     // K and V rows of chunk c into registers: rows before pos from the
     // chunk's stage (its copy waited for, the stage freed once read), row pos
     // from the QKV row, zero past pos
     auto load = [&](int c, uint4(&kr)[kIt], uint4(&vr)[kIt]) -> bool {
-      const int j0 = first + c * kChunk;
+      const int j0 = c * kChunk;
       const bool staged = c < n_cached;
       const int st = c % kDecStages;
       if (staged && !__all_sync(0xffffffffu, mbar_wait(&full[st], (c / kDecStages) & 1))) return false;
@@ -495,7 +482,7 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
     };
     // the online softmax over chunk c's rows
     auto consume = [&](int c, const uint4(&kr)[kIt], const uint4(&vr)[kIt]) {
-      const int j0 = first + c * kChunk + g;
+      const int j0 = c * kChunk + g;
       // scores (log2 units) of this lane's kIt rows; the row's kLPR lanes
       // each hold a partial dot product and sum it by shuffles
       float sc[kIt];
@@ -513,7 +500,7 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
       }
 #pragma unroll
       for (int o = 16; o >= kLPR; o >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
-      // position first + c * kChunk <= pos is in the chunk, so cmax is finite
+      // position c * kChunk <= pos is in the chunk, so cmax is finite
       const float m_new = fmaxf(m, cmax);
       const float alpha = exp2_approx(m - m_new);  // 0 on the first chunk (m = -inf)
       l *= alpha;
@@ -544,65 +531,12 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
   }
-  if (late) {
-    pdl_wait();
-    pdl_trigger();
-  }
-  if constexpr (kShared) {
-    // the prefix's splits s = warp, warp + kDecWarps, ... join this warp's
-    // result: lane i holds dimensions i, i + 32 of each, four splits' loads in
-    // flight
-    if (!producer && pos_ok) {
-      if (g == 0) {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) o_s[warp][dg * kPer + k] = acc[k];
-      }
-      __syncwarp();
-      constexpr int kD = (HS + 31) / 32, kB = 4;
-      float ox[kD];
-#pragma unroll
-      for (int d = 0; d < kD; ++d) ox[d] = lane + 32 * d < HS ? o_s[warp][lane + 32 * d] : 0.f;
-      const size_t step = static_cast<size_t>(NH) * gridDim.y;  // a split's rows
-      const size_t row0 = static_cast<size_t>(h) * gridDim.y + b;
-      for (int s0 = warp; s0 < prefix.splits; s0 += kDecWarps * kB) {
-        float2 ml[kB];
-        float po[kB][kD];
-#pragma unroll
-        for (int i = 0; i < kB; ++i) {
-          const int s = s0 + i * kDecWarps;
-          const size_t at = (s < prefix.splits ? s : s0) * step + row0;
-          ml[i] = prefix.ml[at];
-          if (s >= prefix.splits) ml[i] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-          for (int d = 0; d < kD; ++d) po[i][d] = lane + 32 * d < HS ? prefix.o[at * HS + lane + 32 * d] : 0.f;
-        }
-        float m_new = m;
-#pragma unroll
-        for (int i = 0; i < kB; ++i) m_new = fmaxf(m_new, ml[i].x);
-        const float alpha = exp2_approx(m - m_new);  // 0 for a warp that had no chunk
-        l *= alpha;
-#pragma unroll
-        for (int d = 0; d < kD; ++d) ox[d] *= alpha;
-#pragma unroll
-        for (int i = 0; i < kB; ++i) {
-          const float f = exp2_approx(ml[i].x - m_new);
-          l = fmaf(ml[i].y, f, l);
-#pragma unroll
-          for (int d = 0; d < kD; ++d) ox[d] = fmaf(po[i][d], f, ox[d]);
-        }
-        m = m_new;
-      }
-#pragma unroll
-      for (int d = 0; d < kD; ++d)
-        if (lane + 32 * d < HS) o_s[warp][lane + 32 * d] = ox[d];
-    }
-  }
   if (!producer) {
     if (lane == 0) {
       m_s[warp] = m;
       l_s[warp] = l;
     }
-    if (!kShared && g == 0) {
+    if (g == 0) {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) o_s[warp][dg * kPer + k] = acc[k];
     }
@@ -666,21 +600,21 @@ int launch_attention_f32(float* out, const float* qkv, int B, int T, int C, int 
   return GPT2_ERR_UNSUPPORTED;
 }
 
-template <typename E, typename OutT, int HS, bool kShared = false>
+template <typename E, typename OutT, int HS>
 static void decode_typed(OutT* out, const E* qkv, E* kc, E* vc, int B, int C, int NH, int pos, const int* pos_arr,
-                         const KVRows& rows, cudaStream_t s, const PrefixPartials& prefix = PrefixPartials{}) {
+                         const KVRows& rows, cudaStream_t s) {
   const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(HS));
   // the ring of cache chunks is dynamic shared memory beyond the 48 KB a
   // launch gets without asking (set once per instantiation and device)
   static bool attr_set[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(decode_attn_kernel<E, OutT, HS, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(decode_attn_kernel<E, OutT, HS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kDecSmem) == cudaSuccess)
       attr_set[dev] = true;
   }
-  launch_pdl(decode_attn_kernel<E, OutT, HS, kShared>, dim3(NH, B), dim3(32 * (kDecWarps + 1)), kDecSmem, s, out, qkv,
-             kc, vc, C, NH, pos, pos_arr, rows, scale_log2, prefix);
+  launch_pdl(decode_attn_kernel<E, OutT, HS>, dim3(NH, B), dim3(32 * (kDecWarps + 1)), kDecSmem, s, out, qkv, kc, vc,
+             C, NH, pos, pos_arr, rows, scale_log2);
 }
 
 template <typename E>
@@ -722,31 +656,6 @@ void launch_decode_attention_f32(float* out, const float* qkv, float* kcache, fl
     case 32: decode_typed<float, float, 32>(out, qkv, kcache, vcache, B, C, NH, pos, pos_arr, rows, s); break;
     default: decode_typed<float, float, 64>(out, qkv, kcache, vcache, B, C, NH, pos, pos_arr, rows, s); break;
   }
-}
-
-template <typename E>
-static void shared_typed(void* out, const void* qkv, void* kcache, void* vcache, int B, int C, int NH,
-                         const int* pos_arr, const KVRows& rows, const PrefixPartials& p, cudaStream_t s) {
-  E* o = static_cast<E*>(out);
-  const E* q = static_cast<const E*>(qkv);
-  E* kc = static_cast<E*>(kcache);
-  E* vc = static_cast<E*>(vcache);
-  switch (C / NH) {
-    case 16: decode_typed<E, E, 16, true>(o, q, kc, vc, B, C, NH, 0, pos_arr, rows, s, p); break;
-    case 32: decode_typed<E, E, 32, true>(o, q, kc, vc, B, C, NH, 0, pos_arr, rows, s, p); break;
-    default: decode_typed<E, E, 64, true>(o, q, kc, vc, B, C, NH, 0, pos_arr, rows, s, p); break;
-  }
-}
-
-void launch_shared_decode_attention(void* out, const void* qkv, void* kcache, void* vcache, int op, int B, int C,
-                                    int NH, const int* pos_arr, const KVRows& rows, const PrefixPartials& p,
-                                    cudaStream_t s) {
-  if (op == kOpF16)
-    shared_typed<__half>(out, qkv, kcache, vcache, B, C, NH, pos_arr, rows, p, s);
-  else if (op == kOpBF16)
-    shared_typed<__nv_bfloat16>(out, qkv, kcache, vcache, B, C, NH, pos_arr, rows, p, s);
-  else
-    shared_typed<float>(out, qkv, kcache, vcache, B, C, NH, pos_arr, rows, p, s);
 }
 
 }  // namespace gpt2

@@ -1,15 +1,19 @@
-// attention_shared.cu -- decode attention over positions that every sequence
-// of a batch shares: the partial results of the prefix [0, prefix_len) for all
-// B queries, each key and value read once a query tile instead of once a
-// sequence.  The sequences' own positions and the join are the decode
-// attention kernel's (attention.cu).
+// attention_shared.cu -- decode attention of a batch whose sequences share
+// their first positions [0, prefix_len).
 //
-// For head h the B queries against the prefix are a matrix product of their
-// own, S = Q K^T, O = P V, with the online softmax of FlashAttention's
-// Algorithm 1 per row.  The prefix is split over CTAs (few heads and query
-// tiles would leave most SMs idle); every split keeps its rows' running
-// maximum m, sum l and unnormalised output O, and the join weighs them by
-// 2^(m - max m).
+// Prefix: for head h the B queries against the shared positions are a matrix
+// product of their own, S = Q K^T, O = P V, with the online softmax of
+// FlashAttention's Algorithm 1 per row: each key and value is read once a query
+// tile instead of once a sequence.  The prefix is split over CTAs (few heads
+// and query tiles would leave most SMs idle); every split keeps its rows'
+// running maximum m, sum l and unnormalised output O.
+//   prefix_simt_kernel   fp32 caches, CUDA cores
+//   prefix_mma_kernel    16-bit caches, mma.sync: few sequences, or a head
+//                        size below 64
+//   prefix_tc05_kernel   16-bit caches, tcgen05 (attention_shared_tc.cu): many
+//                        sequences
+// Join: own_join_kernel attends over each sequence's own positions and joins
+// that with the splits' results, which it weighs by 2^(m - max m).
 #include "serve.cuh"
 
 #include <algorithm>
@@ -95,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(float* __restrict
                                                                const E* __restrict__ vcache, int B, int C, int NH,
                                                                int prefix_len, int per_split, KVRows rows,
                                                                float scale_log2) {
-  extern __shared__ __align__(16) uint8_t shared_raw[];
+  extern __shared__ __align__(128) uint8_t shared_raw[];
   auto& sm = *reinterpret_cast<SimtSmem<E, HS>*>(shared_raw);
   constexpr int kD = HS / 16;
   constexpr int kPer = 16 / static_cast<int>(sizeof(E));  // elements per 16-byte load
@@ -465,16 +469,318 @@ __global__ void __launch_bounds__(kThreads) prefix_mma_kernel(float* __restrict_
   }
 }
 
-// Allows a prefix kernel its shared memory, once per instance and device.
-template <typename Smem, typename Kernel>
-cudaError_t allow_smem(bool (&allowed)[kMaxDevices], Kernel kern) {
+// Allows a kernel its shared memory, once per instance and device.
+template <typename Kernel>
+cudaError_t allow_smem(bool (&allowed)[kMaxDevices], Kernel kern, int bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && dev < kMaxDevices && !allowed[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Smem)));
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     allowed[dev] = e == cudaSuccess;
   }
   return e;
+}
+
+// ------------------------------------------------- own positions and join
+// W warps to a (sequence, head) pair walk the positions [prefix_len, pos) in
+// chunks of kIt warp instructions: a K or V row is copied by kLPR lanes with
+// 16-byte cp.async, kRPI rows an instruction, through a ring of kRingStages
+// chunks of the warp's own in shared memory, of which each lane reads back what
+// it copied itself (no barrier).  With the chunk in registers and one in
+// flight, 256 x 16 pairs of 128 positions took 74 us (1.8 TB/s).  The new
+// token's key and value come from the QKV row and are appended.  Then the warps
+// take in the prefix's splits, kRPI at a time, a split's row by the lanes that
+// hold its dimensions.  Each lane group g keeps its own sum and output against
+// the warp's common maximum; one reduction at the end.
+//
+// The kernel may start while the prefix kernel runs (which began only once the
+// QKV projection had finished): own positions run beside the prefix, whose
+// results are waited for before they are read.
+constexpr int kRingStages = 2;
+constexpr int kRingIt = 4;
+constexpr int kRingStageBytes = kRingIt * 2 * 512;  // K and V
+constexpr long long kJoinWarpsPerSm = 16;
+constexpr int join_warps_per_block(int W) { return W > 4 ? W : 4; }
+template <typename E, int HS, int W>
+__global__ void __launch_bounds__(32 * join_warps_per_block(W))
+    own_join_kernel(E* __restrict__ out, const E* __restrict__ qkv, E* __restrict__ kcache, E* __restrict__ vcache,
+                    int B, int C, int NH, const int* __restrict__ pos_arr, KVRows rows, float scale_log2,
+                    PrefixPartials prefix) {
+  constexpr int kPer = 16 / static_cast<int>(sizeof(E));  // elements per 16-byte load
+  constexpr int kLPR = HS / kPer;                          // lanes per row
+  constexpr int kRPI = 32 / kLPR;                          // rows per warp instruction
+  constexpr int kIt = kRingIt;
+  constexpr int kChunk = kIt * kRPI;
+  constexpr int kWarps = join_warps_per_block(W);
+  extern __shared__ __align__(128) uint8_t shared_raw[];
+  __shared__ float m_s[kWarps], l_s[kWarps];
+  __shared__ float o_s[kWarps][HS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane / kLPR, dg = lane % kLPR;
+  const int w = warp % W;
+  uint8_t* ring = shared_raw + warp * (kRingStages * kRingStageBytes) + lane * 16;
+  const int n_pairs = B * NH;
+  const int pair = static_cast<int>(blockIdx.x) * (kWarps / W) + warp / W;
+  const bool mine = pair < n_pairs;
+  const int b = mine ? pair / NH : 0, h = mine ? pair % NH : 0;
+  const int first = prefix.prefix_len;
+  const bool late = prefix.splits > 0;
+  if (!late) {
+    pdl_wait();
+    pdl_trigger();
+  }
+  float m, l, acc[kPer];
+  auto raise = [&](float to) {
+    const float alpha = exp2_approx(m - to);  // 0 at first (m = -inf)
+    l *= alpha;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] *= alpha;
+    m = to;
+  };
+  // the lane groups' sums
+  auto reduce = [&]() {
+#pragma unroll
+    for (int o = 16; o >= kLPR; o >>= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+    }
+  };
+  const int pos = mine ? __ldg(pos_arr + b) : -1;
+  const bool ok = mine && pos >= first && pos < rows.capacity;
+  // (m, l, acc) over the own positions, summed over lane groups only by reduce()
+  auto attend = [&]() {
+    const int* table = rows.table + static_cast<size_t>(b) * rows.max_blocks;
+    auto entry = [&](int j) -> int {  // the block of position j
+      int blk = __ldg(table + (j >> rows.lbs));
+      if (blk < 0 || blk >= rows.num_blocks) {
+        if (h == 0) set_error(GPT2_DEVERR_BLOCK);
+        blk = 0;
+      }
+      return blk;
+    };
+    auto row_at = [&](int blk, int j) -> size_t {
+      return ((static_cast<size_t>(blk) * NH + h) << rows.lbs) + (j & ((1 << rows.lbs) - 1));
+    };
+    const E* qrow = qkv + static_cast<size_t>(b) * 3 * C + h * HS + dg * kPer;
+    // a chunk's block ids: lane i holds that of row i (and of row i + 32 where
+    // a chunk has 64)
+    constexpr int kIds = (kChunk + 31) / 32;
+    int ids[kIds];
+    auto lookup = [&](int j0) {
+#pragma unroll
+      for (int i = 0; i < kIds; ++i) ids[i] = j0 + lane + 32 * i < pos ? entry(j0 + lane + 32 * i) : 0;
+    };
+    // this warp's chunks c = 0, 1, ... begin at first + (w + c W) kChunk
+    int next = first + w * kChunk;  // the next chunk to copy, its block ids looked up
+    if (next < pos) lookup(next);
+    auto copy = [&](int c) {  // chunk c into its stage; an empty group past the end
+      if (next < pos) {
+        uint8_t* dst = ring + (c % kRingStages) * kRingStageBytes;
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+          const int r = g + i * kRPI, j = next + r;
+          const int blk = __shfl_sync(0xffffffffu, ids[(i * kRPI) / 32], r & 31);
+          const bool in = j < pos;
+          const size_t at = (in ? row_at(blk, j) : 0) * HS + dg * kPer;
+          cp_async16(dst + i * 512, kcache + at, in);
+          cp_async16(dst + (kIt + i) * 512, vcache + at, in);
+        }
+        next += W * kChunk;
+        if (next < pos) lookup(next);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int c = 0; c < kRingStages - 1; ++c) copy(c);
+    float q[kPer];
+    {
+      const uint4 raw = __ldg(reinterpret_cast<const uint4*>(qrow));
+      const E* e = reinterpret_cast<const E*>(&raw);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) q[k] = to_f32(e[k]) * scale_log2;
+    }
+    auto dot = [&](const uint4& raw) {
+      const E* e = reinterpret_cast<const E*>(&raw);
+      float d = 0.f;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) d = fmaf(q[k], to_f32(e[k]), d);
+#pragma unroll
+      for (int o = kLPR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      return d;
+    };
+    auto take = [&](float p, const uint4& raw) {
+      const E* e = reinterpret_cast<const E*>(&raw);
+      l += p;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(p, to_f32(e[k]), acc[k]);
+    };
+    for (int c = 0, j0 = first + w * kChunk; j0 < pos; ++c, j0 += W * kChunk) {
+      copy(c + kRingStages - 1);
+      cp_async_wait<kRingStages - 1>();
+      const uint8_t* src = ring + (c % kRingStages) * kRingStageBytes;
+      uint4 kr[kIt], vr[kIt];
+#pragma unroll
+      for (int i = 0; i < kIt; ++i) {
+        kr[i] = *reinterpret_cast<const uint4*>(src + i * 512);
+        vr[i] = *reinterpret_cast<const uint4*>(src + (kIt + i) * 512);
+      }
+      float sc[kIt], cmax = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kIt; ++i) {
+        const float d = dot(kr[i]);
+        sc[i] = j0 + g + i * kRPI < pos ? d : -INFINITY;
+        cmax = fmaxf(cmax, sc[i]);
+      }
+#pragma unroll
+      for (int o = 16; o >= kLPR; o >>= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
+      raise(fmaxf(m, cmax));  // position j0 < pos is in the chunk
+#pragma unroll
+      for (int i = 0; i < kIt; ++i) take(exp2_approx(sc[i] - m), vr[i]);
+    }
+    if (w == 0) {  // the new token, by lane group 0
+      const uint4 kn = __ldg(reinterpret_cast<const uint4*>(qrow + C)), vn = __ldg(reinterpret_cast<const uint4*>(qrow + 2 * C));
+      const float d = dot(kn);
+      raise(fmaxf(m, d));
+      const size_t at = row_at(entry(pos), pos) * HS + dg * kPer;
+      if (g == 0) {
+        take(exp2_approx(d - m), vn);
+        *reinterpret_cast<uint4*>(kcache + at) = kn;
+        *reinterpret_cast<uint4*>(vcache + at) = vn;
+      }
+    }
+  };
+  // takes in this warp's share of the prefix's splits
+  auto take_splits = [&]() {
+    const size_t step = static_cast<size_t>(NH) * B, row0 = static_cast<size_t>(h) * B + b;  // a split's rows
+    constexpr int kB = 4;  // rounds whose loads are in flight together
+    for (int s0 = w * kRPI; s0 < prefix.splits; s0 += W * kRPI * kB) {
+      float2 ml[kB];
+      float4 po[kB][kPer / 4];
+#pragma unroll
+      for (int i = 0; i < kB; ++i) {
+        const int s = s0 + i * W * kRPI + g;
+        ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int k = 0; k < kPer / 4; ++k) po[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s < prefix.splits) {
+          const size_t at = static_cast<size_t>(s) * step + row0;
+          ml[i] = prefix.ml[at];
+          const float4* o4 = reinterpret_cast<const float4*>(prefix.o + at * HS + dg * kPer);
+#pragma unroll
+          for (int k = 0; k < kPer / 4; ++k) po[i][k] = o4[k];
+        }
+      }
+      float to = m;
+#pragma unroll
+      for (int i = 0; i < kB; ++i) to = fmaxf(to, ml[i].x);
+#pragma unroll
+      for (int o = 16; o >= kLPR; o >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+      raise(to);
+#pragma unroll
+      for (int i = 0; i < kB; ++i) {
+        const float f = exp2_approx(ml[i].x - m);  // 0 for no split
+        l = fmaf(ml[i].y, f, l);
+#pragma unroll
+        for (int k = 0; k < kPer / 4; ++k) {
+          acc[4 * k] = fmaf(po[i][k].x, f, acc[4 * k]);
+          acc[4 * k + 1] = fmaf(po[i][k].y, f, acc[4 * k + 1]);
+          acc[4 * k + 2] = fmaf(po[i][k].z, f, acc[4 * k + 2]);
+          acc[4 * k + 3] = fmaf(po[i][k].w, f, acc[4 * k + 3]);
+        }
+      }
+    }
+  };
+  auto write = [&]() {  // lane group 0; a position outside the cache: a zero row
+    const float inv = 1.0f / l;
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    if (ok) {
+      if constexpr (kPer == 4)
+        r = make_uint4(__float_as_uint(acc[0] * inv), __float_as_uint(acc[1] * inv), __float_as_uint(acc[2] * inv),
+                       __float_as_uint(acc[3] * inv));
+      else
+        r = make_uint4(pack2<E>(acc[0] * inv, acc[1] * inv), pack2<E>(acc[2] * inv, acc[3] * inv),
+                       pack2<E>(acc[4] * inv, acc[5] * inv), pack2<E>(acc[6] * inv, acc[7] * inv));
+    }
+    *reinterpret_cast<uint4*>(out + static_cast<size_t>(b) * C + h * HS + dg * kPer) = r;
+  };
+
+  m = -INFINITY;
+  l = 0.f;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+  if (ok) {
+    attend();
+  } else if (mine && h == 0 && lane == 0 && w == 0) {
+    set_error(GPT2_DEVERR_POSITION);
+  }
+  if (late) {
+    pdl_wait();  // the prefix's results
+    pdl_trigger();
+  }
+  if (ok) take_splits();
+  reduce();
+  if constexpr (W > 1) {
+    if (lane == 0) {
+      m_s[warp] = m;
+      l_s[warp] = l;
+    }
+    if (g == 0) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) o_s[warp][dg * kPer + k] = acc[k];
+    }
+    __syncthreads();
+    if (w != 0) return;
+    float M = m;
+#pragma unroll
+    for (int i = 1; i < W; ++i) M = fmaxf(M, m_s[warp + i]);
+    raise(M);  // warp 0 has the new token: M is finite
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      const float f = exp2_approx(m_s[warp + i] - M);  // 0 for a warp that had nothing
+      l = fmaf(l_s[warp + i], f, l);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(o_s[warp + i][dg * kPer + k], f, acc[k]);
+    }
+  }
+  if (mine && g == 0) write();
+}
+
+template <typename E, int HS, int W>
+int join_typed(void* out, const void* qkv, void* kc, void* vc, int B, int C, int NH, const int* pos,
+               const KVRows& rows, const PrefixPartials& p, cudaStream_t s) {
+  static bool allowed[kMaxDevices] = {};
+  constexpr int kWarps = join_warps_per_block(W), kSmem = kWarps * kRingStages * kRingStageBytes;
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(B) * NH + kWarps / W - 1) / (kWarps / W));
+  cudaError_t e = allow_smem(allowed, own_join_kernel<E, HS, W>, kSmem);
+  if (e == cudaSuccess)
+    e = launch_pdl(own_join_kernel<E, HS, W>, dim3(grid), dim3(32 * kWarps), kSmem, s, static_cast<E*>(out),
+                   static_cast<const E*>(qkv), static_cast<E*>(kc), static_cast<E*>(vc), B, C, NH, pos, rows,
+                   1.4426950408889634f / sqrtf(static_cast<float>(HS)), p);
+  return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
+}
+
+// Warps per pair: as many as keep the pairs' warps within about 16 an SM, so
+// that few pairs with many own positions are still read by the whole GPU.
+template <typename E, int HS>
+int join_warps(void* out, const void* qkv, void* kc, void* vc, int B, int C, int NH, const int* pos,
+               const KVRows& rows, const PrefixPartials& p, cudaStream_t s) {
+  const long long pairs = static_cast<long long>(B) * NH, most = kJoinWarpsPerSm * num_sms();
+  if (8 * pairs <= most) return join_typed<E, HS, 8>(out, qkv, kc, vc, B, C, NH, pos, rows, p, s);
+  if (4 * pairs <= most) return join_typed<E, HS, 4>(out, qkv, kc, vc, B, C, NH, pos, rows, p, s);
+  if (2 * pairs <= most) return join_typed<E, HS, 2>(out, qkv, kc, vc, B, C, NH, pos, rows, p, s);
+  return join_typed<E, HS, 1>(out, qkv, kc, vc, B, C, NH, pos, rows, p, s);
+}
+
+template <typename E>
+int join(void* out, const void* qkv, void* kc, void* vc, int B, int C, int NH, const int* pos, const KVRows& rows,
+         const PrefixPartials& p, cudaStream_t s) {
+  switch (C / NH) {
+    case 16: return join_warps<E, 16>(out, qkv, kc, vc, B, C, NH, pos, rows, p, s);
+    case 32: return join_warps<E, 32>(out, qkv, kc, vc, B, C, NH, pos, rows, p, s);
+    case 64: return join_warps<E, 64>(out, qkv, kc, vc, B, C, NH, pos, rows, p, s);
+  }
+  return GPT2_ERR_UNSUPPORTED;
 }
 
 dim3 prefix_grid(const Plan& pl, int B, int NH) { return dim3((B + pl.tile_q - 1) / pl.tile_q, NH, pl.splits); }
@@ -485,7 +791,7 @@ int simt_typed(const PrefixPartials& p, const void* qkv, const void* kc, const v
   static bool allowed[kMaxDevices] = {};
   const Plan pl = plan_of(B, NH, HS, p.prefix_len, false);
   using Smem = SimtSmem<E, HS>;
-  cudaError_t e = allow_smem<Smem>(allowed, prefix_simt_kernel<E, HS>);
+  cudaError_t e = allow_smem(allowed, prefix_simt_kernel<E, HS>, sizeof(Smem));
   if (e == cudaSuccess)
     e = launch_pdl(prefix_simt_kernel<E, HS>, prefix_grid(pl, B, NH), dim3(kThreads), sizeof(Smem), s, p.o, p.ml,
                    static_cast<const E*>(qkv), static_cast<const E*>(kc), static_cast<const E*>(vc), B, C, NH,
@@ -500,7 +806,7 @@ int mma_typed(const PrefixPartials& p, const void* qkv, const void* kc, const vo
   const Plan pl = plan_of(B, NH, HS, p.prefix_len, true);
   using Smem = MmaSmem<HS, WM>;
   static_assert(sizeof(Smem) <= 227 * 1024, "shared memory");
-  cudaError_t e = allow_smem<Smem>(allowed, prefix_mma_kernel<HS, T16, WM>);
+  cudaError_t e = allow_smem(allowed, prefix_mma_kernel<HS, T16, WM>, sizeof(Smem));
   if (e == cudaSuccess)
     e = launch_pdl(prefix_mma_kernel<HS, T16, WM>, prefix_grid(pl, B, NH), dim3(kThreads), sizeof(Smem), s, p.o, p.ml,
                    static_cast<const uint16_t*>(qkv), static_cast<const uint16_t*>(kc),
@@ -582,6 +888,13 @@ int launch_shared_prefix(const PrefixPartials& p, const void* qkv, const void* k
     case 64: return simt_typed<float, 64>(p, qkv, kcache, vcache, B, C, NH, rows, s);
   }
   return GPT2_ERR_UNSUPPORTED;
+}
+
+int launch_own_join(void* out, const void* qkv, void* kcache, void* vcache, int op, int B, int C, int NH,
+                    const int* pos, const KVRows& rows, const PrefixPartials& p, cudaStream_t s) {
+  if (op == kOpF16) return join<__half>(out, qkv, kcache, vcache, B, C, NH, pos, rows, p, s);
+  if (op == kOpBF16) return join<__nv_bfloat16>(out, qkv, kcache, vcache, B, C, NH, pos, rows, p, s);
+  return join<float>(out, qkv, kcache, vcache, B, C, NH, pos, rows, p, s);
 }
 
 }  // namespace gpt2

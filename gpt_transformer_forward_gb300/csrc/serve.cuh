@@ -47,11 +47,10 @@ int launch_shared_prefix(const PrefixPartials& p, const void* qkv, const void* k
 // 64, 16-bit types)
 int launch_shared_prefix_tc05(const PrefixPartials& p, const void* qkv, const void* kcache, const void* vcache, int op,
                               int B, int C, int NH, int tiles_per_split, const KVRows& rows, cudaStream_t s);
-// attention.cu: the sequences' own positions [prefix_len, pos] and the join
-// with the prefix's partial results; the token's key and value are appended
-void launch_shared_decode_attention(void* out, const void* qkv, void* kcache, void* vcache, int op, int B, int C,
-                                    int NH, const int* pos_arr, const KVRows& rows, const PrefixPartials& p,
-                                    cudaStream_t s);
+// the sequences' own positions [prefix_len, pos] and the join with the
+// prefix's partial results; the token's key and value are appended
+int launch_own_join(void* out, const void* qkv, void* kcache, void* vcache, int op, int B, int C, int NH,
+                    const int* pos, const KVRows& rows, const PrefixPartials& p, cudaStream_t s);
 
 // vocab.cu
 int launch_logprobs(float* logprob, float* entropy, float* lse, int* top_ids, float* top_logprobs, const void* logits,
