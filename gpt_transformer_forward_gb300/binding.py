@@ -148,8 +148,10 @@ def header_functions(header: str = "gpt2fwd.h") -> list:
 def _ptr(x):
     if x is None or isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
+    try:  # a torch tensor
         return x.data_ptr()
+    except AttributeError:
+        pass
     if hasattr(x, "ctypes"):
         return x.ctypes.data
     raise TypeError(f"cannot pass {type(x)} as a pointer")
@@ -331,13 +333,20 @@ def gpt2_decode_step_paged(cfg, params, packed, kv, tok, pos, B, logits, probs, 
 LOGPROBS_MAX_TOP = 32
 
 
+_element_types: dict = {}  # torch dtype -> code, filled at the first use
+
+
 def element_type(t) -> int:
     """The GPT2ProbsType code of a tensor's dtype (fp32, fp16 or bf16)."""
-    import torch
-    codes = {torch.float32: GPT2_PROBS_F32, torch.float16: GPT2_PROBS_F16, torch.bfloat16: GPT2_PROBS_BF16}
-    if t.dtype not in codes:
-        raise TypeError(f"element type {t.dtype}: fp32, fp16 or bf16 expected")
-    return codes[t.dtype]
+    code = _element_types.get(t.dtype)
+    if code is None:
+        import torch
+        _element_types.update({torch.float32: GPT2_PROBS_F32, torch.float16: GPT2_PROBS_F16,
+                               torch.bfloat16: GPT2_PROBS_BF16})
+        code = _element_types.get(t.dtype)
+        if code is None:
+            raise TypeError(f"element type {t.dtype}: fp32, fp16 or bf16 expected")
+    return code
 
 
 def paged_build_tables(block_table, slots, next_len, taken_out, cached_len, new_len, free_blocks, num_free, taken_in,

@@ -882,6 +882,7 @@ int paged_build_tables(int* block_table, int* slots, int* next_len, int* taken_o
   TableArgs a{block_table, slots, next_len, taken_out, cached_len, new_len, free_blocks, taken_in, prefix_blocks,
               num_free, prefix_len >> lbs, B, T, num_blocks, lbs, max_blocks_per_seq,
               static_cast<int>(std::min<long long>(cap, 0x7fffffffLL))};
+  PdlScope pdl(true);  // the kernel waits for its predecessor itself
   launch_build_tables(a, as_stream(stream));
   return check_launch();
 }

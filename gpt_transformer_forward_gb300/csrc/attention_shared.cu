@@ -24,26 +24,42 @@ namespace {
 constexpr int kTileQ = 32;    // queries per CTA of the CUDA-core kernel
 constexpr int kTileK = 64;    // keys per step of a warp group
 constexpr int kThreads = 128;
+// A prefix so short, and of so few bytes when every sequence reads it by
+// itself, is left to the kernel of the own positions: one launch, not two (4
+// sequences, 12 heads, prefix 64: 3.2 us against 4.3; prefix 256 4.7 against
+// 4.6, and 2 us less on the host; 64 sequences, prefix 64, 13 MB: 5.6 against
+// 4.6; one sequence, prefix 1000: 8.4 against 4.7).
+constexpr int kDirectLen = 256;
+constexpr long long kDirectBytes = 8LL << 20;
 constexpr int kTcMinBatch = 65;  // sequences from which the tcgen05 kernel takes over (head size 64)
 
 // How a shape is cut: the kernel, queries per CTA, keys per step of a CTA,
 // splits of the prefix over CTAs, positions per split (a multiple of the step)
 // and partial results per split.
-enum Kernel { kSimt, kMma, kTc05 };
+enum Kernel { kNone, kSimt, kMma, kTc05 };
 struct Plan {
   Kernel kernel;
   int tile_q, step_k, splits, per, parts;
 };
 
 // Tensor-core kernel of few sequences: the four warps of a CTA are arranged
-// over 16-row query groups first and over keys with what is left.
-int row_groups(int B) { return B <= 16 ? 1 : B <= 32 ? 2 : 4; }
+// over two or four groups of 16 query rows, over keys with what is left.  (One
+// row group and four of keys holds one CTA an SM: 16 sequences, 16 heads,
+// prefix 16384 18.9 us against 17.0, one sequence of prefix 1000 5.2 against
+// 4.7.)
+int row_groups(int B) { return B <= 32 ? 2 : 4; }
 
-// Enough splits that the CTAs cover the SMs (twice, where two fit an SM), each
-// at least a step long.  The count goes by the shape alone, not by the device:
-// it sizes the caller's workspace.
+// Enough splits that the CTAs cover the SMs (the tcgen05 kernel: one an SM, not
+// two rounds; the CUDA-core kernel two an SM, mma.sync three: what they hold),
+// each at least a step long.  The count goes by the shape alone, not by the
+// device: it sizes the caller's workspace.
 Plan plan_of(int B, int NH, int hs, int prefix_len, bool is16, int* wanted = nullptr) {
-  Plan p;
+  Plan p{kNone, 1, 1, 0, 0, 0};
+  const long long row_bytes = 2LL * hs * (is16 ? 2 : 4);  // of a key and its value
+  if (prefix_len <= kDirectLen && row_bytes * prefix_len * B * NH <= kDirectBytes) {
+    if (wanted != nullptr) *wanted = 0;
+    return p;
+  }
   p.kernel = !is16 ? kSimt : hs == 64 && B >= kTcMinBatch ? kTc05 : kMma;
   p.parts = 1;
   if (p.kernel == kTc05) {
@@ -55,7 +71,8 @@ Plan plan_of(int B, int NH, int hs, int prefix_len, bool is16, int* wanted = nul
     p.step_k = is16 ? kTileK * (4 / row_groups(B)) : kTileK;
   }
   const long long tiles = static_cast<long long>((B + p.tile_q - 1) / p.tile_q) * NH;
-  const long long want = p.kernel == kTc05 ? 152 / tiles : (2 * 152 + tiles - 1) / tiles;
+  const long long want =
+      p.kernel == kTc05 ? 152 / tiles : ((p.kernel == kMma ? 3 : 2) * 152 + tiles - 1) / tiles;
   const long long most = (prefix_len + p.step_k - 1) / p.step_k;
   const int n = static_cast<int>(std::max<long long>(1, std::min(want, most)));
   if (wanted != nullptr) *wanted = n * p.parts;
@@ -482,7 +499,8 @@ cudaError_t allow_smem(bool (&allowed)[kMaxDevices], Kernel kern, int bytes) {
 }
 
 // ------------------------------------------------- own positions and join
-// W warps to a (sequence, head) pair walk the positions [prefix_len, pos) in
+// W warps to a (sequence, head) pair walk the positions [prefix_len, pos) (or,
+// of a short prefix, [0, pos)) in
 // chunks of kIt warp instructions: a K or V row is copied by kLPR lanes with
 // 16-byte cp.async, kRPI rows an instruction, through a ring of kRingStages
 // chunks of the warp's own in shared memory, of which each lane reads back what
@@ -523,7 +541,9 @@ __global__ void __launch_bounds__(32 * join_warps_per_block(W))
   const int pair = static_cast<int>(blockIdx.x) * (kWarps / W) + warp / W;
   const bool mine = pair < n_pairs;
   const int b = mine ? pair / NH : 0, h = mine ? pair % NH : 0;
-  const int first = prefix.prefix_len;
+  // the positions walked here: all of them where the prefix was left to this
+  // kernel
+  const int first = prefix.splits > 0 ? prefix.prefix_len : 0;
   const bool late = prefix.splits > 0;
   if (!late) {
     pdl_wait();
@@ -547,12 +567,12 @@ __global__ void __launch_bounds__(32 * join_warps_per_block(W))
     }
   };
   const int pos = mine ? __ldg(pos_arr + b) : -1;
-  const bool ok = mine && pos >= first && pos < rows.capacity;
+  const bool ok = mine && pos >= prefix.prefix_len && pos < rows.capacity;
   // (m, l, acc) over the own positions, summed over lane groups only by reduce()
   auto attend = [&]() {
     const int* table = rows.table + static_cast<size_t>(b) * rows.max_blocks;
-    auto entry = [&](int j) -> int {  // the block of position j
-      int blk = __ldg(table + (j >> rows.lbs));
+    auto entry = [&](int j) -> int {  // the block of position j; the shared ones' by row 0
+      int blk = __ldg((j < prefix.prefix_len ? rows.table : table) + (j >> rows.lbs));
       if (blk < 0 || blk >= rows.num_blocks) {
         if (h == 0) set_error(GPT2_DEVERR_BLOCK);
         blk = 0;
@@ -819,7 +839,6 @@ template <int HS, typename T16>
 int mma_rows(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc, int B, int C, int NH,
              const KVRows& rows, cudaStream_t s) {
   switch (row_groups(B)) {
-    case 1: return mma_typed<HS, T16, 1>(p, qkv, kc, vc, B, C, NH, rows, s);
     case 2: return mma_typed<HS, T16, 2>(p, qkv, kc, vc, B, C, NH, rows, s);
     default: return mma_typed<HS, T16, 4>(p, qkv, kc, vc, B, C, NH, rows, s);
   }
@@ -861,11 +880,8 @@ size_t shared_prefix_bytes(int B, int NH, int hs, int prefix_len, bool is16) {
 
 PrefixPartials shared_prefix_layout(void* workspace, int B, int NH, int hs, int prefix_len, bool is16) {
   PrefixPartials p;
-  p.splits = 0;
-  if (prefix_len > 0) {
-    const Plan pl = plan_of(B, NH, hs, prefix_len, is16);
-    p.splits = pl.splits * pl.parts;
-  }
+  const Plan pl = plan_of(B, NH, hs, prefix_len, is16);
+  p.splits = pl.splits * pl.parts;
   p.prefix_len = prefix_len;
   const size_t rows = static_cast<size_t>(p.splits) * NH * B;
   p.o = static_cast<float*>(workspace);

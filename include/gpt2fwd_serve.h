@@ -89,8 +89,9 @@ GPT2_API int gpt2_prefill_slots(const GPT2Config* cfg, const float* params, cons
 
 /* ------------------------------------- attention over a shared prefix */
 
-/* Scratch bytes attention_shared_prefix needs (0 for prefix_len 0 or invalid
- * arguments). */
+/* Scratch bytes attention_shared_prefix needs: 0 for invalid arguments and for
+ * a prefix too short to need any.  Enough for this and every smaller batch and
+ * shorter prefix of the same heads and precision. */
 GPT2_API size_t attention_shared_prefix_workspace_size(int B, int C, int NH, int prefix_len, int precision);
 
 /* The decode attention of one layer [NTU "KV Caching"; FlashAttention
@@ -122,7 +123,8 @@ GPT2_API int attention_shared_prefix(void* out, const void* qkv, const GPT2Paged
                                      int C, int NH, int prefix_len, int precision, void* workspace, size_t ws_bytes,
                                      void* stream);
 
-/* Workspace bytes of gpt2_decode_step_shared (0 for invalid arguments). */
+/* Workspace bytes of gpt2_decode_step_shared, for up to B sequences and a
+ * prefix of up to prefix_len positions (0 for invalid arguments). */
 GPT2_API size_t gpt2_shared_workspace_size(const GPT2Config* cfg, int B, int prefix_len, int precision);
 
 /* gpt2_decode_step_paged for sequences that share their first prefix_len

@@ -118,7 +118,9 @@ def own_of(B, most, seed):
     (1, 1, 1, 0, 1), (1, 2, 64, 5, 16), (2, 3, 63, 1, 16), (3, 1, 65, 40, 2), (5, 2, 128, 3, 128), (16, 2, 127, 9, 8),
     (17, 2, 129, 9, 4), (31, 3, 500, 17, 16), (33, 2, 1001, 33, 32), (65, 1, 257, 300, 64), (4, 12, 960, 63, 16),
     (130, 2, 777, 20, 16), (1, 1, 5000, 2, 64), (70, 1, 300, 40, 2), (129, 2, 1500, 9, 128), (300, 1, 130, 3, 256),
-    (66, 1, 1, 2, 1), (128, 1, 128, 5, 8), (128, 3, 129, 5, 8), (520, 1, 400, 5, 32),
+    (66, 1, 1, 2, 1), (128, 1, 128, 5, 8), (2, 3, 257, 1, 16), (3, 1, 321, 40, 2), (5, 2, 384, 3, 128), (17, 2, 300, 9, 4),
+    (16, 1, 4097, 2, 16), (66, 1, 257, 2, 1), (128, 1, 384, 5, 8), (128, 3, 385, 5, 8), (300, 1, 300, 3, 256),
+    (4, 2, 256, 9, 16), (40, 12, 64, 3, 8), (12, 12, 200, 80, 16), (2, 1, 100, 2000, 64), (128, 3, 129, 5, 8), (520, 1, 400, 5, 32),
 ])
 def test_against_64_bits(precision, hs, B, NH, P, most, bs):
     check(make(precision, B, NH, hs, P, own_of(B, most, P), bs, seed=B + P))

@@ -52,7 +52,7 @@ def test_tables_refuse(change, code):
 
 
 def shared_args(**kw):
-    d = dict(out=FAKE, qkv=2 * FAKE, kv=ab.paged_kv(FAKE, FAKE, 64, 16, 32), pos=FAKE, B=4, C=256, NH=4, prefix_len=100,
+    d = dict(out=FAKE, qkv=2 * FAKE, kv=ab.paged_kv(FAKE, FAKE, 64, 16, 32), pos=FAKE, B=4, C=256, NH=4, prefix_len=300,
              precision=ab.GPT2_FP16, workspace=FAKE, ws_bytes=1 << 30)
     d.update(kw)
     return d
@@ -85,7 +85,7 @@ def test_shared_prefix_sizes():
         for P in (1, 64, 65, 1000, 3328, 3329, 20000):
             for B in (1, 16, 17, 32, 33, 64, 65, 128, 129, 300):
                 most = size(B, 768, 12, P, precision)
-                assert most > 0
+                assert most > 0 or P <= 256  # a short prefix may need none
                 for b in (1, B // 2 + 1, B - 1):
                     assert b < 1 or size(b, 768, 12, P, precision) <= most, (precision, P, B, b)
                 for q in (1, P // 2 + 1, P - 1):
@@ -93,7 +93,8 @@ def test_shared_prefix_sizes():
     cfg = inputs.TINY
     base = ab.gpt2_workspace_size(cfg, 3, 1, ab.GPT2_FP16)
     assert ab.gpt2_shared_workspace_size(cfg, 3, 0, ab.GPT2_FP16) == base
-    assert ab.gpt2_shared_workspace_size(cfg, 3, 40, ab.GPT2_FP16) == base + size(3, 64, 4, 40, ab.GPT2_FP16)
+    assert ab.gpt2_shared_workspace_size(cfg, 3, 600, ab.GPT2_FP16) == base + size(3, 64, 4, 600, ab.GPT2_FP16)
+    assert size(3, 64, 4, 600, ab.GPT2_FP16) > 0
     assert ab.gpt2_shared_workspace_size(cfg, 3, -1, ab.GPT2_FP16) == 0
 
 
