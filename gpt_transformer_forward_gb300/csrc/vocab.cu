@@ -129,16 +129,17 @@ struct RowSmem {
   uint4 ring[kStages][kT * kU];
   uint64_t full[kStages], empty[kStages];
   Stat warp[2][kT / 32];            // by the parity of the row: a late reader is at most a row behind
-  Stat block;
   // alternatives
   Key top[GPT2_LOGPROBS_MAX_TOP];   // this block's, largest first
   Key group[kGroups];
   Key cand[kMaxCandidates];
-  uint4 vec[kT];                    // vectors that hold a candidate, and their indexes
-  int vec_at[kT];
   Key tau;                          // the K-th largest group's best vector (0: fewer than K)
-  int n_threads, n_vecs, n_cand;
+  int n_threads, n_cand;
   uint16_t thread[kT];
+  // of the first block of a cluster: what the blocks that share its row found
+  uint64_t joined;                  // one arrival from each of the others
+  Stat part_stat[kMaxParts * (kT / 32)];
+  Key part_top[kMaxParts][GPT2_LOGPROBS_MAX_TOP];
 };
 
 // the threads that compute
@@ -186,24 +187,24 @@ __device__ __forceinline__ void rank_keys(const Key* keys, int n, int K, Put put
 }
 
 // The K largest elements of this block's vectors [lo, hi) into sm.top.  Each
-// thread brings its best vector (best, at vector index best_vec).  A group's
-// best is the largest of its threads', and tau, the K-th largest group's,
-// cannot exceed the K-th largest element: at least K elements are no less than
-// it in the order (value, lower vector first).  Those elements lie with
-// threads whose own best is >= tau, about K of them.  Where only the best can
-// reach tau (`second`, the largest of the thread's other vectors, does not),
-// that vector is read again; the few other threads' vectors are all read
-// again, by all threads together.  The vectors that reach tau are listed, then
-// their elements, which are ranked by counting.
-// Equal values do not add candidates, since vectors are ordered by index; a
-// row in which a few threads hold all the largest elements may exceed the
-// lists and is searched K times instead.  64 groups: with K = 32 about 44
-// elements reach tau (64 ln 2), and ranking 64 keys costs a quarter of 128.
+// thread brings its best vector (its maximum best, at vector index best_vec,
+// read again into raw).  A group's best is the largest of its threads', and tau,
+// the K-th largest group's, cannot exceed the K-th largest element: at least K
+// elements are no less than it in the order (value, lower vector first).  Those
+// elements lie with threads whose own best is >= tau, about K of them.  Where
+// only the best vector can reach tau (`second`, the largest of the thread's
+// others, does not), its elements are listed at once; the few other threads'
+// vectors are all read again, by all threads together.  The listed elements are
+// ranked by counting.  Equal values do not add candidates, since vectors are
+// ordered by index; a row in which a few threads hold all the largest elements
+// may exceed the list and is searched K times instead.  64 groups: with K = 32
+// about 44 elements reach tau (64 ln 2), and ranking 64 keys costs a quarter of
+// ranking 128.
 template <typename T, int kT>
 __device__ __forceinline__ void select_top(RowSmem<kT>& sm, const uint4* row, int lo, int hi, int V, int K, float best,
-                                           float second, int best_vec) {
+                                           float second, int best_vec, const uint4& raw) {
   constexpr int kN = Vec<T>::n, kPer = kT / kGroups;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   const Key mine = best > -INFINITY ? key_of(best, static_cast<uint32_t>(best_vec)) : 0ull;
   Key g = mine;
 #pragma unroll
@@ -212,85 +213,74 @@ __device__ __forceinline__ void select_top(RowSmem<kT>& sm, const uint4* row, in
   if (tid == 0) {
     sm.tau = 0ull;
     sm.n_threads = 0;
-    sm.n_vecs = 0;
     sm.n_cand = 0;
   }
   if (tid < K) sm.top[tid] = 0ull;
   bar<kT>();
   {
     int rank = 0;
-#pragma unroll 8
-    for (int i = tid % kPer; i < kGroups; i += kPer) rank += sm.group[i] > g ? 1 : 0;
+#pragma unroll
+    for (int i = 0; i < kGroups / kPer; ++i) rank += sm.group[tid % kPer + i * kPer] > g ? 1 : 0;
 #pragma unroll
     for (int o = kPer / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
     if (tid % kPer == 0 && rank == K - 1 && g != 0ull) sm.tau = g;  // keys other than 0 are distinct
   }
   bar<kT>();
   const Key tau = sm.tau;
-  // lists are filled by one atomic a warp (their order does not matter: the
-  // elements are ranked), not one an element: serialised on one address, those
-  // took longer than the search itself
-  const int lane = tid & 31;
-  auto place = [&](int* counter, bool in) -> int {  // this thread's place if `in`
-    const uint32_t who = __ballot_sync(0xffffffffu, in);
-    if (who == 0u) return 0;
-    int at = 0;
-    if (lane == 0) at = atomicAdd(counter, __popc(who));
-    return __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
-  };
   const uint32_t tau_value = static_cast<uint32_t>(tau >> 32);
   const int tau_vec = static_cast<int>(0xffffffffu - static_cast<uint32_t>(tau));
+  // lists the elements of this thread's vector v (if `in`) that reach tau.  One
+  // atomic a warp, not one an element: serialised on one address, those took
+  // longer than the search itself.  (The list's order does not matter.)
+  auto list = [&](bool in, int vec, const uint4& bits) {
+    if (!__any_sync(0xffffffffu, in)) return;
+    const Vec<T> v = widen<T>(bits);
+    uint32_t who[kN];
+    int total = 0;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const uint32_t o = ordered(v.x[j]);
+      const bool ge = tau == 0ull || o > tau_value || (o == tau_value && vec <= tau_vec);
+      who[j] = __ballot_sync(0xffffffffu, in && ge && v.x[j] > -INFINITY && vec * kN + j < V);
+      total += __popc(who[j]);
+    }
+    if (total == 0) return;
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&sm.n_cand, total);
+    at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const int to = at + __popc(who[j] & ((1u << lane) - 1u));
+      if ((who[j] >> lane & 1u) != 0u && to < kMaxCandidates)
+        sm.cand[to] = key_of(v.x[j], static_cast<uint32_t>(vec * kN + j));
+      at += __popc(who[j]);
+    }
+  };
   {
     const bool in = mine != 0ull && mine >= tau;
     const bool more = in && second > -INFINITY && ordered(second) >= tau_value;
-    const int at = place(&sm.n_threads, more);
-    if (more) sm.thread[at] = static_cast<uint16_t>(tid);
-    const int to = place(&sm.n_vecs, in && !more);
-    if (in && !more) {  // at most kT of these
-      sm.vec[to] = __ldg(row + best_vec);
-      sm.vec_at[to] = best_vec;
+    const uint32_t who = __ballot_sync(0xffffffffu, more);
+    if (who != 0u) {
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&sm.n_threads, __popc(who));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
+      if (more) sm.thread[at] = static_cast<uint16_t>(tid);
     }
+    list(in && !more, best_vec, raw);
   }
   bar<kT>();
   const int per = (hi - lo + kT - 1) / kT;  // vectors of a thread, at most
   const int total = sm.n_threads * per;
-  auto reaches = [&](float x, int vec) {
-    const uint32_t o = ordered(x);
-    return x > -INFINITY && (tau == 0ull || o > tau_value || (o == tau_value && vec <= tau_vec));
-  };
   for (int i0 = 0; i0 < total; i0 += kT) {  // whole warps
     const int i = i0 + tid;
     const int vec = i < total ? lo + sm.thread[i / per] + (i % per) * kT : hi;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (vec < hi) raw = __ldg(row + vec);
-    Vec<T> v = widen<T>(raw);
-    if (vec * kN + kN > V) {  // (also where there is no vector)
-#pragma unroll
-      for (int j = 0; j < kN; ++j)
-        if (vec >= hi || vec * kN + j >= V) v.x[j] = -INFINITY;
-    }
-    const bool in = vec < hi && reaches(largest(v), vec);
-    const int at = place(&sm.n_vecs, in);
-    if (in && at < kT) {
-      sm.vec[at] = raw;
-      sm.vec_at[at] = vec;
-    }
+    uint4 bits = make_uint4(0u, 0u, 0u, 0u);
+    if (vec < hi) bits = __ldg(row + vec);
+    list(vec < hi, vec, bits);
   }
   if (total > 0) bar<kT>();
-  const int n_vecs = sm.n_vecs;
-  if (n_vecs <= kT) {
-    for (int i0 = 0; i0 < n_vecs * kN; i0 += kT) {
-      const int i = i0 + tid, vec = i < n_vecs * kN ? sm.vec_at[i / kN] : 0, id = vec * kN + i % kN;
-      float x = -INFINITY;
-      if (i < n_vecs * kN && id < V) x = to_f32(reinterpret_cast<const T*>(sm.vec)[i]);
-      const bool in = reaches(x, vec);
-      const int at = place(&sm.n_cand, in);
-      if (in && at < kMaxCandidates) sm.cand[at] = key_of(x, static_cast<uint32_t>(id));
-    }
-  }
-  bar<kT>();
   const int n = sm.n_cand;
-  if (n_vecs <= kT && n <= kMaxCandidates) {
+  if (n <= kMaxCandidates) {
     rank_keys<kT>(sm.cand, n, K, [&](int r, Key k) { sm.top[r] = k; });
   } else {
     Key last = ~0ull;
@@ -343,9 +333,11 @@ __global__ void __launch_bounds__(kT + 32, kT >= 256 ? 3 : 6) logprobs_kernel(co
       mbar_init(&sm.full[i], 1u);
       mbar_init(&sm.empty[i], kT / 32);
     }
+    mbar_init(&sm.joined, static_cast<uint32_t>(max(1, parts - 1)));
     fence_barrier_init();
   }
   __syncthreads();
+  if (parts > 1) cluster_arrive();  // waited for before a block writes to another's shared memory
   pdl_wait();
   pdl_trigger();
   if (wid == kT / 32) {
@@ -367,10 +359,7 @@ __global__ void __launch_bounds__(kT + 32, kT >= 256 ? 3 : 6) logprobs_kernel(co
       for (int i = max(0, q - kStages); i < q; ++i) mbar_wait(&sm.full[i % kStages], (i / kStages) & 1);
     }
     __syncwarp();
-    if (parts > 1) {
-      cluster_sync();
-      cluster_sync();
-    }
+    if (parts > 1) cluster_wait();
     return;
   }
   bool ok = true;  // no wait has given up
@@ -457,48 +446,69 @@ __global__ void __launch_bounds__(kT + 32, kT >= 256 ? 3 : 6) logprobs_kernel(co
       }
     }
     const float best = st.m;
+    // the thread's best vector, which the search will want: asked for here, it
+    // arrives behind the joins
+    uint4 best_raw = make_uint4(0u, 0u, 0u, 0u);
+    if (kTop && best > -INFINITY) best_raw = __ldg(row + best_vec);
     st = warp_join(Stat{st.m, s2.x + s2.y, w2.x + w2.y});
     if (lane == 0) sm.warp[turn][wid] = st;
     if constexpr (kTop) {
-      select_top<T, kT>(sm, row, lo, hi, a.V, a.K, best, second, best_vec);
+      select_top<T, kT>(sm, row, lo, hi, a.V, a.K, best, second, best_vec, best_raw);
     } else {
       bar<kT>();
     }
-    if (wid == 0) st = warp_join(lane < kT / 32 ? sm.warp[turn][lane] : Stat{-INFINITY, 0.f, 0.f});
-    if (parts > 1) {
-      if (tid == 0) sm.block = st;
-      cluster_sync();
-      if (part != 0) {
-        cluster_sync();  // block 0 has read this block's shared memory
-        return;
-      }
-      if (wid == 0) {
-        st = Stat{-INFINITY, 0.f, 0.f};
-        if (lane < parts) {
-          const uint32_t at = mapa_shared(smem_u32(&sm.block), lane);
-          st = Stat{ld_shared_cluster_f32(at), ld_shared_cluster_f32(at + 4), ld_shared_cluster_f32(at + 8)};
-        }
-        st = warp_join(st);
-      }
-    }
     Key top = 0ull;  // lane r of warp 0: the row's alternative r
-    if constexpr (kTop) {
-      static_assert(GPT2_LOGPROBS_MAX_TOP <= 32, "a lane per alternative");
+    if (parts == 1) {
       if (wid == 0) {
-        if (parts == 1) {
-          if (lane < a.K) top = sm.top[lane];
+        st = warp_join(lane < kT / 32 ? sm.warp[turn][lane] : Stat{-INFINITY, 0.f, 0.f});
+        if (kTop && lane < a.K) top = sm.top[lane];
+      }
+    } else {
+      // every block's first warp puts what its block found into the shared
+      // memory of the cluster's first block, which waits for the others'
+      // arrivals.  (Reading the others' memory between two cluster barriers
+      // took 2.9 us a row, more than the row itself.)
+      cluster_wait();
+      if (wid == 0) {
+        if (lane < kT / 32) {
+          const Stat own = sm.warp[turn][lane];
+          const uint32_t to = mapa_shared(smem_u32(&sm.part_stat[part * (kT / 32) + lane]), 0);
+          st_shared_cluster_f32(to, own.m);
+          st_shared_cluster_f32(to + 4, own.s);
+          st_shared_cluster_f32(to + 8, own.w);
+        }
+        if (kTop && lane < a.K) st_shared_cluster_u64(mapa_shared(smem_u32(&sm.part_top[part][lane]), 0), sm.top[lane]);
+        __syncwarp();
+        if (part != 0) {
+          if (lane == 0) mbar_arrive_release_cluster(mapa_shared(smem_u32(&sm.joined), 0));
         } else {
-          Key list[kMaxParts];
+          // (longer than a block of the cluster can wait for its own copies)
+          bool all = false;
+          for (int tries = 0; tries < 3 && !all; ++tries) all = mbar_wait_cluster(&sm.joined, 0);
+          const int n_stats = parts * (kT / 32);
+          static_assert(kMaxParts * (kT / 32) <= 64, "two statistics a lane");
+          st = lane < n_stats ? sm.part_stat[lane] : Stat{-INFINITY, 0.f, 0.f};
+          if (lane + 32 < n_stats) {
+            const Stat more = sm.part_stat[lane + 32];
+            const float m = fmaxf(st.m, more.m);
+            const Stat x = raised(st, m), y = raised(more, m);
+            st = Stat{m, x.s + y.s, x.w + y.w};
+          }
+          st = warp_join(st);
+          if constexpr (kTop) {
+            static_assert(GPT2_LOGPROBS_MAX_TOP <= 32, "a lane per alternative");
+            Key found[kMaxParts];
 #pragma unroll
-          for (int p = 0; p < kMaxParts; ++p)
-            list[p] = p < parts && lane < a.K ? ld_shared_cluster_u64(mapa_shared(smem_u32(&sm.top[lane]), p)) : 0ull;
+            for (int p = 0; p < kMaxParts; ++p) found[p] = p < parts && lane < a.K ? sm.part_top[p][lane] : 0ull;
 #pragma unroll
-          for (int w = kMaxParts / 2; w > 0; w >>= 1)
+            for (int w = kMaxParts / 2; w > 0; w >>= 1)
 #pragma unroll
-            for (int p = 0; p < w; ++p) list[p] = merge_top(list[p], list[p + w], lane);
-          top = list[0];
+              for (int p = 0; p < w; ++p) found[p] = merge_top(found[p], found[p + w], lane);
+            top = found[0];
+          }
         }
       }
+      if (part != 0) return;
     }
     if (wid == 0) {
       const bool nan = !(st.s >= 0.f) || st.m == INFINITY, none = st.s == 0.f;
@@ -521,10 +531,7 @@ __global__ void __launch_bounds__(kT + 32, kT >= 256 ? 3 : 6) logprobs_kernel(co
         }
       }
     }
-    if (parts > 1) {
-      cluster_sync();
-      return;
-    }
+    if (parts > 1) return;
   }
 }
 
