@@ -11,7 +11,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kVocThreads = 256;
 constexpr int kRowThreads = 256;
 constexpr int kMaxParts = 8;  // blocks of a cluster that share a row
-constexpr int kShortRow = 2048;  // vectors; below, blocks of 128 threads
+// Rows of fewer vectors run on blocks of 128 threads, of which six fit an SM:
+// more rows at once hide the search for alternatives (4096 rows of 50257 bf16
+// logits, 6283 vectors, 20 alternatives: 95.9 us against 104.3 on 256 threads;
+// 777 of 32003, 4001 vectors: 20.3 against 21.2).  Without alternatives wide
+// blocks stream a little better (2000 rows of 20000 fp32 logits, 5000 vectors:
+// 27.8 against 29.2).
+constexpr int kShortRowTop = 8192, kShortRow = 4096;
 // From here on the backward takes a row's maximum and sum anew instead of its
 // lse, whose fp32 rounding |lse| 2^-24 is an error of every p (6e-5 here).
 constexpr float kLargeLse = 1024.f;
@@ -227,21 +233,28 @@ __device__ __forceinline__ void select_top(RowSmem<kT>& sm, const uint4* row, in
   }
   bar<kT>();
   const Key tau = sm.tau;
+  // an element reaches tau: x > tau_x, or x == tau_x in a vector no later than
+  // tau's (without tau, 0: any but -inf)
   const uint32_t tau_value = static_cast<uint32_t>(tau >> 32);
-  const int tau_vec = static_cast<int>(0xffffffffu - static_cast<uint32_t>(tau));
+  const float tau_x = tau != 0ull ? value_of(tau_value) : -INFINITY;
+  const int tau_vec = tau != 0ull ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(tau)) : -1;
   // lists the elements of this thread's vector v (if `in`) that reach tau.  One
   // atomic a warp, not one an element: serialised on one address, those took
   // longer than the search itself.  (The list's order does not matter.)
   auto list = [&](bool in, int vec, const uint4& bits) {
     if (!__any_sync(0xffffffffu, in)) return;
-    const Vec<T> v = widen<T>(bits);
+    Vec<T> v = widen<T>(bits);
+    if (vec * kN + kN > V) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+        if (vec * kN + j >= V) v.x[j] = -INFINITY;
+    }
+    const bool early = vec <= tau_vec;
     uint32_t who[kN];
     int total = 0;
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
-      const uint32_t o = ordered(v.x[j]);
-      const bool ge = tau == 0ull || o > tau_value || (o == tau_value && vec <= tau_vec);
-      who[j] = __ballot_sync(0xffffffffu, in && ge && v.x[j] > -INFINITY && vec * kN + j < V);
+      who[j] = __ballot_sync(0xffffffffu, in && (v.x[j] > tau_x || (early && v.x[j] == tau_x)));
       total += __popc(who[j]);
     }
     if (total == 0) return;
@@ -695,7 +708,7 @@ template <typename T>
 int forward_typed(const void* logits, const ForwardArgs& a, cudaStream_t s) {
   const bool top = a.top_ids != nullptr || a.top_logprobs != nullptr;
   const T* l = static_cast<const T*>(logits);
-  const bool small = (a.V + Vec<T>::n - 1) / Vec<T>::n < kShortRow;
+  const bool small = (a.V + Vec<T>::n - 1) / Vec<T>::n < (top ? kShortRowTop : kShortRow);
   const cudaError_t e = small ? (top ? forward_go<T, 128, true>(l, a, s) : forward_go<T, 128, false>(l, a, s))
                               : (top ? forward_go<T, kRowThreads, true>(l, a, s)
                                      : forward_go<T, kRowThreads, false>(l, a, s));
