@@ -148,9 +148,13 @@ struct RowSmem {
   Key part_top[kMaxParts][GPT2_LOGPROBS_MAX_TOP];
 };
 
-// the threads that compute
+// The threads that compute.  Each warp converges first: the instruction counts
+// whole warps, and one that reached it in two parts (the compiler may put the
+// asm into both sides of a branch before it, but not __syncwarp) would count
+// twice and let others through early.
 template <int kT>
 __device__ __forceinline__ void bar() {
+  __syncwarp();
   asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
 }
 
@@ -175,6 +179,7 @@ struct ForwardArgs {
   float* top_logprobs;
   const int* targets;
   int N, V, Vp, K;
+  uint32_t zero;  // 0
 };
 
 // keys[0 .. n), distinct, ranked by counting, two threads to a key; put(rank,
@@ -421,8 +426,17 @@ __global__ void __launch_bounds__(kT + 32, kT >= 256 ? 3 : 6) logprobs_kernel(co
       uint4 raw[kU];
 #pragma unroll
       for (int k = 0; k < kU; ++k) raw[k] = sm.ring[stage][tid + k * kT];
+      // The stage is free once the loads have returned, not once they are
+      // issued: the next bulk copy into it is not ordered behind loads that are
+      // still on their way (issued and not waited for, one in some 10^5 was
+      // overtaken, beside blocks whose searches filled the shared-memory
+      // queue).  The arrival therefore takes an operand from each of the warp's
+      // loads; a.zero is 0, which the compiler does not know.
+      uint32_t got = 0;
+#pragma unroll
+      for (int k = 0; k < kU; ++k) got |= raw[k].x;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.empty[stage]);
+      if (lane == 0) mbar_arrive(&sm.empty[stage] + (got & a.zero));
       if (lo + (c + 1) * kChunk <= min(hi, full_vecs)) {
         float mx = st.m;
 #pragma unroll
@@ -481,6 +495,7 @@ __global__ void __launch_bounds__(kT + 32, kT >= 256 ? 3 : 6) logprobs_kernel(co
       // memory of the cluster's first block, which waits for the others'
       // arrivals.  (Reading the others' memory between two cluster barriers
       // took 2.9 us a row, more than the row itself.)
+      __syncwarp();
       cluster_wait();
       if (wid == 0) {
         if (lane < kT / 32) {
@@ -727,7 +742,7 @@ int backward_typed(void* dlogits, const void* logits, const BackwardArgs& a, int
 
 int launch_logprobs(float* logprob, float* entropy, float* lse, int* top_ids, float* top_logprobs, const void* logits,
                     int logits_type, const int* targets, int N, int V, int Vp, int K, cudaStream_t s) {
-  const ForwardArgs a{logprob, entropy, lse, top_ids, top_logprobs, targets, N, V, Vp, K};
+  const ForwardArgs a{logprob, entropy, lse, top_ids, top_logprobs, targets, N, V, Vp, K, 0u};
   if (logits_type == kProbsF16) return forward_typed<__half>(logits, a, s);
   if (logits_type == kProbsBF16) return forward_typed<__nv_bfloat16>(logits, a, s);
   return forward_typed<float>(logits, a, s);

@@ -106,6 +106,43 @@ def test_against_64_bits(dtype, N, V, Vp, K):
     check(*make(N, V, Vp, dtype, seed=N + V), V, K)
 
 
+@pytest.mark.parametrize("dtype,N,V,Vp,K", [
+    ("fp32", 1000, 20003, 20008, 20), ("fp32", 1500, 40001, 40008, 3), ("fp32", 1900, 33001, 33008, 32),
+    ("bf16", 1300, 50257, 50304, 20), ("fp16", 2500, 9001, 9008, 8), ("fp32", 3000, 3001, 3008, 5),
+    ("bf16", 900, 70001, 70008, 1), ("fp32", 1000, 20003, 20008, 0)])
+def test_blocks_that_walk_many_rows(dtype, N, V, Vp, K):
+    """More rows than the GPU holds blocks, so that a block takes several rows:
+    every row against 64 bits, and the same values from every repeat."""
+    x, t = make(N, V, Vp, dtype, seed=N)
+    xg, tg = x.cuda(), t.cuda()
+    outs = []
+    for _ in range(6):
+        f = [torch.empty(N, device="cuda") for _ in range(3)]
+        ids, top = torch.empty(N, max(K, 1), dtype=torch.int32, device="cuda"), torch.empty(N, max(K, 1), device="cuda")
+        ab.logprobs_forward(*f, ids if K else None, top if K else None, xg, ab.element_type(xg), tg, N, V, Vp, K)
+        outs.append([o.cpu() for o in f + ([ids, top] if K else [])])
+    for again in outs[1:]:
+        for a, b in zip(outs[0], again):
+            assert torch.equal(a, b)
+    z = xg[:, :V].double()
+    logp = torch.log_softmax(z, 1)
+    lse = torch.logsumexp(z, 1).cpu().numpy()
+    d = (z - z.amax(1, keepdim=True)).clamp(min=-200.0)
+    rw = ((d.exp() * -d).sum(1) / d.exp().sum(1)).cpu().numpy()
+    E = (2 * 104 + V / 256 + 16) * u
+    near(outs[0][2].numpy(), lse, E + 2 * u * np.abs(lse), "lse")
+    near(outs[0][1].numpy(), torch.special.entr(logp.exp()).sum(1).cpu().numpy(), 2 * E * (1 + rw), "entropy")
+    lp = logp.gather(1, tg.clamp(min=0).long()[:, None])[:, 0].masked_fill(tg < 0, 0.0).cpu().numpy()
+    near(outs[0][0].numpy(), lp, E + 3 * u * np.abs(lp) + 16 * u, "logprob")
+    if K:
+        # (z distinguishes equal values by id: the lowest first)
+        order = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :K]
+        assert torch.equal(outs[0][3].cuda().long(), order)
+        tp = logp.gather(1, order).cpu().numpy()
+        near(outs[0][4].numpy(), tp, E + 3 * u * np.abs(tp) + 16 * u, "top")
+    no_device_error()
+
+
 @pytest.mark.parametrize("dtype", sorted(TYPES))
 @pytest.mark.parametrize("masked", [0.5, 0.99, 0.9999])
 @pytest.mark.parametrize("N", [1, 40, 1000])
