@@ -21,7 +21,6 @@
 namespace gpt2 {
 namespace {
 
-constexpr int kTileQ = 32;    // queries per CTA of the CUDA-core kernel
 constexpr int kTileK = 64;    // keys per step of a warp group
 constexpr int kThreads = 128;
 // A prefix so short, and of so few bytes when every sequence reads it by
@@ -49,10 +48,14 @@ struct Plan {
 // 4.7.)
 int row_groups(int B) { return B <= 32 ? 2 : 4; }
 
-// Enough splits that the CTAs cover the SMs (the tcgen05 kernel: one an SM, not
-// two rounds; the CUDA-core kernel two an SM, mma.sync three: what they hold),
-// each at least a step long.  The count goes by the shape alone, not by the
-// device: it sizes the caller's workspace.
+// CUDA-core kernel: query rows of a thread (8 of them a CTA's).
+int simt_rows(int B) { return B <= 8 ? 1 : B <= 16 ? 2 : B <= 32 ? 4 : 8; }
+
+// Splits: the CTAs that fit the SMs at once (the tcgen05 kernel one an SM, the
+// CUDA-core kernel two, mma.sync three), or in two rounds where these come out
+// more even: a round lasts its splits' steps and about as long as `start` steps
+// to begin and end.  The count goes by the shape alone, not by the device: it
+// sizes the caller's workspace.
 Plan plan_of(int B, int NH, int hs, int prefix_len, bool is16, int* wanted = nullptr) {
   Plan p{kNone, 1, 1, 0, 0, 0};
   const long long row_bytes = 2LL * hs * (is16 ? 2 : 4);  // of a key and its value
@@ -67,16 +70,24 @@ Plan plan_of(int B, int NH, int hs, int prefix_len, bool is16, int* wanted = nul
     p.step_k = 128;
     p.parts = B <= 128 ? 2 : 1;  // its softmax groups split the keys
   } else {
-    p.tile_q = is16 ? 16 * row_groups(B) : kTileQ;
+    p.tile_q = is16 ? 16 * row_groups(B) : 8 * simt_rows(B);
     p.step_k = is16 ? kTileK * (4 / row_groups(B)) : kTileK;
   }
   const long long tiles = static_cast<long long>((B + p.tile_q - 1) / p.tile_q) * NH;
-  const long long want =
-      p.kernel == kTc05 ? 152 / tiles : ((p.kernel == kMma ? 3 : 2) * 152 + tiles - 1) / tiles;
-  const long long most = (prefix_len + p.step_k - 1) / p.step_k;
-  const int n = static_cast<int>(std::max<long long>(1, std::min(want, most)));
-  if (wanted != nullptr) *wanted = n * p.parts;
-  p.per = ((prefix_len + n - 1) / n + p.step_k - 1) / p.step_k * p.step_k;
+  const long long slots = 152LL * (p.kernel == kTc05 ? 1 : p.kernel == kSimt ? 2 : 3), start = p.kernel == kSimt ? 1 : 3;
+  const long long steps = (prefix_len + p.step_k - 1) / p.step_k;
+  long long n = 1, best = 0;
+  for (long long rounds = 1; rounds <= 2; ++rounds) {
+    const long long fit = std::max(1LL, std::min(steps, rounds * slots / tiles));
+    const long long cost = rounds * ((steps + fit - 1) / fit + start);
+    if (rounds == 1 || cost < best) {
+      n = fit;
+      best = cost;
+    }
+    // (the most that any shape with these tiles and no more steps asks for)
+    if (wanted != nullptr) *wanted = static_cast<int>(fit * p.parts);
+  }
+  p.per = static_cast<int>((steps + n - 1) / n * p.step_k);
   p.splits = (prefix_len + p.per - 1) / p.per;  // at most n
   return p;
 }
@@ -95,98 +106,107 @@ __device__ __forceinline__ void stage_blocks(int* tbl, const KVRows& rows, int k
   }
 }
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;  // 0 source bytes: zero-filled
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ------------------------------------------------------ CUDA-core kernel
-// Any element type, fp32 arithmetic.  128 threads: ty = thread / 16 owns rows
-// 4 ty .. 4 ty + 3, tx = thread % 16 keys tx + 16 i of a step (S) and
-// dimensions tx * HS / 16 .. (O).
-template <typename E, int HS>
+// fp32 caches, fp32 arithmetic.  128 threads: ty = thread / 16 owns the R rows
+// R ty .., tx = thread % 16 keys tx + 16 i of a step (S) and dimensions
+// tx * HS / 16 .. (O).  R = 8 (64 queries) needs 16 shared-memory wavefronts for
+// 128 FMAs a thread where R = 4 needs 24 (256 sequences, 16 heads, prefix 16384:
+// 750 -> 419 us, 41 TFLOP/s); fewer rows for few queries, whose products they
+// would waste.  K and V tiles come by cp.async into two buffers: loaded through
+// registers in a loop, a step waited for eight loads in turn (8 sequences, 12
+// heads, prefix 4000: 29 us).
+template <int HS, int R>
 struct SimtSmem {
   static constexpr int kPad = HS + 4;      // row stride in floats: 16 rows' float4s in distinct banks
   static constexpr int kPPad = kTileK + 4;
-  float q[kTileQ][kPad];
-  float k[kTileK][kPad];
-  float v[kTileK][HS];
-  float p[kTileQ][kPPad];
+  float q[8 * R][kPad];
+  float k[2][kTileK][kPad];
+  float v[2][kTileK][HS];
+  float p[8 * R][kPPad];
   int tbl[kMaxBlocksPerSeq];
 };
 
-template <typename E, int HS>
-__global__ void __launch_bounds__(kThreads) prefix_simt_kernel(float* __restrict__ po, float2* __restrict__ pml,
-                                                               const E* __restrict__ qkv, const E* __restrict__ kcache,
-                                                               const E* __restrict__ vcache, int B, int C, int NH,
-                                                               int prefix_len, int per_split, KVRows rows,
-                                                               float scale_log2) {
+template <int HS, int R>
+__global__ void __launch_bounds__(kThreads, 2)
+    prefix_simt_kernel(float* __restrict__ po, float2* __restrict__ pml, const float* __restrict__ qkv,
+                       const float* __restrict__ kcache, const float* __restrict__ vcache, int B, int C, int NH,
+                       int prefix_len, int per_split, KVRows rows, float scale_log2) {
   extern __shared__ __align__(128) uint8_t shared_raw[];
-  auto& sm = *reinterpret_cast<SimtSmem<E, HS>*>(shared_raw);
-  constexpr int kD = HS / 16;
-  constexpr int kPer = 16 / static_cast<int>(sizeof(E));  // elements per 16-byte load
-  const int b0 = static_cast<int>(blockIdx.x) * kTileQ, h = blockIdx.y, split = blockIdx.z;
+  auto& sm = *reinterpret_cast<SimtSmem<HS, R>*>(shared_raw);
+  constexpr int kD = HS / 16, kChunks = HS / 4;
+  const int b0 = static_cast<int>(blockIdx.x) * (8 * R), h = blockIdx.y, split = blockIdx.z;
   const int k_lo = split * per_split, k_hi = min(prefix_len, k_lo + per_split);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   pdl_wait();  // the QKV projection ahead has finished
   pdl_trigger();
   stage_blocks(sm.tbl, rows, k_lo, k_hi, h == 0 && blockIdx.x == 0);
-  for (int i = threadIdx.x; i < kTileQ * (HS / kPer); i += kThreads) {
-    const int r = i / (HS / kPer), c = i % (HS / kPer) * kPer;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (b0 + r < B) raw = __ldg(reinterpret_cast<const uint4*>(qkv + static_cast<size_t>(b0 + r) * 3 * C + h * HS + c));
-    const E* e = reinterpret_cast<const E*>(&raw);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) sm.q[r][c + j] = to_f32(e[j]) * scale_log2;
+  for (int i = threadIdx.x; i < 8 * R * kChunks; i += kThreads) {
+    const int r = i / kChunks, c = i % kChunks * 4;
+    const bool valid = b0 + r < B;
+    cp_async16(&sm.q[r][c], qkv + static_cast<size_t>(valid ? b0 + r : 0) * 3 * C + h * HS + c, valid);
   }
-  float m[4], l[4], o[4][kD];
+  __syncthreads();  // the block ids
+  const int blk0 = k_lo >> rows.lbs, bs1 = (1 << rows.lbs) - 1;
+  auto load = [&](int buf, int j0) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kTileK * kChunks; i += kThreads) {
+      const int r = i / kChunks, c = i % kChunks * 4, j = j0 + r;
+      const bool valid = j < k_hi;
+      const int jj = valid ? j : k_lo;
+      const size_t row = ((static_cast<size_t>(sm.tbl[(jj >> rows.lbs) - blk0]) * NH + h) << rows.lbs) + (jj & bs1);
+      cp_async16(&sm.k[buf][r][c], kcache + row * HS + c, valid);
+      cp_async16(&sm.v[buf][r][c], vcache + row * HS + c, valid);
+    }
+  };
+  load(0, k_lo);
+  cp_async_commit();
+  float m[R], l[R], o[R][kD];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < R; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
 #pragma unroll
     for (int d = 0; d < kD; ++d) o[r][d] = 0.f;
   }
-  const int blk0 = k_lo >> rows.lbs;
-  for (int j0 = k_lo; j0 < k_hi; j0 += kTileK) {
-    __syncthreads();  // the previous step's tiles have been read (and tbl, q are written)
-    for (int i = threadIdx.x; i < kTileK * (HS / kPer); i += kThreads) {
-      const int r = i / (HS / kPer), c = i % (HS / kPer) * kPer, j = j0 + r;
-      uint4 kr = make_uint4(0u, 0u, 0u, 0u), vr = kr;
-      if (j < k_hi) {
-        const size_t row = ((static_cast<size_t>(sm.tbl[(j >> rows.lbs) - blk0]) * NH + h) << rows.lbs) +
-                           (j & ((1 << rows.lbs) - 1));
-        kr = __ldg(reinterpret_cast<const uint4*>(kcache + row * HS + c));
-        vr = __ldg(reinterpret_cast<const uint4*>(vcache + row * HS + c));
-      }
-      const E* ke = reinterpret_cast<const E*>(&kr);
-      const E* ve = reinterpret_cast<const E*>(&vr);
-#pragma unroll
-      for (int d = 0; d < kPer; ++d) {
-        sm.k[r][c + d] = to_f32(ke[d]);
-        sm.v[r][c + d] = to_f32(ve[d]);
-      }
-    }
+  for (int j0 = k_lo, buf = 0; j0 < k_hi; j0 += kTileK, buf ^= 1) {
+    if (j0 + kTileK < k_hi) load(buf ^ 1, j0 + kTileK);
+    cp_async_commit();
+    cp_async_wait<1>();
     __syncthreads();
-    float s[4][4];
+    float s[R][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[r][i] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
     for (int d = 0; d < HS; d += 4) {
-      float4 qa[4], ka[4];
+      float4 ka[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) qa[r] = *reinterpret_cast<const float4*>(&sm.q[4 * ty + r][d]);
+      for (int i = 0; i < 4; ++i) ka[i] = *reinterpret_cast<const float4*>(&sm.k[buf][tx + 16 * i][d]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ka[i] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * i][d]);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < R; ++r) {
+        const float4 qa = *reinterpret_cast<const float4*>(&sm.q[R * ty + r][d]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          s[r][i] = fmaf(qa[r].x, ka[i].x, fmaf(qa[r].y, ka[i].y, fmaf(qa[r].z, ka[i].z, fmaf(qa[r].w, ka[i].w, s[r][i]))));
+          s[r][i] = fmaf(qa.x, ka[i].x, fmaf(qa.y, ka[i].y, fmaf(qa.z, ka[i].z, fmaf(qa.w, ka[i].w, s[r][i]))));
+      }
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
       float mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (j0 + tx + 16 * i >= k_hi) s[r][i] = -INFINITY;
+        s[r][i] = j0 + tx + 16 * i < k_hi ? s[r][i] * scale_log2 : -INFINITY;
         mx = fmaxf(mx, s[r][i]);
       }
 #pragma unroll
@@ -201,35 +221,46 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(float* __restrict
       for (int i = 0; i < 4; ++i) {
         const float p = exp2_approx(s[r][i] - m_new);
         l[r] += p;  // this thread's keys
-        sm.p[4 * ty + r][tx + 16 * i] = p;
+        sm.p[R * ty + r][tx + 16 * i] = p;
       }
     }
-    __syncwarp();  // rows 4 ty .. are written and read by the 16 threads of ty, half a warp
-#pragma unroll 4
+    __syncwarp();  // rows R ty .. are written and read by the 16 threads of ty, half a warp
+#pragma unroll 2
     for (int j = 0; j < kTileK; j += 4) {
-      float4 pa[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) pa[r] = *reinterpret_cast<const float4*>(&sm.p[4 * ty + r][j]);
+      float vv[4][kD];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float vv[kD];
-#pragma unroll
-        for (int d = 0; d < kD; ++d) vv[d] = sm.v[j + i][tx * kD + d];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float p = i == 0 ? pa[r].x : i == 1 ? pa[r].y : i == 2 ? pa[r].z : pa[r].w;
-#pragma unroll
-          for (int d = 0; d < kD; ++d) o[r][d] = fmaf(p, vv[d], o[r][d]);
+        const float* vr = &sm.v[buf][j + i][tx * kD];
+        if constexpr (kD == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(vr);
+          vv[i][0] = x.x;
+          vv[i][1] = x.y;
+          vv[i][2] = x.z;
+          vv[i][3] = x.w;
+        } else if constexpr (kD == 2) {
+          const float2 x = *reinterpret_cast<const float2*>(vr);
+          vv[i][0] = x.x;
+          vv[i][1] = x.y;
+        } else {
+          vv[i][0] = vr[0];
         }
       }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float4 pa = *reinterpret_cast<const float4*>(&sm.p[R * ty + r][j]);
+#pragma unroll
+        for (int d = 0; d < kD; ++d)
+          o[r][d] = fmaf(pa.x, vv[0][d], fmaf(pa.y, vv[1][d], fmaf(pa.z, vv[2][d], fmaf(pa.w, vv[3][d], o[r][d]))));
+      }
     }
+    __syncthreads();  // this buffer is refilled by the next step's load
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < R; ++r) {
     float sum = l[r];
 #pragma unroll
     for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    const int b = b0 + 4 * ty + r;
+    const int b = b0 + R * ty + r;
     if (b >= B) continue;
     const size_t at = (static_cast<size_t>(split) * NH + h) * B + b;
     if (tx == 0) pml[at] = make_float2(m[r], sum);
@@ -245,15 +276,6 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(float* __restrict
 // into two buffers, rows of HS * 2 bytes with 16-byte chunk c of row r at chunk
 // c ^ (r mod chunks), as in attn_tc_kernel; any block size, since every chunk
 // finds its own block.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;  // 0 source bytes: zero-filled
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
@@ -805,18 +827,30 @@ int join(void* out, const void* qkv, void* kc, void* vc, int B, int C, int NH, c
 
 dim3 prefix_grid(const Plan& pl, int B, int NH) { return dim3((B + pl.tile_q - 1) / pl.tile_q, NH, pl.splits); }
 
-template <typename E, int HS>
+template <int HS, int R>
 int simt_typed(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc, int B, int C, int NH,
                const KVRows& rows, cudaStream_t s) {
   static bool allowed[kMaxDevices] = {};
   const Plan pl = plan_of(B, NH, HS, p.prefix_len, false);
-  using Smem = SimtSmem<E, HS>;
-  cudaError_t e = allow_smem(allowed, prefix_simt_kernel<E, HS>, sizeof(Smem));
+  using Smem = SimtSmem<HS, R>;
+  static_assert(sizeof(Smem) <= 227 * 1024 / 2, "two CTAs an SM");
+  cudaError_t e = allow_smem(allowed, prefix_simt_kernel<HS, R>, sizeof(Smem));
   if (e == cudaSuccess)
-    e = launch_pdl(prefix_simt_kernel<E, HS>, prefix_grid(pl, B, NH), dim3(kThreads), sizeof(Smem), s, p.o, p.ml,
-                   static_cast<const E*>(qkv), static_cast<const E*>(kc), static_cast<const E*>(vc), B, C, NH,
-                   p.prefix_len, pl.per, rows, 1.4426950408889634f / sqrtf(static_cast<float>(HS)));
+    e = launch_pdl(prefix_simt_kernel<HS, R>, prefix_grid(pl, B, NH), dim3(kThreads), sizeof(Smem), s, p.o, p.ml,
+                   static_cast<const float*>(qkv), static_cast<const float*>(kc), static_cast<const float*>(vc), B, C,
+                   NH, p.prefix_len, pl.per, rows, 1.4426950408889634f / sqrtf(static_cast<float>(HS)));
   return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
+}
+
+template <int HS>
+int simt(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc, int B, int C, int NH,
+         const KVRows& rows, cudaStream_t s) {
+  switch (simt_rows(B)) {
+    case 1: return simt_typed<HS, 1>(p, qkv, kc, vc, B, C, NH, rows, s);
+    case 2: return simt_typed<HS, 2>(p, qkv, kc, vc, B, C, NH, rows, s);
+    case 4: return simt_typed<HS, 4>(p, qkv, kc, vc, B, C, NH, rows, s);
+    default: return simt_typed<HS, 8>(p, qkv, kc, vc, B, C, NH, rows, s);
+  }
 }
 
 template <int HS, typename T16, int WM>
@@ -862,7 +896,7 @@ int mma(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc
 size_t partial_rows(int B, int NH, int hs, int prefix_len, bool is16) {
   if (prefix_len <= 0) return 0;
   size_t most = 0;
-  for (int b = 16;; b += b < 64 ? 16 : 32) {
+  for (int b = 8;; b += b < 64 ? 8 : 32) {
     const int c = std::min(b, B);
     int n = 0;
     plan_of(c, NH, hs, prefix_len, is16, &n);
@@ -899,9 +933,9 @@ int launch_shared_prefix(const PrefixPartials& p, const void* qkv, const void* k
   if (op == kOpF16) return mma<__half>(p, qkv, kcache, vcache, B, C, NH, rows, s);
   if (op == kOpBF16) return mma<__nv_bfloat16>(p, qkv, kcache, vcache, B, C, NH, rows, s);
   switch (C / NH) {
-    case 16: return simt_typed<float, 16>(p, qkv, kcache, vcache, B, C, NH, rows, s);
-    case 32: return simt_typed<float, 32>(p, qkv, kcache, vcache, B, C, NH, rows, s);
-    case 64: return simt_typed<float, 64>(p, qkv, kcache, vcache, B, C, NH, rows, s);
+    case 16: return simt<16>(p, qkv, kcache, vcache, B, C, NH, rows, s);
+    case 32: return simt<32>(p, qkv, kcache, vcache, B, C, NH, rows, s);
+    case 64: return simt<64>(p, qkv, kcache, vcache, B, C, NH, rows, s);
   }
   return GPT2_ERR_UNSUPPORTED;
 }
