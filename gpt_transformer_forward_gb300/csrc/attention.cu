@@ -475,8 +475,15 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
         }
       }
       if (staged) {
+        // The stage is free once these loads have returned, not once they are
+        // issued: the next bulk copy into it is not ordered behind loads on
+        // their way.  The arrival takes an operand from each of them, with an
+        // offset of 0 that the compiler does not know (NH is positive).
+        uint32_t got = 0;
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) got |= kr[i].x | vr[i].x;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[st]);
+        if (lane == 0) mbar_arrive(&empty[st] + (got & (NH < 0 ? 1u : 0u)));
       }
       return true;
     };
