@@ -19,6 +19,14 @@ def probs_type(probs) -> int:
     return ab.GPT2_PROBS_F32 if probs is None else _PROBS_TYPE[probs.dtype]
 
 
+def _check_int32(t, name: str, shape) -> None:
+    """The calls take plain pointers: a tensor of another type, shape or
+    layout would be read as something else."""
+    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: contiguous int32 of shape {tuple(shape)} expected, not {t.dtype} of shape "
+                         f"{tuple(t.shape)}{'' if t.is_contiguous() else ', strided'}")
+
+
 class GPT2Model:
     """Parameters (fp32, plus the packed bf16 weights in GPT2_BF16 mode) and a
     workspace sized for batches of up to B sequences of up to T tokens."""
@@ -94,8 +102,9 @@ class GPT2Model:
     # ------------------------------------- many continuations of one prompt
     def prefill_slots(self, tok, logits, kv, slots, probs=None, stream=None):
         """gpt2_forward storing token (b, t) at slot slots[b, t] of kv's pool
-        (none where it is -1)."""
+        (none where it is -1).  slots: contiguous int32 [B, T]."""
         B, T = tok.shape
+        _check_int32(slots, "slots", (B, T))
         ab.gpt2_prefill_slots(self.cfg, self.params, self.packed, tok, B, T, logits, probs, kv, slots, self.workspace,
                               self.ws_bytes, self.precision, stream)
 
@@ -106,16 +115,24 @@ class GPT2Model:
 
     def decode_step_shared(self, kv, tok, pos, prefix_len: int, logits, workspace, probs=None, stream=None):
         """decode_step_paged for sequences that share their first prefix_len
-        positions; workspace from new_shared_workspace."""
+        positions; pos int32 [B]; workspace from new_shared_workspace."""
         B = tok.shape[0]
+        _check_int32(pos, "pos", (B,))
         ab.gpt2_decode_step_shared(self.cfg, self.params, self.packed, kv, tok, pos, B, prefix_len, logits, probs,
                                    workspace, workspace.numel(), self.precision, stream)
 
     def logprobs(self, logits, targets=None, top: int = 0, stream=None) -> dict:
-        """The log probability of each row's target (targets: int32, -1 for
-        none), its entropy, log-sum-exp and `top` alternatives, of logits
-        [..., Vp]; results have the logits' leading shape."""
+        """The log probability of each row's target (targets: int32 of the
+        logits' leading shape, -1 for none), its entropy, log-sum-exp and
+        `top` alternatives, of logits [..., Vp]; results have the logits'
+        leading shape.  Logits are contiguous: to score a part of the
+        positions give the others target -1."""
         shape, Vp = logits.shape[:-1], logits.shape[-1]
+        if not logits.is_contiguous():
+            raise ValueError(f"logits: contiguous rows expected, not strides {logits.stride()} of shape "
+                             f"{tuple(logits.shape)}")
+        if targets is not None:
+            _check_int32(targets, "targets", shape)
         new = lambda *more, dtype=torch.float32: torch.empty(*shape, *more, dtype=dtype, device=logits.device)  # noqa: E731
         r = {"entropy": new(), "lse": new()}
         if targets is not None:

@@ -4,9 +4,11 @@ anything is launched (the addresses here are aligned and never read)."""
 import ctypes
 
 import pytest
+import torch
 
 from gpt_transformer_forward_gb300 import binding as ab
 from gpt_transformer_forward_gb300 import build, inputs
+from gpt_transformer_forward_gb300.runner import GPT2Model
 
 FAKE = 1 << 20
 A, S, AL, W, U = -1, -2, -3, -4, -7  # GPT2_ERR_ARG, _SHAPE, _ALIGN, _WORKSPACE, _UNSUPPORTED
@@ -175,8 +177,44 @@ def test_logprobs_backward_refuses(change, code):
     refused(code, ab.logprobs_backward, **lb_args(**change))
 
 
+@pytest.fixture(scope="module")
+def cpu_model():
+    """A model whose buffers are in host memory, for checks that come before
+    any launch."""
+    w = inputs.WORKLOADS["tiny"]
+    params, _ = inputs.workload_inputs(w, "perturbed")
+    return GPT2Model(w.cfg, params, 2, 4, ab.GPT2_FP32, device="cpu")
+
+
+@pytest.mark.parametrize("logits,targets", [
+    (lambda x: x[:, :-1], None),                                     # rows of part of the positions
+    (lambda x: x.transpose(0, 1), None),
+    (lambda x: x, lambda t: t.long()),
+    (lambda x: x, lambda t: t[:, :-1]),                              # fewer targets than rows
+    (lambda x: x, lambda t: torch.cat([t, t], 1)[:, ::2]),           # strided
+    (lambda x: x, lambda t: t.flatten()),
+    (lambda x: x.double(), None),
+])
+def test_runner_logprobs_refuses_what_it_would_misread(cpu_model, logits, targets):
+    x = torch.zeros(2, 4, cpu_model.cfg.padded_vocab_size)
+    t = torch.zeros(2, 4, dtype=torch.int32)
+    with pytest.raises((ValueError, TypeError)):
+        cpu_model.logprobs(logits(x), targets and targets(t), top=2, stream=0)
+
+
+def test_runner_serving_calls_refuse_what_they_would_misread(cpu_model):
+    tok = torch.zeros(2, 4, dtype=torch.int32)
+    for slots in (torch.zeros(2, 8, dtype=torch.int32)[:, :4], torch.zeros(2, 4, dtype=torch.int64),
+                  torch.zeros(2, 3, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="slots"):
+            cpu_model.prefill_slots(tok, None, None, slots, stream=0)
+    for pos in (torch.zeros(2, dtype=torch.int64), torch.zeros(4, dtype=torch.int32)[::2],
+                torch.zeros(3, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="pos"):
+            cpu_model.decode_step_shared(None, tok[:, 0], pos, 1, None, None, stream=0)
+
+
 def test_element_types():
-    import torch
     assert ab.element_type(torch.empty(1)) == ab.GPT2_PROBS_F32
     assert ab.element_type(torch.empty(1, dtype=torch.bfloat16)) == ab.GPT2_PROBS_BF16
     with pytest.raises(TypeError):
