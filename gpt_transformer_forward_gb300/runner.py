@@ -6,6 +6,8 @@ touches the data is the CUDA library's, reached through `binding`.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import binding as ab
@@ -17,6 +19,15 @@ _PROBS_TYPE = {torch.float32: ab.GPT2_PROBS_F32, torch.float16: ab.GPT2_PROBS_F1
 
 def probs_type(probs) -> int:
     return ab.GPT2_PROBS_F32 if probs is None else _PROBS_TYPE[probs.dtype]
+
+
+def _allocating_on(stream):
+    """Memory allocated within belongs to `stream` (a torch stream or a raw
+    handle; None: the current one), where its kernel runs: that of another
+    stream may still be in use there by work queued earlier."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 def _check_int32(t, name: str, shape) -> None:
@@ -125,20 +136,22 @@ class GPT2Model:
         """The log probability of each row's target (targets: int32 of the
         logits' leading shape, -1 for none), its entropy, log-sum-exp and
         `top` alternatives, of logits [..., Vp]; results have the logits'
-        leading shape.  Logits are contiguous: to score a part of the
-        positions give the others target -1."""
+        leading shape and belong to `stream`.  Logits are contiguous: to
+        score a part of the positions give the others target -1."""
         shape, Vp = logits.shape[:-1], logits.shape[-1]
+        kind = ab.element_type(logits)
         if not logits.is_contiguous():
             raise ValueError(f"logits: contiguous rows expected, not strides {logits.stride()} of shape "
                              f"{tuple(logits.shape)}")
         if targets is not None:
             _check_int32(targets, "targets", shape)
         new = lambda *more, dtype=torch.float32: torch.empty(*shape, *more, dtype=dtype, device=logits.device)  # noqa: E731
-        r = {"entropy": new(), "lse": new()}
-        if targets is not None:
-            r["logprob"] = new()
-        if top:
-            r["top_ids"], r["top_logprobs"] = new(top, dtype=torch.int32), new(top)
+        with _allocating_on(stream):
+            r = {"entropy": new(), "lse": new()}
+            if targets is not None:
+                r["logprob"] = new()
+            if top:
+                r["top_ids"], r["top_logprobs"] = new(top, dtype=torch.int32), new(top)
         ab.logprobs_forward(r.get("logprob"), r["entropy"], r["lse"], r.get("top_ids"), r.get("top_logprobs"), logits,
-                            ab.element_type(logits), targets, r["lse"].numel(), self.cfg.vocab_size, Vp, top, stream)
+                            kind, targets, r["lse"].numel(), self.cfg.vocab_size, Vp, top, stream)
         return r

@@ -410,3 +410,23 @@ def test_runner_logprobs():
     nxt1 = torch.empty(w.B * w.T, dtype=torch.int32, device="cuda")
     ab.gpt2_argmax(nxt1, logits, w.B * w.T, w.cfg.vocab_size, w.cfg.padded_vocab_size)
     assert torch.equal(r["top_ids"][..., 0].reshape(-1), nxt1)
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_runner_logprobs_allocates_on_the_stream_it_runs_on(monkeypatch, raw):
+    w = inputs.WORKLOADS["tiny"]
+    params, _ = inputs.workload_inputs(w, "perturbed")
+    m = GPT2Model(w.cfg, params, 1, 4, ab.GPT2_FP32)
+    logits = torch.randn(5, w.cfg.padded_vocab_size, device="cuda")
+    tg = torch.arange(5, dtype=torch.int32, device="cuda")
+    want = m.logprobs(logits, tg, top=2)
+    s, real, at = torch.cuda.Stream(), torch.empty, []
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: (at.append(torch.cuda.current_stream().cuda_stream),
+                                                         real(*a, **k))[1])
+    torch.cuda.synchronize()
+    got = m.logprobs(logits, tg, top=2, stream=s.cuda_stream if raw else s)
+    assert at == [s.cuda_stream] * 5
+    assert torch.cuda.current_stream().cuda_stream != s.cuda_stream
+    s.synchronize()
+    for k, v in want.items():
+        assert torch.equal(got[k], v), k
