@@ -913,6 +913,8 @@ int gpt2_prefill_slots(const GPT2Config* cfg, const float* params, const void* p
 
 // grid limits of the attention kernels: sequences and heads
 constexpr int kMaxSharedBatch = 65535;
+// positions of a sequence: an int holds them and a step of the kernels beyond
+constexpr int kMaxSharedPositions = 1 << 30;
 
 size_t attention_shared_prefix_workspace_size(int B, int C, int NH, int prefix_len, int precision) {
   if (B <= 0 || B > kMaxSharedBatch || C <= 0 || NH <= 0 || NH > kMaxSharedBatch || C % NH != 0 || prefix_len <= 0 ||
@@ -932,7 +934,7 @@ int attention_shared_prefix(void* out, const void* qkv, const GPT2PagedKVCache* 
                 static_cast<long long>(B) * NH > 0x7fffffffLL,
             GPT2_ERR_SHAPE);
   const long long cap =
-      std::min<long long>(0x7fffffffLL, static_cast<long long>(kvc->max_blocks_per_seq) << lbs);
+      std::min<long long>(kMaxSharedPositions, static_cast<long long>(kvc->max_blocks_per_seq) << lbs);
   RETURN_IF(prefix_len >= cap, GPT2_ERR_SHAPE);  // the new token's position lies behind the prefix
   TRY(check_attention_shape(C, NH));
   if (B == 0) return GPT2_OK;
@@ -970,6 +972,7 @@ int gpt2_decode_step_shared(const GPT2Config* cfg, const float* params, const vo
   RETURN_IF(is16(precision) && packed == nullptr, GPT2_ERR_ARG);
   KVLayout kv;
   TRY(paged_kv(cfg, kvc, 0, &kv));
+  kv.rows.capacity = std::min(kv.rows.capacity, kMaxSharedPositions);
   RETURN_IF(B > kMaxSharedBatch || prefix_len >= kv.rows.capacity, GPT2_ERR_SHAPE);
   RETURN_IF(!aligned16(params) || !aligned16(logits) || (probs && !aligned16(probs)) ||
                 (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||

@@ -108,7 +108,7 @@ GPT2_API size_t attention_shared_prefix_workspace_size(int B, int C, int NH, int
  * prefix_len need not be a multiple of the block size.
  *   kv: one layer's slab [2][num_blocks][NH][block_size][hs], and the table
  *   [B][max_blocks_per_seq]; a sequence holds at most max_blocks_per_seq *
- *   block_size positions.  qkv [B,3C], out [B,C] and the slab have one
+ *   block_size positions, and 2^30.  qkv [B,3C], out [B,C] and the slab have one
  *   element type: fp32 in GPT2_FP32 and GPT2_TF32 (both fp32 arithmetic), the
  *   16-bit type in GPT2_BF16 and GPT2_FP16 (the products over the prefix on
  *   tensor cores with fp32 accumulation, its probabilities rounded to the

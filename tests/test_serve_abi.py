@@ -68,6 +68,7 @@ def shared_args(**kw):
     (dict(kv=ab.paged_kv(FAKE, FAKE, 64, 16, 0)), A),
     (dict(NH=3), S), (dict(kv=ab.paged_kv(FAKE, FAKE, 64, 16, 1025)), S), (dict(prefix_len=512), S),
     (dict(B=65536), S), (dict(C=512), U), (dict(C=96), U),
+    (dict(kv=ab.paged_kv(FAKE, FAKE, 1024, 1 << 21, 1024), prefix_len=1 << 30, ws_bytes=16), S),
     (dict(workspace=None), W), (dict(ws_bytes=16), W),
     (dict(out=FAKE + 8), AL), (dict(qkv=FAKE + 8), AL), (dict(workspace=FAKE + 8), AL), (dict(pos=FAKE + 2), AL),
     (dict(kv=ab.paged_kv(FAKE + 8, FAKE, 64, 16, 32)), AL),
