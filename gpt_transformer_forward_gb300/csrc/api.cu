@@ -987,8 +987,11 @@ int gpt2_decode_step_shared(const GPT2Config* cfg, const float* params, const vo
                      as_stream(stream), nullptr, GPT2_PROBS_F32, nullptr, &p);
 }
 
-// rows of a whole number of 16-byte vectors
-static bool logit_rows_ok(int Vp, int logits_type) { return Vp % (logits_type == GPT2_PROBS_F32 ? 4 : 8) == 0; }
+// rows of a whole number of 16-byte vectors, whose element index and a step
+// of the kernels beyond it an int holds
+static bool logit_rows_ok(int Vp, int logits_type) {
+  return Vp % (logits_type == GPT2_PROBS_F32 ? 4 : 8) == 0 && Vp <= 1 << 30;
+}
 
 int logprobs_forward(float* logprob, float* entropy, float* lse, int* top_ids, float* top_logprobs, const void* logits,
                      int logits_type, const int* targets, int N, int V, int Vp, int K, void* stream) {

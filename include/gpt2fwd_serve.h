@@ -153,7 +153,7 @@ GPT2_API int gpt2_decode_step_shared(const GPT2Config* cfg, const float* params,
  *                 first, equal ones by the lowest id.
  * logits [N,Vp] of logits_type (a GPT2ProbsType: fp32, fp16 or bf16), each row
  * a whole number of 16 bytes (Vp % 4 == 0 for fp32, Vp % 8 == 0 for the
- * 16-bit types) and 16-byte aligned; all outputs fp32 (arithmetic in fp32)
+ * 16-bit types), Vp <= 2^30, and 16-byte aligned; all outputs fp32 (arithmetic in fp32)
  * but top_ids (int32), 4-byte aligned.
  * targets int32 [N], or NULL (then logprob is NULL too); a target of -1 (a
  * padding position) gives logprob 0; one outside [-1, V) sets

@@ -149,6 +149,7 @@ def lp_args(**kw):
     (dict(logits_type=3), A), (dict(logits_type=-1), A), (dict(Vp=14), S), (dict(K=33), S),
     (dict(logits_type=ab.GPT2_PROBS_F16), S), (dict(logits_type=ab.GPT2_PROBS_BF16), S),
     (dict(logits=FAKE + 8), AL), (dict(lse=FAKE + 2), AL), (dict(targets=FAKE + 1), AL),
+    (dict(V=(1 << 30) + 1, Vp=(1 << 30) + 8, logits=FAKE + 8), S),
 ])
 def test_logprobs_refuse(change, code):
     refused(code, ab.logprobs_forward, **lp_args(**change))
@@ -173,6 +174,7 @@ def lb_args(**kw):
     (dict(dlogits=None), A), (dict(logits=None), A), (dict(lse=None), A), (dict(targets=None), A),
     (dict(entropy=None), A), (dict(V=0), A), (dict(Vp=9), A), (dict(logits_type=5), A), (dict(Vp=14), S),
     (dict(logits_type=ab.GPT2_PROBS_F16), S), (dict(dlogits=FAKE + 4), AL), (dict(dentropy=FAKE + 2), AL),
+    (dict(V=(1 << 30) + 1, Vp=(1 << 30) + 8, dlogits=FAKE + 8), S),
 ])
 def test_logprobs_backward_refuses(change, code):
     refused(code, ab.logprobs_backward, **lb_args(**change))
