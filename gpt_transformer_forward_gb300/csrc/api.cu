@@ -568,9 +568,9 @@ size_t gpt2_kvcache_size(const GPT2Config* cfg, int B, int precision) {
 static int shared_attention(void* out, const void* qkv, void* kc, void* vc, int precision, int B, int C, int NH,
                             const int* pos, const KVRows& rows, const PrefixPartials& p, cudaStream_t s) {
   const int op = is16(precision) ? op_of(precision) : kOpTF32;  // an fp32 cache in the other modes
+  // the kernels wait for what is ahead of them themselves
+  PdlScope pdl(true);
   if (p.splits > 0) TRY(launch_shared_prefix(p, qkv, kc, vc, op, B, C, NH, rows, s));
-  // the kernel waits for the prefix's results itself
-  PdlScope pdl(pdl_on() || p.splits > 0);
   TRY(launch_own_join(out, qkv, kc, vc, op, B, C, NH, pos, rows, p, s));
   return check_launch();
 }
