@@ -8,10 +8,10 @@
 // and query tiles would leave most SMs idle); every split keeps its rows'
 // running maximum m, sum l and unnormalised output O.
 //   prefix_simt_kernel   fp32 caches, CUDA cores
-//   prefix_mma_kernel    16-bit caches, mma.sync: few sequences, or a head
-//                        size below 64
+//   prefix_mma_kernel    16-bit caches, mma.sync: few sequences, a short
+//                        prefix, or a head size below 64
 //   prefix_tc05_kernel   16-bit caches, tcgen05 (attention_shared_tc.cu): many
-//                        sequences
+//                        sequences and a long prefix
 // Join: own_join_kernel attends over each sequence's own positions and joins
 // that with the splits' results, which it weighs by 2^(m - max m).
 #include "serve.cuh"
@@ -30,7 +30,17 @@ constexpr int kThreads = 128;
 // 4.6; one sequence, prefix 1000: 8.4 against 4.7).
 constexpr int kDirectLen = 256;
 constexpr long long kDirectBytes = 8LL << 20;
-constexpr int kTcMinBatch = 65;  // sequences from which the tcgen05 kernel takes over (head size 64)
+// The tcgen05 kernel (head size 64) takes over for 65 sequences or more and
+// this many pairs of a query row (rows in tiles of 64) and a shared position: it
+// costs about 4 us more to begin and end, and less per pair.  Prefix part, own
+// positions and join, mma.sync against tcgen05, us: 12 heads, 96 sequences,
+// prefix 960 (1.5 million pairs) 8.1 against 10.1, 4000 (6.1) 12.6 against 11.7;
+// 256 sequences, 960 (2.9) 11.0 against 12.8, 2000 (6.1) 14.2 against 14.5, 4000
+// (12.3) 18.8 against 15.2; 4 heads, 256 sequences, 4000 (4.1) 10.0 against 10.6,
+// 8000 (8.2) 14.3 against 11.6; 16 heads, 129 sequences, 960 (2.9) 10.2 against
+// 10.9, 2000 (6.1) 13.6 against 12.0.
+constexpr int kTcMinBatch = 65;
+constexpr long long kTcMinPairs = 5000000;
 
 // How a shape is cut: the kernel, queries per CTA, keys per step of a CTA,
 // splits of the prefix over CTAs, positions per split (a multiple of the step)
@@ -51,6 +61,9 @@ int row_groups(int B) { return B <= 32 ? 2 : 4; }
 // CUDA-core kernel: query rows of a thread (8 of them a CTA's).
 int simt_rows(int B) { return B <= 8 ? 1 : B <= 16 ? 2 : B <= 32 ? 4 : 8; }
 
+// Pairs of a query row and a shared position, per position.
+long long tc_pairs(int B, int NH) { return static_cast<long long>((B + 63) / 64 * 64) * NH; }
+
 // Splits: the CTAs that fit the SMs at once (the tcgen05 kernel one an SM, the
 // CUDA-core kernel two, mma.sync three), or in two rounds where these come out
 // more even: a round lasts its splits' steps and about as long as `start` steps
@@ -63,7 +76,8 @@ Plan plan_of(int B, int NH, int hs, int prefix_len, bool is16, int* wanted = nul
     if (wanted != nullptr) *wanted = 0;
     return p;
   }
-  p.kernel = !is16 ? kSimt : hs == 64 && B >= kTcMinBatch ? kTc05 : kMma;
+  const bool tc = is16 && hs == 64 && B >= kTcMinBatch && tc_pairs(B, NH) * prefix_len >= kTcMinPairs;
+  p.kernel = !is16 ? kSimt : tc ? kTc05 : kMma;
   p.parts = 1;
   if (p.kernel == kTc05) {
     p.tile_q = 256;
@@ -898,15 +912,21 @@ int mma(const PrefixPartials& p, const void* qkv, const void* kc, const void* vc
 // Partial rows a workspace holds: those of the worst batch of at most B
 // sequences, so that one workspace serves smaller batches and, as the wanted
 // splits grow with it, shorter prefixes too.  The worst of the batches with
-// the same query tiles is the one with full tiles.
+// the same query tiles is the one with full tiles.  Where the tcgen05 kernel
+// takes the prefix, the longest one that mma.sync takes may need more.
 size_t partial_rows(int B, int NH, int hs, int prefix_len, bool is16) {
   if (prefix_len <= 0) return 0;
   size_t most = 0;
   for (int b = 8;; b += b < 64 ? 8 : 32) {
     const int c = std::min(b, B);
     int n = 0;
-    plan_of(c, NH, hs, prefix_len, is16, &n);
+    const bool tc = plan_of(c, NH, hs, prefix_len, is16, &n).kernel == kTc05;
     most = std::max(most, static_cast<size_t>(n) * c);
+    const int shorter = tc ? static_cast<int>((kTcMinPairs - 1) / tc_pairs(c, NH)) : 0;  // than prefix_len
+    if (shorter > 0) {
+      plan_of(c, NH, hs, shorter, is16, &n);
+      most = std::max(most, static_cast<size_t>(n) * c);
+    }
     if (b >= B) return most * NH;
   }
 }

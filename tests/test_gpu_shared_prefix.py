@@ -260,6 +260,91 @@ def test_cache_past_32_bits():
     no_device_error()
 
 
+# ---------------------------------------- many sequences, a long prefix
+# (16-bit caches with heads of 64 take another kernel from this work on)
+def long_case(precision, B, NH, P, own, bs, **kw):
+    assert B >= 65 and (B + 63) // 64 * 64 * NH * P >= 5_000_000
+    return make(precision, B, NH, 64, P, own, bs, **kw)
+
+
+@pytest.mark.parametrize("precision", [ab.GPT2_FP16, ab.GPT2_BF16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("B,NH,P,most,bs", [
+    (65, 16, 2500, 3, 64), (128, 16, 2443, 5, 16), (129, 13, 2004, 9, 4), (200, 13, 1561, 20, 2), (257, 8, 1999, 3, 128),
+    (300, 16, 978, 7, 256), (66, 40, 1000, 2, 1), (520, 1, 8690, 5, 32), (100, 4, 9999, 2, 64), (128, 16, 2560, 5, 8),
+])
+def test_long_prefix_of_many_sequences(precision, B, NH, P, most, bs):
+    check(long_case(precision, B, NH, P, own_of(B, most, P), bs, seed=B + P))
+
+
+@pytest.mark.parametrize("precision", [ab.GPT2_FP16, ab.GPT2_BF16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("B,NH", [(70, 20), (150, 14)])
+def test_long_prefix_with_rising_scores(precision, B, NH):
+    P = 2000
+    c = long_case(precision, B, NH, P, own_of(B, 30, 3), 16, seed=4, qscale=1.0)
+    blk, at = c["table"][0, :P // 16].long().repeat_interleave(16), torch.arange(P) % 16
+    c["pool"][0, blk, 0, at] = torch.linspace(0.2, 8.0, P)[:, None].expand(P, 64).to(c["pool"].dtype)
+    c["qkv"].view(B, 3, NH, 64)[:, 0, 0] = 1.0
+    c["pool"][0, c["table"][0, 1850 // 16].long(), 1, 1850 % 16] *= 6
+    check(c)
+
+
+@pytest.mark.parametrize("precision", [ab.GPT2_FP16, ab.GPT2_BF16], ids=["fp16", "bf16"])
+def test_long_prefix_reads_nothing_behind_it(precision):
+    """NaN in every slot that no position reaches, the rest of the prefix's
+    last block among them."""
+    P, B, NH = 2001, 70, 20
+    c = long_case(precision, B, NH, P, own_of(B, 9, 2), 16, seed=7)
+    used = torch.zeros(c["pool"].shape[1], 16, dtype=torch.bool)
+    for b in range(B):
+        j = torch.arange(0 if b == 0 else P, int(c["pos"][b]) + 1)
+        used[c["table"][b].long()[j // 16], j % 16] = True
+    c["pool"].permute(1, 3, 0, 2, 4)[~used] = float("nan")
+    out, _ = run(c)
+    ref, tol = reference(c)
+    assert (np.abs(out.double().numpy().reshape(ref.shape) - ref) <= tol).all()
+    no_device_error()
+
+
+def test_long_prefix_flags_bad_blocks_and_positions():
+    P, B, NH = 2000, 130, 14
+    c = long_case(ab.GPT2_FP16, B, NH, P, own_of(B, 20, 1), 16, seed=3)
+    good = run(c)[0]
+    for value in (-1, 10**6):
+        bad = dict(c, table=c["table"].clone())
+        bad["table"][0, 60] = value
+        run(bad)
+        assert ab.gpt2_get_error() == ab.DEVERR_BLOCK
+    bad = dict(c, pos=c["pos"].clone())
+    bad["pos"][[0, 64, 128]] = torch.tensor([P - 1, -1, 2**31 - 1], dtype=torch.int32)
+    out, _ = run(bad)
+    assert ab.gpt2_get_error() == ab.DEVERR_POSITION
+    rest = torch.ones(B, dtype=torch.bool)
+    rest[[0, 64, 128]] = False
+    assert (out[~rest] == 0).all() and torch.equal(out[rest], good[rest])
+
+
+@pytest.mark.parametrize("B", [70, 130])
+def test_long_prefix_repeats_streams_and_graphs(B):
+    c = long_case(ab.GPT2_BF16, B, 20, 2000, own_of(B, 9, 5), 16, seed=6)
+    first = run(c)[0]
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        assert torch.equal(run(c)[0], first)
+    g = {k: c[k].cuda() for k in ("pool", "qkv", "table", "pos")}
+    nb = ab.attention_shared_prefix_workspace_size(B + 100, 20 * 64, 20, 9000, ab.GPT2_BF16)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    out = torch.zeros(B, 20 * 64, dtype=torch.bfloat16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(c, g["pool"], g["qkv"], g["table"], g["pos"], out, ws=ws)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), first)
+    no_device_error()
+
+
 # ------------------------------------------------------------- the model
 LOGIT_TOL = {ab.GPT2_BF16: 2e-2, ab.GPT2_FP16: 2e-2, ab.GPT2_TF32: 2e-2, ab.GPT2_FP32: 1e-4}
 

@@ -101,6 +101,24 @@ def test_shared_prefix_sizes():
     assert ab.gpt2_shared_workspace_size(cfg, 3, -1, ab.GPT2_FP16) == 0
 
 
+@pytest.mark.parametrize("NH", [1, 4, 12, 16])
+def test_shared_prefix_sizes_where_the_kernel_changes(NH):
+    # 16-bit caches with heads of 64: the kernel, and with it the splits, goes
+    # by the batch and by batch x heads x prefix
+    size = ab.attention_shared_prefix_workspace_size
+    lengths = sorted({int(257 * 1.17 ** i) for i in range(34)} | {-(-5000000 // (r * NH)) + d for r in (128, 192, 256, 320)
+                                                                 for d in (-1, 0, 1)})
+    batches = (1, 33, 64, 65, 100, 128, 129, 192, 200, 256, 257, 300)
+    got = {(B, P): size(B, 64 * NH, NH, P, ab.GPT2_BF16) for B in batches for P in lengths}
+    for B in batches:
+        for k, P in enumerate(lengths):
+            assert got[B, P] > 0
+            assert k == 0 or got[B, lengths[k - 1]] <= got[B, P], (B, lengths[k - 1], P)
+    for P in lengths:
+        for k in range(1, len(batches)):
+            assert got[batches[k - 1], P] <= got[batches[k], P], (batches[k - 1], batches[k], P)
+
+
 def step_args(**kw):
     d = dict(cfg=inputs.TINY, params=FAKE, packed=FAKE, kv=ab.paged_kv(FAKE, FAKE, 64, 16, 4), tok=FAKE, pos=FAKE, B=4,
              prefix_len=32, logits=FAKE, probs=None, workspace=FAKE, ws_bytes=1 << 30, precision=ab.GPT2_FP16)
