@@ -32,15 +32,18 @@ constexpr int kDirectLen = 256;
 constexpr long long kDirectBytes = 8LL << 20;
 // The tcgen05 kernel (head size 64) takes over for 65 sequences or more and
 // this many pairs of a query row (rows in tiles of 64) and a shared position: it
-// costs about 4 us more to begin and end, and less per pair.  Prefix part, own
-// positions and join, mma.sync against tcgen05, us: 12 heads, 96 sequences,
+// costs about 4 us more to begin and end, and less per pair.  Whole calls with
+// up to 32 own positions, mma.sync against tcgen05, us: 12 heads, 96 sequences,
 // prefix 960 (1.5 million pairs) 8.1 against 10.1, 4000 (6.1) 12.6 against 11.7;
-// 256 sequences, 960 (2.9) 11.0 against 12.8, 2000 (6.1) 14.2 against 14.5, 4000
-// (12.3) 18.8 against 15.2; 4 heads, 256 sequences, 4000 (4.1) 10.0 against 10.6,
-// 8000 (8.2) 14.3 against 11.6; 16 heads, 129 sequences, 960 (2.9) 10.2 against
-// 10.9, 2000 (6.1) 13.6 against 12.0.
+// 4 heads, 256 sequences, 4000 (4.1) 10.0 against 10.6, 8000 (8.2) 14.3 against
+// 11.6; 16 heads, 129 sequences, 960 (2.9) 9.9 against 10.9, 256 sequences, 2000
+// (8.2) 18.1 against 16.5.  The own positions' lengths, which only the device
+// knows, count too: over a short prefix tcgen05 has few CTAs, and the SMs it
+// leaves attend to own positions meanwhile (12 heads, 128 sequences, prefix 512:
+// own 1 5.4 against 7.5, own 64 10.7 against 9.3).
 constexpr int kTcMinBatch = 65;
 constexpr long long kTcMinPairs = 5000000;
+constexpr long long kRoomyPairs = 3000000;  // below: mma.sync with two CTAs an SM (plan_of)
 
 // How a shape is cut: the kernel, queries per CTA, keys per step of a CTA,
 // splits of the prefix over CTAs, positions per split (a multiple of the step)
@@ -65,7 +68,10 @@ int simt_rows(int B) { return B <= 8 ? 1 : B <= 16 ? 2 : B <= 32 ? 4 : 8; }
 long long tc_pairs(int B, int NH) { return static_cast<long long>((B + 63) / 64 * 64) * NH; }
 
 // Splits: the CTAs that fit the SMs at once (the tcgen05 kernel one an SM, the
-// CUDA-core kernel two, mma.sync three), or in two rounds where these come out
+// CUDA-core kernel two, mma.sync three, but two where many sequences share a
+// short prefix, which leaves registers for the kernel of the own positions to
+// run beside it: 12 heads, 128 sequences, prefix 960, 64 own positions 10.4 us
+// against 12.0; with 4 heads and prefix 8000 11.5 against 9.9), or in two rounds where these come out
 // more even: a round lasts its splits' steps and about as long as `start` steps
 // to begin and end.  The count goes by the shape alone, not by the device: it
 // sizes the caller's workspace.
@@ -76,7 +82,8 @@ Plan plan_of(int B, int NH, int hs, int prefix_len, bool is16, int* wanted = nul
     if (wanted != nullptr) *wanted = 0;
     return p;
   }
-  const bool tc = is16 && hs == 64 && B >= kTcMinBatch && tc_pairs(B, NH) * prefix_len >= kTcMinPairs;
+  const long long pairs = tc_pairs(B, NH) * prefix_len;
+  const bool tc = is16 && hs == 64 && B >= kTcMinBatch && pairs >= kTcMinPairs;
   p.kernel = !is16 ? kSimt : tc ? kTc05 : kMma;
   p.parts = 1;
   if (p.kernel == kTc05) {
@@ -88,7 +95,9 @@ Plan plan_of(int B, int NH, int hs, int prefix_len, bool is16, int* wanted = nul
     p.step_k = is16 ? kTileK * (4 / row_groups(B)) : kTileK;
   }
   const long long tiles = static_cast<long long>((B + p.tile_q - 1) / p.tile_q) * NH;
-  const long long slots = 152LL * (p.kernel == kTc05 ? 1 : p.kernel == kSimt ? 2 : 3), start = p.kernel == kSimt ? 1 : 3;
+  const bool roomy = p.kernel == kMma && B >= kTcMinBatch && pairs < kRoomyPairs;
+  const long long slots = 152LL * (p.kernel == kTc05 ? 1 : p.kernel == kSimt || roomy ? 2 : 3);
+  const long long start = p.kernel == kSimt ? 1 : 3;
   const long long steps = (prefix_len + p.step_k - 1) / p.step_k;
   long long n = 1, best = 0;
   for (long long rounds = 1; rounds <= 2; ++rounds) {
@@ -530,6 +539,12 @@ cudaError_t allow_smem(bool (&allowed)[kMaxDevices], Kernel kern, int bytes) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && dev < kMaxDevices && !allowed[dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // an SM that is split between shared memory and L1 in another way must run
+    // empty before a kernel that wants more starts there: the own positions
+    // would wait for the prefix (128 sequences, 12 heads, prefix 512, 32 own
+    // positions: 9.2 us against 7.6)
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     allowed[dev] = e == cudaSuccess;
   }
   return e;

@@ -106,8 +106,8 @@ def test_shared_prefix_sizes_where_the_kernel_changes(NH):
     # 16-bit caches with heads of 64: the kernel, and with it the splits, goes
     # by the batch and by batch x heads x prefix
     size = ab.attention_shared_prefix_workspace_size
-    lengths = sorted({int(257 * 1.17 ** i) for i in range(34)} | {-(-5000000 // (r * NH)) + d for r in (128, 192, 256, 320)
-                                                                 for d in (-1, 0, 1)})
+    lengths = sorted({int(257 * 1.17 ** i) for i in range(34)} | {-(-n // (r * NH)) + d for n in (3000000, 5000000)
+                                                                 for r in (128, 192, 256, 320) for d in (-1, 0, 1)})
     batches = (1, 33, 64, 65, 100, 128, 129, 192, 200, 256, 257, 300)
     got = {(B, P): size(B, 64 * NH, NH, P, ab.GPT2_BF16) for B in batches for P in lengths}
     for B in batches:
