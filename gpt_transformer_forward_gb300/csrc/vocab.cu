@@ -4,7 +4,7 @@
 // HBM bounds both for many rows: 4096 rows of 50257 fp32 logits take 117 us (7.0
 // TB/s, above the measured copy bandwidth, which counts writes), 125 us with one
 // alternative, 131 us with 20, and the gradient 246 us (6.7 TB/s).  Few rows are
-// bound by latency: one row 2.6 us, with 20 alternatives 5.4 us (about 2500
+// bound by latency: one row 2.6 us, with 20 alternatives 5.5 us (about 2500
 // cycles to load its part of the row, 3500 to search it, 3500 to join the
 // blocks of the cluster and write).  16-bit rows halve the bytes but not the
 // instructions: 4096 of bf16 72 us, with 20 alternatives 96 us.
