@@ -450,18 +450,22 @@ __global__ void __launch_bounds__(kThreads) prefix_mma_kernel(float* __restrict_
         }
       }
       // O += P V: P's accumulator layout is the A-operand layout of k-steps.
-      // Its values, at most 1, are rounded to the operands' type
+      // Its values, at most 1, enter as sums of two values of the operands'
+      // type: rounded to one, they lost what the decode attention that does
+      // not share a prefix keeps
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        uint32_t pa[4];
-        pa[0] = pack2<T16>(s[2 * ks][0], s[2 * ks][1]);
-        pa[1] = pack2<T16>(s[2 * ks][2], s[2 * ks][3]);
-        pa[2] = pack2<T16>(s[2 * ks + 1][0], s[2 * ks + 1][1]);
-        pa[3] = pack2<T16>(s[2 * ks + 1][2], s[2 * ks + 1][3]);
+        uint32_t pa[4], pl[4];
+        split2<T16>(s[2 * ks][0], s[2 * ks][1], pa[0], pl[0]);
+        split2<T16>(s[2 * ks][2], s[2 * ks][3], pa[1], pl[1]);
+        split2<T16>(s[2 * ks + 1][0], s[2 * ks + 1][1], pa[2], pl[2]);
+        split2<T16>(s[2 * ks + 1][2], s[2 * ks + 1][3], pa[3], pl[3]);
 #pragma unroll
         for (int dp = 0; dp < kDT / 2; ++dp) {
           uint32_t r0, r1, r2, r3;
           ldsm_x4_t(vb + swz<HS>(ks * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), dp * 2 + (lane >> 4)), r0, r1, r2, r3);
+          mma16<T16>(o[2 * dp], pl, r0, r1);
+          mma16<T16>(o[2 * dp + 1], pl, r2, r3);
           mma16<T16>(o[2 * dp], pa, r0, r1);
           mma16<T16>(o[2 * dp + 1], pa, r2, r3);
         }

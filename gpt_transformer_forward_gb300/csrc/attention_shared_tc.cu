@@ -7,8 +7,9 @@
 // 128 keys, as the forward attention kernel computes them (attention_tc.cu,
 // whose hand-offs this kernel keeps: three S accumulators in TMEM that P is
 // written over, one warp issuing S, one issuing P V, a thread per query row, a
-// rescale only where a row's maximum grows by more than 2^8).  No mask but the
-// end of the prefix.  A CTA takes one split of one head and runs two softmax
+// rescale only where a row's maximum grows by more than 2^8).  P enters P V as
+// hi + lo, two values of the operand type: twice the products of P V for what
+// one rounded value loses.  No mask but the end of the prefix.  A CTA takes one split of one head and runs two softmax
 // groups of 128 threads:
 //   more than 128 sequences: both groups see every key tile, group x with
 //   query tile x (256 queries, each key tile loaded once for them);
@@ -25,12 +26,13 @@
 // Every wait is bounded; after a timeout the CTA drains its copies and MMAs,
 // frees TMEM and returns.
 //
-// Measured: 256 sequences, 16 heads, prefix 16384 (17.2 GFLOP, 67 MB): 29 us,
-// 590 TFLOP/s, exponential unit and tensor pipe 33 % busy each: as in the forward
-// kernel, the cycle of a score buffer (exponentials, P V, the next S and their
-// hand-offs) sets the pace.  Four softmax groups of 64-key tiles with an S
+// Measured: 256 sequences, 16 heads, prefix 16384 (17.2 GFLOP, 67 MB), the whole
+// call with up to 255 own positions 65 us; with P rounded to one value 56, of
+// which this kernel 29, exponential unit and tensor pipe 33 % busy each: as in
+// the forward kernel, the cycle of a score buffer (exponentials, P V, the next S and their
+// hand-offs) sets the pace.  (Then four softmax groups of 64-key tiles with an S
 // buffer each were slower, with one issuing warp for S and one for P V (39 us)
-// and with an issuing warp a group (36 us).
+// and with an issuing warp a group (36 us).)
 #include "serve.cuh"
 
 namespace gpt2 {
@@ -253,9 +255,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t vdsc = smem_desc_sw128_mn(smem_u32(smem + L::v + (j % kKV) * kTileBytes), 1024);
         const bool first = s < st.groups;
 #pragma unroll
-        for (int kk = 0; kk < kTK / 16; ++kk)  // P: 16 keys = 8 TMEM columns; V: 16 rows of 128 bytes
-          tc_mma_ts_warp(tmem + kTmemO + x * kHS, p_tmem + kk * 8, vdsc + kk * (2048 / 16), kIdescPV,
+        for (int kk = 0; kk < kTK / 16; ++kk) {  // P: 16 keys = 8 TMEM columns; V: 16 rows of 128 bytes
+          const uint32_t p = p_tmem + (kk >> 1) * 32 + (kk & 1) * 8;  // 32 keys: 16 columns of hi, 16 of lo
+          tc_mma_ts_warp(tmem + kTmemO + x * kHS, p + 16, vdsc + kk * (2048 / 16), kIdescPV,
                          (!first || kk > 0) ? 1u : 0u);
+          tc_mma_ts_warp(tmem + kTmemO + x * kHS, p, vdsc + kk * (2048 / 16), kIdescPV, 1u);
+        }
         tc_commit_warp(&o_done[s % kRing]);
         if (s + st.groups >= st.count()) tc_commit_warp(&o_final[x]);
         if (st.last_user(s)) tc_commit_warp(&kv_empty[j % kKV]);
@@ -283,10 +288,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_live = (valid + 31) >> 5;
       const int s_prev = i > 0 ? st.step(x, i - 1) : 0;
       float2 sum2 = make_float2(0.f, 0.f);
-      auto store_p = [&](int c, const uint32_t(&pk)[16]) { tmem_st_32x32b_x16(lane_base + s_col + 16 * c, pk); };
-      // p = exp2(s * scale - m) of 32 keys, rounded to the operand type into
-      // P, and their fp32 sum; a chunk that sums above 2^8 in some row is
-      // neither stored nor summed and the function returns false
+      // 32 keys' P over their scores: 16 columns of hi, 16 of lo
+      auto store_p = [&](int c, const uint32_t(&pk)[32]) { tmem_st_32x32b_x32(lane_base + s_col + 32 * c, pk); };
+      // p = exp2(s * scale - m) of 32 keys into P, each as the sum hi + lo of
+      // two values of the operand type (rounded to one, it lost what the decode
+      // attention that does not share a prefix keeps), and their fp32 sum; a
+      // chunk that sums above 2^8 in some row is neither stored nor summed and
+      // the function returns false
       auto softmax_chunk = [&](int c, const uint32_t(&cur)[32], bool check, auto full) -> bool {
         constexpr bool kFull = decltype(full)::value;
         const float2 sc = make_float2(a.scale_log2, a.scale_log2), nm = make_float2(-m_run, -m_run);
@@ -302,12 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         float2 sq[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t pk[16];
+        uint32_t pk[32];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float2 p = make_float2(exp2_approx(xv[e].x), exp2_approx(xv[e].y));
           sq[e & 3] = __fadd2_rn(sq[e & 3], p);
-          pk[e] = pack2<T16>(p.x, p.y);
+          split2<T16>(p.x, p.y, pk[e], pk[16 + e]);
         }
         const float2 cs = __fadd2_rn(__fadd2_rn(sq[0], sq[1]), __fadd2_rn(sq[2], sq[3]));
         if (check && __any_sync(0xffffffffu, cs.x + cs.y > kRescaleSum)) return false;
@@ -333,9 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr bool kFull = decltype(full)::value;
           if (!go) return;
           if (!kFull && c >= n_live) {
-            uint32_t pk[16];
+            uint32_t pk[32];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] = 0u;
+            for (int e = 0; e < 32; ++e) pk[e] = 0u;
             store_p(c, pk);
             return;
           }
@@ -399,13 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_wait();  // the P chunks written so far are readable
 #pragma unroll 1
           for (int c = 0; c < fail; ++c) {
-            uint32_t pk[16];
-            tmem_ld_32x32b_x16(lane_base + s_col + 16 * c, pk);
-            tmem_ld_wait();
+            uint32_t pk[32];
+            tmem_ld_32x32b_x32(lane_base + s_col + 32 * c, pk);
+            tmem_ld_wait_regs(pk);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float2 v = unpack2<T16>(pk[e]);
-              pk[e] = pack2<T16>(v.x * alpha, v.y * alpha);
+              const float2 v = unpack2<T16>(pk[e]), w = unpack2<T16>(pk[16 + e]);
+              split2<T16>((v.x + w.x) * alpha, (v.y + w.y) * alpha, pk[e], pk[16 + e]);
             }
             store_p(c, pk);
           }

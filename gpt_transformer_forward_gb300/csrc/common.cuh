@@ -661,6 +661,17 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
   }
 }
 
+// Two floats as the sums hi + lo of two values of type T each, packed as by
+// pack2: off by half a step of T twice over (2^-16 relative for bf16; for fp16
+// 2^-22, or half its smallest step, 2^-25, where that is more).  Finite floats
+// within T's range.
+template <typename T>
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack2<T>(x, y);
+  const float2 h = unpack2<T>(hi);
+  lo = pack2<T>(x - h.x, y - h.y);
+}
+
 template <typename T>
 __device__ __forceinline__ T from_f32(float x) {
   if constexpr (std::is_same<T, float>::value)

@@ -111,8 +111,9 @@ GPT2_API size_t attention_shared_prefix_workspace_size(int B, int C, int NH, int
  *   block_size positions, and 2^30.  qkv [B,3C], out [B,C] and the slab have one
  *   element type: fp32 in GPT2_FP32 and GPT2_TF32 (both fp32 arithmetic), the
  *   16-bit type in GPT2_BF16 and GPT2_FP16 (the products over the prefix on
- *   tensor cores with fp32 accumulation, its probabilities rounded to the
- *   16-bit type).
+ *   tensor cores with fp32 accumulation, its probabilities as sums of two
+ *   values of the 16-bit type: off by 2^-16 relative in bf16, by 2^-22 or an
+ *   absolute 2^-25 in fp16).
  * Head size 16, 32 or 64.  pos: DEVICE int32 [B]; a pos[b] outside
  * [prefix_len, capacity) sets GPT2_DEVERR_POSITION_BIT, leaves the cache
  * unwritten and gives a zero row.  A reached table entry outside [0,
@@ -128,9 +129,9 @@ GPT2_API int attention_shared_prefix(void* out, const void* qkv, const GPT2Paged
 GPT2_API size_t gpt2_shared_workspace_size(const GPT2Config* cfg, int B, int prefix_len, int precision);
 
 /* gpt2_decode_step_paged for sequences that share their first prefix_len
- * positions (attention_shared_prefix in every layer): the same cache, table,
- * positions and results, the prefix's keys and values read once a layer
- * instead of once a sequence.  0 <= prefix_len < the capacity of a sequence
+ * positions (attention_shared_prefix in every layer): the same cache, table
+ * and positions, and the same results but for another order of fp32 sums, the
+ * prefix's keys and values read once a layer instead of once a sequence.  0 <= prefix_len < the capacity of a sequence
  * (0: nothing is shared).  Workspace of gpt2_shared_workspace_size bytes. */
 GPT2_API int gpt2_decode_step_shared(const GPT2Config* cfg, const float* params, const void* packed,
                                      const GPT2PagedKVCache* kv, const int* tok, const int* pos, int B, int prefix_len,

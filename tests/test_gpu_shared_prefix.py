@@ -345,6 +345,48 @@ def test_long_prefix_repeats_streams_and_graphs(B):
     no_device_error()
 
 
+# ------------------------------------------- the prefix's probabilities
+@pytest.mark.parametrize("precision", [ab.GPT2_FP16, ab.GPT2_BF16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("B,NH,P", [(3, 5, 700), (40, 4, 1000), (70, 20, 2000), (150, 14, 2000)])
+def test_probabilities_keep_more_than_16_bits(precision, B, NH, P):
+    """Few keys dominate and the values' signs cancel, so that what the
+    probabilities lose shows beside the output's own rounding.  Keys and queries
+    are nonzero in one dimension: a score is one product (its factor of log2
+    units and the subtracted maximum: 4 u |s| more).  Probabilities enter the
+    products as the sum of two 16-bit values, off by w^2 relative, or in fp16 by
+    2^-25 (half its smallest step) where that is more, but never by more than
+    themselves."""
+    hs, bs = 64, 16
+    c = make(precision, B, NH, hs, P, own_of(B, 20, B), bs, seed=B, qscale=1.0)
+    g = torch.Generator().manual_seed(B + P)
+    rank = torch.stack([torch.randperm(P, generator=g) for _ in range(NH)])  # [NH, P]
+    blk, at = c["table"][0].long()[torch.arange(P) // bs], torch.arange(P) % bs
+    c["pool"][0] = 0
+    c["pool"][0, blk, :, at, 0] = (-4.0 * rank.clamp(max=60)).t().to(c["pool"].dtype)  # whole numbers: exact
+    c["pool"][1] = torch.randint(0, 2, c["pool"][1].shape, generator=g).to(c["pool"].dtype) * 2 - 1
+    if P % bs:
+        mine = c["table"][:, P // bs].long()
+        c["pool"][:, mine, :, :P % bs] = c["pool"][:, mine[:1], :, :P % bs].clone()
+    x = c["qkv"].view(B, 3, NH, hs)
+    x[:, :2] = 0
+    x[:, 0, :, 0] = torch.tensor([0.5, 1.0, 0.75])[torch.arange(B) % 3][:, None].to(x.dtype)
+    x[:, 1, :, 0] = -48
+    out, _ = run(c)
+    no_device_error()
+    q, k, v = c["qkv"].double().numpy().reshape(B, 3, NH, hs).transpose(1, 0, 2, 3)
+    ref, sabs, vmax = shared_attention(q, k, v, c["pool"].double().numpy(), c["table"].numpy(), c["pos"].numpy(), P, bs)
+    w = HALF[DT[precision]]
+    n = c["pos"].numpy()[:, None] + 1
+    lost = np.full((B, NH), w * w)
+    if precision == ab.GPT2_FP16:
+        s = q[:, :, 0][:, :, None] * (-4.0 * rank.clamp(max=60)).numpy() / 8  # [B, NH, P]
+        lost += np.minimum(np.exp(s), 2.0 ** -25).sum(2)  # the largest is 0
+    tol = (2 * 5 * u * sabs + 8 * u + (n / 16 + 64) * u + lost) * vmax
+    tol = tol[..., None] + w * np.abs(ref)
+    err = np.abs(out.double().numpy().reshape(ref.shape) - ref)
+    assert (err <= tol).all(), f"{(err > tol).sum()} off, worst {(err / tol).max():.3f} of the tolerance"
+
+
 # ------------------------------------------------------------- the model
 LOGIT_TOL = {ab.GPT2_BF16: 2e-2, ab.GPT2_FP16: 2e-2, ab.GPT2_TF32: 2e-2, ab.GPT2_FP32: 1e-4}
 
