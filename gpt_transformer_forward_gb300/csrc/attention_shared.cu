@@ -723,11 +723,18 @@ __global__ void __launch_bounds__(32 * join_warps_per_block(W))
       const uint4 kn = __ldg(reinterpret_cast<const uint4*>(qrow + C)), vn = __ldg(reinterpret_cast<const uint4*>(qrow + 2 * C));
       const float d = dot(kn);
       raise(fmaxf(m, d));
-      const size_t at = row_at(entry(pos), pos) * HS + dg * kPer;
+      // A bad entry is read as block 0, but nothing is stored through it: that
+      // block is another sequence's, or the prefix's, which is being read.
+      const int blk = __ldg(table + (pos >> rows.lbs));
+      const bool in = blk >= 0 && blk < rows.num_blocks;
+      if (!in && h == 0) set_error(GPT2_DEVERR_BLOCK);
       if (g == 0) {
         take(exp2_approx(d - m), vn);
-        *reinterpret_cast<uint4*>(kcache + at) = kn;
-        *reinterpret_cast<uint4*>(vcache + at) = vn;
+        if (in) {
+          const size_t at = row_at(blk, pos) * HS + dg * kPer;
+          *reinterpret_cast<uint4*>(kcache + at) = kn;
+          *reinterpret_cast<uint4*>(vcache + at) = vn;
+        }
       }
     }
   };

@@ -117,7 +117,8 @@ GPT2_API size_t attention_shared_prefix_workspace_size(int B, int C, int NH, int
  * Head size 16, 32 or 64.  pos: DEVICE int32 [B]; a pos[b] outside
  * [prefix_len, capacity) sets GPT2_DEVERR_POSITION_BIT, leaves the cache
  * unwritten and gives a zero row.  A reached table entry outside [0,
- * num_blocks) sets GPT2_DEVERR_BLOCK_BIT (block 0 is used).  Sequences'
+ * num_blocks) sets GPT2_DEVERR_BLOCK_BIT: block 0 is read in its place, and at
+ * pos[b] nothing is appended.  Sequences'
  * positions pos[b] lie in blocks of their own.  out must not alias qkv.
  * Workspace: 16-byte aligned, attention_shared_prefix_workspace_size bytes. */
 GPT2_API int attention_shared_prefix(void* out, const void* qkv, const GPT2PagedKVCache* kv, const int* pos, int B,

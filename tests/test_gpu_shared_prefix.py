@@ -199,6 +199,32 @@ def test_bad_blocks(precision, where):
         assert ab.gpt2_get_error() == ab.DEVERR_BLOCK
 
 
+@pytest.mark.parametrize("precision", ALL, ids=[NAMES[p] for p in ALL])
+@pytest.mark.parametrize("B,NH,P", [(4, 2, 96), (4, 2, 688), (70, 40, 1008)])
+def test_nothing_is_appended_through_a_bad_entry(precision, B, NH, P):
+    """A sequence at a block border whose next entry is missing (the state of a
+    request that waits for a block), or past the pool: the cache keeps every
+    other sequence's positions and its own, and no output changes."""
+    own = own_of(B, 40, 3)
+    own[2] = 32
+    c = make(precision, B, NH, 64, P, own, 16, seed=5)
+    good = check(c)
+    for value in (-1, c["pool"].shape[1], -2**31):
+        bad = dict(c, table=c["table"].clone())
+        bad["table"][2, (P + 32) // 16] = value
+        out, pool = run(bad)
+        assert ab.gpt2_get_error() == ab.DEVERR_BLOCK
+        assert torch.equal(out, good)  # the new token's key and value come from qkv
+        want = c["pool"].clone()
+        k, v = c["qkv"].view(B, 3, NH, 64)[:, 1:].unbind(1)
+        for b in range(B):
+            if b != 2:
+                at = int(c["pos"][b])
+                blk = int(c["table"][b, at // 16])
+                want[0, blk, :, at % 16], want[1, blk, :, at % 16] = k[b], v[b]
+        assert torch.equal(pool, want)
+
+
 def test_entries_that_are_not_reached_may_hold_anything():
     # rows other than 0 over the prefix's whole blocks
     c = make(ab.GPT2_FP16, 5, 2, 64, 96, [4, 0, 30, 2, 9], 16, seed=3)
