@@ -368,7 +368,12 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
     }
     fence_barrier_init();
   }
+  // A bad table entry is read as block 0, but the new token's key and value are
+  // not stored through it: block 0 is another sequence's.
+  bool append = pos_ok;
   if (rows.table != nullptr && pos_ok) {
+    const int last = __ldg(rows.table + static_cast<size_t>(b) * rows.max_blocks + (pos >> rows.lbs));
+    append = last >= 0 && last < rows.num_blocks;
     for (int i = threadIdx.x; i <= (pos >> rows.lbs); i += blockDim.x) {
       int blk = __ldg(rows.table + static_cast<size_t>(b) * rows.max_blocks + i);
       if (blk < 0 || blk >= rows.num_blocks) {
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1))
     // this token's key and value: used for position pos, and appended
     const uint4* kq = reinterpret_cast<const uint4*>(qkv + static_cast<size_t>(b) * 3 * C + C + h * HS) + dg;
     const uint4* vq = reinterpret_cast<const uint4*>(qkv + static_cast<size_t>(b) * 3 * C + 2 * C + h * HS) + dg;
-    if (threadIdx.x < kLPR) {
+    if (threadIdx.x < kLPR && append) {
       reinterpret_cast<uint4*>(kcache + row(pos) * HS)[dg] = __ldg(kq);
       reinterpret_cast<uint4*>(vcache + row(pos) * HS)[dg] = __ldg(vq);
     }

@@ -367,7 +367,8 @@ GPT2_API int gpt2_adamw(float* params, const float* grads, float* m, float* v, s
  *                sequence b is in block block_table[b][p / block_size],
  *                slot p % block_size.  Entries a call never reaches may hold
  *                anything; an entry it reaches outside [0, num_blocks) sets
- *                GPT2_DEVERR_BLOCK_BIT (block 0 is used instead).
+ *                GPT2_DEVERR_BLOCK_BIT (block 0 is read instead, and nothing
+ *                is stored through it).
  *   block_size:  positions per block, a power of two;
  *   max_blocks_per_seq: row length of block_table, 1 .. 1024.
  * A sequence can hold min(maxT, max_blocks_per_seq * block_size)

@@ -146,3 +146,35 @@ def test_paged_flags_bad_table_entries_and_positions():
     m.decode_step_paged(kv, dev(np.zeros(B, np.int32)), dev(pos), out)
     assert ab.gpt2_get_error() & ab.DEVERR_POSITION
     assert ab.gpt2_get_error() == 0  # read and cleared; the device stays usable
+
+
+@pytest.mark.parametrize("precision", [ab.GPT2_FP32, ab.GPT2_TF32, ab.GPT2_BF16, ab.GPT2_FP16],
+                         ids=["fp32", "tf32", "bf16", "fp16"])
+def test_nothing_is_appended_through_a_bad_entry(precision):
+    """A sequence at a block border whose next table entry is missing or past
+    the pool: every other position of the pool stays, and so do the others'
+    logits."""
+    cfg = inputs.TINY
+    B, P = 4, 16
+    m = GPT2Model(cfg, inputs.make_params(cfg, 133), B, P, precision)
+    kv, (pool, table) = paged(m, B, 16, 0, 134)
+    lg, _ = m.new_outputs(B, P, probs=False)
+    m.prefill_paged(dev(inputs.make_tokens(135, B, P, cfg.vocab_size)), lg, kv)
+    before = pool.clone()
+    tok, pos = dev(np.arange(B, dtype=np.int32)), dev(np.full(B, P, np.int32))
+    good, _ = m.new_outputs(B, None, probs=False)
+    m.decode_step_paged(kv, tok, pos, good)
+    no_device_error()
+    e = 2 if precision in (ab.GPT2_BF16, ab.GPT2_FP16) else 4
+    view = lambda p: p.view(cfg.num_layers, 2, kv.num_blocks, cfg.num_heads, 16, -1)  # noqa: E731
+    assert view(pool).shape[-1] == cfg.head_size * e
+    want, missing = pool.clone(), int(table[2, 1])
+    view(want)[:, :, missing, :, 0] = view(before)[:, :, missing, :, 0]
+    for value in (-1, kv.num_blocks):
+        pool.copy_(before)
+        table[2, 1] = value
+        out, _ = m.new_outputs(B, None, probs=False)
+        m.decode_step_paged(kv, tok, pos, out)
+        assert ab.gpt2_get_error() == ab.DEVERR_BLOCK
+        assert torch.equal(pool, want)
+        assert torch.equal(out, good)
