@@ -81,8 +81,10 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(TableArgs a, 
       return __ldg(a.free_blocks + taken + start + (j - r.have));
     };
     const int t0 = sub * 32 + lane, step = wpr * 32;
+    // the shared positions' entries, whatever is granted: a decode step over
+    // the shared prefix reads them through row 0, also where that one waits
+    for (int j = t0; j < n_pre; j += step) row[j] = __ldg(a.prefix_blocks + j);
     if (ok) {
-      for (int j = t0; j < n_pre; j += step) row[j] = block_of(j);
       for (int j = r.have + t0; j < r.have + r.want; j += step) row[j] = block_of(j);
     }
     if (a.slots != nullptr) {

@@ -45,9 +45,10 @@ extern "C" {
  *   free_blocks[taken_in[0] + end[b] - (need - have) + i],  i = 0, 1, ...;
  * slots[b][t] = block * bs + offset of position cached_len[b] + t for t <
  * new_len[b] (-1 for t >= new_len[b]); next_len[b] = cached_len[b] +
- * new_len[b].  A request that does not get its blocks keeps its row and its
- * length (next_len[b] = cached_len[b]) and its slots are -1: the caller sees
- * by next_len who has to wait.  taken_out[0] = taken_in[0] + the blocks
+ * new_len[b].  A request that does not get its blocks keeps its row (but for
+ * the shared prefix's entries, below) and its length (next_len[b] =
+ * cached_len[b]) and its slots are -1: the caller sees by next_len who has to
+ * wait.  taken_out[0] = taken_in[0] + the blocks
  * given, always a prefix of the free blocks that were left.
  *   block_table  int32 [B][max_blocks_per_seq], updated in place
  *   slots        int32 [B][T] or NULL; next_len int32 [B] or NULL;
@@ -61,8 +62,9 @@ extern "C" {
  *   prefix_blocks, prefix_len: prefix_len > 0 (a multiple of block_size):
  *                every request's first prefix_len positions are the shared
  *                ones in these prefix_len / block_size blocks (int32, DEVICE),
- *                which are written to the granted rows; cached_len counts
- *                them.  NULL and 0 otherwise.
+ *                which are written to every row, granted or not
+ *                (attention_shared_prefix reads them through row 0);
+ *                cached_len counts them.  NULL and 0 otherwise.
  * On the device: a negative length, new_len[b] > T, a sequence past
  * max_blocks_per_seq * block_size positions, or cached_len[b] < prefix_len
  * sets GPT2_DEVERR_POSITION_BIT and refuses the request, which then needs no

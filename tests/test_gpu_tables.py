@@ -176,3 +176,27 @@ def test_another_stream():
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
         check(c)
+
+
+@pytest.mark.parametrize("refused", ["waits", "bad length"])
+def test_every_row_gets_the_shared_prefix(refused):
+    """Request 0 gets nothing while the others, whose last block has room, are
+    granted: its row holds the prefix's blocks all the same, since a decode step
+    over the shared prefix reads them there."""
+    B, bs, P, maxb, num_blocks = 5, 4, 24, 10, 40
+    table = np.full((B, maxb), -1, np.int32)
+    pre = np.arange(30, 30 + P // bs, dtype=np.int32)
+    cached = np.array([P, P + 1, P + 2, P + 3, P + 1], np.int32)
+    table[1:, P // bs] = np.arange(3, 3 + B - 1)
+    new = np.array([1 if refused == "waits" else 2, 1, 1, 1, 0], np.int32)
+    want = table.copy()
+    want[:, :P // bs] = pre
+    t = dev(table)
+    nxt = torch.zeros(B, dtype=torch.int32, device="cuda")
+    slots = torch.zeros(B, 1, dtype=torch.int32, device="cuda")
+    ab.paged_build_tables(t, slots, nxt, None, dev(cached), dev(new), None, 0, None, dev(pre), P, B, 1, num_blocks, bs,
+                          maxb)
+    assert ab.gpt2_get_error() == (0 if refused == "waits" else ab.DEVERR_POSITION)
+    np.testing.assert_array_equal(t.cpu().numpy(), want)
+    np.testing.assert_array_equal(nxt.cpu().numpy(), [P, P + 2, P + 3, P + 4, P + 1])
+    np.testing.assert_array_equal(slots.cpu().numpy()[:, 0], [-1, 13, 18, 23, -1])
