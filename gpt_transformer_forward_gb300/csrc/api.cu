@@ -638,7 +638,8 @@ static int run_forward(const GPT2Config* cfg, const float* params, const void* p
   if (!decode)
     launch_encoder(x, tok, params + po.wte, params + po.wpe, N, T, C, V, s);
   else
-    launch_encoder_pos(x, tok, params + po.wte, params + po.wpe, B, decode_pos, pos_arr, maxT, C, V, s);
+    launch_encoder_pos(x, tok, params + po.wte, params + po.wpe, B, decode_pos, pos_arr, maxT, C, V,
+                       shared != nullptr, s);
   TRY(check_launch());
   TRY(mark(GPT2_STAGE_ENCODER));
 

@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(32 * join_warps_per_block(W))
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
   if (ok) {
     attend();
-  } else if (mine && h == 0 && lane == 0 && w == 0) {
+  } else if (mine && h == 0 && lane == 0 && w == 0 && pos != -1) {  // -1: no token in this step
     set_error(GPT2_DEVERR_POSITION);
   }
   if (late) {

@@ -64,9 +64,10 @@ struct KVRows {
 void launch_encoder(float* out, const int* tok, const float* wte, const float* wpe, int N, int T, int C, int V,
                     cudaStream_t s);
 // Decode-step encoder: row b is token tok[b] at position pos (pos_arr[b]
-// when pos_arr is given; one outside [0, maxT) is flagged and read as 0).
+// when pos_arr is given; one outside [0, maxT) is flagged, but for -1 where
+// idle, and read as 0).
 void launch_encoder_pos(float* out, const int* tok, const float* wte, const float* wpe, int B, int pos,
-                        const int* pos_arr, int maxT, int C, int V, cudaStream_t s);
+                        const int* pos_arr, int maxT, int C, int V, bool idle, cudaStream_t s);
 void launch_layernorm_f32(float* out, float* mean, float* rstd, const float* inp, const float* w, const float* b,
                           int N, int C, cudaStream_t s);
 // LayerNorm writing the 16-bit operand type T (bf16 or fp16)

@@ -53,9 +53,11 @@ __global__ void __launch_bounds__(256) encoder_kernel(float4* __restrict__ out, 
 }
 
 // Decode-step encoder: row b is token tok[b] at position pos (or pos_arr[b]).
+// idle: a position of -1 is a sequence without a token in this step, not a
+// mistake to flag.
 __global__ void encoder_pos_kernel(float4* __restrict__ out, const int* __restrict__ tok,
                                    const float4* __restrict__ wte, const float4* __restrict__ wpe, int B, int pos_all,
-                                   const int* __restrict__ pos_arr, int maxT, int C4, int V) {
+                                   const int* __restrict__ pos_arr, int maxT, int C4, int V, bool idle) {
   pdl_wait();  // tok comes from the argmax before it
   pdl_trigger();
   const int idx = blockIdx.x * blockDim.x + threadIdx.x;
@@ -68,7 +70,7 @@ __global__ void encoder_pos_kernel(float4* __restrict__ out, const int* __restri
   }
   int pos = pos_arr != nullptr ? __ldg(pos_arr + b) : pos_all;
   if (pos < 0 || pos >= maxT) {
-    if (c == 0) set_error(GPT2_DEVERR_POSITION);
+    if (c == 0 && !(idle && pos == -1)) set_error(GPT2_DEVERR_POSITION);
     pos = 0;
   }
   const float4 a = __ldg(wte + static_cast<size_t>(ix) * C4 + c);
@@ -85,12 +87,12 @@ void launch_encoder(float* out, const int* tok, const float* wte, const float* w
 }
 
 void launch_encoder_pos(float* out, const int* tok, const float* wte, const float* wpe, int B, int pos,
-                        const int* pos_arr, int maxT, int C, int V, cudaStream_t s) {
+                        const int* pos_arr, int maxT, int C, int V, bool idle, cudaStream_t s) {
   const int C4 = C / 4;
   const int threads = 256;
   launch_pdl(encoder_pos_kernel, dim3((B * C4 + threads - 1) / threads), dim3(threads), 0, s,
              reinterpret_cast<float4*>(out), tok, reinterpret_cast<const float4*>(wte),
-             reinterpret_cast<const float4*>(wpe), B, pos, pos_arr, maxT, C4, V);
+             reinterpret_cast<const float4*>(wpe), B, pos, pos_arr, maxT, C4, V, idle);
 }
 
 // -------------------------------------------------------------- LayerNorm

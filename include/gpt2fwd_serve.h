@@ -116,9 +116,10 @@ GPT2_API size_t attention_shared_prefix_workspace_size(int B, int C, int NH, int
  *   tensor cores with fp32 accumulation, its probabilities as sums of two
  *   values of the 16-bit type: off by 2^-16 relative in bf16, by 2^-22 or an
  *   absolute 2^-25 in fp16).
- * Head size 16, 32 or 64.  pos: DEVICE int32 [B]; a pos[b] outside
- * [prefix_len, capacity) sets GPT2_DEVERR_POSITION_BIT, leaves the cache
- * unwritten and gives a zero row.  A reached table entry outside [0,
+ * Head size 16, 32 or 64.  pos: DEVICE int32 [B]; -1 is a sequence without a
+ * token in this step (one that waits for a block, or has ended): a zero row,
+ * nothing appended.  Any other pos[b] outside [prefix_len, capacity) sets
+ * GPT2_DEVERR_POSITION_BIT too.  A reached table entry outside [0,
  * num_blocks) sets GPT2_DEVERR_BLOCK_BIT: block 0 is read in its place, and at
  * pos[b] nothing is appended.  Sequences'
  * positions pos[b] lie in blocks of their own.  out must not alias qkv.
@@ -132,10 +133,16 @@ GPT2_API int attention_shared_prefix(void* out, const void* qkv, const GPT2Paged
 GPT2_API size_t gpt2_shared_workspace_size(const GPT2Config* cfg, int B, int prefix_len, int precision);
 
 /* gpt2_decode_step_paged for sequences that share their first prefix_len
- * positions (attention_shared_prefix in every layer): the same cache, table
- * and positions, and the same results but for another order of fp32 sums, the
- * prefix's keys and values read once a layer instead of once a sequence.  0 <= prefix_len < the capacity of a sequence
- * (0: nothing is shared).  Workspace of gpt2_shared_workspace_size bytes. */
+ * positions (attention_shared_prefix in every layer): the same cache, table and
+ * positions, and the same results but for another order of fp32 sums, the
+ * prefix's keys and values read once a layer instead of once a sequence.  A
+ * sequence at pos[b] = -1 has no token in this step: nothing is appended for it
+ * and its logits and probs mean nothing, the others' are as they were without
+ * it.  A loop over paged_build_tables passes cached_len[b] where next_len[b] >
+ * cached_len[b] and -1 where the request got no block: its table entry at that
+ * position names no block of its own. 0 <= prefix_len < the capacity of a
+ * sequence (0: nothing is shared).  Workspace of gpt2_shared_workspace_size
+ * bytes. */
 GPT2_API int gpt2_decode_step_shared(const GPT2Config* cfg, const float* params, const void* packed,
                                      const GPT2PagedKVCache* kv, const int* tok, const int* pos, int B, int prefix_len,
                                      float* logits, float* probs, void* workspace, size_t ws_bytes, int precision,

@@ -225,6 +225,31 @@ def test_nothing_is_appended_through_a_bad_entry(precision, B, NH, P):
         assert torch.equal(pool, want)
 
 
+@pytest.mark.parametrize("precision", ALL, ids=[NAMES[p] for p in ALL])
+@pytest.mark.parametrize("B,NH,P", [(4, 2, 96), (4, 2, 700), (70, 40, 1000)])
+def test_sequences_without_a_token(precision, B, NH, P):
+    """pos -1: a zero row, nothing appended, nothing flagged, whatever the row of
+    the table holds; the other rows are as with it."""
+    c = make(precision, B, NH, 64, P, own_of(B, 40, 3), 16, seed=5)
+    good = check(c)
+    idle = dict(c, pos=c["pos"].clone(), table=c["table"].clone())
+    idle["pos"][[1, B - 1]] = -1
+    idle["table"][1] = 0
+    idle["table"][B - 1] = -1
+    out, pool = run(idle)
+    no_device_error()
+    rest = torch.ones(B, dtype=torch.bool)
+    rest[[1, B - 1]] = False
+    assert (out[~rest] == 0).all() and torch.equal(out[rest], good[rest])
+    want = c["pool"].clone()
+    k, v = c["qkv"].view(B, 3, NH, 64)[:, 1:].unbind(1)
+    for b in rest.nonzero()[:, 0].tolist():
+        at = int(c["pos"][b])
+        blk = int(c["table"][b, at // 16])
+        want[0, blk, :, at % 16], want[1, blk, :, at % 16] = k[b], v[b]
+    assert torch.equal(pool, want)
+
+
 def test_entries_that_are_not_reached_may_hold_anything():
     # rows other than 0 over the prefix's whole blocks
     c = make(ab.GPT2_FP16, 5, 2, 64, 96, [4, 0, 30, 2, 9], 16, seed=3)
@@ -522,3 +547,68 @@ def test_prefill_slots_leaves_padding_out():
         m.prefill_slots(tg, lg1, kv, slots)
         assert ab.gpt2_get_error() == ab.DEVERR_BLOCK
         assert torch.equal(view(pool), want)
+
+
+@pytest.mark.parametrize("precision", ALL, ids=[NAMES[p] for p in ALL])
+def test_decode_loop_when_blocks_run_out(precision):
+    """Continuations of one prompt with too few free blocks: those that get none
+    wait (position -1) while the others go on, and go on themselves once there
+    are blocks.  Every step stores at the granted slots and nowhere else (block
+    0, which the entries of a new table name, is the prompt's), and a token's
+    logits are those of a loop in which nobody waits."""
+    w = inputs.WORKLOADS["tiny"]
+    cfg = w.cfg
+    params, _ = inputs.workload_inputs(w, "perturbed")
+    B, bs, shared, n_own = 6, 4, 20, 9
+    maxb = -(-(shared + n_own) // bs)
+    n_pre, num_blocks = shared // bs, shared // bs + B * (maxb - shared // bs) + 1
+    rng = np.random.default_rng(8)
+    seq = rng.integers(0, cfg.vocab_size, (B, shared + n_own)).astype(np.int32)
+    seq[:, :shared] = seq[0, :shared]
+    m = GPT2Model(cfg, params, B, shared, precision)
+    ids = dev(np.concatenate([np.arange(n_pre), n_pre + rng.permutation(num_blocks - n_pre)]).astype(np.int32))
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    lg, _ = m.new_outputs(1, shared, probs=False)
+    toks = dev(seq)
+
+    def loop(free_at):
+        """free_at(step): how many free blocks there are by then."""
+        pool = m.new_paged_kvcache(num_blocks, bs)
+        view = lambda p: p.view(cfg.num_layers, 2, num_blocks, cfg.num_heads, bs, -1)  # noqa: E731
+        table = i32(B, maxb)
+        kv = ab.paged_kv(pool, table, num_blocks, bs, maxb)
+        m.prefill_slots(toks[:1, :shared].contiguous(), lg, kv, torch.arange(shared, dtype=torch.int32, device="cuda")[None])
+        lens, taken = [torch.full((B,), shared, dtype=torch.int32, device="cuda"), i32(B)], [i32(1), i32(1)]
+        slots, ws = i32(B, 1), m.new_shared_workspace(B, shared)
+        pre, free = ids[:n_pre].clone(), ids[n_pre:].clone()
+        got, waited, step = {}, 0, 0
+        while int(lens[step % 2].min()) < shared + n_own and step < 40:
+            a, b = step % 2, 1 - step % 2
+            new = (lens[a] < shared + n_own).int()  # none for a sequence that has ended
+            ab.paged_build_tables(table, slots, lens[b], taken[b], lens[a], new, free, free_at(step), taken[a], pre,
+                                  shared, B, 1, num_blocks, bs, maxb)
+            pos = torch.where(lens[b] > lens[a], lens[a], -1).int()
+            tok = toks.gather(1, pos.long().clamp(min=0)[:, None])[:, 0].contiguous()
+            logits, _ = m.new_outputs(B, None, probs=False)
+            before = pool.clone()
+            m.decode_step_shared(kv, tok, pos, shared, logits, ws)
+            changed = (view(pool) != view(before)).any(5).any(3).any(1).any(0)  # [block, offset]
+            assert set(changed.flatten().nonzero()[:, 0].tolist()) == {x for x in slots[:, 0].tolist() if x >= 0}
+            for r, p in enumerate(pos.tolist()):
+                if p >= 0:
+                    got[r, p] = logits[r, :cfg.vocab_size].clone()
+                else:
+                    waited += int(new[r])
+            step += 1
+        no_device_error()
+        return got, waited
+
+    ample, none = loop(lambda step: num_blocks - n_pre)
+    short, some = loop(lambda step: 4 if step < 3 else 7 if step < 6 else num_blocks - n_pre)
+    assert none == 0 and some > 0
+    assert sorted(ample) == sorted(short) == [(b, p) for b in range(B) for p in range(shared, shared + n_own)]
+    for at in ample:
+        assert torch.equal(short[at], ample[at]), at
+    ref, _ = oracle.forward(cfg, params, seq)
+    for (b, p), x in ample.items():
+        assert_close(host(x), ref[b, p, :cfg.vocab_size], atol=LOGIT_TOL[precision], what=f"sequence {b} position {p}")
