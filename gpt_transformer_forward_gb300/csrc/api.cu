@@ -863,7 +863,7 @@ int paged_build_tables(int* block_table, int* slots, int* next_len, int* taken_o
   RETURN_IF(taken_out != nullptr && taken_out == taken_in, GPT2_ERR_ARG);
   RETURN_IF(next_len != nullptr && (next_len == cached_len || next_len == new_len), GPT2_ERR_ARG);
   const long long cap = static_cast<long long>(max_blocks_per_seq) << lbs;
-  RETURN_IF(B > kMaxTableRequests || max_blocks_per_seq > kMaxBlocksPerSeq ||
+  RETURN_IF(B > kMaxTableRequests || T > kMaxTablePositions || max_blocks_per_seq > kMaxBlocksPerSeq ||
                 (static_cast<long long>(num_blocks) << lbs) > 0x7fffffffLL || prefix_len % block_size != 0 ||
                 prefix_len > cap,
             GPT2_ERR_SHAPE);

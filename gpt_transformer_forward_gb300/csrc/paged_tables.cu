@@ -141,7 +141,7 @@ void launch_build_tables(const TableArgs& a, cudaStream_t s) {
   const int ctas = 4 * num_sms();
   const int per = (a.B + ctas - 1) / ctas;
   int wpr = kTabThreads / 32;
-  while (wpr > 1 && (wpr * per > kTabThreads / 32 || wpr * 32 >= 2 * a.T)) wpr /= 2;
+  while (wpr > 1 && (wpr * per > kTabThreads / 32 || wpr * 16 >= a.T)) wpr /= 2;
   launch_pdl(build_tables_kernel, dim3((a.B + per - 1) / per), dim3(kTabThreads), 0, s, a, per, wpr);
 }
 

@@ -8,6 +8,7 @@ namespace gpt2 {
 
 // paged_tables.cu
 constexpr int kMaxTableRequests = 65536;
+constexpr int kMaxTablePositions = 1 << 30;  // new ones of a request: an int holds them and a step of the loops beyond
 struct TableArgs {
   int* table;
   int* slots;

@@ -70,8 +70,8 @@ extern "C" {
  * sets GPT2_DEVERR_POSITION_BIT and refuses the request, which then needs no
  * block; a block id outside [0, num_blocks) that a slot needs sets
  * GPT2_DEVERR_BLOCK_BIT and leaves that slot -1.
- * B <= 65536, max_blocks_per_seq <= 1024, num_blocks * block_size < 2^31,
- * block_size a power of two.  Pointers 4-byte aligned. */
+ * B <= 65536, T <= 2^30, max_blocks_per_seq <= 1024, num_blocks * block_size
+ * < 2^31, block_size a power of two.  Pointers 4-byte aligned. */
 GPT2_API int paged_build_tables(int* block_table, int* slots, int* next_len, int* taken_out, const int* cached_len,
                                 const int* new_len, const int* free_blocks, int num_free, const int* taken_in,
                                 const int* prefix_blocks, int prefix_len, int B, int T, int num_blocks, int block_size,

@@ -53,6 +53,11 @@ def test_tables_refuse(change, code):
     refused(code, ab.paged_build_tables, **{**TABLES, **change})
 
 
+@pytest.mark.parametrize("change", [dict(T=(1 << 30) + 1), dict(T=2**31 - 1), dict(T=2**31 - 1, B=1, slots=None)])
+def test_tables_refuse_more_new_positions_than_their_loops_count(change):
+    refused(S, ab.paged_build_tables, **{**TABLES, **change})
+
+
 def shared_args(**kw):
     d = dict(out=FAKE, qkv=2 * FAKE, kv=ab.paged_kv(FAKE, FAKE, 64, 16, 32), pos=FAKE, B=4, C=256, NH=4, prefix_len=300,
              precision=ab.GPT2_FP16, workspace=FAKE, ws_bytes=1 << 30)
