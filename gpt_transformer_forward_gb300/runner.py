@@ -145,7 +145,7 @@ class GPT2Model:
                              f"{tuple(logits.shape)}")
         if targets is not None:
             _check_int32(targets, "targets", shape)
-        new = lambda *more, dtype=torch.float32: torch.empty(*shape, *more, dtype=dtype, device=logits.device)  # noqa: E731
+        new = lambda *more, dtype=torch.float32: torch.empty((*shape, *more), dtype=dtype, device=logits.device)  # noqa: E731
         with _allocating_on(stream):
             r = {"entropy": new(), "lse": new()}
             if targets is not None:

@@ -240,6 +240,19 @@ def test_runner_serving_calls_refuse_what_they_would_misread(cpu_model):
             cpu_model.decode_step_shared(None, tok[:, 0], pos, 1, None, None, stream=0)
 
 
+def test_runner_logprobs_takes_a_single_row(cpu_model, monkeypatch):
+    """Logits [Vp] are one row, whose results have no leading shape."""
+    calls = []
+    monkeypatch.setattr(ab, "logprobs_forward", lambda *a: calls.append(a))
+    r = cpu_model.logprobs(torch.zeros(cpu_model.cfg.padded_vocab_size), torch.tensor(3, dtype=torch.int32), top=2)
+    assert {k: tuple(v.shape) for k, v in r.items()} == dict(entropy=(), lse=(), logprob=(), top_ids=(2,),
+                                                             top_logprobs=(2,))
+    assert calls[0][8:12] == (1, cpu_model.cfg.vocab_size, cpu_model.cfg.padded_vocab_size, 2)
+    r = cpu_model.logprobs(torch.zeros(cpu_model.cfg.padded_vocab_size))
+    assert {k: tuple(v.shape) for k, v in r.items()} == dict(entropy=(), lse=())
+    assert [c[7] is None for c in calls] == [False, True]
+
+
 def test_element_types():
     assert ab.element_type(torch.empty(1)) == ab.GPT2_PROBS_F32
     assert ab.element_type(torch.empty(1, dtype=torch.bfloat16)) == ab.GPT2_PROBS_BF16
