@@ -113,9 +113,10 @@ class GPT2Model:
     # ------------------------------------- many continuations of one prompt
     def prefill_slots(self, tok, logits, kv, slots, probs=None, stream=None):
         """gpt2_forward storing token (b, t) at slot slots[b, t] of kv's pool
-        (none where it is -1).  slots: contiguous int32 [B, T]."""
+        (none where it is -1).  tok, slots: contiguous int32 [B, T]."""
         B, T = tok.shape
         _check_int32(slots, "slots", (B, T))
+        _check_int32(tok, "tok", (B, T))
         ab.gpt2_prefill_slots(self.cfg, self.params, self.packed, tok, B, T, logits, probs, kv, slots, self.workspace,
                               self.ws_bytes, self.precision, stream)
 
@@ -126,9 +127,11 @@ class GPT2Model:
 
     def decode_step_shared(self, kv, tok, pos, prefix_len: int, logits, workspace, probs=None, stream=None):
         """decode_step_paged for sequences that share their first prefix_len
-        positions; pos int32 [B]; workspace from new_shared_workspace."""
+        positions; tok, pos: contiguous int32 [B], position -1 for a sequence
+        without a token in this step; workspace from new_shared_workspace."""
         B = tok.shape[0]
         _check_int32(pos, "pos", (B,))
+        _check_int32(tok, "tok", (B,))
         ab.gpt2_decode_step_shared(self.cfg, self.params, self.packed, kv, tok, pos, B, prefix_len, logits, probs,
                                    workspace, workspace.numel(), self.precision, stream)
 

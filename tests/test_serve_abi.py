@@ -253,6 +253,20 @@ def test_runner_logprobs_takes_a_single_row(cpu_model, monkeypatch):
     assert [c[7] is None for c in calls] == [False, True]
 
 
+@pytest.mark.parametrize("tok", [
+    lambda t: t.long(),                              # the default type of token ids: every second one would be 0
+    lambda t: torch.cat([t, t], -1)[..., ::2],       # strided, as a column of a longer sequence
+    lambda t: t.to(torch.int16),
+])
+def test_runner_serving_calls_refuse_tokens_they_would_misread(cpu_model, tok):
+    t = torch.ones(2, 4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="tok"):
+        cpu_model.prefill_slots(tok(t), None, None, torch.zeros(2, 4, dtype=torch.int32), stream=0)
+    with pytest.raises(ValueError, match="tok"):
+        cpu_model.decode_step_shared(None, tok(t[:, 0].contiguous()), torch.ones(2, dtype=torch.int32), 1, None,
+                                     torch.zeros(1, dtype=torch.uint8), stream=0)
+
+
 def test_element_types():
     assert ab.element_type(torch.empty(1)) == ab.GPT2_PROBS_F32
     assert ab.element_type(torch.empty(1, dtype=torch.bfloat16)) == ab.GPT2_PROBS_BF16
