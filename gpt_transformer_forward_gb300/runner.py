@@ -38,6 +38,17 @@ def _check_int32(t, name: str, shape) -> None:
                          f"{tuple(t.shape)}{'' if t.is_contiguous() else ', strided'}")
 
 
+def _check_outputs(logits, probs, shape) -> None:
+    """Buffers of another type or size than the fp32 rows that a call writes
+    would be written past their end."""
+    for name, t in (("logits", logits), ("probs", probs)):
+        if name == "probs" and t is None:
+            continue
+        if t is None or t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+            got = "none" if t is None else f"{t.dtype} of shape {tuple(t.shape)}{'' if t.is_contiguous() else ', strided'}"
+            raise ValueError(f"{name}: contiguous fp32 of shape {tuple(shape)} expected, not {got}")
+
+
 class GPT2Model:
     """Parameters (fp32, plus the packed bf16 weights in GPT2_BF16 mode) and a
     workspace sized for batches of up to B sequences of up to T tokens."""
@@ -117,6 +128,7 @@ class GPT2Model:
         B, T = tok.shape
         _check_int32(slots, "slots", (B, T))
         _check_int32(tok, "tok", (B, T))
+        _check_outputs(logits, probs, (B, T, self.cfg.padded_vocab_size))
         ab.gpt2_prefill_slots(self.cfg, self.params, self.packed, tok, B, T, logits, probs, kv, slots, self.workspace,
                               self.ws_bytes, self.precision, stream)
 
@@ -132,6 +144,9 @@ class GPT2Model:
         B = tok.shape[0]
         _check_int32(pos, "pos", (B,))
         _check_int32(tok, "tok", (B,))
+        _check_outputs(logits, probs, (B, self.cfg.padded_vocab_size))
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace: new_shared_workspace's expected")
         ab.gpt2_decode_step_shared(self.cfg, self.params, self.packed, kv, tok, pos, B, prefix_len, logits, probs,
                                    workspace, workspace.numel(), self.precision, stream)
 

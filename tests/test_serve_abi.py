@@ -267,6 +267,38 @@ def test_runner_serving_calls_refuse_tokens_they_would_misread(cpu_model, tok):
                                      torch.zeros(1, dtype=torch.uint8), stream=0)
 
 
+@pytest.mark.parametrize("which", ["logits", "probs"])
+@pytest.mark.parametrize("change", [
+    lambda t: t.half(),                              # half the bytes that are written
+    lambda t: t.double(),
+    lambda t: t[:1].contiguous(),                    # fewer rows
+    lambda t: t[..., :-4].contiguous(),              # rows without the padding
+    lambda t: torch.cat([t, t], -1)[..., ::2],
+])
+def test_runner_serving_calls_refuse_outputs_they_would_overrun(cpu_model, monkeypatch, which, change):
+    reached = []
+    for name in ("gpt2_prefill_slots", "gpt2_decode_step_shared"):
+        monkeypatch.setattr(ab, name, lambda *a, name=name: reached.append(name))
+    tok = torch.ones(2, 4, dtype=torch.int32)
+    Vp = cpu_model.cfg.padded_vocab_size
+    ws = torch.zeros(1, dtype=torch.uint8)
+    for call, shape in ((lambda lg, pr: cpu_model.prefill_slots(tok, lg, None, tok, pr), (2, 4, Vp)),
+                        (lambda lg, pr: cpu_model.decode_step_shared(None, tok[:, 0].contiguous(), tok[:, 0].contiguous(),
+                                                                     1, lg, ws, pr), (2, Vp))):
+        good = [torch.zeros(shape), torch.zeros(shape)]
+        call(*good)
+        call(good[0], None)
+        bad = [change(t) if which == n else t for n, t in zip(("logits", "probs"), good)]
+        with pytest.raises(ValueError, match=which):
+            call(*bad)
+    with pytest.raises(ValueError, match="logits"):
+        cpu_model.prefill_slots(tok, None, None, tok)
+    with pytest.raises(ValueError, match="workspace"):
+        cpu_model.decode_step_shared(None, tok[:, 0].contiguous(), tok[:, 0].contiguous(), 1, torch.zeros(2, Vp),
+                                     torch.zeros(64))
+    assert reached == ["gpt2_prefill_slots"] * 2 + ["gpt2_decode_step_shared"] * 2
+
+
 def test_element_types():
     assert ab.element_type(torch.empty(1)) == ab.GPT2_PROBS_F32
     assert ab.element_type(torch.empty(1, dtype=torch.bfloat16)) == ab.GPT2_PROBS_BF16
