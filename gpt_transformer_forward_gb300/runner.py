@@ -49,6 +49,16 @@ def _check_outputs(logits, probs, shape) -> None:
             raise ValueError(f"{name}: contiguous fp32 of shape {tuple(shape)} expected, not {got}")
 
 
+def _check_device(device, **tensors) -> None:
+    """Kernels run on the current device and take plain addresses: those of host
+    memory or of another device are not theirs to read."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, the model is on {device}")
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        raise ValueError(f"the model is on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
 class GPT2Model:
     """Parameters (fp32, plus the packed bf16 weights in GPT2_BF16 mode) and a
     workspace sized for batches of up to B sequences of up to T tokens."""
@@ -129,6 +139,7 @@ class GPT2Model:
         _check_int32(slots, "slots", (B, T))
         _check_int32(tok, "tok", (B, T))
         _check_outputs(logits, probs, (B, T, self.cfg.padded_vocab_size))
+        _check_device(self.params.device, tok=tok, slots=slots, logits=logits, probs=probs)
         ab.gpt2_prefill_slots(self.cfg, self.params, self.packed, tok, B, T, logits, probs, kv, slots, self.workspace,
                               self.ws_bytes, self.precision, stream)
 
@@ -147,6 +158,7 @@ class GPT2Model:
         _check_outputs(logits, probs, (B, self.cfg.padded_vocab_size))
         if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace: new_shared_workspace's expected")
+        _check_device(self.params.device, tok=tok, pos=pos, logits=logits, probs=probs, workspace=workspace)
         ab.gpt2_decode_step_shared(self.cfg, self.params, self.packed, kv, tok, pos, B, prefix_len, logits, probs,
                                    workspace, workspace.numel(), self.precision, stream)
 
@@ -163,6 +175,7 @@ class GPT2Model:
                              f"{tuple(logits.shape)}")
         if targets is not None:
             _check_int32(targets, "targets", shape)
+        _check_device(self.params.device, logits=logits, targets=targets)
         new = lambda *more, dtype=torch.float32: torch.empty((*shape, *more), dtype=dtype, device=logits.device)  # noqa: E731
         with _allocating_on(stream):
             r = {"entropy": new(), "lse": new()}

@@ -2,12 +2,13 @@
 bound, sizes answer without a GPU, and invalid arguments are refused before
 anything is launched (the addresses here are aligned and never read)."""
 import ctypes
+import types
 
 import pytest
 import torch
 
 from gpt_transformer_forward_gb300 import binding as ab
-from gpt_transformer_forward_gb300 import build, inputs
+from gpt_transformer_forward_gb300 import build, inputs, runner
 from gpt_transformer_forward_gb300.runner import GPT2Model
 
 FAKE = 1 << 20
@@ -297,6 +298,30 @@ def test_runner_serving_calls_refuse_outputs_they_would_overrun(cpu_model, monke
         cpu_model.decode_step_shared(None, tok[:, 0].contiguous(), tok[:, 0].contiguous(), 1, torch.zeros(2, Vp),
                                      torch.zeros(64))
     assert reached == ["gpt2_prefill_slots"] * 2 + ["gpt2_decode_step_shared"] * 2
+
+
+def test_runner_serving_calls_refuse_tensors_of_another_device(cpu_model, monkeypatch):
+    for name in ("gpt2_prefill_slots", "gpt2_decode_step_shared", "logprobs_forward"):
+        monkeypatch.setattr(ab, name, lambda *a: None)
+    Vp = cpu_model.cfg.padded_vocab_size
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    prefill = dict(tok=i(2, 4), logits=torch.zeros(2, 4, Vp), kv=None, slots=i(2, 4), probs=torch.zeros(2, 4, Vp))
+    step = dict(kv=None, tok=i(2), pos=i(2), prefix_len=1, logits=torch.zeros(2, Vp),
+                workspace=torch.zeros(1, dtype=torch.uint8), probs=torch.zeros(2, Vp))
+    rows = dict(logits=torch.zeros(3, Vp), targets=i(3))
+    for call, args in ((cpu_model.prefill_slots, prefill), (cpu_model.decode_step_shared, step),
+                       (cpu_model.logprobs, rows)):
+        call(**args)
+        for name, t in args.items():
+            if torch.is_tensor(t):
+                with pytest.raises(ValueError, match=name):
+                    call(**{**args, name: t.to("meta")})
+    # the model's device is the current one
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    second = types.SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="current"):
+        runner._check_device(torch.device("cuda", 1), logits=second)
+    runner._check_device(torch.device("cuda", 0), logits=types.SimpleNamespace(device=torch.device("cuda", 0)))
 
 
 def test_element_types():
