@@ -430,3 +430,60 @@ def test_runner_logprobs_allocates_on_the_stream_it_runs_on(monkeypatch, raw):
     s.synchronize()
     for k, v in want.items():
         assert torch.equal(got[k], v), k
+
+
+@pytest.mark.parametrize("inplace", [True, False], ids=["in place", "apart"])
+def test_gradient_of_rows_past_32_bits(inplace):
+    """Both sides of the row that holds element 2^31, and the last rows, against
+    64 bits, with the target's term and the padding's zeros; the uniform rows
+    between them (p = 1 / V, log p + H = 0 but for roundings) for their one
+    value and their target's."""
+    V, Vp = 50300, 50304
+    N = 2 ** 31 // Vp + 40
+    at = torch.cat([2 ** 31 // Vp + torch.arange(-4, 5), torch.arange(N - 6, N)])
+    g0 = torch.Generator().manual_seed(4)
+    rows = (torch.randn(len(at), Vp, generator=g0) * 3).bfloat16()
+    x = torch.zeros(N, Vp, dtype=torch.bfloat16, device="cuda")
+    x[at.cuda()] = rows.cuda()
+    t = torch.randint(0, V, (N,), generator=g0, dtype=torch.int32)
+    g, h = torch.randn(N, generator=g0), torch.randn(N, generator=g0)
+    x64 = rows[:, :V].double().numpy()
+    ref = logprobs(x64, t[at].numpy(), 0)
+    lse, ent = torch.full((N,), float(np.log(V))), torch.full((N,), float(np.log(V)))
+    lse[at], ent[at] = torch.from_numpy(ref["lse"]).float(), torch.from_numpy(ref["entropy"]).float()
+    d = x if inplace else torch.full_like(x, 3.0)
+    ab.logprobs_backward(d, x, ab.element_type(x), t.cuda(), lse.cuda(), ent.cuda(), g.cuda(), h.cuda(), N, V, Vp)
+    no_device_error()
+    got = d[at.cuda()].cpu()
+    want = logprobs_grad(x64, t[at].numpy(), ent[at].double().numpy(), g[at].double().numpy(), h[at].double().numpy())
+    tol = grad_tol(x64, ref, want, g[at], h[at], x.dtype)
+    err = np.abs(got[:, :V].double().numpy() - want)
+    assert (err <= tol).all(), (err - tol).max()
+    rest = torch.ones(N, dtype=torch.bool)
+    rest[at] = False
+    gd, td = g.cuda(), t.cuda().long()
+    # -g / V, its entropy term off by h / V (|log V| (4 + 2) + 8) u, each rounded to bf16
+    size = gd.abs() / V * (2.0 ** -8 + 1e-5) + h.cuda().abs() / V * 80 * u + 2.0 ** -126
+    own = d.gather(1, td[:, None])[:, 0].float()
+    assert ((own - gd * (1 - 1 / V)).abs() <= size + gd.abs() * 2.0 ** -8)[rest.cuda()].all()
+    d.scatter_(1, td[:, None], 0.0)
+    for lo in range(0, N, 4096):
+        r = torch.arange(lo, min(N, lo + 4096))
+        r = r[rest[r]].cuda()
+        y = d[r]
+        assert (y[:, V:] == 0).all()
+        hit = torch.zeros(len(r), V, dtype=torch.bool, device="cuda").scatter_(1, td[r, None], True)
+        assert (((y[:, :V].float() + gd[r, None] / V).abs() <= size[r, None]) | hit).all()
+
+
+def test_runner_logprobs_of_a_single_row():
+    w = inputs.WORKLOADS["tiny"]
+    params, _ = inputs.workload_inputs(w, "perturbed")
+    m = GPT2Model(w.cfg, params, 1, 4, ab.GPT2_FP32)
+    logits = torch.randn(1, w.cfg.padded_vocab_size, device="cuda")
+    tg = torch.tensor([5], dtype=torch.int32, device="cuda")
+    want, got = m.logprobs(logits, tg, top=3), m.logprobs(logits[0], tg[0], top=3)
+    assert sorted(got) == sorted(want)
+    for k in want:
+        assert torch.equal(got[k], want[k][0]), k
+    no_device_error()
