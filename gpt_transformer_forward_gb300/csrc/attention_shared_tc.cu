@@ -27,7 +27,7 @@
 // frees TMEM and returns.
 //
 // Measured: 256 sequences, 16 heads, prefix 16384 (17.2 GFLOP, 67 MB), the whole
-// call with up to 255 own positions 65 us; with P rounded to one value 56, of
+// call with up to 255 own positions 60 us; with P rounded to one value 56, of
 // which this kernel 29, exponential unit and tensor pipe 33 % busy each: as in
 // the forward kernel, the cycle of a score buffer (exponentials, P V, the next S and their
 // hand-offs) sets the pace.  (Then four softmax groups of 64-key tiles with an S

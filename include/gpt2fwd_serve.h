@@ -114,7 +114,7 @@ GPT2_API size_t attention_shared_prefix_workspace_size(int B, int C, int NH, int
  *   element type: fp32 in GPT2_FP32 and GPT2_TF32 (both fp32 arithmetic), the
  *   16-bit type in GPT2_BF16 and GPT2_FP16 (the products over the prefix on
  *   tensor cores with fp32 accumulation, its probabilities as sums of two
- *   values of the 16-bit type: off by 2^-16 relative in bf16, by 2^-22 or an
+ *   values of the 16-bit type: off by 2^-15 relative in bf16, by 2^-22 or an
  *   absolute 2^-25 in fp16).
  * Head size 16, 32 or 64.  pos: DEVICE int32 [B]; -1 is a sequence without a
  * token in this step (one that waits for a block, or has ended): a zero row,

@@ -404,9 +404,10 @@ def test_probabilities_keep_more_than_16_bits(precision, B, NH, P):
     probabilities lose shows beside the output's own rounding.  Keys and queries
     are nonzero in one dimension: a score is one product (its factor of log2
     units and the subtracted maximum: 4 u |s| more).  Probabilities enter the
-    products as the sum of two 16-bit values, off by w^2 relative, or in fp16 by
-    2^-25 (half its smallest step) where that is more, but never by more than
-    themselves."""
+    products as the sum of two 16-bit values.  In fp16 both are rounded: off by
+    w^2 relative, or by 2^-25 (half its smallest step) where that is more, but
+    never by more than themselves.  In bf16 the first is cut off, which leaves
+    less than a step, 2 w, and the second rounds that: 2 w^2."""
     hs, bs = 64, 16
     c = make(precision, B, NH, hs, P, own_of(B, 20, B), bs, seed=B, qscale=1.0)
     g = torch.Generator().manual_seed(B + P)
@@ -428,7 +429,7 @@ def test_probabilities_keep_more_than_16_bits(precision, B, NH, P):
     ref, sabs, vmax = shared_attention(q, k, v, c["pool"].double().numpy(), c["table"].numpy(), c["pos"].numpy(), P, bs)
     w = HALF[DT[precision]]
     n = c["pos"].numpy()[:, None] + 1
-    lost = np.full((B, NH), w * w)
+    lost = np.full((B, NH), w * w if precision == ab.GPT2_FP16 else 2 * w * w)
     if precision == ab.GPT2_FP16:
         s = q[:, :, 0][:, :, None] * (-4.0 * rank.clamp(max=60)).numpy() / 8  # [B, NH, P]
         lost += np.minimum(np.exp(s), 2.0 ** -25).sum(2)  # the largest is 0
