@@ -38,6 +38,13 @@ def _check_int32(t, name: str, shape) -> None:
                          f"{tuple(t.shape)}{'' if t.is_contiguous() else ', strided'}")
 
 
+def _check_fp32_probs(probs) -> None:
+    """Only forward writes probabilities of other types; into a 16-bit buffer the
+    fp32 rows of the other calls go past its end."""
+    if probs is not None and probs.dtype != torch.float32:
+        raise ValueError(f"probs: fp32 expected, not {probs.dtype}")
+
+
 def _check_outputs(logits, probs, shape) -> None:
     """Buffers of another type or size than the fp32 rows that a call writes
     would be written past their end."""
@@ -113,6 +120,7 @@ class GPT2Model:
                                        probs_type=probs_type(probs))
 
     def decode_step(self, kvcache, tok, pos: int, logits, probs=None, stream=None):
+        _check_fp32_probs(probs)
         B = tok.shape[0]
         ab.gpt2_decode_step(self.cfg, self.params, self.packed, kvcache, tok, B, pos, logits, probs,
                             self.workspace, self.ws_bytes, self.precision, stream)
@@ -120,6 +128,7 @@ class GPT2Model:
     def prefill_paged(self, tok, logits, kv, probs=None, stream=None):
         """gpt2_forward writing positions [0, T) through the paged cache kv
         (a binding.GPT2PagedKVCache)."""
+        _check_fp32_probs(probs)
         B, T = tok.shape
         ab.gpt2_prefill_paged(self.cfg, self.params, self.packed, tok, B, T, logits, probs, kv, self.workspace,
                               self.ws_bytes, self.precision, stream)
@@ -127,6 +136,7 @@ class GPT2Model:
     def decode_step_paged(self, kv, tok, pos, logits, probs=None, stream=None):
         """One decode step, sequence b at position pos[b] (a device int32
         tensor)."""
+        _check_fp32_probs(probs)
         B = tok.shape[0]
         ab.gpt2_decode_step_paged(self.cfg, self.params, self.packed, kv, tok, pos, B, logits, probs, self.workspace,
                                   self.ws_bytes, self.precision, stream)

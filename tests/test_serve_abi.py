@@ -324,6 +324,24 @@ def test_runner_serving_calls_refuse_tensors_of_another_device(cpu_model, monkey
     runner._check_device(torch.device("cuda", 0), logits=types.SimpleNamespace(device=torch.device("cuda", 0)))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_runner_calls_that_write_fp32_probs_refuse_others(cpu_model, monkeypatch, dtype):
+    reached = []
+    for name in ("gpt2_decode_step", "gpt2_prefill_paged", "gpt2_decode_step_paged"):
+        monkeypatch.setattr(ab, name, lambda *a, name=name: reached.append(name))
+    tok = torch.ones(2, 4, dtype=torch.int32)
+    lg, pr = cpu_model.new_outputs(2, 4, probs_dtype=dtype)
+    lg1, pr1 = cpu_model.new_outputs(2, None, probs_dtype=dtype)
+    for call in (lambda p4, p1: cpu_model.decode_step(None, tok[:, 0], 3, lg1, p1),
+                 lambda p4, p1: cpu_model.prefill_paged(tok, lg, None, p4),
+                 lambda p4, p1: cpu_model.decode_step_paged(None, tok[:, 0], tok[:, 0], lg1, p1)):
+        with pytest.raises(ValueError, match="probs"):
+            call(pr, pr1)
+        call(pr.float(), pr1.float())
+        call(None, None)
+    assert len(reached) == 6
+
+
 def test_element_types():
     assert ab.element_type(torch.empty(1)) == ab.GPT2_PROBS_F32
     assert ab.element_type(torch.empty(1, dtype=torch.bfloat16)) == ab.GPT2_PROBS_BF16
