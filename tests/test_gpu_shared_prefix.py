@@ -613,3 +613,50 @@ def test_decode_loop_when_blocks_run_out(precision):
     ref, _ = oracle.forward(cfg, params, seq)
     for (b, p), x in ample.items():
         assert_close(host(x), ref[b, p, :cfg.vocab_size], atol=LOGIT_TOL[precision], what=f"sequence {b} position {p}")
+
+
+@pytest.mark.parametrize("precision", ALL, ids=[NAMES[p] for p in ALL])
+def test_the_first_request_waits(precision):
+    """A new request in row 0, through which the shared positions are read, gets
+    no block while the others have room: their logits are those of a step whose
+    row 0 was granted all along."""
+    w = inputs.WORKLOADS["tiny"]
+    cfg = w.cfg
+    params, _ = inputs.workload_inputs(w, "perturbed")
+    B, bs, shared, maxb = 5, 4, 20, 8
+    n_pre, num_blocks = shared // bs, shared // bs + 5 + 1
+    m = GPT2Model(cfg, params, B, shared, precision)
+    toks = dev(inputs.make_tokens(9, B, shared, cfg.vocab_size))
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    pool = m.new_paged_kvcache(num_blocks, bs)
+    # blocks 1 .. n_pre are the prompt's; 0 is nobody's
+    pre = torch.arange(1, n_pre + 1, dtype=torch.int32, device="cuda")
+    free = torch.arange(n_pre + 1, num_blocks, dtype=torch.int32, device="cuda")
+    table = torch.full((B, maxb), -1, dtype=torch.int32, device="cuda")
+    kv = ab.paged_kv(pool, table, num_blocks, bs, maxb)
+    lg, _ = m.new_outputs(1, shared, probs=False)
+    m.prefill_slots(toks[:1].contiguous(), lg, kv, torch.arange(bs, bs + shared, dtype=torch.int32, device="cuda")[None])
+    ws = m.new_shared_workspace(B, shared)
+
+    def step(lens, taken, tok):
+        nxt, after = i32(B), i32(1)
+        ab.paged_build_tables(table, None, nxt, after, lens, None, free, len(free), taken, pre, shared, B, 1, num_blocks,
+                              bs, maxb)
+        pos = torch.where(nxt > lens, lens, -1).int()
+        logits, _ = m.new_outputs(B, None, probs=False)
+        m.decode_step_shared(kv, tok, pos, shared, logits, ws)
+        return nxt, after, pos, logits[:, :cfg.vocab_size]
+
+    lens, taken, pos, _ = step(torch.full((B,), shared, dtype=torch.int32, device="cuda"), i32(1), toks[:, 0].contiguous())
+    assert pos.tolist() == [shared] * B and int(taken) == B
+    kept = pool.clone()
+    _, _, pos, want = step(lens, taken, toks[:, 1].contiguous())
+    assert pos.tolist() == [shared + 1] * B
+    pool.copy_(kept)
+    table[0] = -1
+    fresh = lens.clone()
+    fresh[0] = shared
+    nxt, _, pos, got = step(fresh, taken, toks[:, 1].contiguous())
+    assert pos.tolist() == [-1] + [shared + 1] * (B - 1) and int(nxt[0]) == shared
+    assert torch.equal(got[1:], want[1:])
+    no_device_error()
