@@ -25,22 +25,26 @@ constexpr int kTileK = 64;    // keys per step of a warp group
 constexpr int kThreads = 128;
 // A prefix so short, and of so few bytes when every sequence reads it by
 // itself, is left to the kernel of the own positions: one launch, not two (4
-// sequences, 12 heads, prefix 64: 3.2 us against 4.3; prefix 256 4.7 against
-// 4.6, and 2 us less on the host; 64 sequences, prefix 64, 13 MB: 5.6 against
-// 4.6; one sequence, prefix 1000: 8.4 against 4.7).
+// sequences, 12 heads, prefix 64: 3.0 us against 4.5; prefix 256 4.4 against
+// 4.7, and 2 us less on the host; 64 sequences, prefix 64, 13 MB: 6.0 against
+// 4.6; one sequence, prefix 1000: 7.8 against 4.8).
 constexpr int kDirectLen = 256;
 constexpr long long kDirectBytes = 8LL << 20;
 // The tcgen05 kernel (head size 64) takes over for 65 sequences or more and
 // this many pairs of a query row (rows in tiles of 64) and a shared position: it
 // costs about 4 us more to begin and end, and less per pair.  Whole calls with
 // up to 32 own positions, mma.sync against tcgen05, us: 12 heads, 96 sequences,
-// prefix 960 (1.5 million pairs) 8.1 against 10.1, 4000 (6.1) 12.6 against 11.7;
-// 4 heads, 256 sequences, 4000 (4.1) 10.0 against 10.6, 8000 (8.2) 14.3 against
-// 11.6; 16 heads, 129 sequences, 960 (2.9) 9.9 against 10.9, 256 sequences, 2000
-// (8.2) 18.1 against 16.5.  The own positions' lengths, which only the device
-// knows, count too: over a short prefix tcgen05 has few CTAs, and the SMs it
-// leaves attend to own positions meanwhile (12 heads, 128 sequences, prefix 512:
-// own 1 5.4 against 7.5, own 64 10.7 against 9.3).
+// prefix 960 (1.5 million pairs) 9.1 against 10.9, 4000 (6.1) 13.6 against 12.7,
+// 128 sequences, 4000 (6.1) 13.9 against 14.6; 4 heads, 256 sequences, 4000
+// (4.1) 11.7 against 11.8, 8000 (8.2) 16.1 against 13.5; 16 heads, 192
+// sequences, 960 (2.9) 12.6 against 13.4, 2000 (6.1) 16.5 against 15.8.
+// The own positions' lengths, which only the device knows, count too: over a
+// short prefix tcgen05 has few CTAs, and the SMs it leaves attend to own
+// positions meanwhile.  Own 1, 64, 128 and 255, 12 heads: 128 sequences, prefix
+// 512 6.0 / 9.4 / 15.7 / 26.3 against 9.4 / 9.5 / 14.2 / 23.6; prefix 960 7.4 /
+// 9.5 / 15.6 / 25.7 against 11.0 / 14.6 / 21.2 / 31.8; 256 sequences, prefix 512
+// 10.2 / 15.0 / 25.3 / 43.0 against 11.9 / 17.1 / 24.8 / 40.9.  So a short prefix
+// with 128 own positions or more is up to 10 % slower here than with tcgen05.
 constexpr int kTcMinBatch = 65;
 constexpr long long kTcMinPairs = 5000000;
 constexpr long long kRoomyPairs = 3000000;  // below: mma.sync with two CTAs an SM (plan_of)
@@ -57,8 +61,8 @@ struct Plan {
 // Tensor-core kernel of few sequences: the four warps of a CTA are arranged
 // over two or four groups of 16 query rows, over keys with what is left.  (One
 // row group and four of keys holds one CTA an SM: 16 sequences, 16 heads,
-// prefix 16384 18.9 us against 17.0, one sequence of prefix 1000 5.2 against
-// 4.7.)
+// prefix 16384 22.9 us against 18.8, one sequence of prefix 1000 5.3 against
+// 4.8.)
 int row_groups(int B) { return B <= 32 ? 2 : 4; }
 
 // CUDA-core kernel: query rows of a thread (8 of them a CTA's).
@@ -70,11 +74,11 @@ long long tc_pairs(int B, int NH) { return static_cast<long long>((B + 63) / 64 
 // Splits: the CTAs that fit the SMs at once (the tcgen05 kernel one an SM, the
 // CUDA-core kernel two, mma.sync three, but two where many sequences share a
 // short prefix, which leaves registers for the kernel of the own positions to
-// run beside it: 12 heads, 128 sequences, prefix 960, 64 own positions 10.4 us
-// against 12.0; with 4 heads and prefix 8000 11.5 against 9.9), or in two rounds where these come out
-// more even: a round lasts its splits' steps and about as long as `start` steps
-// to begin and end.  The count goes by the shape alone, not by the device: it
-// sizes the caller's workspace.
+// run beside it: 12 heads, 128 sequences, prefix 960, 64 own positions 9.4 us
+// against 11.6; with 4 heads, 96 sequences and prefix 8000 13.0 against 11.7),
+// or in two rounds where these come out more even: a round lasts its splits'
+// steps and about as long as `start` steps to begin and end.  The count goes by
+// the shape alone, not by the device: it sizes the caller's workspace.
 Plan plan_of(int B, int NH, int hs, int prefix_len, bool is16, int* wanted = nullptr) {
   Plan p{kNone, 1, 1, 0, 0, 0};
   const long long row_bytes = 2LL * hs * (is16 ? 2 : 4);  // of a key and its value
@@ -140,14 +144,14 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // ------------------------------------------------------ CUDA-core kernel
-// fp32 caches, fp32 arithmetic.  128 threads: ty = thread / 16 owns the R rows
+// fp32 caches, fp32 arithmetic (in the TF32 mode too).  128 threads: ty = thread / 16 owns the R rows
 // R ty .., tx = thread % 16 keys tx + 16 i of a step (S) and dimensions
 // tx * HS / 16 .. (O).  R = 8 (64 queries) needs 16 shared-memory wavefronts for
 // 128 FMAs a thread where R = 4 needs 24 (256 sequences, 16 heads, prefix 16384:
 // 750 -> 419 us, 41 TFLOP/s); fewer rows for few queries, whose products they
 // would waste.  K and V tiles come by cp.async into two buffers: loaded through
 // registers in a loop, a step waited for eight loads in turn (8 sequences, 12
-// heads, prefix 4000: 29 us).
+// heads, prefix 4000: 29 us against 12.1).
 template <int HS, int R>
 struct SimtSmem {
   static constexpr int kPad = HS + 4;      // row stride in floats: 16 rows' float4s in distinct banks
@@ -299,7 +303,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 // into two buffers, rows of HS * 2 bytes with 16-byte chunk c of row r at chunk
 // c ^ (r mod chunks), as in attn_tc_kernel; any block size, since every chunk
 // finds its own block.  64 sequences, 16 heads of 64, prefix 16384 (67 MB, 4.3
-// GFLOP): 20.8 us, 3.2 TB/s, tensor pipe 43 % busy, three CTAs an SM.
+// GFLOP and half as much again for P's second value): 26.0 us, 2.6 TB/s, tensor
+// pipe 51 % busy, issue slots 41 %, three CTAs an SM; 1.9 warps an issue slot
+// wait out fixed latencies, 1.0 the tensor pipe.  With P rounded to one value
+// 20.8 us.
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
@@ -546,7 +553,7 @@ cudaError_t allow_smem(bool (&allowed)[kMaxDevices], Kernel kern, int bytes) {
     // an SM that is split between shared memory and L1 in another way must run
     // empty before a kernel that wants more starts there: the own positions
     // would wait for the prefix (128 sequences, 12 heads, prefix 512, 32 own
-    // positions: 9.2 us against 7.6)
+    // positions: 8.5 us against 6.9)
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     allowed[dev] = e == cudaSuccess;
@@ -574,7 +581,9 @@ cudaError_t allow_smem(bool (&allowed)[kMaxDevices], Kernel kern, int bytes) {
 // ring took 74 us; products on mma.sync with the query as one of 16 rows, and
 // bulk copies instead of cp.async, the same as this; several pairs a warp, their
 // states kept so that all own positions run beside the prefix, 82 us where
-// prefix and own positions one after the other take 56.
+// prefix and own positions one after the other took 56 (61 since the prefix's
+// probabilities are two values).  A pair's own positions are at most one CTA's
+// work: 4 sequences of 12 heads with 4000 of them take 29 us, 0.8 TB/s.
 constexpr int kRingStages = 2;
 constexpr int kRingIt = 4;
 constexpr int kRingStageBytes = kRingIt * 2 * 512;  // K and V

@@ -26,11 +26,13 @@
 // Every wait is bounded; after a timeout the CTA drains its copies and MMAs,
 // frees TMEM and returns.
 //
-// Measured: 256 sequences, 16 heads, prefix 16384 (17.2 GFLOP, 67 MB), the whole
-// call with up to 255 own positions 60 us; with P rounded to one value 56, of
-// which this kernel 29, exponential unit and tensor pipe 33 % busy each: as in
-// the forward kernel, the cycle of a score buffer (exponentials, P V, the next S and their
-// hand-offs) sets the pace.  (Then four softmax groups of 64-key tiles with an S
+// Measured: 256 sequences, 16 heads, prefix 16384 (17.2 GFLOP and half as much
+// again for P's second value, 67 MB), bf16: 36 us (29 with P rounded to one
+// value), tensor pipe 39 % busy, exponential unit 27 %, issue slots 45 %, and 2.6
+// warps an issue slot stalled on the long scoreboard (loads from TMEM, polls of
+// barriers): as in the forward kernel, the cycle of a score buffer
+// (exponentials, P V, the next S and their hand-offs) sets the pace.
+// (With P rounded to one value four softmax groups of 64-key tiles with an S
 // buffer each were slower, with one issuing warp for S and one for P V (39 us)
 // and with an issuing warp a group (36 us).)
 #include "serve.cuh"

@@ -7,7 +7,8 @@
 // bound by latency: one row 2.6 us, with 20 alternatives 5.5 us (about 2500
 // cycles to load its part of the row, 3500 to search it, 3500 to join the
 // blocks of the cluster and write).  16-bit rows halve the bytes but not the
-// instructions: 4096 of bf16 72 us, with 20 alternatives 96 us.
+// instructions: 4096 of bf16 72 us (5.7 TB/s), with 20 alternatives 96 us (4.3
+// TB/s), issue slots 70 % and the ALU pipe 50 and 55 % busy.
 #include "serve.cuh"
 
 #include <algorithm>
@@ -27,7 +28,10 @@ constexpr int kMaxParts = 8;  // blocks of a cluster that share a row
 // 27.8 against 29.2).
 constexpr int kShortRowTop = 8192, kShortRow = 4096;
 // From here on the backward takes a row's maximum and sum anew instead of its
-// lse, whose fp32 rounding |lse| 2^-24 is an error of every p (6e-5 here).
+// lse, whose fp32 rounding |lse| 2^-24 is an error of every p (6e-5 here, at
+// most 3e-5 below).  Every block of a row reads the whole row twice for that,
+// value by value: 4096 rows of 50257 fp32 logits 470 us against 246, of bf16 233
+// against 127; 100 of bf16 22 against 5.9.
 constexpr float kLargeLse = 1024.f;
 
 // 16 bytes of logits as floats
@@ -216,7 +220,9 @@ __device__ __forceinline__ void rank_keys(const Key* keys, int n, int K, Put put
 // vectors are all read again, by all threads together.  The listed elements are
 // ranked by counting.  Equal values do not add candidates, since vectors are
 // ordered by index; a row in which a few threads hold all the largest elements
-// may exceed the list and is searched K times instead.  64 groups: with K = 32
+// may exceed the list and is searched K times instead (4096 rows of 50257 fp32
+// logits, 20 alternatives, all large ones with 24 of 256 threads: 4.3 ms against
+// 0.13).  64 groups: with K = 32
 // about 44 elements reach tau (64 ln 2), and ranking 64 keys costs a quarter of
 // ranking 128.
 template <typename T, int kT>

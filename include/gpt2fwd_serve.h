@@ -188,7 +188,9 @@ GPT2_API int logprobs_forward(float* logprob, float* entropy, float* lse, int* t
  * NULL gradient is zero.  A row with target -1 (or one outside [-1, V), which
  * sets GPT2_DEVERR_TOKEN_BIT) gets no gradient through its logprob; a token
  * of probability 0 gets none but the target's own dlogprob; a row with every
- * token ruled out gets zeros.  dlogits has the type and layout of logits and
+ * token ruled out gets zeros.  p is taken from lse, whose fp32 rounding is a
+ * relative error of |lse| 2^-24 in it; from |lse| = 1024 on the row's maximum
+ * and sum are taken anew instead (about twice the time).  dlogits has the type and layout of logits and
  * may be logits itself. */
 GPT2_API int logprobs_backward(void* dlogits, const void* logits, int logits_type, const int* targets,
                                const float* lse, const float* entropy, const float* dlogprob, const float* dentropy,
