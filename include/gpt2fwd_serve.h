@@ -48,8 +48,10 @@ extern "C" {
  * new_len[b].  A request that does not get its blocks keeps its row (but for
  * the shared prefix's entries, below) and its length (next_len[b] =
  * cached_len[b]) and its slots are -1: the caller sees by next_len who has to
- * wait.  taken_out[0] = taken_in[0] + the blocks
- * given, always a prefix of the free blocks that were left.
+ * wait, and gives that request no position to decode at (-1 in
+ * gpt2_decode_step_shared), since its entry there names no block of its own.
+ * taken_out[0] = taken_in[0] + the blocks given, always a prefix of the free
+ * blocks that were left.
  *   block_table  int32 [B][max_blocks_per_seq], updated in place
  *   slots        int32 [B][T] or NULL; next_len int32 [B] or NULL;
  *   taken_out    int32 [1] or NULL; none of the outputs may overlap an input
