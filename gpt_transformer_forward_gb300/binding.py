@@ -22,7 +22,7 @@ PRECISIONS = {"fp32": GPT2_FP32, "tf32": GPT2_TF32, "bf16": GPT2_BF16, "fp16": G
 GPT2_OK = 0
 ERRORS = {-1: "GPT2_ERR_ARG", -2: "GPT2_ERR_SHAPE", -3: "GPT2_ERR_ALIGN", -4: "GPT2_ERR_WORKSPACE",
           -5: "GPT2_ERR_CUDA", -6: "GPT2_ERR_DEVICE", -7: "GPT2_ERR_UNSUPPORTED"}
-DEVERR_TOKEN, DEVERR_TIMEOUT, DEVERR_POSITION, DEVERR_BLOCK = 1, 2, 4, 8
+DEVERR_TOKEN, DEVERR_TIMEOUT, DEVERR_POSITION, DEVERR_BLOCK, DEVERR_TREE = 1, 2, 4, 8, 16
 
 
 class GPT2Error(RuntimeError):
@@ -52,11 +52,18 @@ class GPT2PagedKVCache(ctypes.Structure):
                 ("block_size", ctypes.c_int), ("max_blocks_per_seq", ctypes.c_int)]
 
 
+class GPT2LogitRules(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("history", "history_len", "prompt_len", "repetition", "presence",
+                                               "frequency", "bias_ids", "bias_values", "masks", "mask_rows")] + [
+        (n, ctypes.c_int) for n in ("history_stride", "num_bias", "num_masks")]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
 _CFG = ctypes.POINTER(GPT2Config)
 _PKV = ctypes.POINTER(GPT2PagedKVCache)
+_RULES = ctypes.POINTER(GPT2LogitRules)
 
 # name -> (restype, argtypes), in the order of include/gpt2fwd.h
 _SIGNATURES = {
@@ -108,6 +115,16 @@ _SERVE_SIGNATURES = {
     "logprobs_backward": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
 }
 
+# the same for include/gpt2fwd_draft.h
+_DRAFT_SIGNATURES = {
+    "attention_tree_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
+    "attention_tree": (_I, [_P, _P, _PKV, _P, _P, _I, _I, _I, _I, _I, _P, _Z, _P]),
+    "gpt2_tree_workspace_size": (_Z, [_CFG, _I, _I, _I]),
+    "gpt2_decode_step_tree": (_I, [_CFG, _P, _P, _PKV, _P, _P, _P, _I, _I, _P, _P, _P, _Z, _I, _P]),
+    "logits_adjust": (_I, [_P, _P, _I, _RULES, _P, _P, _I, _I, _I, _I, _P]),
+    "gpt2_accept_tree": (_I, [_P, _P, _P, _P, _P, _CFG, _PKV, _P, _P, _P, _P, _I, _I, _I, _P]),
+}
+
 _handle = None
 
 
@@ -123,7 +140,7 @@ def _lib():
             raise ImportError(f"libgpt2fwd.so is not built ({path}); run "
                               "`python -m gpt_transformer_forward_gb300.build`")
         h = ctypes.CDLL(path)
-        for name, (res, args) in {**_SIGNATURES, **_SERVE_SIGNATURES}.items():
+        for name, (res, args) in {**_SIGNATURES, **_SERVE_SIGNATURES, **_DRAFT_SIGNATURES}.items():
             fn = getattr(h, name)
             fn.restype = res
             fn.argtypes = args
@@ -399,6 +416,59 @@ def logprobs_backward(dlogits, logits, logits_type, targets, lse, entropy, dlogp
     _check("logprobs_backward", _lib().logprobs_backward(
         _ptr(dlogits), _ptr(logits), logits_type, _ptr(targets), _ptr(lse), _ptr(entropy), _ptr(dlogprob),
         _ptr(dentropy), N, V, Vp, _stream(stream)))
+
+
+# ------------------------------------------- gpt2fwd_draft.h
+TREE_MAX_NODES = 64
+LOGIT_MAX_BIASES = 1023
+LOGIT_MAX_HISTORY = 1 << 20
+
+
+def attention_tree_workspace_size(B, N, C, NH, precision) -> int:
+    return _lib().attention_tree_workspace_size(B, N, C, NH, precision)
+
+
+def attention_tree(out, qkv, kv, pos, parent, B, N, C, NH, precision, workspace=None, ws_bytes=0, stream=None):
+    """kv: one layer's slab and the block table (paged_kv)."""
+    _check("attention_tree", _lib().attention_tree(
+        _ptr(out), _ptr(qkv), ctypes.byref(kv) if kv is not None else None, _ptr(pos), _ptr(parent), B, N, C, NH,
+        precision, _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def gpt2_tree_workspace_size(cfg, B, N, precision) -> int:
+    return _lib().gpt2_tree_workspace_size(_cfg(cfg), B, N, precision)
+
+
+def gpt2_decode_step_tree(cfg, params, packed, kv, tok, parent, pos, B, N, logits, probs, workspace, ws_bytes,
+                          precision, stream=None):
+    _check("gpt2_decode_step_tree", _lib().gpt2_decode_step_tree(
+        _cfg(cfg), _ptr(params), _ptr(packed), ctypes.byref(kv) if kv is not None else None, _ptr(tok), _ptr(parent),
+        _ptr(pos), B, N, _ptr(logits), _ptr(probs), _ptr(workspace), ws_bytes, precision, _stream(stream)))
+
+
+def logit_rules(history=None, history_len=None, prompt_len=None, history_stride=0, repetition=None, presence=None,
+                frequency=None, bias_ids=None, bias_values=None, num_bias=0, masks=None, mask_rows=None,
+                num_masks=0) -> GPT2LogitRules:
+    """The C struct of logits_adjust (device tensors or addresses); it keeps
+    what it was made of."""
+    kept = (history, history_len, prompt_len, repetition, presence, frequency, bias_ids, bias_values, masks, mask_rows)
+    r = GPT2LogitRules(*map(_ptr, kept), history_stride, num_bias, num_masks)
+    r.kept = kept
+    return r
+
+
+def logits_adjust(out, logits, logits_type, rules, tok, parent, B, N, V, Vp, stream=None):
+    _check("logits_adjust", _lib().logits_adjust(
+        _ptr(out), _ptr(logits), logits_type, ctypes.byref(rules) if rules is not None else None, _ptr(tok),
+        _ptr(parent), B, N, V, Vp, _stream(stream)))
+
+
+def gpt2_accept_tree(path, count, emitted, next_tok, next_pos, cfg, kv, tok, parent, next, pos, B, N, precision,
+                     stream=None):
+    _check("gpt2_accept_tree", _lib().gpt2_accept_tree(
+        _ptr(path), _ptr(count), _ptr(emitted), _ptr(next_tok), _ptr(next_pos), _cfg(cfg) if cfg is not None else None,
+        ctypes.byref(kv) if kv is not None else None, _ptr(tok), _ptr(parent), _ptr(next), _ptr(pos), B, N, precision,
+        _stream(stream)))
 
 
 def gpt2_forward_profile(cfg, params, packed, tok, B, T, logits, probs, workspace, ws_bytes, precision,

@@ -20,6 +20,7 @@
 #include <string>
 #include <vector>
 
+#include "draft.cuh"
 #include "serve.cuh"
 
 namespace gpt2 {
@@ -575,6 +576,20 @@ static int shared_attention(void* out, const void* qkv, void* kc, void* vc, int 
   return check_launch();
 }
 
+// Attention of a tree of drafted tokens a sequence (launch_attention_tree).
+struct TreeStep {
+  const int* parent;
+  int N;
+  TreePartials part;
+};
+static int tree_attention(void* out, const void* qkv, void* kc, void* vc, int precision, int B, int C, int NH,
+                          const int* pos, const KVRows& rows, const TreeStep& t, cudaStream_t s) {
+  const int op = is16(precision) ? op_of(precision) : kOpTF32;  // an fp32 cache in the other modes
+  PdlScope pdl(true);  // the kernels wait for what is ahead of them themselves
+  TRY(launch_attention_tree(out, qkv, kc, vc, op, pos, t.parent, B, t.N, C, NH, rows, t.part, s));
+  return check_launch();
+}
+
 // The body shared by the full forward pass and the decode step.  decode
 // false: rows are B sequences x T tokens at positions 0..T-1 (their keys and
 // values written into kv when it is given: a prefill); decode true: rows are
@@ -582,11 +597,12 @@ static int shared_attention(void* out, const void* qkv, void* kc, void* vc, int 
 // is given (T == 1), attending over and appending to kv.
 // slots (a prefill): tokens go to slots[b*T + t] of kv's pool instead.
 // shared (a decode step): kv's sequences share their first positions.
+// tree (a decode step): rows are B sequences x T nodes of their trees.
 static int run_forward(const GPT2Config* cfg, const float* params, const void* packed, const int* tok, int B, int T,
                        bool decode, int decode_pos, const int* pos_arr, float* logits, void* probs,
                        const KVLayout* kv, void* workspace, size_t ws_bytes, int precision, cudaStream_t s,
                        StageProfiler* prof = nullptr, int probs_type = GPT2_PROBS_F32, const int* slots = nullptr,
-                       const PrefixPartials* shared = nullptr) {
+                       const PrefixPartials* shared = nullptr, const TreeStep* tree = nullptr) {
   auto mark = [&](int stage) { return prof ? prof->record(stage) : GPT2_OK; };
   const int C = cfg->channels, L = cfg->num_layers, NH = cfg->num_heads, V = cfg->vocab_size;
   const int Vp = cfg->padded_vocab_size, maxT = cfg->max_seq_len;
@@ -637,6 +653,8 @@ static int run_forward(const GPT2Config* cfg, const float* params, const void* p
 
   if (!decode)
     launch_encoder(x, tok, params + po.wte, params + po.wpe, N, T, C, V, s);
+  else if (tree != nullptr)
+    launch_encoder_tree(x, tok, tree->parent, pos_arr, params + po.wte, params + po.wpe, B, T, kv->rows.capacity, C, V, s);
   else
     launch_encoder_pos(x, tok, params + po.wte, params + po.wpe, B, decode_pos, pos_arr, maxT, C, V,
                        shared != nullptr, s);
@@ -677,6 +695,10 @@ static int run_forward(const GPT2Config* cfg, const float* params, const void* p
       } else {
         TRY(launch_attention_16(att, true, qkv, op, B, T, C, NH, s));
       }
+    } else if (tree != nullptr) {
+      const size_t e = kv_elem_bytes(precision);
+      uint8_t* kc = static_cast<uint8_t*>(kv->base) + l * kv_slab * e;
+      TRY(tree_attention(att, qkv, kc, kc + kv_half * e, precision, B, C, NH, pos_arr, kv->rows, *tree, s));
     } else if (shared != nullptr) {
       const size_t e = kv_elem_bytes(precision);
       uint8_t* kc = static_cast<uint8_t*>(kv->base) + l * kv_slab * e;
@@ -1027,6 +1049,137 @@ int logprobs_backward(void* dlogits, const void* logits, int logits_type, const 
   PdlScope pdl(true);  // the kernel waits for its predecessor itself
   TRY(launch_logprobs_backward(dlogits, logits, logits_type, targets, lse, entropy, dlogprob, dentropy, N, V, Vp,
                                as_stream(stream)));
+  return check_launch();
+}
+
+// --------------------------------------------------- gpt2fwd_draft.h
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+size_t attention_tree_workspace_size(int B, int N, int C, int NH, int precision) {
+  if (B <= 0 || B > kMaxSharedBatch || N <= 0 || N > kMaxNodes || C <= 0 || NH <= 0 || NH > kMaxSharedBatch ||
+      C % NH != 0 || !valid_precision(precision) || check_attention_shape(C, NH) != GPT2_OK)
+    return 0;
+  return tree_partial_bytes(N, C / NH);
+}
+
+int attention_tree(void* out, const void* qkv, const GPT2PagedKVCache* kvc, const int* pos, const int* parent, int B,
+                   int N, int C, int NH, int precision, void* workspace, size_t ws_bytes, void* stream) {
+  RETURN_IF(!out || !qkv || !pos || kvc == nullptr || kvc->pool == nullptr || kvc->block_table == nullptr,
+            GPT2_ERR_ARG);
+  RETURN_IF(B < 0 || N <= 0 || C <= 0 || NH <= 0 || !valid_precision(precision) || out == qkv, GPT2_ERR_ARG);
+  const int lbs = log2_exact(kvc->block_size);
+  RETURN_IF(lbs < 0 || kvc->num_blocks <= 0 || kvc->max_blocks_per_seq <= 0, GPT2_ERR_ARG);
+  RETURN_IF(C % NH != 0 || N > kMaxNodes || kvc->max_blocks_per_seq > kMaxBlocksPerSeq || B > kMaxSharedBatch ||
+                NH > kMaxSharedBatch || static_cast<long long>(B) * NH > 0x7fffffffLL || C > 0x7fffffff / 3,
+            GPT2_ERR_SHAPE);
+  TRY(check_attention_shape(C, NH));
+  if (B == 0) return GPT2_OK;
+  RETURN_IF(workspace == nullptr || ws_bytes < attention_tree_workspace_size(B, N, C, NH, precision),
+            GPT2_ERR_WORKSPACE);
+  RETURN_IF(!aligned16(out) || !aligned16(qkv) || !aligned16(kvc->pool) || !aligned16(workspace) ||
+                !aligned4(kvc->block_table) || !aligned4(pos) || !aligned4(parent),
+            GPT2_ERR_ALIGN);
+  const long long cap =
+      std::min<long long>(kMaxSharedPositions, static_cast<long long>(kvc->max_blocks_per_seq) << lbs);
+  const size_t e = kv_elem_bytes(precision);
+  const size_t half = static_cast<size_t>(kvc->num_blocks) * kvc->block_size * C;
+  uint8_t* kc = static_cast<uint8_t*>(kvc->pool);
+  const KVRows rows{kvc->block_table, lbs, kvc->max_blocks_per_seq, kvc->num_blocks, static_cast<int>(cap),
+                    static_cast<int>(cap)};
+  const TreeStep t{parent, N, tree_partial_layout(workspace, N, C / NH)};
+  return tree_attention(out, qkv, kc, kc + half * e, precision, B, C, NH, pos, rows, t, as_stream(stream));
+}
+
+size_t gpt2_tree_workspace_size(const GPT2Config* cfg, int B, int N, int precision) {
+  if (check_config(cfg) != GPT2_OK || N <= 0 || N > kMaxNodes || B <= 0 || B > kMaxSharedBatch) return 0;
+  const size_t base = gpt2_workspace_size(cfg, B, N, precision);
+  const size_t part = attention_tree_workspace_size(B, N, cfg->channels, cfg->num_heads, precision);
+  return base == 0 || part == 0 ? 0 : base + part;
+}
+
+int gpt2_decode_step_tree(const GPT2Config* cfg, const float* params, const void* packed, const GPT2PagedKVCache* kvc,
+                          const int* tok, const int* parent, const int* pos, int B, int N, float* logits, float* probs,
+                          void* workspace, size_t ws_bytes, int precision, void* stream) {
+  TRY(check_config(cfg));
+  RETURN_IF(!params || !tok || !pos || !logits || !workspace || !valid_precision(precision), GPT2_ERR_ARG);
+  RETURN_IF(B <= 0 || N <= 0, GPT2_ERR_ARG);
+  TRY(check_attention_shape(cfg->channels, cfg->num_heads));
+  RETURN_IF(is16(precision) && packed == nullptr, GPT2_ERR_ARG);
+  KVLayout kv;
+  TRY(paged_kv(cfg, kvc, 0, &kv));
+  kv.rows.capacity = std::min(kv.rows.capacity, kMaxSharedPositions);
+  RETURN_IF(B > kMaxSharedBatch || N > kMaxNodes, GPT2_ERR_SHAPE);
+  RETURN_IF(!aligned16(params) || !aligned16(logits) || (probs && !aligned16(probs)) || !aligned4(tok) ||
+                !aligned4(parent) || !aligned4(pos) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+                (packed && (reinterpret_cast<uintptr_t>(packed) & 255u) != 0),
+            GPT2_ERR_ALIGN);
+  RETURN_IF(ws_bytes < gpt2_tree_workspace_size(cfg, B, N, precision), GPT2_ERR_WORKSPACE);
+  const size_t base = gpt2_workspace_size(cfg, B, N, precision);
+  const TreeStep t{parent, N,
+                   tree_partial_layout(static_cast<uint8_t*>(workspace) + base, N, cfg->channels / cfg->num_heads)};
+  PdlScope pdl(is16(precision));
+  return run_forward(cfg, params, packed, tok, B, N, true, 0, pos, logits, probs, &kv, workspace, base, precision,
+                     as_stream(stream), nullptr, GPT2_PROBS_F32, nullptr, nullptr, &t);
+}
+
+int logits_adjust(void* out, const void* logits, int logits_type, const GPT2LogitRules* r, const int* tok,
+                  const int* parent, int B, int N, int V, int Vp, void* stream) {
+  RETURN_IF(!out || !logits || !r || !valid_probs_type(logits_type), GPT2_ERR_ARG);
+  RETURN_IF(B < 0 || N <= 0 || V <= 0 || Vp < V || r->history_stride < 0 || r->num_bias < 0 || r->num_masks < 0,
+            GPT2_ERR_ARG);
+  RETURN_IF((r->history_stride > 0 && !r->history) || (r->num_bias > 0 && (!r->bias_ids || !r->bias_values)) ||
+                (r->num_masks > 0 && (!r->masks || !r->mask_rows)),
+            GPT2_ERR_ARG);
+  RETURN_IF(N > kMaxNodes || B > kMaxSharedBatch || !logit_rows_ok(Vp, logits_type) ||
+                r->history_stride > GPT2_LOGIT_MAX_HISTORY || r->num_bias > GPT2_LOGIT_MAX_BIASES,
+            GPT2_ERR_SHAPE);
+  RETURN_IF(!aligned16(out) || !aligned16(logits), GPT2_ERR_ALIGN);
+  for (const void* p : {static_cast<const void*>(r->history), static_cast<const void*>(r->history_len),
+                        static_cast<const void*>(r->prompt_len), static_cast<const void*>(r->repetition),
+                        static_cast<const void*>(r->presence), static_cast<const void*>(r->frequency),
+                        static_cast<const void*>(r->bias_ids), static_cast<const void*>(r->bias_values),
+                        static_cast<const void*>(r->masks), static_cast<const void*>(r->mask_rows),
+                        static_cast<const void*>(tok), static_cast<const void*>(parent)})
+    RETURN_IF(!aligned4(p), GPT2_ERR_ALIGN);
+  if (B == 0) return GPT2_OK;
+  PdlScope pdl(true);
+  TRY(launch_logits_adjust(out, logits, logits_type, *r, tok, parent, B, N, V, Vp, as_stream(stream)));
+  return check_launch();
+}
+
+int gpt2_accept_tree(int* path, int* count, int* emitted, int* next_tok, int* next_pos, const GPT2Config* cfg,
+                     const GPT2PagedKVCache* kvc, const int* tok, const int* parent, const int* next, const int* pos,
+                     int B, int N, int precision, void* stream) {
+  RETURN_IF(!tok || !next || !pos || B < 0 || N <= 0, GPT2_ERR_ARG);
+  RETURN_IF(N > kMaxNodes || B > kMaxSharedBatch, GPT2_ERR_SHAPE);
+  int* const outputs[] = {path, count, emitted, next_tok, next_pos};
+  const int* const inputs[] = {tok, parent, next, pos};
+  for (int i = 0; i < 5; ++i) {
+    RETURN_IF(!aligned4(outputs[i]), GPT2_ERR_ALIGN);
+    for (const int* p : inputs) RETURN_IF(outputs[i] != nullptr && outputs[i] == p, GPT2_ERR_ARG);
+    for (int j = 0; j < i; ++j) RETURN_IF(outputs[i] != nullptr && outputs[i] == outputs[j], GPT2_ERR_ARG);
+  }
+  for (const int* p : inputs) RETURN_IF(!aligned4(p), GPT2_ERR_ALIGN);
+  AcceptArgs a{path, count, emitted, next_tok, next_pos, tok, parent, next, pos, N, 0, 0, 0, nullptr, 0,
+               KVRows{nullptr, 0, 0, 0, kMaxSharedPositions, kMaxSharedPositions}};
+  if (kvc != nullptr) {
+    RETURN_IF(!valid_precision(precision), GPT2_ERR_ARG);
+    TRY(check_config(cfg));
+    TRY(check_attention_shape(cfg->channels, cfg->num_heads));
+    KVLayout kv;
+    TRY(paged_kv(cfg, kvc, 0, &kv));
+    a.rows = kv.rows;
+    a.rows.capacity = std::min(a.rows.capacity, kMaxSharedPositions);
+    a.NH = cfg->num_heads;
+    a.layers = cfg->num_layers;
+    a.row_vecs = static_cast<int>(cfg->channels / cfg->num_heads * kv_elem_bytes(precision) / 16);
+    a.pool = static_cast<uint4*>(kv.base);
+    a.half_vecs = kv.layer_elems / 2 * kv_elem_bytes(precision) / 16;
+    RETURN_IF(2LL * a.layers * a.NH * a.row_vecs > 0x3fffffffLL, GPT2_ERR_SHAPE);
+  }
+  if (B == 0) return GPT2_OK;
+  PdlScope pdl(true);
+  TRY(launch_accept_tree(a, B, as_stream(stream)));
   return check_launch();
 }
 

@@ -14,6 +14,7 @@
 //                        sequences and a long prefix
 // Join: own_join_kernel attends over each sequence's own positions and joins
 // that with the splits' results, which it weighs by 2^(m - max m).
+#include "mma_sync.cuh"
 #include "serve.cuh"
 
 #include <algorithm>
@@ -131,16 +132,6 @@ __device__ __forceinline__ void stage_blocks(int* tbl, const KVRows& rows, int k
     }
     tbl[j - j0] = blk;
   }
-}
-
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;  // 0 source bytes: zero-filled
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // ------------------------------------------------------ CUDA-core kernel
@@ -307,39 +298,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 // pipe 51 % busy, issue slots 41 %, three CTAs an SM; 1.9 warps an issue slot
 // wait out fixed latencies, 1.0 the tensor pipe.  With P rounded to one value
 // 20.8 us.
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr));
-}
-template <typename T>
-__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (std::is_same<T, __half>::value) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  } else {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-}
-
-template <int HS>
-__device__ __forceinline__ uint32_t swz(int row, int chunk) {
-  constexpr int kChunks = HS / 8;
-  return static_cast<uint32_t>(row * (HS * 2) + ((chunk ^ (row & (kChunks - 1))) << 4));
-}
-
 template <int HS, int WM>
 struct MmaSmem {
   static constexpr int WK = 4 / WM;
@@ -541,24 +499,6 @@ __global__ void __launch_bounds__(kThreads) prefix_mma_kernel(float* __restrict_
     for (int dt = 0; dt < kDT; ++dt)
       *reinterpret_cast<float2*>(po + at * HS + dt * 8 + 2 * tig) = make_float2(o[dt][2 * r], o[dt][2 * r + 1]);
   }
-}
-
-// Allows a kernel its shared memory, once per instance and device.
-template <typename Kernel>
-cudaError_t allow_smem(bool (&allowed)[kMaxDevices], Kernel kern, int bytes) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && dev < kMaxDevices && !allowed[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    // an SM that is split between shared memory and L1 in another way must run
-    // empty before a kernel that wants more starts there: the own positions
-    // would wait for the prefix (128 sequences, 12 heads, prefix 512, 32 own
-    // positions: 8.5 us against 6.9)
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    allowed[dev] = e == cudaSuccess;
-  }
-  return e;
 }
 
 // ------------------------------------------------- own positions and join

@@ -20,6 +20,7 @@
 #define GPT2_DEVERR_TIMEOUT 2u    // a pipeline wait gave up (bounded spin)
 #define GPT2_DEVERR_POSITION 4u   // a position outside [0, maxT) or past a sequence's cache
 #define GPT2_DEVERR_BLOCK 8u      // a block-table entry outside [0, num_blocks)
+#define GPT2_DEVERR_TREE 16u      // a tree node's parent, or a row's mask, outside its range
 
 namespace gpt2 {
 
