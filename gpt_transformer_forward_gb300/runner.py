@@ -196,3 +196,90 @@ class GPT2Model:
         ab.logprobs_forward(r.get("logprob"), r["entropy"], r["lse"], r.get("top_ids"), r.get("top_logprobs"), logits,
                             kind, targets, r["lse"].numel(), self.cfg.vocab_size, Vp, top, stream)
         return r
+
+    # ------------------------------------------------ trees of drafted tokens
+    def new_tree_workspace(self, B: int, N: int):
+        """A workspace for decode_step_tree with up to B trees of up to N nodes."""
+        nbytes = ab.gpt2_tree_workspace_size(self.cfg, B, N, self.precision)
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+
+    def decode_step_tree(self, kv, tok, pos, logits, workspace, parent=None, probs=None, stream=None):
+        """One step for a tree of tokens a sequence: tok (and parent, None for
+        chains): contiguous int32 [B, N], pos: int32 [B], -1 for a sequence
+        without a tree in this step; logits (and probs) fp32 [B, N, Vp];
+        workspace from new_tree_workspace."""
+        B, N = tok.shape
+        _check_int32(tok, "tok", (B, N))
+        _check_int32(pos, "pos", (B,))
+        if parent is not None:
+            _check_int32(parent, "parent", (B, N))
+        _check_outputs(logits, probs, (B, N, self.cfg.padded_vocab_size))
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace: new_tree_workspace's expected")
+        _check_device(self.params.device, tok=tok, pos=pos, parent=parent, logits=logits, probs=probs,
+                      workspace=workspace)
+        ab.gpt2_decode_step_tree(self.cfg, self.params, self.packed, kv, tok, parent, pos, B, N, logits, probs,
+                                 workspace, workspace.numel(), self.precision, stream)
+
+    def adjust_logits(self, logits, tok=None, parent=None, out=None, *, history=None, history_len=None,
+                      prompt_len=None, repetition=None, presence=None, frequency=None, bias_ids=None,
+                      bias_values=None, masks=None, mask_rows=None, stream=None):
+        """Penalties, biases and masks on logits [B, N, Vp] (or [B, Vp]: one row a
+        sequence), in place or into `out`, which is returned.  tok, parent: int32
+        [B, N], the trees; history [B, H], history_len, prompt_len [B], bias_ids
+        [B, M]: int32; repetition, presence, frequency [B], bias_values [B, M]:
+        fp32; masks: int32 [G, ceil(V / 32)], mask_rows int32 of the logits'
+        leading shape.  All contiguous."""
+        V, Vp = self.cfg.vocab_size, self.cfg.padded_vocab_size
+        if logits.dim() not in (2, 3) or logits.shape[-1] != Vp or not logits.is_contiguous():
+            raise ValueError(f"logits: contiguous rows of {Vp} expected, not shape {tuple(logits.shape)}, strides "
+                             f"{logits.stride()}")
+        kind = ab.element_type(logits)
+        out = logits if out is None else out
+        if out.dtype != logits.dtype or out.shape != logits.shape or not out.is_contiguous():
+            raise ValueError(f"out: contiguous {logits.dtype} of shape {tuple(logits.shape)} expected, not {out.dtype} "
+                             f"of shape {tuple(out.shape)}")
+        lead = tuple(logits.shape[:-1])
+        B, N = lead if len(lead) == 2 else (lead[0], 1)
+        rows = lambda t: t.shape[1] if t is not None and t.dim() == 2 else 0  # noqa: E731
+        H, M = rows(history), rows(bias_ids)
+        G = masks.shape[0] if masks is not None else 0
+        ints = dict(tok=(tok, (B, N)), parent=(parent, (B, N)), history=(history, (B, H)),
+                    history_len=(history_len, (B,)), prompt_len=(prompt_len, (B,)), bias_ids=(bias_ids, (B, M)),
+                    masks=(masks, (G, (V + 31) // 32)), mask_rows=(mask_rows, lead))
+        for name, (t, shape) in ints.items():
+            if t is not None:
+                _check_int32(t, name, shape)
+        floats = dict(repetition=(repetition, (B,)), presence=(presence, (B,)), frequency=(frequency, (B,)),
+                      bias_values=(bias_values, (B, M)))
+        for name, (t, shape) in floats.items():
+            if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != shape):
+                raise ValueError(f"{name}: contiguous fp32 of shape {shape} expected, not {t.dtype} of shape "
+                                 f"{tuple(t.shape)}")
+        for a, b in (("history_len", "history"), ("prompt_len", "history"), ("bias_values", "bias_ids"),
+                     ("bias_ids", "bias_values"), ("mask_rows", "masks"), ("masks", "mask_rows")):
+            given = {**ints, **floats}
+            if given[a][0] is not None and given[b][0] is None:
+                raise ValueError(f"{a} without {b}")
+        _check_device(self.params.device, logits=logits, out=out, **{n: t for n, (t, _) in {**ints, **floats}.items()})
+        rules = ab.logit_rules(history, history_len, prompt_len, H, repetition, presence, frequency, bias_ids,
+                               bias_values, M, masks, mask_rows, G)
+        ab.logits_adjust(out, logits, kind, rules, tok, parent, B, N, V, Vp, stream)
+        return out
+
+    def accept_tree(self, kv, tok, chosen, pos, parent=None, stream=None) -> dict:
+        """The path of each tree that agrees with `chosen` (each node's next
+        token), its rows of the cache moved together (kv None: no cache): path,
+        emitted [B, N], count, next_tok, next_pos [B], which belong to `stream`.
+        tok, chosen, parent: contiguous int32 [B, N], pos: int32 [B]."""
+        B, N = tok.shape
+        for name, t in (("tok", tok), ("chosen", chosen), ("parent", parent)):
+            if t is not None:
+                _check_int32(t, name, (B, N))
+        _check_int32(pos, "pos", (B,))
+        _check_device(self.params.device, tok=tok, chosen=chosen, parent=parent, pos=pos)
+        with _allocating_on(stream):
+            new = lambda *s: torch.empty(s, dtype=torch.int32, device=tok.device)  # noqa: E731
+            r = dict(path=new(B, N), count=new(B), emitted=new(B, N), next_tok=new(B), next_pos=new(B))
+        ab.gpt2_accept_tree(*r.values(), self.cfg, kv, tok, parent, chosen, pos, B, N, self.precision, stream)
+        return r

@@ -16,7 +16,11 @@
  * A step of a loop: paged_build_tables for the nodes' positions,
  * gpt2_decode_step_tree, logits_adjust, gpt2_argmax over the B * N rows (or any
  * sampler), gpt2_accept_tree, whose next_tok and next_pos are the next tree's
- * first node and place.  No call allocates, synchronises or copies between host
+ * first node and place.  A row of the block table keeps the blocks behind the
+ * accepted positions for the next tree: the lengths that paged_build_tables gets
+ * and returns are those of the positions that have blocks, its new_len is what
+ * pos + N has more, and a sequence whose length stays below pos + N waits (-1
+ * for its pos).  No call allocates, synchronises or copies between host
  * and device: all of them can be captured into a CUDA graph.  Results do not
  * depend on timing.  Calls that run at the same time need outputs and
  * workspaces of their own.  Pointers are of the device that is current at the

@@ -4,9 +4,11 @@ anything is launched (the addresses here are aligned and never read)."""
 import ctypes
 
 import pytest
+import torch
 
 from gpt_transformer_forward_gb300 import binding as ab
 from gpt_transformer_forward_gb300 import build, inputs
+from gpt_transformer_forward_gb300.runner import GPT2Model
 
 FAKE = 1 << 20
 A, S, AL, W, U = -1, -2, -3, -4, -7  # GPT2_ERR_ARG, _SHAPE, _ALIGN, _WORKSPACE, _UNSUPPORTED
@@ -154,3 +156,76 @@ def test_nothing_to_do_is_no_launch():
     ab.logits_adjust(**adjust_args(B=0), stream=0)
     ab.gpt2_accept_tree(**accept_args(B=0), stream=0)
     ab.gpt2_accept_tree(**accept_args(B=0, kv=None, cfg=None), stream=0)
+
+
+@pytest.fixture(scope="module")
+def cpu_model():
+    """A model whose buffers are in host memory, for checks that come before
+    any launch."""
+    w = inputs.WORKLOADS["tiny"]
+    params, _ = inputs.workload_inputs(w, "perturbed")
+    return GPT2Model(w.cfg, params, 2, 4, ab.GPT2_FP32, device="cpu")
+
+
+def calls_of(m, monkeypatch):
+    """The runner's calls with good arguments, and what they reach."""
+    reached = []
+    for name in ("gpt2_decode_step_tree", "logits_adjust", "gpt2_accept_tree"):
+        monkeypatch.setattr(ab, name, lambda *a, name=name: reached.append(name))
+    Vp, V = m.cfg.padded_vocab_size, m.cfg.vocab_size
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    f = lambda *s: torch.zeros(*s)  # noqa: E731
+    step = dict(kv=None, tok=i(2, 3), pos=i(2), logits=f(2, 3, Vp), workspace=torch.zeros(1, dtype=torch.uint8),
+                parent=i(2, 3), probs=f(2, 3, Vp))
+    adjust = dict(logits=f(2, 3, Vp), tok=i(2, 3), parent=i(2, 3), out=f(2, 3, Vp), history=i(2, 9), history_len=i(2),
+                  prompt_len=i(2), repetition=f(2), presence=f(2), frequency=f(2), bias_ids=i(2, 5), bias_values=f(2, 5),
+                  masks=i(4, (V + 31) // 32), mask_rows=i(2, 3))
+    accept = dict(kv=None, tok=i(2, 3), chosen=i(2, 3), pos=i(2), parent=i(2, 3))
+    return reached, [(m.decode_step_tree, step), (m.adjust_logits, adjust), (m.accept_tree, accept)]
+
+
+def test_runner_calls_reach_the_library(cpu_model, monkeypatch):
+    reached, calls = calls_of(cpu_model, monkeypatch)
+    for call, args in calls:
+        call(**args)
+    calls[0][0](**{**calls[0][1], "parent": None, "probs": None})
+    x = calls[1][1]["logits"]
+    assert calls[1][0](x) is x and calls[1][0](x[:, 0].contiguous()).shape == x[:, 0].shape
+    r = calls[2][0](**{**calls[2][1], "parent": None})
+    assert {k: tuple(v.shape) for k, v in r.items()} == dict(path=(2, 3), count=(2,), emitted=(2, 3), next_tok=(2,),
+                                                             next_pos=(2,))
+    assert sorted(reached) == sorted(["gpt2_decode_step_tree", "logits_adjust", "gpt2_accept_tree"] * 2 + ["logits_adjust"])
+
+
+@pytest.mark.parametrize("change", [
+    lambda t: t.to(torch.int64 if t.dtype == torch.int32 else torch.float64),
+    lambda t: torch.cat([t, t], -1)[..., ::2],                # strided
+    lambda t: torch.cat([t, t]),                              # more rows
+    lambda t: t[..., :-1].contiguous(),                       # shorter rows
+    lambda t: t.to("meta"),
+])
+def test_runner_calls_refuse_what_they_would_misread(cpu_model, monkeypatch, change):
+    reached, calls = calls_of(cpu_model, monkeypatch)
+    for call, args in calls:
+        for name, t in args.items():
+            if not torch.is_tensor(t) or name == "workspace":
+                continue
+            bad = change(t)
+            if bad.dtype == t.dtype and bad.device == t.device and bad.is_contiguous() and (
+                    (name == "history" and bad.shape == (2, 8)) or (name == "masks" and len(bad) == 8)):
+                continue  # a history of another length, other masks
+            with pytest.raises((ValueError, TypeError)):
+                call(**{**args, name: bad})
+    assert not reached
+
+
+def test_runner_calls_refuse_parts_without_their_others(cpu_model, monkeypatch):
+    reached, calls = calls_of(cpu_model, monkeypatch)
+    adjust, args = calls[1]
+    for gone in ("history", "bias_ids", "bias_values", "masks", "mask_rows"):
+        with pytest.raises(ValueError):
+            adjust(**{**args, gone: None})
+    step, args = calls[0]
+    with pytest.raises(ValueError, match="workspace"):
+        step(**{**args, "workspace": torch.zeros(8)})
+    assert not reached
