@@ -2,14 +2,16 @@
 // rows of logits.
 //
 // A CTA takes a segment of the vocabulary for the rows of some nodes of one
-// sequence.  What the history and the biases say about each of the segment's
-// tokens is one 32-bit word in shared memory,
-//   bits 0..20   times in the output, counted by integer atomics,
-//   bit 21       in the prompt,
-//   bits 22..31  the bias's place in the list plus 1 (the largest: the last),
-// made once for all of these rows; a row's own path is counted in before it and
-// out behind it.  Then the row's segment is read, and written, once: a token
-// whose word is 0 is copied (in place: not touched).
+// sequence.  Few of its tokens stand in the history, the biases or the node's
+// path: it finds those of the history and the biases once for all of its rows,
+// and gives each a slot that holds
+//   bits 0..20 of one word   times in the output, counted by integer atomics,
+//   bit 21                   whether it stands in the prompt,
+//   another word             the last of its biases.
+// A row's segment then goes through shared memory by bulk copies, where only the
+// tokens with a slot, those of the node's path and, under a mask, what it rules
+// out are changed.  In place nothing goes through: the tokens that change are
+// read and written where they stand.
 #include "draft.cuh"
 
 #include <algorithm>
@@ -17,11 +19,12 @@
 namespace gpt2 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kSegBytes = 16384;  // of a segment, at most
+constexpr int kStages = 3;        // rows in flight
+constexpr int kSegWords = kSegBytes / 2 / 32;  // mask words of a segment, at most
 constexpr uint32_t kPrompt = 1u << 21, kCountMask = kPrompt - 1;
-constexpr int kBiasShift = 22;
 static_assert(GPT2_LOGIT_MAX_HISTORY + kMaxNodes < (1 << 21), "a count fits its bits");
-static_assert(GPT2_LOGIT_MAX_BIASES < (1 << 10), "a bias's place fits its bits");
 
 struct AdjustArgs {
   void* out;
@@ -32,223 +35,429 @@ struct AdjustArgs {
   int B, N, V, Vp;
   int seg;     // tokens of a segment, a multiple of 32
   int nodes;   // rows of a CTA
-  bool words;  // anything but masks
+  int stages;  // rows in flight, at most kStages
+  int slots;   // tokens of a segment that a history and biases can name at most
 };
 
 struct Penalty {
   float repetition, presence, frequency;
   bool repeats;  // a repetition penalty is given
+  const float* some;  // the first kThreads biases, in shared memory
   const float* bias;
 };
-__device__ __forceinline__ float adjust_one(float x, uint32_t w, const Penalty& p) {
+template <typename E>
+__device__ __forceinline__ E adjust_one(E logit, uint32_t w, int bias, const Penalty& p) {
+  float x = to_f32(logit);
   const uint32_t count = w & kCountMask;
-  if (p.repeats && (w & (kPrompt | kCountMask)) != 0) x = x > 0.f ? x / p.repetition : x * p.repetition;
+  if (p.repeats && w != 0) x = x > 0.f ? x / p.repetition : x * p.repetition;
   if (count != 0) x = x - p.frequency * static_cast<float>(count) - p.presence;
-  if (w >> kBiasShift) x += __ldg(p.bias + (w >> kBiasShift) - 1);
-  return x;
+  if (bias >= 0) x += bias < kThreads ? p.some[bias] : __ldg(p.bias + bias);
+  return from_f32<E>(x);
 }
 
-template <typename E>
-struct Vec {
-  static constexpr int kN = 16 / static_cast<int>(sizeof(E));
-  union {
-    uint4 raw;
-    E e[kN];
-  };
-  __device__ Vec() {}
-};
+// The value of the bits of word `m`'s bytes as masks: byte k of the result is 0xff
+// where the top bit of the byte of m that nibble k of `sel` (8 + its number) names
+// is set.
+__device__ __forceinline__ uint32_t spread(uint32_t m, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(m), "r"(sel));
+  return r;
+}
 
+// A 16-byte vector with -inf in the places whose bit of `allowed` is 0.  Four bits
+// go to the top bits of four bytes by a product (their copies meet nowhere), and
+// from there over their elements: 13 instructions for 8 elements where a test and a
+// choice each took 40 (777 x 32003 bf16, all rows masked: 33.2 -> 31.3 us).
+template <typename E>
+__device__ __forceinline__ uint4 ruled_out(const uint4& v, uint32_t allowed) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (sizeof(E) == 4) {
+    const uint32_t m = (allowed & 15u) * 0x10204080u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t keep = spread(m, 0x8888u + 0x1111u * q);
+      w[q] = (w[q] & keep) | (0xff800000u & ~keep);
+    }
+  } else {
+    constexpr uint32_t kLowest = std::is_same<E, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t m = (allowed >> (q / 2 * 4) & 15u) * 0x10204080u;
+      const uint32_t keep = spread(m, q % 2 == 0 ? 0x9988u : 0xbbaau);
+      w[q] = (w[q] & keep) | (kLowest & ~keep);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+
+// Dynamic shared memory: [stages] segments of a row (not in place); where a
+// history or biases are given, per token of the segment whether it has a slot, a
+// bit each, and which; per slot its token and its two words.
 template <typename E, bool kInPlace>
-__global__ void __launch_bounds__(kThreads) logits_adjust_kernel(AdjustArgs a) {
-  using V16 = Vec<E>;
-  constexpr int kN = V16::kN;
-  extern __shared__ __align__(16) uint32_t words[];  // [seg], where anything but masks is given
-  __shared__ unsigned long long sets[kMaxNodes];
-  __shared__ int toks[kMaxNodes];
+__global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a) {
+  constexpr int kN = 16 / static_cast<int>(sizeof(E));
+  extern __shared__ __align__(128) uint8_t shared_raw[];
+  __shared__ __align__(8) uint64_t full[kStages];
+  __shared__ unsigned long long sets[kMaxNodes], same[kMaxNodes];
+  __shared__ int toks[kMaxNodes], mask_rows[kMaxNodes];
+  __shared__ uint32_t mask[kSegWords];
+  __shared__ float some_biases[kThreads];
   __shared__ unsigned long long here;  // nodes whose token lies in the segment
+  __shared__ int n_slots;
   const int tid = threadIdx.x, lane = tid & 31;
   const int v0 = static_cast<int>(blockIdx.x) * a.seg, v1 = min(a.V, v0 + a.seg);
   const int b = blockIdx.z, n0 = static_cast<int>(blockIdx.y) * a.nodes, n1 = min(a.N, n0 + a.nodes);
   const bool report = blockIdx.x == 0 && blockIdx.y == 0;
+  // columns of the segment; the last one's go on over the padding, which is
+  // written directly
+  const bool last = v0 + a.seg >= a.V;
+  const int columns = (v1 - v0 + kN - 1) / kN * kN;  // whole vectors, of Vp >= V at most
+  const size_t stage_bytes = kInPlace ? 0 : a.seg * sizeof(E);
+  uint32_t* has_slot = reinterpret_cast<uint32_t*>(shared_raw + a.stages * stage_bytes);
+  uint32_t* word = has_slot + a.seg / 32;
+  int* bias = reinterpret_cast<int*>(word + a.slots);
+  uint16_t* slot_of = reinterpret_cast<uint16_t*>(bias + a.slots);
+  uint16_t* token_of = slot_of + a.seg;
+  const size_t row0 = static_cast<size_t>(b) * a.N;
+  const GPT2LogitRules& r = a.r;
+  auto src = [&](int i) { return static_cast<const E*>(a.logits) + (row0 + i) * a.Vp + v0; };
+  auto dst = [&](int i) { return static_cast<E*>(a.out) + (row0 + i) * a.Vp + v0; };
+  auto load = [&](int i) {  // one thread; rows of missing nodes are read for nothing at the start
+    uint64_t* bar = full + (i - n0) % a.stages;
+    mbar_arrive_expect_tx(bar, columns * sizeof(E));
+    bulk_load(shared_raw + (i - n0) % a.stages * stage_bytes, src(i), columns * sizeof(E), bar);
+  };
   pdl_wait();
   pdl_trigger();
-  if (a.words) {
-    for (int x = tid; x < a.seg / 4; x += kThreads) reinterpret_cast<uint4*>(words)[x] = make_uint4(0u, 0u, 0u, 0u);
+  // Every load that waits for nothing is on its way before the first value is
+  // used: a CTA's time is mostly the latencies that follow each other.
+  int p[2] = {-2, -2}, t[2] = {-1, -1}, first_mask = -1, my_mask = -1;
+  if (r.num_masks > 0) {
+    const int i = tid - 32;
+    if (i >= n0 && i < n1) my_mask = __ldg(r.mask_rows + row0 + i);
+    first_mask = __ldg(r.mask_rows + row0 + n0);
   }
   if (tid < 32) {
-    const int* row = a.parent != nullptr ? a.parent + static_cast<size_t>(b) * a.N : nullptr;
-    const int p[2] = {tree_parent(row, lane, a.N), tree_parent(row, lane + 32, a.N)};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = lane + 32 * u;
+      p[u] = tree_parent(a.parent != nullptr ? a.parent + row0 : nullptr, i, a.N);
+      if (a.tok != nullptr && i < a.N) t[u] = __ldg(a.tok + row0 + i);
+    }
+  }
+  constexpr int kAhead = 4;
+  const int* hist = r.history + static_cast<size_t>(b) * r.history_stride;
+  const int* ids = r.bias_ids + static_cast<size_t>(b) * r.num_bias;
+  int early[kAhead], early_id = -1, len = 0, prompt = 0;
+  float early_bias = 0.f;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) early[k] = -1;
+  if (a.slots > 0) {
+    if (r.history_stride > 0) {
+      len = r.history_len != nullptr ? __ldg(r.history_len + b) : r.history_stride;
+      prompt = r.prompt_len != nullptr ? __ldg(r.prompt_len + b) : 0;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (tid + k * kThreads < r.history_stride) early[k] = __ldg(hist + tid + k * kThreads);
+    }
+    if (tid < r.num_bias) {
+      early_id = __ldg(ids + tid);
+      early_bias = __ldg(r.bias_values + static_cast<size_t>(b) * r.num_bias + tid);
+    }
+    for (int x = tid; x < a.seg / 32; x += kThreads) has_slot[x] = 0;
+  }
+  const Penalty pen{r.repetition != nullptr ? __ldg(r.repetition + b) : 1.f,
+                    r.presence != nullptr ? __ldg(r.presence + b) : 0.f,
+                    r.frequency != nullptr ? __ldg(r.frequency + b) : 0.f, r.repetition != nullptr,
+                    some_biases, r.bias_values != nullptr ? r.bias_values + static_cast<size_t>(b) * r.num_bias : nullptr};
+  // behind the small loads, which would wait for these otherwise
+  if (!kInPlace && tid == 0) {
+    for (int s = 0; s < a.stages; ++s) mbar_init(full + s, 1);
+    fence_barrier_init();
+    for (int i = n0; i < min(n1, n0 + a.stages); ++i) load(i);
+  }
+  // the mask words of the segment that this thread holds for the next row
+  constexpr int kMaskWords = kSegWords / kThreads;
+  uint32_t held[kMaskWords];
+  auto fetch_mask = [&](int g) {
+    if (g < 0 || g >= r.num_masks) return;
+    const unsigned* m = r.masks + static_cast<size_t>(g) * ((a.V + 31) / 32) + v0 / 32;
+#pragma unroll
+    for (int k = 0; k < kMaskWords; ++k) {
+      const int x = tid + k * kThreads;
+      held[k] = v0 + x * 32 < v1 ? __ldg(m + x) : 0u;
+    }
+  };
+  if (tid < 32) {
     const TreeSets ts = tree_sets(p, a.N, a.N, report);
     unsigned long long in = 0;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int i = lane + 32 * u;
-      int t = -1;
-      if (a.tok != nullptr && i < a.N && ts.set[u] != 0) {
-        t = __ldg(a.tok + static_cast<size_t>(b) * a.N + i);
-        if (t < -1 || t >= a.V) {
-          if (report) set_error(GPT2_DEVERR_TOKEN);
-          t = -1;
-        }
+      if (ts.set[u] == 0) t[u] = -1;
+      if (t[u] < -1 || t[u] >= a.V) {
+        if (report) set_error(GPT2_DEVERR_TOKEN);
+        t[u] = -1;
       }
-      if (t < v0 || t >= v1) t = -1;
+      const bool inside = t[u] >= v0 && t[u] < v1;
       sets[i] = ts.set[u];
-      toks[i] = t - v0;
-      in |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, t >= 0)) << (32 * u);
+      toks[i] = inside ? t[u] - v0 : -1;
+      in |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, inside)) << (32 * u);
     }
-    if (lane == 0) here = in;
+    __syncwarp();
+    // which of these nodes have the same token
+    unsigned long long eq[2] = {0, 0};
+    for (unsigned long long left = in; left != 0; left &= left - 1) {
+      const int j = __ffsll(static_cast<long long>(left)) - 1, tj = toks[j];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (toks[lane + 32 * u] == tj) eq[u] |= 1ull << j;
+    }
+    same[lane] = eq[0];
+    same[lane + 32] = eq[1];
+    if (lane == 0) {
+      here = in;
+      n_slots = 0;
+    }
+  } else if (tid < 32 + kMaxNodes) {
+    const int i = tid - 32;
+    mask_rows[i] = my_mask;
+  }
+  if (r.num_masks > 0) fetch_mask(first_mask);
+  some_biases[tid] = early_bias;
+  if (len < 0 || len > r.history_stride || prompt < 0 || prompt > len) {
+    if (report && tid == 0) set_error(GPT2_DEVERR_POSITION);
+    len = min(max(len, 0), r.history_stride);
+    prompt = min(max(prompt, 0), len);
   }
   __syncthreads();
-  const GPT2LogitRules& r = a.r;
-  if (a.words) {
+  if (a.slots > 0) {
     // a token of a list that lies in the segment; -1 otherwise
-    auto token = [&](int t) {
+    auto token = [&](int t, bool say) {
       if (t < -1 || t >= a.V) {
-        if (report) set_error(GPT2_DEVERR_TOKEN);
+        if (say && report) set_error(GPT2_DEVERR_TOKEN);
         return -1;
       }
       return t >= v0 && t < v1 ? t - v0 : -1;
     };
-    if (r.num_bias > 0) {
-      const int* ids = r.bias_ids + static_cast<size_t>(b) * r.num_bias;
-      for (int x = tid; x < r.num_bias; x += kThreads) {
-        const int t = token(__ldg(ids + x));
-        if (t >= 0) atomicMax(&words[t], static_cast<uint32_t>(x + 1) << kBiasShift);
+    auto id_at = [&](int x) { return x < kThreads ? early_id : __ldg(ids + x); };
+    // a slot for each of up to kAhead tokens of a thread that has none yet (whole
+    // warps call)
+    auto take = [&](const int (&t)[kAhead]) {
+      bool first[kAhead];
+      unsigned who[kAhead];
+      int n = 0;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        first[k] = t[k] >= 0 && (atomicOr(&has_slot[t[k] >> 5], 1u << (t[k] & 31)) >> (t[k] & 31) & 1) == 0;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        who[k] = __ballot_sync(0xffffffffu, first[k]);
+        n += __popc(who[k]);
       }
-      __syncthreads();  // nothing else stands in the words yet
+      if (n == 0) return;
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&n_slots, n);
+      at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (first[k]) {
+          const int slot = at + __popc(who[k] & ((1u << lane) - 1));
+          slot_of[t[k]] = static_cast<uint16_t>(slot);
+          token_of[slot] = static_cast<uint16_t>(t[k]);
+          word[slot] = 0;
+          bias[slot] = -1;
+        }
+        at += __popc(who[k]);
+      }
+    };
+    int t[kAhead];
+    for (int x0 = 0; x0 < r.num_bias; x0 += kAhead * kThreads) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int x = x0 + tid + k * kThreads;
+        t[k] = x < r.num_bias ? token(id_at(x), true) : -1;
+      }
+      take(t);
     }
-    if (r.history_stride > 0) {
-      int n = r.history_len != nullptr ? __ldg(r.history_len + b) : r.history_stride;
-      int m = r.prompt_len != nullptr ? __ldg(r.prompt_len + b) : 0;
-      if (n < 0 || n > r.history_stride || m < 0 || m > n) {
-        if (report && tid == 0) set_error(GPT2_DEVERR_POSITION);
-        n = min(max(n, 0), r.history_stride);
-        m = min(max(m, 0), n);
+    for (int x0 = 0; x0 < len; x0 += kAhead * kThreads) {
+      int raw[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int x = x0 + tid + k * kThreads;
+        raw[k] = x0 == 0 ? early[k] : x < len ? __ldg(hist + x) : -1;
       }
-      const int* hist = r.history + static_cast<size_t>(b) * r.history_stride;
-#pragma unroll 4
-      for (int x = tid; x < n; x += kThreads) {
-        const int t = token(__ldg(hist + x));
-        if (t < 0) continue;
-        if (x < m)
-          atomicOr(&words[t], kPrompt);
-        else
-          atomicAdd(&words[t], 1u);
-      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) t[k] = x0 + tid + k * kThreads < len ? token(raw[k], true) : -1;
+      take(t);
     }
     __syncthreads();
+    for (int x = tid; x < r.num_bias; x += kThreads) {
+      const int t = token(id_at(x), false);
+      if (t >= 0) atomicMax(&bias[slot_of[t]], x);
+    }
+    auto count = [&](int x, int t) {
+      if (t < 0) return;
+      if (x < prompt)
+        atomicOr(&word[slot_of[t]], kPrompt);
+      else
+        atomicAdd(&word[slot_of[t]], 1u);
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int x = tid + k * kThreads;
+      if (x < len) count(x, token(early[k], false));
+    }
+#pragma unroll 4
+    for (int x = tid + kAhead * kThreads; x < len; x += kThreads) count(x, token(__ldg(hist + x), false));
+    __syncthreads();
   }
-  const Penalty pen{r.repetition != nullptr ? __ldg(r.repetition + b) : 1.f,
-                    r.presence != nullptr ? __ldg(r.presence + b) : 0.f,
-                    r.frequency != nullptr ? __ldg(r.frequency + b) : 0.f, r.repetition != nullptr,
-                    r.bias_values != nullptr ? r.bias_values + static_cast<size_t>(b) * r.num_bias : nullptr};
   const unsigned long long in_segment = here;
-  const E lowest = from_f32<E>(-INFINITY);
-  const int mask_words = (a.V + 31) / 32;
-  // vectors of the segment; the last one's goes on over the padding
-  const int end = v0 + a.seg >= a.V ? a.Vp : v0 + a.seg, vecs = (end - v0) / kN;
-  // counts the nodes `path` in (1) or out (-1)
-  auto count = [&](unsigned long long path, uint32_t by) {
-    if (tid < kMaxNodes && (path >> tid & 1)) atomicAdd(&words[toks[tid]], by);
-  };
-  unsigned long long counted = 0;  // what the words hold of a path
+  const int slots = a.slots > 0 ? n_slots : 0, vecs = columns / kN;
+  const uint4 lowest = ruled_out<E>(make_uint4(0u, 0u, 0u, 0u), 0u);
+  uint32_t phases = 0, pending = kInPlace ? 0 : (1u << min(a.stages, n1 - n0)) - 1;  // a bit a stage
+  bool alive = true;  // every copy came
   for (int i = n0; i < n1; ++i) {
+    const int stage = (i - n0) % a.stages;
     const unsigned long long set = sets[i];
-    if (set == 0) continue;  // a missing node's row stays
-    const unsigned long long path = set & in_segment;
-    if (path != counted) {
-      __syncthreads();  // the row before is done
-      count(path & ~counted, 1u);
-      count(counted & ~path, ~0u);
-      __syncthreads();
-      counted = path;
-    }
-    const size_t row = (static_cast<size_t>(b) * a.N + i);
-    const uint32_t* mask = nullptr;
-    bool none = false;  // a bad mask row: everything is ruled out
-    if (r.num_masks > 0) {
-      const int g = __ldg(r.mask_rows + row);
-      if (g >= 0 && g < r.num_masks) {
-        mask = r.masks + static_cast<size_t>(g) * mask_words;
-      } else if (g != -1) {
-        none = true;
-        if (blockIdx.x == 0 && tid == 0) set_error(GPT2_DEVERR_TREE);
+    const int g = mask_rows[i];
+    const bool none = g < -1 || g >= r.num_masks;  // a bad mask row: everything is ruled out
+    const bool masked = set != 0 && r.num_masks > 0 && g != -1;
+    if (masked) {
+      if (none && blockIdx.x == 0 && tid == 0) set_error(GPT2_DEVERR_TREE);
+#pragma unroll
+      for (int k = 0; k < kMaskWords; ++k) {
+        const int x = tid + k * kThreads;
+        if (x < a.seg / 32) mask[x] = none ? 0u : held[k];
       }
     }
-    const E* src = static_cast<const E*>(a.logits) + row * a.Vp + v0;
-    E* dst = static_cast<E*>(a.out) + row * a.Vp + v0;
-    constexpr int kAhead = 4;
-    for (int x0 = tid; x0 < vecs; x0 += kThreads * kAhead) {
-      V16 l[kAhead];
-      uint32_t allowed[kAhead];
-      bool plain[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int x = x0 + k * kThreads, v = v0 + x * kN;
-        if (x >= vecs) continue;
-        allowed[k] = (1u << kN) - 1;
-        if (v + kN > a.V) allowed[k] = v < a.V ? (1u << (a.V - v)) - 1 : 0;
-        if (mask != nullptr && v < a.V) allowed[k] &= __ldg(mask + (v >> 5)) >> (v & 31);
-        if (none) allowed[k] = 0;
-        plain[k] = true;
-        if (a.words && x * kN < a.seg) {
-          const uint4* w = reinterpret_cast<const uint4*>(words + x * kN);
-#pragma unroll
-          for (int q = 0; q < kN / 4; ++q) {
-            const uint4 y = w[q];
-            plain[k] &= (y.x | y.y | y.z | y.w) == 0;
+    if (r.num_masks > 0 && i + 1 < n1) fetch_mask(mask_rows[i + 1]);
+    bool there = true;
+    if (pending >> stage & 1) {
+      pending ^= 1u << stage;
+      there = mbar_wait(full + stage, phases >> stage & 1);
+      phases ^= 1u << stage;
+    }
+    if (set != 0) {
+      E* x = kInPlace ? dst(i) : reinterpret_cast<E*>(shared_raw + stage * stage_bytes);
+      // the node's path: a token that stands on it twice is the first one's
+      const unsigned long long path = set & in_segment;
+      bool mine = false;
+      E was = from_f32<E>(0.f);
+      if (path != 0) {
+        if (tid < kMaxNodes && (path >> tid & 1)) {
+          mine = (same[tid] & path & ((1ull << tid) - 1)) == 0;
+          if (mine) was = x[toks[tid]];
+        }
+        __syncthreads();
+      }
+      for (int e = tid; e < slots; e += kThreads) {
+        const int t = token_of[e];
+        x[t] = adjust_one(x[t], word[e], bias[e], pen);
+      }
+      if (path != 0) {
+        __syncthreads();
+        if (mine) {
+          const int t = toks[tid];
+          const bool known = slots > 0 && (has_slot[t >> 5] >> (t & 31) & 1) != 0;
+          const int e = known ? slot_of[t] : 0;
+          x[t] = adjust_one(was, (known ? word[e] : 0u) + __popcll(same[tid] & path), known ? bias[e] : -1, pen);
+        }
+      }
+      if (masked || last) {
+        __syncthreads();
+        if (masked) {
+          uint4* x4 = reinterpret_cast<uint4*>(x);
+#pragma unroll 4
+          for (int at = tid; at < vecs; at += kThreads) {
+            const uint32_t bits = mask[at * kN / 32] >> (at * kN % 32) & ((1u << kN) - 1);
+            if (bits != (1u << kN) - 1) x4[at] = ruled_out<E>(x4[at], bits);
           }
         }
-        const bool all = allowed[k] == (1u << kN) - 1;
-        if (!kInPlace || (allowed[k] != 0 && !(all && plain[k])))
-          l[k].raw = __ldcs(reinterpret_cast<const uint4*>(src) + x);
-      }
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int x = x0 + k * kThreads;
-        if (x >= vecs) continue;
-        const bool all = allowed[k] == (1u << kN) - 1;
-        if (kInPlace && all && plain[k]) continue;
-        if (!plain[k]) {
-#pragma unroll
-          for (int e = 0; e < kN; ++e) {
-            const uint32_t w = words[x * kN + e];
-            if (w != 0 && (allowed[k] >> e & 1)) l[k].e[e] = from_f32<E>(adjust_one(to_f32(l[k].e[e]), w, pen));
+        if (last) {  // the padding, the rest of the last vector first
+          __syncthreads();
+          const int ragged = (v1 - v0) % kN;
+          if (tid == 0 && ragged != 0) {
+            uint4* p = reinterpret_cast<uint4*>(x) + vecs - 1;
+            *p = ruled_out<E>(*p, (1u << ragged) - 1);
           }
+          uint4* pad = reinterpret_cast<uint4*>(dst(i)) + vecs;
+          for (int at = tid; at < (a.Vp - v0) / kN - vecs; at += kThreads) pad[at] = lowest;
         }
-        if (!all) {
-#pragma unroll
-          for (int e = 0; e < kN; ++e)
-            if ((allowed[k] >> e & 1) == 0) l[k].e[e] = lowest;
-        }
-        __stcs(reinterpret_cast<uint4*>(dst) + x, l[k].raw);
       }
+    }
+    if (!kInPlace) {
+      fence_proxy_async_smem();
+      // where a copy did not come (flagged by the wait) the others are awaited and
+      // nothing more is stored
+      alive = __syncthreads_and(there) && alive;
+      const int next = i + a.stages - 1;
+      const bool more = alive && i > n0 && next < n1 && sets[next] != 0;
+      if (more) pending |= 1u << (next - n0) % a.stages;
+      if (tid == 0) {
+        if (alive && set != 0) bulk_store(dst(i), shared_raw + stage * stage_bytes, columns * sizeof(E));
+        bulk_commit_group();
+        if (more) {  // into the stage of the row before, once that is read out
+          bulk_wait_group_read<1>();
+          load(next);
+        }
+      }
+    } else if (masked) {
+      __syncthreads();  // the mask's words are replaced
     }
   }
+  if (!kInPlace && tid == 0) bulk_wait_group_read<0>();
+}
+
+template <typename E, bool kInPlace>
+int adjust_launch(const AdjustArgs& a, cudaStream_t s) {
+  static bool allowed[kMaxDevices] = {};
+  auto bytes = [](size_t stages, size_t seg, size_t slots) {
+    return stages * seg * sizeof(E) + (slots > 0 ? seg / 8 + seg * 2 + slots * 10 : 0);
+  };
+  constexpr size_t kMaxSeg = kSegBytes / sizeof(E);
+  const size_t most = bytes(kInPlace ? 0 : kStages, kMaxSeg, kMaxSeg);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < kMaxDevices && !allowed[dev]) {
+    e = cudaFuncSetAttribute(logits_adjust_kernel<E, kInPlace>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(most));
+    allowed[dev] = e == cudaSuccess;
+  }
+  const dim3 grid((a.V + a.seg - 1) / a.seg, (a.N + a.nodes - 1) / a.nodes, a.B);
+  if (e == cudaSuccess)
+    e = launch_pdl(logits_adjust_kernel<E, kInPlace>, grid, dim3(kThreads), bytes(kInPlace ? 0 : a.stages, a.seg, a.slots),
+                   s, a);
+  return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
 }
 
 template <typename E>
-int adjust_typed(const AdjustArgs& a, cudaStream_t s) {
-  const dim3 grid((a.V + a.seg - 1) / a.seg, (a.N + a.nodes - 1) / a.nodes, a.B);
-  const size_t smem = a.words ? a.seg * sizeof(uint32_t) : 0;
-  const cudaError_t e = a.out == a.logits ? launch_pdl(logits_adjust_kernel<E, true>, grid, dim3(kThreads), smem, s, a)
-                                          : launch_pdl(logits_adjust_kernel<E, false>, grid, dim3(kThreads), smem, s, a);
-  return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
+int adjust_typed(AdjustArgs a, cudaStream_t s) {
+  // segments and groups of rows as large as still leave some CTAs to each SM, and
+  // no more than 16 rows, which makes the last CTAs end together (64 sequences of
+  // 64 nodes, 50257 fp32: 64 rows 317 us, 32 293, 16 284, 8 311)
+  const long long want = 4LL * num_sms();
+  a.nodes = std::min(a.N, 16);
+  a.seg = kSegBytes / static_cast<int>(sizeof(E));
+  auto segments = [&]() { return static_cast<long long>((a.V + a.seg - 1) / a.seg) * a.B; };
+  while (a.seg > 1024 && segments() < want) a.seg /= 2;
+  while (a.nodes > 1 && segments() * ((a.N + a.nodes - 1) / a.nodes) < want) a.nodes = (a.nodes + 1) / 2;
+  a.stages = std::min(kStages, a.nodes);
+  a.slots = std::min(a.seg, (a.r.history_stride + a.r.num_bias + 7) / 8 * 8);
+  return a.out == a.logits ? adjust_launch<E, true>(a, s) : adjust_launch<E, false>(a, s);
 }
 
 }  // namespace
 
 int launch_logits_adjust(void* out, const void* logits, int logits_type, const GPT2LogitRules& r, const int* tok,
                          const int* parent, int B, int N, int V, int Vp, cudaStream_t s) {
-  AdjustArgs a{out, logits, r, tok, parent, B, N, V, Vp, 0, 0, false};
-  a.words = r.history_stride > 0 || r.num_bias > 0 || tok != nullptr;
-  // segments as long as still leave a CTA or two to each SM
-  const long long want = 4LL * num_sms();
-  a.nodes = N;
-  a.seg = 8192;
-  while (a.seg > 1024 && static_cast<long long>((V + a.seg - 1) / a.seg) * B < want) a.seg /= 2;
-  while (a.nodes > 1 && static_cast<long long>((V + a.seg - 1) / a.seg) * ((N + a.nodes - 1) / a.nodes) * B < want)
-    a.nodes = (a.nodes + 1) / 2;
+  const AdjustArgs a{out, logits, r, tok, parent, B, N, V, Vp, 0, 0, 0, 0};
   if (logits_type == GPT2_PROBS_F32) return adjust_typed<float>(a, s);
   if (logits_type == GPT2_PROBS_F16) return adjust_typed<__half>(a, s);
   return adjust_typed<__nv_bfloat16>(a, s);
