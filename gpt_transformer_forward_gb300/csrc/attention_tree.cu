@@ -1,16 +1,17 @@
 // attention_tree.cu -- attention of a tree of drafted tokens a sequence over its
 // cached positions and the tree itself.
 //
-// For a pair (sequence b, head h) the N nodes' queries against the n = pos[b] + N
-// keys are a matrix product of their own, S = Q K^T, O = P V, with the online
-// softmax of FlashAttention's Algorithm 1 per row; a node sees the cached
-// positions and, among the last N keys, those of its path (a 64-bit set a node).
-// Every key and value is read once for all nodes.
+// For a pair (sequence b, head h) the N nodes' queries against the cached keys
+// and the nodes' own are a matrix product of their own, S = Q K^T, O = P V, with
+// the online softmax of FlashAttention's Algorithm 1 per row; a node sees the
+// cached positions and, among the nodes' keys, those of its path (a 64-bit set a
+// node).  Every key and value is read once for all nodes.
 //
-// The lengths are known on the device only, and differ: all pairs' tiles of 64
-// keys, one pair behind the other, are cut into equal shares of one CTA each.  A
-// share begins and ends inside pairs; a pair that lies in several shares leaves
-// the running maximum m, sum l and unnormalised output O of each part in the
+// The lengths are known on the device only, and differ.  A pair is a row of
+// steps: the nodes' own keys, then tiles of cached ones.  All pairs' steps, one
+// pair behind the other, are cut into equal shares of one CTA each; a share
+// begins and ends inside pairs.  A pair that lies in several shares leaves the
+// running maximum m, sum l and unnormalised output O of each part in the
 // workspace, which tree_join_kernel joins in order.
 //   tree_mma_kernel    16-bit caches, mma.sync
 //   tree_simt_kernel   fp32 caches, CUDA cores
@@ -22,12 +23,12 @@
 namespace gpt2 {
 namespace {
 
-constexpr int kTile = 64;      // keys of a tile
-constexpr int kThreads = 128;
-// Shares at most: three CTAs on each of 152 SMs.  The workspace holds their
-// parts, so the count goes by nothing else.
-constexpr int kMaxCtas = 456;
-constexpr int kMinTiles = 2;   // of a share
+constexpr int kThreads = 128;  // of tree_simt_kernel and tree_join_kernel
+// Shares at most: eight CTAs on each of 152 SMs.  The workspace holds their parts,
+// so the count goes by the number of nodes alone.
+constexpr int ctas_per_sm(int N) { return N <= 16 ? 8 : N <= 32 ? 4 : 2; }
+constexpr int max_ctas(int N) { return 152 * ctas_per_sm(N); }
+constexpr int kMinSteps = 2;   // of a share
 
 struct TreeArgs {
   void* out;
@@ -53,48 +54,56 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs& a, int b, bool report) {
   if (!ok && p != -1 && report) set_error(GPT2_DEVERR_POSITION);
   return {ok ? p : 0, ok ? min(a.N, a.rows.capacity - p) : 0};
 }
-__device__ __forceinline__ int tiles_of(const TreeArgs& a, const Seq& q) { return (q.pos + a.N + kTile - 1) / kTile; }
+// Steps of a pair with tiles of K cached keys.
+template <int K>
+__device__ __forceinline__ int steps_of(const Seq& q) {
+  return 1 + (q.pos + K - 1) / K;
+}
 
-// A place in the row of all pairs' tiles.
+// A place in the row of all pairs' steps: step t of a pair, 0 the nodes' own keys,
+// t > 0 cached keys [(t - 1) K, t K).
 struct Place {
-  int b, h, t, tiles;
+  int b, h, t, steps;
   Seq seq;
 };
+template <int K>
 __device__ __forceinline__ void enter(const TreeArgs& a, Place& p) {
   p.seq = seq_of(a, p.b, false);
-  p.tiles = tiles_of(a, p.seq);
+  p.steps = steps_of<K>(p.seq);
 }
-// The next tile; behind the last one of all, nothing that may be read.
+// The next step; behind the last one of all, nothing that may be read.
+template <int K>
 __device__ __forceinline__ void advance(const TreeArgs& a, Place& p) {
-  if (++p.t < p.tiles) return;
+  if (++p.t < p.steps) return;
   p.t = 0;
   if (++p.h < a.NH) return;
   p.h = 0;
-  if (++p.b < a.B) enter(a, p);
+  if (++p.b < a.B) enter<K>(a, p);
 }
 
-// This CTA's share [begin, end) of the tiles and where it begins (the whole warp
-// calls, every warp for itself).  `per`: the tiles of a share.
+// This CTA's share [begin, end) of the steps and where it begins (the whole warp
+// calls, every warp for itself).  `per`: the steps of a share.
 struct Share {
   long long begin, end, per;
   Place at;
 };
+template <int K>
 __device__ __forceinline__ Share share_of(const TreeArgs& a) {
   const int lane = threadIdx.x & 31;
-  auto tiles_at = [&](int b) { return b < a.B ? tiles_of(a, seq_of(a, b, false)) : 0; };
+  auto steps_at = [&](int b) { return b < a.B ? steps_of<K>(seq_of(a, b, false)) : 0; };
   long long total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, tiles_at(b0 + lane));
+  for (int b0 = 0; b0 < a.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, steps_at(b0 + lane));
   total *= a.NH;
   Share s;
   const long long per = (total + gridDim.x - 1) / gridDim.x;
-  s.per = per > kMinTiles ? per : kMinTiles;
+  s.per = per > kMinSteps ? per : kMinSteps;
   s.begin = min(total, s.per * blockIdx.x);
   s.end = min(total, s.begin + s.per);
   s.at = Place{0, 0, 0, 1, {0, 0}};
   if (s.begin >= s.end) return s;
-  long long before = 0;  // tiles of the sequences ahead, of one head
+  long long before = 0;  // steps of the sequences ahead, of one head
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int mine = tiles_at(b0 + lane);
+    const int mine = steps_at(b0 + lane);
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -104,12 +113,12 @@ __device__ __forceinline__ Share share_of(const TreeArgs& a) {
     const unsigned past = __ballot_sync(0xffffffffu, (before + incl) * a.NH > s.begin);
     if (past != 0) {
       const int l = __ffs(past) - 1;
-      const int tiles = __shfl_sync(0xffffffffu, mine, l);
+      const int steps = __shfl_sync(0xffffffffu, mine, l);
       const long long rest = s.begin - (before + __shfl_sync(0xffffffffu, incl - mine, l)) * a.NH;
       s.at.b = b0 + l;
-      s.at.h = static_cast<int>(rest / tiles);
-      s.at.t = static_cast<int>(rest % tiles);
-      enter(a, s.at);
+      s.at.h = static_cast<int>(rest / steps);
+      s.at.t = static_cast<int>(rest % steps);
+      enter<K>(a, s.at);
       return s;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
@@ -120,14 +129,6 @@ __device__ __forceinline__ Share share_of(const TreeArgs& a) {
 // The row of position j of a sequence's head in a cache half, from its block id.
 __device__ __forceinline__ size_t cache_row(const TreeArgs& a, int blk, int h, int j) {
   return ((static_cast<size_t>(blk) * a.NH + h) << a.rows.lbs) + (j & ((1 << a.rows.lbs) - 1));
-}
-
-// The columns of tile t that node set `set` sees, a bit each.
-__device__ __forceinline__ unsigned long long seen_in(unsigned long long set, int t, int pos) {
-  const int first = t * kTile - pos;  // the node of column 0
-  if (first >= 64) return 0;
-  if (first >= 0) return set >> first;
-  return first <= -64 ? ~0ull : (set << -first) | ((1ull << -first) - 1);
 }
 
 // What is to be joined: entry i holds the pair, the CTA in which it begins and
@@ -145,7 +146,7 @@ struct Part {
 };
 __device__ __forceinline__ Part end_part(const TreeArgs& a, const Share& s, const Place& p, long long i, bool from_start,
                                          int4& open) {
-  const int last = p.tiles - 1 - p.t;  // tiles of the pair behind this one
+  const int last = p.steps - 1 - p.t;  // steps of the pair behind this one
   const bool whole = from_start && last == 0;
   if (from_start) {
     const int pair = p.b * a.NH + p.h;
@@ -173,187 +174,202 @@ __device__ __forceinline__ bool any_not_finite(const uint4& v) {
 }
 
 // ------------------------------------------------------ tensor-core kernel
-// mma.sync m16n8k16, fp32 accumulators.  Four warps: WM groups of 16 nodes times
-// WK = 4 / WM groups of the tile's keys.  Tiles come by cp.async through a ring
-// of three stages, rows of HS * 2 bytes with swizzled 16-byte chunks; any block
-// size, since every chunk finds its own block, whose id is looked up a tile
-// ahead.
-constexpr int kStages = 3;
+// mma.sync m16n8k16, fp32 accumulators.  A CTA is WM warps of 16 nodes each that
+// share every step's keys, which come by TMA through a ring in shared memory (a
+// copy per block of the cache that a tile touches, one where blocks are as long as
+// tiles); up to 16 nodes a CTA is one warp, eight of them an SM, that needs no
+// barrier but the copies'.  Block ids are looked up a step ahead.
 template <int HS, int WM>
-struct TreeSmem {
-  static constexpr int WK = 4 / WM;
-  static constexpr int kJoinRow = HS + 4;
-  struct Stage {
-    uint8_t k[kTile * HS * 2];
-    uint8_t v[kTile * HS * 2];
-    uint8_t q[WM * 16 * HS * 2];  // where a pair begins
-  } stage[kStages];
-  float o[WK > 1 ? 4 - WM : 1][WK > 1 ? 16 : 1][kJoinRow];
-  float2 ml[4][16];
+struct TreeRing {
+  static constexpr int kKeys = WM == 1 ? 32 : 64;   // of a tile
+  static constexpr int kRow = HS * 2;               // bytes of a key
+  static constexpr int kTileBytes = kKeys * kRow;
+  static constexpr int kNodeBytes = 16 * WM * kRow;  // of the nodes' queries, keys or values
+  static constexpr int kStage = 2 * kTileBytes > 3 * kNodeBytes ? 2 * kTileBytes : 3 * kNodeBytes;
+  static constexpr int kStages = (WM == 4 ? 4 : 3) * (HS == 64 ? 1 : 2);
+  // The ring begins at a multiple of 1024 bytes, the barriers stand behind it: with
+  // shared memory of the kernel's own beside it the dynamic one begins anywhere.
+  static constexpr int kSmem = 1024 + kStages * kStage + kStages * 8;
+  static constexpr CUtensorMapSwizzle kSwizzle = HS == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                 : HS == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                            : CU_TENSOR_MAP_SWIZZLE_32B;
 };
+// Byte offset of 16-byte chunk c of row r in a tile that TMA wrote with that
+// swizzle: the chunk's number is combined with the 128-byte line's.
+template <int HS>
+__device__ __forceinline__ uint32_t tile_at(int r, int c) {
+  constexpr int kChunks = HS / 8;
+  return static_cast<uint32_t>(r * (HS * 2) + ((c ^ (r / (8 / kChunks) & (kChunks - 1))) << 4));
+}
 
 template <int HS, typename T16, int WM>
-__global__ void __launch_bounds__(kThreads) tree_mma_kernel(TreeArgs a) {
-  constexpr int WK = 4 / WM, KW = kTile / WK;  // keys of a warp
-  constexpr int kNT = KW / 8, kPS = KW / 16;   // score column tiles, k-steps of P V
+__global__ void __launch_bounds__(32 * WM)
+    tree_mma_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                    const __grid_constant__ CUtensorMap map_qkv, TreeArgs a) {
+  using Ring = TreeRing<HS, WM>;
+  constexpr int K = Ring::kKeys, kStages = Ring::kStages;
   constexpr int kKS = HS / 16, kDT = HS / 8, kChunks = HS / 8;
-  constexpr int kCopies = kTile * kChunks / kThreads;  // 16-byte chunks of a K tile a thread copies
-  using Smem = TreeSmem<HS, WM>;
-  extern __shared__ __align__(128) uint8_t shared_raw[];
-  auto& sm = *reinterpret_cast<Smem*>(shared_raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wm = warp % WM, wk = warp / WM;
+  extern __shared__ uint8_t tree_ring_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tree_ring_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * Ring::kStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;  // warp: its nodes are 16 warp ..
   const int g = lane >> 2, tig = lane & 3;
-  const uint16_t* qkv = static_cast<const uint16_t*>(a.qkv);
   uint16_t* kcache = static_cast<uint16_t*>(a.kcache);
   uint16_t* vcache = static_cast<uint16_t*>(a.vcache);
-  const int C3 = 3 * a.C;
+  auto sync = [&]() {
+    if constexpr (WM == 1)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+    tma_prefetch_desc(&map_qkv);
+    for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1);
+    fence_barrier_init();
+  }
   pdl_wait();  // the QKV projection ahead has finished
   pdl_trigger();
-  const Share sh = share_of(a);
+  const Share sh = share_of<K>(a);
   int4 open = make_int4(-1, 0, 0, 0);
+  sync();  // the barriers
 
-  // copies run up to two tiles ahead of the products, across pairs
+  // The share's copies, in order; a share that begins inside a pair has one step
+  // more at the start, for the queries.  Warp 0 issues them.
+  const int lead = sh.begin < sh.end && sh.at.t > 0 ? 1 : 0;
+  const long long n_steps = sh.end - sh.begin + lead;
   Place ld = sh.at;
-  long long ld_i = sh.begin;
-  int ids[kCopies];
-  auto lookup = [&]() {
+  long long ld_i = -lead;  // of the share's steps
+  constexpr int kIds = (K + 31) / 32;
+  int ids[kIds];
+  const int box = min(K, 1 << a.rows.lbs), boxes = K / box;  // of a tile
+  // a tiled copy begins at a multiple of 128 bytes in shared memory; smaller boxes
+  // (one position of 32 dimensions, one or two of 16) are copied by 16 bytes
+  const bool tiled = box * Ring::kRow >= 128;
+  auto lookup = [&]() {  // lane i: the blocks of a tile's boxes i and i + 32
+    if (ld.t == 0) return;
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const int j = ld.t * kTile + (static_cast<int>(threadIdx.x) + i * kThreads) / kChunks;
-      ids[i] = j < ld.seq.pos ? __ldg(a.rows.table + static_cast<size_t>(ld.b) * a.rows.max_blocks + (j >> a.rows.lbs)) : 0;
+    for (int u = 0; u < kIds; ++u) {
+      const int j = (ld.t - 1) * K + (lane + 32 * u) * box;
+      ids[u] = lane + 32 * u < boxes && j < ld.seq.pos
+                   ? __ldg(a.rows.table + static_cast<size_t>(ld.b) * a.rows.max_blocks + (j >> a.rows.lbs))
+                   : 0;
     }
   };
-  auto copy = [&](int stage) {
-    if (ld_i < sh.end) {
-      auto& st = sm.stage[stage];
+  auto copy = [&](int stage) {  // warp 0
+    if (ld_i + lead >= n_steps) return;
+    uint8_t* st = ring + stage * Ring::kStage;
+    uint64_t* bar = full + stage;
+    if (ld_i < 0 || ld.t == 0) {
+      if (lane == 0) {
+        const int x = ld.h * HS, y = ld.b * a.N;
+        mbar_arrive_expect_tx(bar, (ld_i < 0 ? 1 : 3) * Ring::kNodeBytes);
+        tma_load_2d(st, &map_qkv, bar, x, y);
+        if (ld_i >= 0) {
+          tma_load_2d(st + Ring::kNodeBytes, &map_qkv, bar, a.C + x, y);
+          tma_load_2d(st + 2 * Ring::kNodeBytes, &map_qkv, bar, 2 * a.C + x, y);
+        }
+      }
+    } else {
+      const int j0 = (ld.t - 1) * K, left = ld.seq.pos - j0;
+      const int n = min(boxes, (left + box - 1) / box);  // boxes that hold a cached position
+      if (lane == 0) mbar_arrive_expect_tx(bar, 2 * n * box * Ring::kRow);
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        const int x = static_cast<int>(threadIdx.x) + i * kThreads;
-        const int r = x / kChunks, c = x % kChunks, j = ld.t * kTile + r, node = j - ld.seq.pos;
-        const uint16_t *ks, *vs;
-        const bool valid = node < a.N;
-        if (node < 0) {
-          int blk = ids[i];
-          if (blk < 0 || blk >= a.rows.num_blocks) {
-            if (ld.h == 0) set_error(GPT2_DEVERR_BLOCK);
-            blk = 0;
+      for (int u = 0; u < kIds; ++u) {
+        const int i = lane + 32 * u;
+        if (i >= n) continue;
+        if (ids[u] < 0 || ids[u] >= a.rows.num_blocks) {
+          if (ld.h == 0) set_error(GPT2_DEVERR_BLOCK);
+          ids[u] = 0;
+        }
+        if (tiled) {
+          const int y = (j0 + i * box) & ((1 << a.rows.lbs) - 1), to = i * box * Ring::kRow;
+          tma_load_4d(st + to, &map_k, bar, 0, y, ld.h, ids[u]);
+          tma_load_4d(st + Ring::kTileBytes + to, &map_v, bar, 0, y, ld.h, ids[u]);
+        }
+      }
+      if (!tiled) {
+        __syncwarp();
+        for (int x0 = 0; x0 < n * box * kChunks; x0 += 32) {
+          const int x = x0 + lane, r = x / kChunks, c = x % kChunks, i = r >> a.rows.lbs;
+          int blk = __shfl_sync(0xffffffffu, ids[0], i & 31);
+          if constexpr (kIds > 1) {
+            const int high = __shfl_sync(0xffffffffu, ids[kIds - 1], i & 31);
+            if (i >= 32) blk = high;
           }
-          const size_t at = cache_row(a, blk, ld.h, j) * HS + c * 8;
-          ks = kcache + at;
-          vs = vcache + at;
-        } else {
-          ks = qkv + (static_cast<size_t>(ld.b) * a.N + (valid ? node : 0)) * C3 + a.C + ld.h * HS + c * 8;
-          vs = ks + a.C;
-        }
-        cp_async16(st.k + swz<HS>(r, c), ks, valid);
-        cp_async16(st.v + swz<HS>(r, c), vs, valid);
-      }
-      if (ld.t == 0 || ld_i == sh.begin) {
-        for (int x = threadIdx.x; x < WM * 16 * kChunks; x += kThreads) {
-          const int r = x / kChunks, c = x % kChunks;
-          const bool valid = r < a.N;
-          cp_async16(st.q + swz<HS>(r, c),
-                     qkv + (static_cast<size_t>(ld.b) * a.N + (valid ? r : 0)) * C3 + ld.h * HS + c * 8, valid);
+          if (x < n * box * kChunks) {
+            const size_t from = cache_row(a, blk, ld.h, j0 + r) * HS + c * 8;
+            bulk_load(st + tile_at<HS>(r, c), kcache + from, 16, bar);
+            bulk_load(st + Ring::kTileBytes + tile_at<HS>(r, c), vcache + from, 16, bar);
+          }
         }
       }
-      advance(a, ld);
-      if (++ld_i < sh.end) lookup();
     }
-    cp_async_commit();
+    if (ld_i >= 0) advance<K>(a, ld);
+    ++ld_i;
+    if (ld_i + lead < n_steps) lookup();
   };
-  if (sh.begin < sh.end) lookup();
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) copy(s);
+  if (warp == 0) {
+    if (n_steps > 0 && lead == 0) lookup();
+    for (int s = 0; s < kStages - 1; ++s) copy(s);
+  }
 
   Place at = sh.at;
-  bool from_start = false, have_sets = false;
-  int par[2] = {-2, -2};
-  unsigned long long set[2] = {0, 0}, live = 0;  // rows g and g + 8; the nodes that are there
+  bool from_start = false;
+  unsigned long long set[2] = {0, 0};  // rows g and g + 8, known from the pair's first step on
   uint32_t qf[kKS][4];
   float o[kDT][4], m_r[2], l_r[2];
-  for (long long i = sh.begin; i < sh.end; ++i) {
-    const int stage = static_cast<int>((i - sh.begin) % kStages);
-    cp_async_wait<kStages - 2>();
-    __syncthreads();  // the tile is there, and every warp is past the one whose stage is refilled now
-    copy((stage + kStages - 1) % kStages);
-    const auto& st = sm.stage[stage];
-    if (i == sh.begin || at.t == 0) {
-      from_start = at.t == 0;
-      have_sets = false;
+  auto begin_pair = [&](const uint8_t* q) {
 #pragma unroll
-      for (int x = 0; x < kDT; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
-      m_r[0] = m_r[1] = -INFINITY;
-      l_r[0] = l_r[1] = 0.f;
-      const int* row = a.parent != nullptr ? a.parent + static_cast<size_t>(at.b) * a.N : nullptr;
+    for (int x = 0; x < kDT; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
+    m_r[0] = m_r[1] = -INFINITY;
+    l_r[0] = l_r[1] = 0.f;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) par[u] = at.seq.live > 0 ? tree_parent(row, lane + 32 * u, a.N) : -2;
-      if (from_start && at.h == 0 && threadIdx.x == 0) seq_of(a, at.b, true);
+    for (int ks = 0; ks < kKS; ++ks)
+      ldsm_x4(smem_u32(q) + tile_at<HS>(warp * 16 + (lane & 15), ks * 2 + (lane >> 4)), qf[ks][0], qf[ks][1], qf[ks][2],
+              qf[ks][3]);
+  };
+  // rows of a tile that hold no key: 0 times what stands there may not be 0
+  auto zero_rows = [&](uint8_t* v, int from, int to) {
+    for (int x = lane; x < (to - from) * kChunks; x += 32)
+      *reinterpret_cast<uint4*>(v + from * Ring::kRow + x * 16) = make_uint4(0u, 0u, 0u, 0u);  // whole rows: any order
+    fence_proxy_async_smem();  // before the next copy into the stage
+    __syncwarp();
+  };
+  // The online softmax and O += P V over 8 NT keys, of which rows g and g + 8 see
+  // those of `seen` where `some` is set.  odd: a value may not be finite.
+  auto attend = [&](auto nt_c, const uint8_t* kt, const uint8_t* vt, bool some, const unsigned long long (&seen)[2],
+                    bool odd) {
+    constexpr int NT = decltype(nt_c)::value;
+    float s[NT][4];
 #pragma unroll
-      for (int ks = 0; ks < kKS; ++ks)
-        ldsm_x4(smem_u32(st.q) + swz<HS>(wm * 16 + (lane & 15), ks * 2 + (lane >> 4)), qf[ks][0], qf[ks][1], qf[ks][2],
-                qf[ks][3]);
-    }
-    const bool tree = (at.t + 1) * kTile > at.seq.pos;  // nodes are among the tile's keys
-    unsigned long long seen[2] = {~0ull, ~0ull};
-    bool odd = false;  // a value that is not finite: 0 times it is not 0
-    if (tree) {
-      if (!have_sets) {
-        have_sets = true;
-        const TreeSets ts = tree_sets(par, a.N, at.seq.live, at.h == 0 && warp == 0);
-        set[0] = tree_set_of(ts, wm * 16 + g);
-        set[1] = tree_set_of(ts, wm * 16 + g + 8);
-        live = tree_live(ts);
-      }
-      bool bad = false;
-#pragma unroll 1
-      for (int x = threadIdx.x; x < kTile * kChunks; x += kThreads) {
-        const int r = x / kChunks, c = x % kChunks, j = at.t * kTile + r, node = j - at.seq.pos;
-        if (node < 0 || node >= a.N) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(st.v + swz<HS>(r, c));
-        bad |= any_not_finite<T16>(v);
-        if ((live >> node & 1) == 0) continue;
-        const int blk = __ldg(a.rows.table + static_cast<size_t>(at.b) * a.rows.max_blocks + (j >> a.rows.lbs));
-        if (blk < 0 || blk >= a.rows.num_blocks) {
-          if (at.h == 0) set_error(GPT2_DEVERR_BLOCK);
-          continue;
-        }
-        const size_t to = cache_row(a, blk, at.h, j) * HS + c * 8;
-        *reinterpret_cast<uint4*>(kcache + to) = *reinterpret_cast<const uint4*>(st.k + swz<HS>(r, c));
-        *reinterpret_cast<uint4*>(vcache + to) = v;
-      }
-      odd = __syncthreads_or(bad);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) seen[r] = seen_in(set[r], at.t, at.seq.pos) >> (wk * KW);
-    }
-    float s[kNT][4];
-#pragma unroll
-    for (int x = 0; x < kNT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
-    const uint32_t kb = smem_u32(st.k), vb = smem_u32(st.v);
+    for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+    const uint32_t kb = smem_u32(kt), vb = smem_u32(vt);
 #pragma unroll
     for (int ks = 0; ks < kKS; ++ks) {
 #pragma unroll
-      for (int np = 0; np < kNT / 2; ++np) {
+      for (int np = 0; np < NT / 2; ++np) {
         uint32_t r0, r1, r2, r3;
-        ldsm_x4(kb + swz<HS>(wk * KW + np * 16 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)), r0, r1, r2,
-                r3);
+        ldsm_x4(kb + tile_at<HS>(np * 16 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)), r0, r1, r2, r3);
         mma16<T16>(s[2 * np], qf[ks], r0, r1);
         mma16<T16>(s[2 * np + 1], qf[ks], r2, r3);
       }
     }
-    if (tree) {
+    if (some) {
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if ((seen[e >> 1] >> (nt * 8 + 2 * tig + (e & 1)) & 1) == 0) s[nt][e] = -INFINITY;
     }
-    // online softmax in log2 units: rows g (e = 0, 1) and g + 8 (e = 2, 3)
+    // in log2 units: rows g (e = 0, 1) and g + 8 (e = 2, 3)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float mx = -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) mx = fmax3(mx, s[nt][2 * r], s[nt][2 * r + 1]);
+      for (int nt = 0; nt < NT; ++nt) mx = fmax3(mx, s[nt][2 * r], s[nt][2 * r + 1]);
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const float m_new = fmaxf(m_r[r], mx * a.scale_log2);
@@ -362,7 +378,7 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(TreeArgs a) {
       m_r[r] = m_new;
       float sum = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt) {
         s[nt][2 * r] = exp2_approx(fmaf(s[nt][2 * r], a.scale_log2, -ref));
         s[nt][2 * r + 1] = exp2_approx(fmaf(s[nt][2 * r + 1], a.scale_log2, -ref));
         sum += s[nt][2 * r] + s[nt][2 * r + 1];
@@ -375,11 +391,11 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(TreeArgs a) {
       }
     }
     if (!odd) {
-      // O += P V: P's accumulator layout is the A-operand layout of k-steps.  Its
-      // values, at most 1, enter as sums of two values of the operands' type, so
-      // that a node's row has the precision of a decode step's
+      // P's accumulator layout is the A-operand layout of k-steps.  Its values, at
+      // most 1, enter as sums of two values of the operands' type, so that a node's
+      // row has the precision of a decode step's
 #pragma unroll
-      for (int ks = 0; ks < kPS; ++ks) {
+      for (int ks = 0; ks < NT / 2; ++ks) {
         uint32_t pa[4], pl[4];
         split2<T16>(s[2 * ks][0], s[2 * ks][1], pa[0], pl[0]);
         split2<T16>(s[2 * ks][2], s[2 * ks][3], pa[1], pl[1]);
@@ -388,8 +404,7 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(TreeArgs a) {
 #pragma unroll
         for (int dp = 0; dp < kDT / 2; ++dp) {
           uint32_t r0, r1, r2, r3;
-          ldsm_x4_t(vb + swz<HS>(wk * KW + ks * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), dp * 2 + (lane >> 4)), r0, r1,
-                    r2, r3);
+          ldsm_x4_t(vb + tile_at<HS>(ks * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), dp * 2 + (lane >> 4)), r0, r1, r2, r3);
           mma16<T16>(o[2 * dp], pl, r0, r1);
           mma16<T16>(o[2 * dp + 1], pl, r2, r3);
           mma16<T16>(o[2 * dp], pa, r0, r1);
@@ -397,10 +412,10 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(TreeArgs a) {
         }
       }
     } else {
-      // a node's value holds an infinity or a NaN, which only the rows that see
-      // it may take in: key by key, each probability from the lane that holds it
+      // a node's value holds an infinity or a NaN, which only the rows that see it
+      // may take in: key by key, each probability from the lane that holds it
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll 1
         for (int x = 0; x < 8; ++x) {
           const int key = nt * 8 + x, from = (lane & ~3) | (x >> 1);
@@ -412,8 +427,7 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(TreeArgs a) {
             const float p = (x & 1) ? p1 : p0;
 #pragma unroll
             for (int dt = 0; dt < kDT; ++dt) {
-              const uint32_t raw = *reinterpret_cast<const uint32_t*>(st.v + swz<HS>(wk * KW + key, dt) + 4 * tig);
-              const float2 v = unpack2<T16>(raw);
+              const float2 v = unpack2<T16>(*reinterpret_cast<const uint32_t*>(vt + tile_at<HS>(key, dt) + 4 * tig));
               o[dt][2 * r] = fmaf(p, v.x, o[dt][2 * r]);
               o[dt][2 * r + 1] = fmaf(p, v.y, o[dt][2 * r + 1]);
             }
@@ -421,84 +435,99 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(TreeArgs a) {
         }
       }
     }
-    if (at.t + 1 == at.tiles || i + 1 == sh.end) {  // the pair's part in this share is done
+  };
+  uint32_t stage = 0, phase = 0;
+  for (long long n = 0; n < n_steps; ++n) {
+    const bool came = mbar_wait(full + stage, phase);
+    // the step's keys are there, and every warp is past the step whose stage is
+    // refilled now; a copy that did not come (flagged by the wait) ends the share
+    const bool lost = WM == 1 ? __any_sync(0xffffffffu, !came) : __syncthreads_or(!came);
+    if (lost) {
+      if (warp == 0)
+        for (long long k = n; k < ld_i + lead; ++k) mbar_wait(full + k % kStages, k / kStages & 1);
+      break;
+    }
+    if (warp == 0) copy((stage + kStages - 1) % kStages);
+    uint8_t* st = ring + stage * Ring::kStage;
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+    if (n < lead) {  // the queries of the pair inside which the share begins
+      begin_pair(st);
+      from_start = false;
+      continue;
+    }
+    if (at.t == 0) {
+      from_start = true;
+      begin_pair(st);
+      const int* row = a.parent != nullptr ? a.parent + static_cast<size_t>(at.b) * a.N : nullptr;
+      int par[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) par[u] = at.seq.live > 0 ? tree_parent(row, lane + 32 * u, a.N) : -2;
+      const bool report = at.h == 0 && warp == 0;
+      if (report && lane == 0) seq_of(a, at.b, true);
+      const TreeSets ts = tree_sets(par, a.N, at.seq.live, report);
+      set[0] = tree_set_of(ts, warp * 16 + g);
+      set[1] = tree_set_of(ts, warp * 16 + g + 8);
+      const unsigned long long live = tree_live(ts);
+      const uint8_t* kt = st + Ring::kNodeBytes;
+      uint8_t* vt = st + 2 * Ring::kNodeBytes;
+      // this warp's nodes are stored; every warp looks at all values
+      bool bad = false;
+      for (int x = lane; x < a.N * kChunks; x += 32) {
+        const int node = x / kChunks, c = x % kChunks;
+        const uint4 v = *reinterpret_cast<const uint4*>(vt + tile_at<HS>(node, c));
+        bad |= any_not_finite<T16>(v);
+        if (node / 16 != warp || (live >> node & 1) == 0) continue;
+        const int j = at.seq.pos + node;
+        const int blk = __ldg(a.rows.table + static_cast<size_t>(at.b) * a.rows.max_blocks + (j >> a.rows.lbs));
+        if (blk < 0 || blk >= a.rows.num_blocks) {
+          if (at.h == 0) set_error(GPT2_DEVERR_BLOCK);
+          continue;
+        }
+        const size_t to = cache_row(a, blk, at.h, j) * HS + c * 8;
+        *reinterpret_cast<uint4*>(kcache + to) = *reinterpret_cast<const uint4*>(kt + tile_at<HS>(node, c));
+        *reinterpret_cast<uint4*>(vcache + to) = v;
+      }
+      zero_rows(vt, a.N, 16 * WM);
+      attend(std::integral_constant<int, 2 * WM>{}, kt, vt, true, set, __any_sync(0xffffffffu, bad));
+    } else {
+      const int valid = at.seq.pos - (at.t - 1) * K;
+      const unsigned long long cols = valid >= K ? ~0ull : (1ull << valid) - 1;
+      const unsigned long long seen[2] = {cols, cols};
+      if (valid < K) zero_rows(st + Ring::kTileBytes, valid, K);
+      attend(std::integral_constant<int, K / 8>{}, st, st + Ring::kTileBytes, valid < K, seen, false);
+    }
+    const long long i = sh.begin + n - lead;
+    if (at.t + 1 == at.steps || i + 1 == sh.end) {  // the pair's part in this share is done
       const Part part = end_part(a, sh, at, i, from_start, open);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         l_r[r] += __shfl_xor_sync(0xffffffffu, l_r[r], 1);
         l_r[r] += __shfl_xor_sync(0xffffffffu, l_r[r], 2);
-      }
-      if constexpr (WK > 1) {  // the key groups' results join in shared memory
+        const int node = warp * 16 + g + 8 * r;
+        if (node >= a.N) continue;
+        const bool missing = from_start && set[r] == 0;
+        if (part.whole) {
+          const float inv = 1.0f / l_r[r];
+          uint16_t* to = static_cast<uint16_t*>(a.out) + (static_cast<size_t>(at.b) * a.N + node) * a.C + at.h * HS;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (tig == 0) sm.ml[warp][g + 8 * r] = make_float2(m_r[r], l_r[r]);
-        if (wk > 0) {
+          for (int dt = 0; dt < kDT; ++dt)
+            *reinterpret_cast<uint32_t*>(to + dt * 8 + 2 * tig) =
+                missing ? 0u : pack2<T16>(o[dt][2 * r] * inv, o[dt][2 * r + 1] * inv);
+        } else {
+          const size_t to = part.slot * a.N + node;
+          // a sum of -1 tells the join that the node is missing
+          if (tig == 0) a.part.ml[to] = make_float2(m_r[r], missing ? -1.f : l_r[r]);
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int dt = 0; dt < kDT; ++dt)
-              *reinterpret_cast<float2*>(&sm.o[warp - WM][g + 8 * r][dt * 8 + 2 * tig]) =
-                  make_float2(o[dt][2 * r], o[dt][2 * r + 1]);
-        }
-        __syncthreads();
-        if (wk == 0) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float M = m_r[r];
-#pragma unroll
-            for (int w = 1; w < WK; ++w) M = fmaxf(M, sm.ml[wm + w * WM][g + 8 * r].x);
-            const float ref = M == -INFINITY ? 0.f : M;
-            const float f = exp2_approx(m_r[r] - ref);
-            m_r[r] = M;
-            l_r[r] *= f;
-#pragma unroll
-            for (int dt = 0; dt < kDT; ++dt) {
-              o[dt][2 * r] *= f;
-              o[dt][2 * r + 1] *= f;
-            }
-#pragma unroll
-            for (int w = 1; w < WK; ++w) {
-              const float2 ml = sm.ml[wm + w * WM][g + 8 * r];
-              const float fw = exp2_approx(ml.x - ref);
-              l_r[r] = fmaf(ml.y, fw, l_r[r]);
-#pragma unroll
-              for (int dt = 0; dt < kDT; ++dt) {
-                const float2 ow = *reinterpret_cast<const float2*>(&sm.o[wm + (w - 1) * WM][g + 8 * r][dt * 8 + 2 * tig]);
-                o[dt][2 * r] = fmaf(ow.x, fw, o[dt][2 * r]);
-                o[dt][2 * r + 1] = fmaf(ow.y, fw, o[dt][2 * r + 1]);
-              }
-            }
-          }
-        }
-      }
-      if (wk == 0) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int node = wm * 16 + g + 8 * r;
-          if (node >= a.N) continue;
-          const bool there = set[r] != 0;  // known where have_sets
-          if (part.whole) {
-            const float inv = there ? 1.0f / l_r[r] : 0.f;
-            uint16_t* to = static_cast<uint16_t*>(a.out) + (static_cast<size_t>(at.b) * a.N + node) * a.C + at.h * HS;
-#pragma unroll
-            for (int dt = 0; dt < kDT; ++dt)
-              *reinterpret_cast<uint32_t*>(to + dt * 8 + 2 * tig) =
-                  there ? pack2<T16>(o[dt][2 * r] * inv, o[dt][2 * r + 1] * inv) : 0u;
-          } else {
-            const size_t to = part.slot * a.N + node;
-            // a sum of -1 tells the join that the node is missing
-            if (tig == 0) a.part.ml[to] = make_float2(m_r[r], have_sets && !there ? -1.f : l_r[r]);
-#pragma unroll
-            for (int dt = 0; dt < kDT; ++dt)
-              *reinterpret_cast<float2*>(a.part.o + to * HS + dt * 8 + 2 * tig) =
-                  make_float2(o[dt][2 * r], o[dt][2 * r + 1]);
-          }
+          for (int dt = 0; dt < kDT; ++dt)
+            *reinterpret_cast<float2*>(a.part.o + to * HS + dt * 8 + 2 * tig) = make_float2(o[dt][2 * r], o[dt][2 * r + 1]);
         }
       }
     }
-    advance(a, at);
+    advance<K>(a, at);
   }
-  cp_async_wait<0>();
   if (!split_by_pair(a) && threadIdx.x == 0) a.part.split[blockIdx.x] = open;
 }
 
@@ -506,13 +535,15 @@ __global__ void __launch_bounds__(kThreads) tree_mma_kernel(TreeArgs a) {
 // fp32 caches, fp32 arithmetic (in the TF32 mode too).  128 threads: ty = thread
 // / 16 owns nodes R ty .., tx = thread % 16 keys tx + 16 i of a tile (S) and
 // dimensions tx * HS / 16 .. (O); tiles by cp.async into two buffers.
+constexpr int kSimtKeys = 64;  // of a tile, and at most as many nodes
+static_assert(kSimtKeys >= kMaxNodes, "the nodes' keys are one step");
 template <int HS, int R>
 struct TreeSimtSmem {
   static constexpr int kPad = HS + 4;  // row stride in floats: 16 rows' float4s in distinct banks
-  static constexpr int kPPad = kTile + 4;
+  static constexpr int kPPad = kSimtKeys + 4;
   float q[8 * R][kPad];
-  float k[2][kTile][kPad];
-  float v[2][kTile][HS];
+  float k[2][kSimtKeys][kPad];
+  float v[2][kSimtKeys][HS];
   float p[8 * R][kPPad];
 };
 
@@ -529,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeArgs a) {
   const int C3 = 3 * a.C;
   pdl_wait();  // the QKV projection ahead has finished
   pdl_trigger();
-  const Share sh = share_of(a);
+  constexpr int K = kSimtKeys;
+  const Share sh = share_of<K>(a);
   int4 open = make_int4(-1, 0, 0, 0);
 
   Place ld = sh.at;
@@ -537,12 +569,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeArgs a) {
   auto copy = [&](int buf) {
     if (ld_i < sh.end) {
       const int* table = a.rows.table + static_cast<size_t>(ld.b) * a.rows.max_blocks;
+      const float* nodes = qkv + static_cast<size_t>(ld.b) * a.N * C3 + a.C + ld.h * HS;
 #pragma unroll 4
-      for (int x = threadIdx.x; x < kTile * kChunks; x += kThreads) {
-        const int r = x / kChunks, c = x % kChunks * 4, j = ld.t * kTile + r, node = j - ld.seq.pos;
-        const float *ks, *vs;
-        const bool valid = node < a.N;
-        if (node < 0) {
+      for (int x = threadIdx.x; x < K * kChunks; x += kThreads) {
+        const int r = x / kChunks, c = x % kChunks * 4, j = (ld.t - 1) * K + r;
+        const bool valid = ld.t == 0 ? r < a.N : j < ld.seq.pos;  // zeros otherwise
+        const float *ks = qkv, *vs = qkv;
+        if (valid && ld.t == 0) {
+          ks = nodes + static_cast<size_t>(r) * C3 + c;
+          vs = ks + a.C;
+        } else if (valid) {
           int blk = __ldg(table + (j >> a.rows.lbs));
           if (blk < 0 || blk >= a.rows.num_blocks) {
             if (ld.h == 0) set_error(GPT2_DEVERR_BLOCK);
@@ -551,30 +587,25 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeArgs a) {
           const size_t at = cache_row(a, blk, ld.h, j) * HS + c;
           ks = kcache + at;
           vs = vcache + at;
-        } else {
-          ks = qkv + (static_cast<size_t>(ld.b) * a.N + (valid ? node : 0)) * C3 + a.C + ld.h * HS + c;
-          vs = ks + a.C;
         }
         cp_async16(&sm.k[buf][r][c], ks, valid);
         cp_async16(&sm.v[buf][r][c], vs, valid);
       }
-      advance(a, ld);
+      advance<K>(a, ld);
       ++ld_i;
     }
     cp_async_commit();
   };
   copy(0);
   Place at = sh.at;
-  bool from_start = false, have_sets = false;
+  bool from_start = false;
   TreeSets ts = {{0, 0}};
-  unsigned long long live = 0;
   float m[R], l[R], o[R][kD];
   int buf = 0;
   for (long long i = sh.begin; i < sh.end; ++i, buf ^= 1) {
     copy(buf ^ 1);
     if (i == sh.begin || at.t == 0) {
       from_start = at.t == 0;
-      have_sets = false;
       if (from_start && at.h == 0 && threadIdx.x == 0) seq_of(a, at.b, true);
       for (int x = threadIdx.x; x < 8 * R * kChunks; x += kThreads) {
         const int r = x / kChunks, c = x % kChunks * 4;
@@ -593,25 +624,20 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeArgs a) {
     }
     cp_async_wait<1>();
     __syncthreads();
-    const bool tree = (at.t + 1) * kTile > at.seq.pos;
     unsigned long long seen[R];
-    bool odd = false;
-    if (tree) {
-      if (!have_sets) {
-        have_sets = true;
-        const int* row = a.parent != nullptr ? a.parent + static_cast<size_t>(at.b) * a.N : nullptr;
-        int par[2];
+    bool odd = false;  // a value that is not finite: 0 times it is not 0
+    if (at.t == 0) {
+      const int* row = a.parent != nullptr ? a.parent + static_cast<size_t>(at.b) * a.N : nullptr;
+      int par[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) par[u] = at.seq.live > 0 ? tree_parent(row, lane + 32 * u, a.N) : -2;
-        ts = tree_sets(par, a.N, at.seq.live, at.h == 0 && warp == 0);
-        live = tree_live(ts);
-      }
+      for (int u = 0; u < 2; ++u) par[u] = at.seq.live > 0 ? tree_parent(row, lane + 32 * u, a.N) : -2;
+      ts = tree_sets(par, a.N, at.seq.live, at.h == 0 && warp == 0);
+      const unsigned long long live = tree_live(ts);
       bool bad = false;
 #pragma unroll 1
-      for (int x = threadIdx.x; x < kTile * kChunks; x += kThreads) {
-        const int r = x / kChunks, c = x % kChunks * 4, j = at.t * kTile + r, node = j - at.seq.pos;
-        if (node < 0 || node >= a.N) continue;
-        const float4 v = *reinterpret_cast<const float4*>(&sm.v[buf][r][c]);
+      for (int x = threadIdx.x; x < a.N * kChunks; x += kThreads) {
+        const int node = x / kChunks, c = x % kChunks * 4, j = at.seq.pos + node;
+        const float4 v = *reinterpret_cast<const float4*>(&sm.v[buf][node][c]);
         bad |= !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w));
         if ((live >> node & 1) == 0) continue;
         const int blk = __ldg(a.rows.table + static_cast<size_t>(at.b) * a.rows.max_blocks + (j >> a.rows.lbs));
@@ -620,13 +646,17 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeArgs a) {
           continue;
         }
         const size_t to = cache_row(a, blk, at.h, j) * HS + c;
-        *reinterpret_cast<float4*>(kcache + to) = *reinterpret_cast<const float4*>(&sm.k[buf][r][c]);
+        *reinterpret_cast<float4*>(kcache + to) = *reinterpret_cast<const float4*>(&sm.k[buf][node][c]);
         *reinterpret_cast<float4*>(vcache + to) = v;
       }
       odd = __syncthreads_or(bad);
     }
+    const int valid = at.seq.pos - (at.t - 1) * K;  // of a cached tile
 #pragma unroll
-    for (int r = 0; r < R; ++r) seen[r] = tree ? seen_in(tree_set_of(ts, R * ty + r), at.t, at.seq.pos) : ~0ull;
+    for (int r = 0; r < R; ++r) {
+      const unsigned long long set = tree_set_of(ts, R * ty + r);
+      seen[r] = at.t == 0 ? set : valid >= K ? ~0ull : (1ull << valid) - 1;
+    }
     float s[R][4];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -671,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeArgs a) {
     __syncwarp();  // rows R ty .. are written and read by the 16 threads of ty, half a warp
     if (!odd) {
 #pragma unroll 2
-      for (int j = 0; j < kTile; j += 4) {
+      for (int j = 0; j < K; j += 4) {
         float vv[4][kD];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -700,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeArgs a) {
       }
     } else {  // only the rows that see a value that is not finite may take it in
 #pragma unroll 1
-      for (int j = 0; j < kTile; ++j) {
+      for (int j = 0; j < K; ++j) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           if ((seen[r] >> j & 1) == 0) continue;
@@ -710,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeArgs a) {
         }
       }
     }
-    if (at.t + 1 == at.tiles || i + 1 == sh.end) {  // the pair's part in this share is done
+    if (at.t + 1 == at.steps || i + 1 == sh.end) {  // the pair's part in this share is done
       const Part part = end_part(a, sh, at, i, from_start, open);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -720,22 +750,22 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeArgs a) {
         const unsigned long long set = tree_set_of(ts, R * ty + r);
         const int node = R * ty + r;
         if (node >= a.N) continue;
-        const bool there = set != 0;  // known where have_sets
+        const bool missing = from_start && set == 0;
         if (part.whole) {
           const float inv = 1.0f / sum;
           float* to = static_cast<float*>(a.out) + (static_cast<size_t>(at.b) * a.N + node) * a.C + at.h * HS + tx * kD;
 #pragma unroll
-          for (int d = 0; d < kD; ++d) to[d] = there ? o[r][d] * inv : 0.f;
+          for (int d = 0; d < kD; ++d) to[d] = missing ? 0.f : o[r][d] * inv;
         } else {
           const size_t to = part.slot * a.N + node;
-          if (tx == 0) a.part.ml[to] = make_float2(m[r], have_sets && !there ? -1.f : sum);
+          if (tx == 0) a.part.ml[to] = make_float2(m[r], missing ? -1.f : sum);
 #pragma unroll
           for (int d = 0; d < kD; ++d) a.part.o[to * HS + tx * kD + d] = o[r][d];
         }
       }
     }
     __syncthreads();  // this buffer is refilled, and the queries are replaced, from here on
-    advance(a, at);
+    advance<K>(a, at);
   }
   cp_async_wait<0>();
   if (!split_by_pair(a) && threadIdx.x == 0) a.part.split[blockIdx.x] = open;
@@ -804,7 +834,7 @@ __global__ void __launch_bounds__(kThreads) tree_join_kernel(TreeArgs a) {
 }
 
 // Shares: as many as the SMs hold at once.
-int ctas_of(int per_sm) { return std::min(kMaxCtas, per_sm * num_sms()); }
+int ctas_of(int N, int per_sm) { return std::min(max_ctas(N), per_sm * num_sms()); }
 
 template <typename E, int HS>
 int join(const TreeArgs& a, int ctas, cudaStream_t s) {
@@ -818,11 +848,30 @@ int join(const TreeArgs& a, int ctas, cudaStream_t s) {
 template <int HS, typename T16, int WM>
 int mma_typed(const TreeArgs& a, cudaStream_t s) {
   static bool allowed[kMaxDevices] = {};
-  constexpr int kSmem = sizeof(TreeSmem<HS, WM>);
-  static_assert(kSmem <= 227 * 1024 / 3, "three CTAs an SM");
-  const int ctas = ctas_of(3);
-  cudaError_t e = allow_smem(allowed, tree_mma_kernel<HS, T16, WM>, kSmem);
-  if (e == cudaSuccess) e = launch_pdl(tree_mma_kernel<HS, T16, WM>, dim3(ctas), dim3(kThreads), kSmem, s, a);
+  using Ring = TreeRing<HS, WM>;
+  constexpr int kPerSm = 8 / WM;
+  static_assert(kPerSm * (Ring::kSmem + 1024) <= 228 * 1024, "the CTAs of an SM");
+  const CUtensorMapDataType dt =
+      std::is_same<T16, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap mk, mv, mq;
+  {
+    const uint64_t bs = 1ull << a.rows.lbs, row = HS * 2;
+    const uint64_t dims[4] = {HS, bs, static_cast<uint64_t>(a.NH), static_cast<uint64_t>(a.rows.num_blocks)};
+    const uint64_t strides[3] = {row, row * bs, row * bs * a.NH};
+    const uint32_t box[4] = {HS, static_cast<uint32_t>(std::min<uint64_t>(Ring::kKeys, bs)), 1, 1};
+    if (!encode_tensor_map(&mk, dt, 4, a.kcache, dims, strides, box, Ring::kSwizzle) ||
+        !encode_tensor_map(&mv, dt, 4, a.vcache, dims, strides, box, Ring::kSwizzle))
+      return GPT2_ERR_CUDA;
+  }
+  {
+    const uint64_t dims[2] = {3ull * a.C, static_cast<uint64_t>(a.B) * a.N}, strides[1] = {6ull * a.C};
+    const uint32_t box[2] = {HS, 16 * WM};
+    if (!encode_tensor_map(&mq, dt, 2, a.qkv, dims, strides, box, Ring::kSwizzle)) return GPT2_ERR_CUDA;
+  }
+  const int ctas = ctas_of(a.N, kPerSm);
+  cudaError_t e = allow_smem(allowed, tree_mma_kernel<HS, T16, WM>, Ring::kSmem);
+  if (e == cudaSuccess)
+    e = launch_pdl(tree_mma_kernel<HS, T16, WM>, dim3(ctas), dim3(32 * WM), Ring::kSmem, s, mk, mv, mq, a);
   return e == cudaSuccess ? join<T16, HS>(a, ctas, s) : note_cuda_error(e);
 }
 
@@ -838,7 +887,7 @@ int simt_typed(const TreeArgs& a, cudaStream_t s) {
   static bool allowed[kMaxDevices] = {};
   constexpr int kSmem = sizeof(TreeSimtSmem<HS, R>);
   static_assert(kSmem <= 227 * 1024 / 2, "two CTAs an SM");
-  const int ctas = ctas_of(2);
+  const int ctas = ctas_of(a.N, 2);
   cudaError_t e = allow_smem(allowed, tree_simt_kernel<HS, R>, kSmem);
   if (e == cudaSuccess) e = launch_pdl(tree_simt_kernel<HS, R>, dim3(ctas), dim3(kThreads), kSmem, s, a);
   return e == cudaSuccess ? join<float, HS>(a, ctas, s) : note_cuda_error(e);
@@ -864,12 +913,14 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 size_t tree_partial_bytes(int N, int hs) {
-  const size_t rows = 2ull * kMaxCtas * N;
-  return round256(rows * hs * sizeof(float)) + round256(rows * sizeof(float2)) + kMaxCtas * sizeof(int4);
+  // enough for every smaller tree: of up to 16 nodes more CTAs leave parts
+  size_t rows = 0;
+  for (int n : {std::min(N, 16), std::min(N, 32), N}) rows = std::max<size_t>(rows, 2ull * max_ctas(n) * n);
+  return round256(rows * hs * sizeof(float)) + round256(rows * sizeof(float2)) + max_ctas(1) * sizeof(int4);
 }
 
 TreePartials tree_partial_layout(void* workspace, int N, int hs) {
-  const size_t rows = 2ull * kMaxCtas * N;
+  const size_t rows = 2ull * max_ctas(N) * N;
   uint8_t* p = static_cast<uint8_t*>(workspace);
   TreePartials r;
   r.o = reinterpret_cast<float*>(p);

@@ -102,7 +102,7 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
 template <typename E, bool kInPlace>
 __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a) {
   constexpr int kN = 16 / static_cast<int>(sizeof(E));
-  extern __shared__ __align__(128) uint8_t shared_raw[];
+  extern __shared__ __align__(16) uint8_t shared_raw[];
   __shared__ __align__(8) uint64_t full[kStages];
   __shared__ unsigned long long sets[kMaxNodes], same[kMaxNodes];
   __shared__ int toks[kMaxNodes], mask_rows[kMaxNodes];
