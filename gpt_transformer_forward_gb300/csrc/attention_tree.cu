@@ -8,25 +8,28 @@
 // node).  Every key and value is read once for all nodes.
 //
 // The lengths are known on the device only, and differ.  A pair is a row of
-// steps: the nodes' own keys, then tiles of cached ones.  All pairs' steps, one
-// pair behind the other, are cut into equal shares of one CTA each; a share
-// begins and ends inside pairs.  A pair that lies in several shares leaves the
-// running maximum m, sum l and unnormalised output O of each part in the
-// workspace, which tree_join_kernel joins in order.
+// steps: the nodes' own keys, then tiles of cached ones.  With many pairs that
+// cannot be very long, each is a CTA's, whose groups of warps take its steps in
+// turn and are joined in shared memory.  Otherwise all pairs' steps, one pair
+// behind the other, are cut into equal shares of one CTA each; a share begins and
+// ends inside pairs.  A pair that lies in several shares leaves the running
+// maximum m, sum l and unnormalised output O of each part in the workspace, which
+// tree_join_kernel joins in order.
 //   tree_mma_kernel    16-bit caches, mma.sync
 //   tree_simt_kernel   fp32 caches, CUDA cores
 #include "draft.cuh"
 #include "mma_sync.cuh"
 
 #include <algorithm>
+#include <cstdlib>
 
 namespace gpt2 {
 namespace {
 
 constexpr int kThreads = 128;  // of tree_simt_kernel and tree_join_kernel
-// Shares at most: eight CTAs on each of 152 SMs.  The workspace holds their parts,
+// Shares at most: twelve CTAs on each of 152 SMs.  The workspace holds their parts,
 // so the count goes by the number of nodes alone.
-constexpr int ctas_per_sm(int N) { return N <= 16 ? 8 : N <= 32 ? 4 : 2; }
+constexpr int ctas_per_sm(int N) { return N <= 16 ? 12 : N <= 32 ? 6 : 3; }
 constexpr int max_ctas(int N) { return 152 * ctas_per_sm(N); }
 constexpr int kMinSteps = 2;   // of a share
 
@@ -177,7 +180,7 @@ __device__ __forceinline__ bool any_not_finite(const uint4& v) {
 // mma.sync m16n8k16, fp32 accumulators.  A CTA is WM warps of 16 nodes each that
 // share every step's keys, which come by TMA through a ring in shared memory (a
 // copy per block of the cache that a tile touches, one where blocks are as long as
-// tiles); up to 16 nodes a CTA is one warp, eight of them an SM, that needs no
+// tiles); up to 16 nodes a CTA is one warp, twelve of them an SM, that needs no
 // barrier but the copies'.  Block ids are looked up a step ahead.
 template <int HS, int WM>
 struct TreeRing {
@@ -186,10 +189,10 @@ struct TreeRing {
   static constexpr int kTileBytes = kKeys * kRow;
   static constexpr int kNodeBytes = 16 * WM * kRow;  // of the nodes' queries, keys or values
   static constexpr int kStage = 2 * kTileBytes > 3 * kNodeBytes ? 2 * kTileBytes : 3 * kNodeBytes;
-  static constexpr int kStages = (WM == 4 ? 4 : 3) * (HS == 64 ? 1 : 2);
+  static constexpr int kStages = (WM == 4 ? 3 : 2) * (HS == 64 ? 1 : 2);
   // The ring begins at a multiple of 1024 bytes, the barriers stand behind it: with
   // shared memory of the kernel's own beside it the dynamic one begins anywhere.
-  static constexpr int kSmem = 1024 + kStages * kStage + kStages * 8;
+  static constexpr int smem(int groups) { return 1024 + groups * kStages * (kStage + 8); }
   static constexpr CUtensorMapSwizzle kSwizzle = HS == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
                                                  : HS == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                             : CU_TENSOR_MAP_SWIZZLE_32B;
@@ -202,45 +205,69 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
   return static_cast<uint32_t>(r * (HS * 2) + ((c ^ (r / (8 / kChunks) & (kChunks - 1))) << 4));
 }
 
-template <int HS, typename T16, int WM>
-__global__ void __launch_bounds__(32 * WM)
+// A barrier of a group's threads that also ORs a predicate over them.
+template <int WM>
+__device__ __forceinline__ bool group_or(int group, bool pred) {
+  if constexpr (WM == 1)
+    return __any_sync(0xffffffffu, pred);
+  else
+    return bar_or(1 + group, 32 * WM, pred);
+}
+
+// kPairs: a CTA takes one pair, its 4 / WM groups of WM warps the steps in turn.
+// Otherwise a CTA is one group that takes a share.
+template <int HS, typename T16, int WM, bool kPairs>
+__global__ void __launch_bounds__(kPairs ? 128 : 32 * WM, kPairs ? 3 : 12 / WM)
     tree_mma_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                     const __grid_constant__ CUtensorMap map_qkv, TreeArgs a) {
   using Ring = TreeRing<HS, WM>;
   constexpr int K = Ring::kKeys, kStages = Ring::kStages;
   constexpr int kKS = HS / 16, kDT = HS / 8, kChunks = HS / 8;
+  constexpr int WK = kPairs ? 4 / WM : 1;  // groups
   extern __shared__ uint8_t tree_ring_raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tree_ring_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * Ring::kStage);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;  // warp: its nodes are 16 warp ..
+  uint8_t* rings = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tree_ring_raw) + 1023) & ~uintptr_t(1023));
+  const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / WM;
+  const int warp = (threadIdx.x >> 5) % WM;  // of the group: its nodes are 16 warp ..
+  uint8_t* ring = rings + group * (kStages * Ring::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(rings + WK * (kStages * Ring::kStage)) + group * kStages;
   const int g = lane >> 2, tig = lane & 3;
   uint16_t* kcache = static_cast<uint16_t*>(a.kcache);
   uint16_t* vcache = static_cast<uint16_t*>(a.vcache);
-  auto sync = [&]() {
-    if constexpr (WM == 1)
-      __syncwarp();
-    else
-      __syncthreads();
-  };
-  if (threadIdx.x == 0) {
-    tma_prefetch_desc(&map_k);
-    tma_prefetch_desc(&map_v);
-    tma_prefetch_desc(&map_qkv);
+  if (warp == 0 && lane == 0) {
+    if (group == 0) {
+      tma_prefetch_desc(&map_k);
+      tma_prefetch_desc(&map_v);
+      tma_prefetch_desc(&map_qkv);
+    }
     for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1);
     fence_barrier_init();
   }
   pdl_wait();  // the QKV projection ahead has finished
   pdl_trigger();
-  const Share sh = share_of<K>(a);
+  Share sh;
+  if constexpr (kPairs) {
+    sh.at = Place{static_cast<int>(blockIdx.x / a.NH), static_cast<int>(blockIdx.x % a.NH), group, 0, {0, 0}};
+    enter<K>(a, sh.at);
+    sh.begin = 0;
+    sh.end = group < sh.at.steps ? (sh.at.steps - group + WK - 1) / WK : 0;
+  } else {
+    sh = share_of<K>(a);
+  }
+  auto forward = [&](Place& p) {  // to this group's next step
+    if constexpr (kPairs)
+      p.t += WK;
+    else
+      advance<K>(a, p);
+  };
   int4 open = make_int4(-1, 0, 0, 0);
-  sync();  // the barriers
+  group_or<WM>(group, false);  // the barriers
 
   // The share's copies, in order; a share that begins inside a pair has one step
   // more at the start, for the queries.  Warp 0 issues them.
   const int lead = sh.begin < sh.end && sh.at.t > 0 ? 1 : 0;
-  const long long n_steps = sh.end - sh.begin + lead;
+  const int n_steps = static_cast<int>(sh.end - sh.begin) + lead;  // (2^31 of them would take hours)
   Place ld = sh.at;
-  long long ld_i = -lead;  // of the share's steps
+  int ld_i = -lead;  // of the share's steps
   constexpr int kIds = (K + 31) / 32;
   int ids[kIds];
   const int box = min(K, 1 << a.rows.lbs), boxes = K / box;  // of a tile
@@ -307,7 +334,7 @@ __global__ void __launch_bounds__(32 * WM)
         }
       }
     }
-    if (ld_i >= 0) advance<K>(a, ld);
+    if (ld_i >= 0) forward(ld);
     ++ld_i;
     if (ld_i + lead < n_steps) lookup();
   };
@@ -384,10 +411,12 @@ __global__ void __launch_bounds__(32 * WM)
         sum += s[nt][2 * r] + s[nt][2 * r + 1];
       }
       l_r[r] = l_r[r] * alpha + sum;
+      if (__any_sync(0xffffffffu, alpha != 1.f)) {  // a maximum rises in few of the steps
 #pragma unroll
-      for (int dt = 0; dt < kDT; ++dt) {
-        o[dt][2 * r] *= alpha;
-        o[dt][2 * r + 1] *= alpha;
+        for (int dt = 0; dt < kDT; ++dt) {
+          o[dt][2 * r] *= alpha;
+          o[dt][2 * r + 1] *= alpha;
+        }
       }
     }
     if (!odd) {
@@ -401,14 +430,21 @@ __global__ void __launch_bounds__(32 * WM)
         split2<T16>(s[2 * ks][2], s[2 * ks][3], pa[1], pl[1]);
         split2<T16>(s[2 * ks + 1][0], s[2 * ks + 1][1], pa[2], pl[2]);
         split2<T16>(s[2 * ks + 1][2], s[2 * ks + 1][3], pa[3], pl[3]);
+        uint32_t vf[kDT / 2][4];
+#pragma unroll
+        for (int dp = 0; dp < kDT / 2; ++dp)
+          ldsm_x4_t(vb + tile_at<HS>(ks * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), dp * 2 + (lane >> 4)), vf[dp][0],
+                    vf[dp][1], vf[dp][2], vf[dp][3]);
+        // products into the same sums stand apart
 #pragma unroll
         for (int dp = 0; dp < kDT / 2; ++dp) {
-          uint32_t r0, r1, r2, r3;
-          ldsm_x4_t(vb + tile_at<HS>(ks * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), dp * 2 + (lane >> 4)), r0, r1, r2, r3);
-          mma16<T16>(o[2 * dp], pl, r0, r1);
-          mma16<T16>(o[2 * dp + 1], pl, r2, r3);
-          mma16<T16>(o[2 * dp], pa, r0, r1);
-          mma16<T16>(o[2 * dp + 1], pa, r2, r3);
+          mma16<T16>(o[2 * dp], pl, vf[dp][0], vf[dp][1]);
+          mma16<T16>(o[2 * dp + 1], pl, vf[dp][2], vf[dp][3]);
+        }
+#pragma unroll
+        for (int dp = 0; dp < kDT / 2; ++dp) {
+          mma16<T16>(o[2 * dp], pa, vf[dp][0], vf[dp][1]);
+          mma16<T16>(o[2 * dp + 1], pa, vf[dp][2], vf[dp][3]);
         }
       }
     } else {
@@ -437,14 +473,13 @@ __global__ void __launch_bounds__(32 * WM)
     }
   };
   uint32_t stage = 0, phase = 0;
-  for (long long n = 0; n < n_steps; ++n) {
+  for (int n = 0; n < n_steps; ++n) {
     const bool came = mbar_wait(full + stage, phase);
     // the step's keys are there, and every warp is past the step whose stage is
     // refilled now; a copy that did not come (flagged by the wait) ends the share
-    const bool lost = WM == 1 ? __any_sync(0xffffffffu, !came) : __syncthreads_or(!came);
-    if (lost) {
+    if (group_or<WM>(group, !came)) {
       if (warp == 0)
-        for (long long k = n; k < ld_i + lead; ++k) mbar_wait(full + k % kStages, k / kStages & 1);
+        for (int k = n; k < ld_i + lead; ++k) mbar_wait(full + k % kStages, k / kStages & 1);
       break;
     }
     if (warp == 0) copy((stage + kStages - 1) % kStages);
@@ -500,7 +535,7 @@ __global__ void __launch_bounds__(32 * WM)
       attend(std::integral_constant<int, K / 8>{}, st, st + Ring::kTileBytes, valid < K, seen, false);
     }
     const long long i = sh.begin + n - lead;
-    if (at.t + 1 == at.steps || i + 1 == sh.end) {  // the pair's part in this share is done
+    if (!kPairs && (at.t + 1 == at.steps || i + 1 == sh.end)) {  // the pair's part in this share is done
       const Part part = end_part(a, sh, at, i, from_start, open);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -526,9 +561,82 @@ __global__ void __launch_bounds__(32 * WM)
         }
       }
     }
-    advance<K>(a, at);
+    forward(at);
   }
-  if (!split_by_pair(a) && threadIdx.x == 0) a.part.split[blockIdx.x] = open;
+  if constexpr (!kPairs) {
+    if (!split_by_pair(a) && threadIdx.x == 0) a.part.split[blockIdx.x] = open;
+  } else {
+    // the groups' results join where their rings were; group 0, which has the
+    // nodes' own step, writes the rows
+    constexpr int kRowF = HS + 4;  // floats
+    static_assert(16 * WM * (kRowF + 2) * 4 <= kStages * Ring::kStage, "a group's results fit in its ring");
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (sh.end == 0) {  // no step
+        m_r[r] = -INFINITY;
+        l_r[r] = 0.f;
+      }
+      l_r[r] += __shfl_xor_sync(0xffffffffu, l_r[r], 1);
+      l_r[r] += __shfl_xor_sync(0xffffffffu, l_r[r], 2);
+    }
+    if (WK > 1) {
+      __syncthreads();
+      float* mine = reinterpret_cast<float*>(ring);
+      if (group > 0) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float* row = mine + (warp * 16 + g + 8 * r) * (kRowF + 2);
+          if (tig == 0) *reinterpret_cast<float2*>(row + HS) = make_float2(m_r[r], l_r[r]);
+          if (sh.end > 0) {
+#pragma unroll
+            for (int dt = 0; dt < kDT; ++dt)
+              *reinterpret_cast<float2*>(row + dt * 8 + 2 * tig) = make_float2(o[dt][2 * r], o[dt][2 * r + 1]);
+          }
+        }
+      }
+      __syncthreads();
+      if (group > 0) return;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = (warp * 16 + g + 8 * r) * (kRowF + 2);
+        auto other = [&](int k) { return reinterpret_cast<const float*>(rings + k * (kStages * Ring::kStage)) + row; };
+        float M = m_r[r];
+#pragma unroll
+        for (int k = 1; k < WK; ++k) M = fmaxf(M, other(k)[HS]);
+        const float ref = M == -INFINITY ? 0.f : M, f = exp2_approx(m_r[r] - ref);
+        l_r[r] *= f;
+#pragma unroll
+        for (int dt = 0; dt < kDT; ++dt) {
+          o[dt][2 * r] *= f;
+          o[dt][2 * r + 1] *= f;
+        }
+#pragma unroll
+        for (int k = 1; k < WK; ++k) {
+          const float2 ml = *reinterpret_cast<const float2*>(other(k) + HS);
+          if (ml.x == -INFINITY && ml.y == 0.f) continue;  // a group without a step leaves no row
+          const float w = exp2_approx(ml.x - ref);
+          l_r[r] = fmaf(ml.y, w, l_r[r]);
+#pragma unroll
+          for (int dt = 0; dt < kDT; ++dt) {
+            const float2 x = *reinterpret_cast<const float2*>(other(k) + dt * 8 + 2 * tig);
+            o[dt][2 * r] = fmaf(x.x, w, o[dt][2 * r]);
+            o[dt][2 * r + 1] = fmaf(x.y, w, o[dt][2 * r + 1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int node = warp * 16 + g + 8 * r;
+      if (node >= a.N) continue;
+      const float inv = 1.0f / l_r[r];
+      uint16_t* to = static_cast<uint16_t*>(a.out) + (static_cast<size_t>(at.b) * a.N + node) * a.C + at.h * HS;
+#pragma unroll
+      for (int dt = 0; dt < kDT; ++dt)
+        *reinterpret_cast<uint32_t*>(to + dt * 8 + 2 * tig) =
+            set[r] != 0 ? pack2<T16>(o[dt][2 * r] * inv, o[dt][2 * r + 1] * inv) : 0u;
+    }
+  }
 }
 
 // ------------------------------------------------------ CUDA-core kernel
@@ -845,12 +953,19 @@ int join(const TreeArgs& a, int ctas, cudaStream_t s) {
   return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
 }
 
-template <int HS, typename T16, int WM>
+// Whether each pair is a CTA's.
+bool by_pairs(const TreeArgs& a) {
+  const long long pairs = static_cast<long long>(a.B) * a.NH;
+  if (getenv("TREE_PAIRS")) return atoi(getenv("TREE_PAIRS"));
+  return pairs >= 152 && (a.rows.capacity <= 4096 || pairs >= 4 * 456);
+}
+
+template <int HS, typename T16, int WM, bool kPairs>
 int mma_typed(const TreeArgs& a, cudaStream_t s) {
   static bool allowed[kMaxDevices] = {};
   using Ring = TreeRing<HS, WM>;
-  constexpr int kPerSm = 8 / WM;
-  static_assert(kPerSm * (Ring::kSmem + 1024) <= 228 * 1024, "the CTAs of an SM");
+  constexpr int kPerSm = kPairs ? 3 : 12 / WM, kSmem = Ring::smem(kPairs ? 4 / WM : 1);
+  static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "the CTAs of an SM");
   const CUtensorMapDataType dt =
       std::is_same<T16, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap mk, mv, mq;
@@ -868,18 +983,20 @@ int mma_typed(const TreeArgs& a, cudaStream_t s) {
     const uint32_t box[2] = {HS, 16 * WM};
     if (!encode_tensor_map(&mq, dt, 2, a.qkv, dims, strides, box, Ring::kSwizzle)) return GPT2_ERR_CUDA;
   }
-  const int ctas = ctas_of(a.N, kPerSm);
-  cudaError_t e = allow_smem(allowed, tree_mma_kernel<HS, T16, WM>, Ring::kSmem);
+  cudaError_t e = allow_smem(allowed, tree_mma_kernel<HS, T16, WM, kPairs>, kSmem);
+  const int ctas = kPairs ? a.B * a.NH : ctas_of(a.N, kPerSm);
   if (e == cudaSuccess)
-    e = launch_pdl(tree_mma_kernel<HS, T16, WM>, dim3(ctas), dim3(32 * WM), Ring::kSmem, s, mk, mv, mq, a);
-  return e == cudaSuccess ? join<T16, HS>(a, ctas, s) : note_cuda_error(e);
+    e = launch_pdl(tree_mma_kernel<HS, T16, WM, kPairs>, dim3(ctas), dim3(kPairs ? 128 : 32 * WM), kSmem, s, mk, mv, mq, a);
+  if (e != cudaSuccess) return note_cuda_error(e);
+  return kPairs ? GPT2_OK : join<T16, HS>(a, ctas, s);
 }
 
 template <int HS, typename T16>
 int mma(const TreeArgs& a, cudaStream_t s) {
-  if (a.N <= 16) return mma_typed<HS, T16, 1>(a, s);
-  if (a.N <= 32) return mma_typed<HS, T16, 2>(a, s);
-  return mma_typed<HS, T16, 4>(a, s);
+  const bool pairs = by_pairs(a);
+  if (a.N <= 16) return pairs ? mma_typed<HS, T16, 1, true>(a, s) : mma_typed<HS, T16, 1, false>(a, s);
+  if (a.N <= 32) return pairs ? mma_typed<HS, T16, 2, true>(a, s) : mma_typed<HS, T16, 2, false>(a, s);
+  return pairs ? mma_typed<HS, T16, 4, true>(a, s) : mma_typed<HS, T16, 4, false>(a, s);
 }
 
 template <int HS, int R>
