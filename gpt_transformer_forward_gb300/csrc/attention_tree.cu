@@ -17,8 +17,7 @@
 // tree_join_kernel joins in order.
 //   tree_mma_kernel    16-bit caches, mma.sync
 //   tree_simt_kernel   fp32 caches, CUDA cores
-#include "draft.cuh"
-#include "mma_sync.cuh"
+#include "tree_share.cuh"
 
 #include <algorithm>
 #include <cstdlib>
@@ -26,155 +25,7 @@
 namespace gpt2 {
 namespace {
 
-constexpr int kThreads = 128;  // of tree_simt_kernel and tree_join_kernel
-// Shares at most: twelve CTAs on each of 152 SMs.  The workspace holds their parts,
-// so the count goes by the number of nodes alone.
-constexpr int ctas_per_sm(int N) { return N <= 16 ? 12 : N <= 32 ? 6 : 3; }
-constexpr int max_ctas(int N) { return 152 * ctas_per_sm(N); }
-constexpr int kMinSteps = 2;   // of a share
-
-struct TreeArgs {
-  void* out;
-  const void* qkv;
-  void* kcache;
-  void* vcache;
-  const int* pos;
-  const int* parent;
-  int B, N, C, NH;
-  KVRows rows;
-  float scale_log2;
-  TreePartials part;
-};
-
-// A sequence's cached positions and the nodes that have a place behind them;
-// none of either where it has no tree in this step.
-struct Seq {
-  int pos, live;
-};
-__device__ __forceinline__ Seq seq_of(const TreeArgs& a, int b, bool report) {
-  const int p = __ldg(a.pos + b);
-  const bool ok = p >= 0 && p < a.rows.capacity;
-  if (!ok && p != -1 && report) set_error(GPT2_DEVERR_POSITION);
-  return {ok ? p : 0, ok ? min(a.N, a.rows.capacity - p) : 0};
-}
-// Steps of a pair with tiles of K cached keys.
-template <int K>
-__device__ __forceinline__ int steps_of(const Seq& q) {
-  return 1 + (q.pos + K - 1) / K;
-}
-
-// A place in the row of all pairs' steps: step t of a pair, 0 the nodes' own keys,
-// t > 0 cached keys [(t - 1) K, t K).
-struct Place {
-  int b, h, t, steps;
-  Seq seq;
-};
-template <int K>
-__device__ __forceinline__ void enter(const TreeArgs& a, Place& p) {
-  p.seq = seq_of(a, p.b, false);
-  p.steps = steps_of<K>(p.seq);
-}
-// The next step; behind the last one of all, nothing that may be read.
-template <int K>
-__device__ __forceinline__ void advance(const TreeArgs& a, Place& p) {
-  if (++p.t < p.steps) return;
-  p.t = 0;
-  if (++p.h < a.NH) return;
-  p.h = 0;
-  if (++p.b < a.B) enter<K>(a, p);
-}
-
-// This CTA's share [begin, end) of the steps and where it begins (the whole warp
-// calls, every warp for itself).  `per`: the steps of a share.
-struct Share {
-  long long begin, end, per;
-  Place at;
-};
-template <int K>
-__device__ __forceinline__ Share share_of(const TreeArgs& a) {
-  const int lane = threadIdx.x & 31;
-  auto steps_at = [&](int b) { return b < a.B ? steps_of<K>(seq_of(a, b, false)) : 0; };
-  long long total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, steps_at(b0 + lane));
-  total *= a.NH;
-  Share s;
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  s.per = per > kMinSteps ? per : kMinSteps;
-  s.begin = min(total, s.per * blockIdx.x);
-  s.end = min(total, s.begin + s.per);
-  s.at = Place{0, 0, 0, 1, {0, 0}};
-  if (s.begin >= s.end) return s;
-  long long before = 0;  // steps of the sequences ahead, of one head
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int mine = steps_at(b0 + lane);
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, (before + incl) * a.NH > s.begin);
-    if (past != 0) {
-      const int l = __ffs(past) - 1;
-      const int steps = __shfl_sync(0xffffffffu, mine, l);
-      const long long rest = s.begin - (before + __shfl_sync(0xffffffffu, incl - mine, l)) * a.NH;
-      s.at.b = b0 + l;
-      s.at.h = static_cast<int>(rest / steps);
-      s.at.t = static_cast<int>(rest % steps);
-      enter<K>(a, s.at);
-      return s;
-    }
-    before += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  return s;
-}
-
-// The row of position j of a sequence's head in a cache half, from its block id.
-__device__ __forceinline__ size_t cache_row(const TreeArgs& a, int blk, int h, int j) {
-  return ((static_cast<size_t>(blk) * a.NH + h) << a.rows.lbs) + (j & ((1 << a.rows.lbs) - 1));
-}
-
-// What is to be joined: entry i holds the pair, the CTA in which it begins and
-// the one in which it ends, or -1.  With no more pairs than CTAs, pair i's entry,
-// written by the CTA in which it begins; otherwise CTA i's: at most one pair
-// begins in a share and goes on in the next.
-__device__ __forceinline__ bool split_by_pair(const TreeArgs& a) {
-  return static_cast<long long>(a.B) * a.NH <= gridDim.x;
-}
-
-// A pair's part in this share, at the end of it.
-struct Part {
-  bool whole;   // the pair lies in this share
-  size_t slot;  // of the workspace otherwise
-};
-__device__ __forceinline__ Part end_part(const TreeArgs& a, const Share& s, const Place& p, long long i, bool from_start,
-                                         int4& open) {
-  const int last = p.steps - 1 - p.t;  // steps of the pair behind this one
-  const bool whole = from_start && last == 0;
-  if (from_start) {
-    const int pair = p.b * a.NH + p.h;
-    const int4 e = whole ? make_int4(-1, 0, 0, 0)
-                         : make_int4(pair, static_cast<int>(blockIdx.x), static_cast<int>((i + last) / s.per), 0);
-    if (split_by_pair(a)) {
-      if (threadIdx.x == 0) a.part.split[pair] = e;
-    } else if (!whole) {
-      open = e;
-    }
-  }
-  return {whole, 2 * static_cast<size_t>(blockIdx.x) + (from_start ? 1 : 0)};
-}
-
-template <typename T16>
-__device__ __forceinline__ bool any_not_finite(const uint4& v) {
-  constexpr uint32_t kExp = std::is_same<T16, __half>::value ? 0x7c00u : 0x7f80u;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-    bad |= (w & kExp) == kExp || ((w >> 16) & kExp) == kExp;
-  }
-  return bad;
-}
+using namespace tree;
 
 // ------------------------------------------------------ tensor-core kernel
 // mma.sync m16n8k16, fp32 accumulators.  A CTA is WM warps of 16 nodes each that
@@ -197,14 +48,6 @@ struct TreeRing {
                                                  : HS == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                             : CU_TENSOR_MAP_SWIZZLE_32B;
 };
-// Byte offset of 16-byte chunk c of row r in a tile that TMA wrote with that
-// swizzle: the chunk's number is combined with the 128-byte line's.
-template <int HS>
-__device__ __forceinline__ uint32_t tile_at(int r, int c) {
-  constexpr int kChunks = HS / 8;
-  return static_cast<uint32_t>(r * (HS * 2) + ((c ^ (r / (8 / kChunks) & (kChunks - 1))) << 4));
-}
-
 // A barrier of a group's threads that also ORs a predicate over them.
 template <int WM>
 __device__ __forceinline__ bool group_or(int group, bool pred) {
@@ -536,7 +379,7 @@ __global__ void __launch_bounds__(kPairs ? 128 : 32 * WM, kPairs ? 3 : 12 / WM)
     }
     const long long i = sh.begin + n - lead;
     if (!kPairs && (at.t + 1 == at.steps || i + 1 == sh.end)) {  // the pair's part in this share is done
-      const Part part = end_part(a, sh, at, i, from_start, open);
+      const Part part = end_part(a, sh, at, i, from_start, open, threadIdx.x == 0);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         l_r[r] += __shfl_xor_sync(0xffffffffu, l_r[r], 1);
@@ -637,246 +480,6 @@ __global__ void __launch_bounds__(kPairs ? 128 : 32 * WM, kPairs ? 3 : 12 / WM)
             set[r] != 0 ? pack2<T16>(o[dt][2 * r] * inv, o[dt][2 * r + 1] * inv) : 0u;
     }
   }
-}
-
-// ------------------------------------------------------ CUDA-core kernel
-// fp32 caches, fp32 arithmetic (in the TF32 mode too).  128 threads: ty = thread
-// / 16 owns nodes R ty .., tx = thread % 16 keys tx + 16 i of a tile (S) and
-// dimensions tx * HS / 16 .. (O); tiles by cp.async into two buffers.
-constexpr int kSimtKeys = 64;  // of a tile, and at most as many nodes
-static_assert(kSimtKeys >= kMaxNodes, "the nodes' keys are one step");
-template <int HS, int R>
-struct TreeSimtSmem {
-  static constexpr int kPad = HS + 4;  // row stride in floats: 16 rows' float4s in distinct banks
-  static constexpr int kPPad = kSimtKeys + 4;
-  float q[8 * R][kPad];
-  float k[2][kSimtKeys][kPad];
-  float v[2][kSimtKeys][HS];
-  float p[8 * R][kPPad];
-};
-
-template <int HS, int R>
-__global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeArgs a) {
-  extern __shared__ __align__(128) uint8_t shared_raw[];
-  auto& sm = *reinterpret_cast<TreeSimtSmem<HS, R>*>(shared_raw);
-  constexpr int kD = HS / 16, kChunks = HS / 4;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const float* qkv = static_cast<const float*>(a.qkv);
-  float* kcache = static_cast<float*>(a.kcache);
-  float* vcache = static_cast<float*>(a.vcache);
-  const int C3 = 3 * a.C;
-  pdl_wait();  // the QKV projection ahead has finished
-  pdl_trigger();
-  constexpr int K = kSimtKeys;
-  const Share sh = share_of<K>(a);
-  int4 open = make_int4(-1, 0, 0, 0);
-
-  Place ld = sh.at;
-  long long ld_i = sh.begin;
-  auto copy = [&](int buf) {
-    if (ld_i < sh.end) {
-      const int* table = a.rows.table + static_cast<size_t>(ld.b) * a.rows.max_blocks;
-      const float* nodes = qkv + static_cast<size_t>(ld.b) * a.N * C3 + a.C + ld.h * HS;
-#pragma unroll 4
-      for (int x = threadIdx.x; x < K * kChunks; x += kThreads) {
-        const int r = x / kChunks, c = x % kChunks * 4, j = (ld.t - 1) * K + r;
-        const bool valid = ld.t == 0 ? r < a.N : j < ld.seq.pos;  // zeros otherwise
-        const float *ks = qkv, *vs = qkv;
-        if (valid && ld.t == 0) {
-          ks = nodes + static_cast<size_t>(r) * C3 + c;
-          vs = ks + a.C;
-        } else if (valid) {
-          int blk = __ldg(table + (j >> a.rows.lbs));
-          if (blk < 0 || blk >= a.rows.num_blocks) {
-            if (ld.h == 0) set_error(GPT2_DEVERR_BLOCK);
-            blk = 0;
-          }
-          const size_t at = cache_row(a, blk, ld.h, j) * HS + c;
-          ks = kcache + at;
-          vs = vcache + at;
-        }
-        cp_async16(&sm.k[buf][r][c], ks, valid);
-        cp_async16(&sm.v[buf][r][c], vs, valid);
-      }
-      advance<K>(a, ld);
-      ++ld_i;
-    }
-    cp_async_commit();
-  };
-  copy(0);
-  Place at = sh.at;
-  bool from_start = false;
-  TreeSets ts = {{0, 0}};
-  float m[R], l[R], o[R][kD];
-  int buf = 0;
-  for (long long i = sh.begin; i < sh.end; ++i, buf ^= 1) {
-    copy(buf ^ 1);
-    if (i == sh.begin || at.t == 0) {
-      from_start = at.t == 0;
-      if (from_start && at.h == 0 && threadIdx.x == 0) seq_of(a, at.b, true);
-      for (int x = threadIdx.x; x < 8 * R * kChunks; x += kThreads) {
-        const int r = x / kChunks, c = x % kChunks * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < a.N)
-          v = __ldg(reinterpret_cast<const float4*>(qkv + (static_cast<size_t>(at.b) * a.N + r) * C3 + at.h * HS + c));
-        *reinterpret_cast<float4*>(&sm.q[r][c]) = v;
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-#pragma unroll
-        for (int d = 0; d < kD; ++d) o[r][d] = 0.f;
-      }
-    }
-    cp_async_wait<1>();
-    __syncthreads();
-    unsigned long long seen[R];
-    bool odd = false;  // a value that is not finite: 0 times it is not 0
-    if (at.t == 0) {
-      const int* row = a.parent != nullptr ? a.parent + static_cast<size_t>(at.b) * a.N : nullptr;
-      int par[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) par[u] = at.seq.live > 0 ? tree_parent(row, lane + 32 * u, a.N) : -2;
-      ts = tree_sets(par, a.N, at.seq.live, at.h == 0 && warp == 0);
-      const unsigned long long live = tree_live(ts);
-      bool bad = false;
-#pragma unroll 1
-      for (int x = threadIdx.x; x < a.N * kChunks; x += kThreads) {
-        const int node = x / kChunks, c = x % kChunks * 4, j = at.seq.pos + node;
-        const float4 v = *reinterpret_cast<const float4*>(&sm.v[buf][node][c]);
-        bad |= !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w));
-        if ((live >> node & 1) == 0) continue;
-        const int blk = __ldg(a.rows.table + static_cast<size_t>(at.b) * a.rows.max_blocks + (j >> a.rows.lbs));
-        if (blk < 0 || blk >= a.rows.num_blocks) {
-          if (at.h == 0) set_error(GPT2_DEVERR_BLOCK);
-          continue;
-        }
-        const size_t to = cache_row(a, blk, at.h, j) * HS + c;
-        *reinterpret_cast<float4*>(kcache + to) = *reinterpret_cast<const float4*>(&sm.k[buf][node][c]);
-        *reinterpret_cast<float4*>(vcache + to) = v;
-      }
-      odd = __syncthreads_or(bad);
-    }
-    const int valid = at.seq.pos - (at.t - 1) * K;  // of a cached tile
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const unsigned long long set = tree_set_of(ts, R * ty + r);
-      seen[r] = at.t == 0 ? set : valid >= K ? ~0ull : (1ull << valid) - 1;
-    }
-    float s[R][4];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) s[r][x] = 0.f;
-#pragma unroll 2
-    for (int d = 0; d < HS; d += 4) {
-      float4 ka[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) ka[x] = *reinterpret_cast<const float4*>(&sm.k[buf][tx + 16 * x][d]);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float4 qa = *reinterpret_cast<const float4*>(&sm.q[R * ty + r][d]);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          s[r][x] = fmaf(qa.x, ka[x].x, fmaf(qa.y, ka[x].y, fmaf(qa.z, ka[x].z, fmaf(qa.w, ka[x].w, s[r][x]))));
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        s[r][x] = (seen[r] >> (tx + 16 * x) & 1) != 0 ? s[r][x] * a.scale_log2 : -INFINITY;
-        mx = fmaxf(mx, s[r][x]);
-      }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-      const float m_new = fmaxf(m[r], mx), ref = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = exp2_approx(m[r] - ref);
-      m[r] = m_new;
-      l[r] *= alpha;
-#pragma unroll
-      for (int d = 0; d < kD; ++d) o[r][d] *= alpha;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float p = exp2_approx(s[r][x] - ref);
-        l[r] += p;  // this thread's keys
-        sm.p[R * ty + r][tx + 16 * x] = p;
-      }
-    }
-    __syncwarp();  // rows R ty .. are written and read by the 16 threads of ty, half a warp
-    if (!odd) {
-#pragma unroll 2
-      for (int j = 0; j < K; j += 4) {
-        float vv[4][kD];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float* vr = &sm.v[buf][j + x][tx * kD];
-          if constexpr (kD == 4) {
-            const float4 y = *reinterpret_cast<const float4*>(vr);
-            vv[x][0] = y.x;
-            vv[x][1] = y.y;
-            vv[x][2] = y.z;
-            vv[x][3] = y.w;
-          } else if constexpr (kD == 2) {
-            const float2 y = *reinterpret_cast<const float2*>(vr);
-            vv[x][0] = y.x;
-            vv[x][1] = y.y;
-          } else {
-            vv[x][0] = vr[0];
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float4 pa = *reinterpret_cast<const float4*>(&sm.p[R * ty + r][j]);
-#pragma unroll
-          for (int d = 0; d < kD; ++d)
-            o[r][d] = fmaf(pa.x, vv[0][d], fmaf(pa.y, vv[1][d], fmaf(pa.z, vv[2][d], fmaf(pa.w, vv[3][d], o[r][d]))));
-        }
-      }
-    } else {  // only the rows that see a value that is not finite may take it in
-#pragma unroll 1
-      for (int j = 0; j < K; ++j) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          if ((seen[r] >> j & 1) == 0) continue;
-          const float p = sm.p[R * ty + r][j];
-#pragma unroll
-          for (int d = 0; d < kD; ++d) o[r][d] = fmaf(p, sm.v[buf][j][tx * kD + d], o[r][d]);
-        }
-      }
-    }
-    if (at.t + 1 == at.steps || i + 1 == sh.end) {  // the pair's part in this share is done
-      const Part part = end_part(a, sh, at, i, from_start, open);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float sum = l[r];
-#pragma unroll
-        for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        const unsigned long long set = tree_set_of(ts, R * ty + r);
-        const int node = R * ty + r;
-        if (node >= a.N) continue;
-        const bool missing = from_start && set == 0;
-        if (part.whole) {
-          const float inv = 1.0f / sum;
-          float* to = static_cast<float*>(a.out) + (static_cast<size_t>(at.b) * a.N + node) * a.C + at.h * HS + tx * kD;
-#pragma unroll
-          for (int d = 0; d < kD; ++d) to[d] = missing ? 0.f : o[r][d] * inv;
-        } else {
-          const size_t to = part.slot * a.N + node;
-          if (tx == 0) a.part.ml[to] = make_float2(m[r], missing ? -1.f : sum);
-#pragma unroll
-          for (int d = 0; d < kD; ++d) a.part.o[to * HS + tx * kD + d] = o[r][d];
-        }
-      }
-    }
-    __syncthreads();  // this buffer is refilled, and the queries are replaced, from here on
-    advance<K>(a, at);
-  }
-  cp_async_wait<0>();
-  if (!split_by_pair(a) && threadIdx.x == 0) a.part.split[blockIdx.x] = open;
 }
 
 // ------------------------------------------------------------------- join
@@ -999,30 +602,20 @@ int mma(const TreeArgs& a, cudaStream_t s) {
   return pairs ? mma_typed<HS, T16, 4, true>(a, s) : mma_typed<HS, T16, 4, false>(a, s);
 }
 
-template <int HS, int R>
-int simt_typed(const TreeArgs& a, cudaStream_t s) {
-  static bool allowed[kMaxDevices] = {};
-  constexpr int kSmem = sizeof(TreeSimtSmem<HS, R>);
-  static_assert(kSmem <= 227 * 1024 / 2, "two CTAs an SM");
-  const int ctas = ctas_of(a.N, 2);
-  cudaError_t e = allow_smem(allowed, tree_simt_kernel<HS, R>, kSmem);
-  if (e == cudaSuccess) e = launch_pdl(tree_simt_kernel<HS, R>, dim3(ctas), dim3(kThreads), kSmem, s, a);
-  return e == cudaSuccess ? join<float, HS>(a, ctas, s) : note_cuda_error(e);
-}
-
-template <int HS>
-int simt(const TreeArgs& a, cudaStream_t s) {
-  if (a.N <= 8) return simt_typed<HS, 1>(a, s);
-  if (a.N <= 16) return simt_typed<HS, 2>(a, s);
-  if (a.N <= 32) return simt_typed<HS, 4>(a, s);
-  return simt_typed<HS, 8>(a, s);
-}
-
 template <int HS>
 int typed(const TreeArgs& a, int op, cudaStream_t s) {
+  int ctas = 0;
+  if constexpr (HS == 64) {
+    if (op != kOpTF32 && a.N > 32 && !(getenv("TREE_TC") && atoi(getenv("TREE_TC")) == 0)) {
+      const int rc = launch_tc05(a, op, &ctas, s);
+      if (rc != GPT2_OK) return rc;
+      return op == kOpF16 ? join<__half, HS>(a, ctas, s) : join<__nv_bfloat16, HS>(a, ctas, s);
+    }
+  }
   if (op == kOpF16) return mma<HS, __half>(a, s);
   if (op == kOpBF16) return mma<HS, __nv_bfloat16>(a, s);
-  return simt<HS>(a, s);
+  const int rc = launch_simt(a, HS, &ctas, s);
+  return rc == GPT2_OK ? join<float, HS>(a, ctas, s) : rc;
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }

@@ -1,0 +1,574 @@
+// attention_tree_tc.cu -- attention of trees of more than 32 nodes over 16-bit
+// caches (attention_tree.cu) on the tcgen05 tensor cores, head size 64.
+//
+// A step is 128 keys (the nodes' own: 64).  The up to 64 queries stand twice in
+// the 128 rows of the A operand, so S = Q K^T has every score twice: rows 0-63
+// keep the first 64 keys' and rows 64-127 the others', each zeroes the other half
+// of its probabilities, and one product O += P V gives two results a node, over
+// the even and the odd halves of the keys.  Thus all four quarters of the tensor
+// memory's lanes, and with them all schedulers, share the exponentials.  Steps
+// alternate between two softmax groups of 128 threads with an O of their own,
+// which makes four results a node; they join in shared memory where a pair's part
+// in the share ends.
+//
+// As in the forward attention (attention_tc.cu): three S accumulators in TMEM that
+// P is written over (16 columns of hi and 16 of lo for 32 keys: P enters the
+// product as the sum of two values of the operand type), one warp issuing S, one
+// issuing P V, a rescale only where a row's maximum grows by more than 2^8.
+//   warp 0      loads by TMA: the queries of a pair's part (two buffers), then its
+//               steps' keys and values through a ring of three stages;
+//   warp 1      TMEM and the S products; warp 10 the P V products;
+//   warps 2-5, 6-9  the softmax groups.  The one that has the nodes' step stores
+//               their keys and values in the cache, zeroes the rows of the tile
+//               that hold none (0 times what stands there may not be 0), and takes
+//               infinities and NaN out of the others, which are added at the end
+//               to the rows that see them.
+// Every wait is bounded; after a timeout the CTA drains its copies and MMAs, frees
+// TMEM and returns.
+#include "tree_share.cuh"
+
+namespace gpt2 {
+namespace {
+
+using namespace tree;
+
+constexpr int kRows = 128;  // TMEM lanes: the queries, twice
+constexpr int kTK = 128;    // keys of a step
+constexpr int kHS = 64;
+constexpr int kTileBytes = 128 * kHS * 2;  // 128 rows of 128 bytes
+constexpr int kRing = 3;    // S accumulators (and P) in TMEM
+constexpr int kKV = 3;      // K/V stages
+constexpr int kSoftmaxWarps = 4;  // per group
+constexpr int kPvWarp = 2 + 2 * kSoftmaxWarps;
+constexpr int kTcThreads = 32 * (kPvWarp + 1);
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemS = 0;           // S buffer r at 128 r
+constexpr uint32_t kTmemO = kRing * kTK;  // O of group x at 384 + 64 x
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kJoinRow = kHS + 4;          // floats: rows' float4s in distinct banks
+
+struct Smem {
+  static constexpr int q = 0;                       // two buffers
+  static constexpr int k = q + 2 * kTileBytes;      // kKV stages of K
+  static constexpr int v = k + kKV * kTileBytes;    // kKV stages of V
+  static constexpr int join = v + kKV * kTileBytes;  // [4][64][kJoinRow] floats
+  static constexpr int ml = join + 4 * kMaxNodes * kJoinRow * 4;  // [4][64] float2
+  static constexpr int sets = ml + 4 * kMaxNodes * 8;             // [2][64] 64-bit sets
+  static constexpr int bars = sets + 2 * kMaxNodes * 8;
+  // q_full[2], q_empty[2], kv_full[kKV], kv_empty[kKV], s_full[2][kRing], p_full[kRing], o_done[kRing], o_final[2],
+  // o_free[2], drain
+  static constexpr int n_bars = 4 + 2 * kKV + 4 * kRing + 4 + 1;
+  static constexpr int misc = bars + n_bars * 8;  // TMEM address, odd[2]
+  static constexpr int total = misc + 16;
+  static constexpr int alloc = total + 1024;
+};
+static_assert(Smem::alloc <= 227 * 1024, "shared memory");
+
+// A pair's part in a share: n steps from place p (whose t is the first) on.
+struct Parts {
+  const TreeArgs& a;
+  const Share& sh;
+  Place p;
+  long long i;  // of p, among all steps
+  int n, s;     // s: its first step among the share's
+  int f;        // its number
+  __device__ __forceinline__ Parts(const TreeArgs& args, const Share& share) : a(args), sh(share), p(share.at), i(share.begin), s(0), f(0) {
+    count();
+  }
+  __device__ __forceinline__ void count() {
+    const long long left = sh.end - i;
+    n = static_cast<int>(min(static_cast<long long>(p.steps - p.t), left));
+  }
+  __device__ __forceinline__ bool more() const { return i < sh.end; }
+  __device__ __forceinline__ void next() {
+    i += n;
+    s += n;
+    ++f;
+    p.t += n - 1;
+    advance<kTK>(a, p);
+    count();
+  }
+};
+
+template <typename T16>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    tree_tc05_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     const __grid_constant__ CUtensorMap map_qkv, TreeArgs a) {
+  using L = Smem;
+  extern __shared__ uint8_t tree_tc_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tree_tc_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::bars);
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* kv_full = q_empty + 2;
+  uint64_t* kv_empty = kv_full + kKV;
+  // S is signalled per group and slot: a group walks only its own steps (see
+  // attn_tc05_kernel on why a shared barrier's parity would be ambiguous)
+  uint64_t* s_full = kv_empty + kKV;
+  uint64_t* p_full = s_full + 2 * kRing;
+  uint64_t* o_done = p_full + kRing;
+  uint64_t* o_final = o_done + kRing;
+  uint64_t* o_free = o_final + 2;
+  uint64_t* drain = o_free + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::misc);
+  int* odd = reinterpret_cast<int*>(smem + L::misc + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr uint32_t kFmt = std::is_same<T16, __half>::value ? 0u : 1u;
+  constexpr uint32_t kIdescS = make_idesc(kFmt, kRows, kTK);
+  constexpr uint32_t kIdescPV = make_idesc(kFmt, kRows, kHS) | (1u << 16);  // B (V) MN-major
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1u);
+      mbar_init(&q_empty[i], 1u);
+      mbar_init(&o_final[i], 1u);
+      mbar_init(&o_free[i], kSoftmaxWarps);
+    }
+    for (int i = 0; i < kKV; ++i) {
+      mbar_init(&kv_full[i], 1u);
+      mbar_init(&kv_empty[i], 1u);
+    }
+    for (int r = 0; r < 2 * kRing; ++r) mbar_init(&s_full[r], 1u);
+    for (int r = 0; r < kRing; ++r) {
+      mbar_init(&p_full[r], kSoftmaxWarps);
+      mbar_init(&o_done[r], 1u);
+    }
+    mbar_init(drain, 2u);
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+    tma_prefetch_desc(&map_qkv);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // the QKV projection ahead has finished
+  pdl_trigger();
+  const Share sh = share_of<kTK>(a);
+  Parts part(a, sh);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    const int box = min(kTK, 1 << a.rows.lbs), boxes = kTK / box;  // of a step
+    constexpr int kIds = kTK / 32;
+    bool ok = true;
+    for (; part.more() && ok; part.next()) {
+      const int f = part.f, x = part.p.h * kHS, y = part.p.b * a.N;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[f & 1], ((f >> 1) & 1) ^ 1)))) break;
+      if (lane == 0) {
+        uint8_t* q = smem + L::q + (f & 1) * kTileBytes;
+        mbar_arrive_expect_tx(&q_full[f & 1], kTileBytes);
+        tma_load_2d(q, &map_qkv, &q_full[f & 1], x, y);
+        tma_load_2d(q + kTileBytes / 2, &map_qkv, &q_full[f & 1], x, y);
+      }
+      const int* table = a.rows.table + static_cast<size_t>(part.p.b) * a.rows.max_blocks;
+      int ids[kIds];
+      auto lookup = [&](int t) {  // lane i: the blocks of step t's boxes i, i + 32, ..
+#pragma unroll
+        for (int u = 0; u < kIds; ++u) {
+          const int j = (t - 1) * kTK + (lane + 32 * u) * box;
+          ids[u] = t > 0 && lane + 32 * u < boxes && j < part.p.seq.pos ? __ldg(table + (j >> a.rows.lbs)) : 0;
+        }
+      };
+      lookup(part.p.t);
+      for (int k = 0; k < part.n; ++k) {
+        const int s = part.s + k, t = part.p.t + k, stg = s % kKV;
+        // (a timeout seen by any lane stops all of them)
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stg], ((s / kKV) & 1) ^ 1)))) break;
+        uint8_t* kd = smem + L::k + stg * kTileBytes;
+        uint8_t* vd = smem + L::v + stg * kTileBytes;
+        if (t == 0) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&kv_full[stg], kTileBytes);
+            tma_load_2d(kd, &map_qkv, &kv_full[stg], a.C + x, y);
+            tma_load_2d(vd, &map_qkv, &kv_full[stg], 2 * a.C + x, y);
+          }
+        } else {
+          const int j0 = (t - 1) * kTK;
+          const int n = min(boxes, (part.p.seq.pos - j0 + box - 1) / box);  // boxes that hold a cached position
+          if (lane == 0) mbar_arrive_expect_tx(&kv_full[stg], 2 * n * box * 128);
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < kIds; ++u) {
+            const int i = lane + 32 * u;
+            if (i >= n) continue;
+            int blk = ids[u];
+            if (blk < 0 || blk >= a.rows.num_blocks) {
+              if (part.p.h == 0) set_error(GPT2_DEVERR_BLOCK);
+              blk = 0;
+            }
+            const int row = (j0 + i * box) & ((1 << a.rows.lbs) - 1);
+            tma_load_4d(kd + i * box * 128, &map_k, &kv_full[stg], 0, row, part.p.h, blk);
+            tma_load_4d(vd + i * box * 128, &map_v, &kv_full[stg], 0, row, part.p.h, blk);
+          }
+        }
+        if (k + 1 < part.n) lookup(t + 1);
+      }
+    }
+    // the copies issued here land before the CTA may exit: those of the last
+    // stages, waited for again (after a timeout with the same limit)
+    if (!ok && lane == 0) {
+      for (int stg = 0; stg < kKV; ++stg) mbar_wait(&kv_full[stg], 0), mbar_wait(&kv_full[stg], 1);
+      for (int x = 0; x < 2; ++x) mbar_wait(&q_full[x], 0), mbar_wait(&q_full[x], 1);
+    }
+    __syncwarp();
+  } else if (warp == 1 || warp == kPvWarp) {
+    // ------------------------------------------------------------- MMAs
+    // the whole warp runs the loop, one lane issues
+    bool ok = true;
+    int used[2] = {0, 0};  // P V: the parts that group x had steps of
+    for (; part.more() && ok; part.next()) {
+      if (warp == 1) {
+        // S(s) = Q K^T into slot s % 3, once P V of step s - 3 has read P there
+        ok = __all_sync(0xffffffffu, mbar_wait(&q_full[part.f & 1], (part.f >> 1) & 1));
+        for (int k = 0; k < part.n && ok; ++k) {
+          const int s = part.s + k;
+          if (s >= kRing) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[s % kRing], ((s - kRing) / kRing) & 1));
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[s % kKV], (s / kKV) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t qd = smem_desc_sw128(smem_u32(smem + L::q + (part.f & 1) * kTileBytes));
+          const uint64_t kdsc = smem_desc_sw128(smem_u32(smem + L::k + (s % kKV) * kTileBytes));
+#pragma unroll
+          for (int kk = 0; kk < kHS / 16; ++kk)  // 16 dimensions = 32 bytes = 2 in the descriptor's address field
+            tc_mma_warp<false>(tmem + kTmemS + (s % kRing) * kTK, qd + 2 * kk, kdsc + 2 * kk, kIdescS, kk > 0 ? 1u : 0u);
+          tc_commit_warp(&s_full[(s & 1) * kRing + s % kRing]);
+        }
+        if (ok) tc_commit_warp(&q_empty[part.f & 1]);
+      } else {
+        // O_x += P(s) V; the group's first step of a part overwrites O_x
+        for (int k = 0; k < part.n && ok; ++k) {
+          const int s = part.s + k, x = s & 1;
+          const bool first = k < 2;
+          if (first && used[x]++ > 0) ok = __all_sync(0xffffffffu, mbar_wait(&o_free[x], (used[x] - 2) & 1));
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&p_full[s % kRing], (s / kRing) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t p_tmem = tmem + kTmemS + (s % kRing) * kTK;
+          const uint64_t vdsc = smem_desc_sw128_mn(smem_u32(smem + L::v + (s % kKV) * kTileBytes), 1024);
+          const int ksteps = part.p.t + k == 0 ? kMaxNodes / 16 : kTK / 16;  // the nodes are 64 keys
+#pragma unroll
+          for (int kk = 0; kk < kTK / 16; ++kk) {  // P: 16 keys = 8 TMEM columns; V: 16 rows of 128 bytes
+            if (kk >= ksteps) break;
+            const uint32_t p = p_tmem + (kk >> 1) * 32 + (kk & 1) * 8;  // 32 keys: 16 columns of hi, 16 of lo
+            tc_mma_ts_warp(tmem + kTmemO + x * kHS, p + 16, vdsc + kk * (2048 / 16), kIdescPV,
+                           (!first || kk > 0) ? 1u : 0u);
+            tc_mma_ts_warp(tmem + kTmemO + x * kHS, p, vdsc + kk * (2048 / 16), kIdescPV, 1u);
+          }
+          tc_commit_warp(&o_done[s % kRing]);
+          if (k + 2 >= part.n) tc_commit_warp(&o_final[x]);
+          tc_commit_warp(&kv_empty[s % kKV]);
+        }
+      }
+    }
+    tc_commit_warp(drain);
+    mbar_wait(drain, 0);
+  } else {
+    // ---------------------------------------------------------- softmax (warps 2-9)
+    const int x = (warp - 2) / kSoftmaxWarps;
+    const int tg = ((warp - 2) % kSoftmaxWarps) * 32 + lane;  // of the group's threads
+    const int qw = warp & 3;  // TMEM lane quadrant this warp may access
+    const int half = qw >> 1, row = (qw & 1) * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(qw * 32) << 16);
+    uint16_t* kcache = static_cast<uint16_t*>(a.kcache);
+    uint16_t* vcache = static_cast<uint16_t*>(a.vcache);
+    float* join = reinterpret_cast<float*>(smem + L::join);
+    float2* join_ml = reinterpret_cast<float2*>(smem + L::ml);
+    uint32_t s_par = 0;  // bit r: parity of this group's next phase of s_full[x][r]
+    uint32_t final_par = 0;
+    int4 open = make_int4(-1, 0, 0, 0);
+    for (; part.more(); part.next()) {
+      const Place& p = part.p;
+      unsigned long long* sets = reinterpret_cast<unsigned long long*>(smem + L::sets) + (part.f & 1) * kMaxNodes;
+      bool ok = true;
+      float m_run = -INFINITY, l_run = 0.f;
+      int done = 0;  // this group's steps of the part
+      for (int k = (x ^ part.s) & 1; k < part.n; k += 2, ++done) {
+        const int s = part.s + k, r = s % kRing, t = p.t + k;
+        const uint32_t s_col = kTmemS + r * kTK;
+        unsigned long long bits;  // the keys of this row's half that it sees
+        int valid = kTK;          // keys of the step
+        if (t == 0) {
+          const int* parents = a.parent != nullptr ? a.parent + static_cast<size_t>(p.b) * a.N : nullptr;
+          int par[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) par[u] = p.seq.live > 0 ? tree_parent(parents, lane + 32 * u, a.N) : -2;
+          const bool report = p.h == 0 && tg < 32;
+          if (report && lane == 0) seq_of(a, p.b, true);
+          const TreeSets ts = tree_sets(par, a.N, p.seq.live, report);
+          const unsigned long long mine = tree_set_of(ts, row), live = tree_live(ts);
+          bits = half == 0 ? mine : 0;
+          if (half == 0) sets[row] = mine;
+          // (every thread reaches the group's barrier below, whatever its wait returned)
+          ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[s % kKV], (s / kKV) & 1));
+          const uint8_t* kd = smem + L::k + (s % kKV) * kTileBytes;
+          uint8_t* vd = smem + L::v + (s % kKV) * kTileBytes;
+          bool bad = false;
+          for (int c0 = tg; ok && c0 < kMaxNodes * 8; c0 += 32 * kSoftmaxWarps) {
+            const int node = c0 >> 3, c = c0 & 7;
+            uint4* vp = reinterpret_cast<uint4*>(vd + tile_at<kHS>(node, c));
+            if (node >= a.N) {
+              *vp = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+            const uint4 v = *vp;
+            if (any_not_finite<T16>(v)) {
+              bad = true;
+              uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              constexpr uint32_t kExp = std::is_same<T16, __half>::value ? 0x7c00u : 0x7f80u;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if ((w[q] & kExp) == kExp) w[q] &= 0xffff0000u;
+                if ((w[q] >> 16 & kExp) == kExp) w[q] &= 0xffffu;
+              }
+              *vp = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if ((live >> node & 1) == 0) continue;
+            const int j = p.seq.pos + node;
+            const int blk = __ldg(a.rows.table + static_cast<size_t>(p.b) * a.rows.max_blocks + (j >> a.rows.lbs));
+            if (blk < 0 || blk >= a.rows.num_blocks) {
+              if (p.h == 0) set_error(GPT2_DEVERR_BLOCK);
+              continue;
+            }
+            const size_t to = cache_row(a, blk, p.h, j) * kHS + c * 8;
+            *reinterpret_cast<uint4*>(kcache + to) = *reinterpret_cast<const uint4*>(kd + tile_at<kHS>(node, c));
+            *reinterpret_cast<uint4*>(vcache + to) = v;
+          }
+          fence_proxy_async_smem();
+          bad = bar_or(4 + x, 32 * kSoftmaxWarps, bad);
+          if (tg == 0) odd[part.f & 1] = bad;
+          if (!ok) break;
+        } else {
+          valid = min(kTK, p.seq.pos - (t - 1) * kTK);
+          const int mine = valid - 64 * half;
+          bits = mine >= 64 ? ~0ull : mine <= 0 ? 0ull : (1ull << mine) - 1;
+          if (valid < kTK) {  // the rows of the last tile that hold no key
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[s % kKV], (s / kKV) & 1)))) break;
+            uint8_t* vd = smem + L::v + (s % kKV) * kTileBytes;
+            for (int c = tg; c < (kTK - valid) * 8; c += 32 * kSoftmaxWarps)
+              *reinterpret_cast<uint4*>(vd + valid * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+          }
+        }
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x * kRing + r], (s_par >> r) & 1u)))) break;
+        s_par ^= 1u << r;
+        tc_fence_after();
+        uint32_t zero[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) zero[e] = 0u;
+        if (__any_sync(0xffffffffu, bits != 0)) {
+          uint32_t sc[2][32];
+          tmem_ld_32x32b_x32(lane_base + s_col + 64 * half, sc[0]);
+          tmem_ld_32x32b_x32(lane_base + s_col + 64 * half + 32, sc[1]);
+          tmem_ld_wait_regs(sc[0]);
+          tmem_ld_wait_regs(sc[1]);
+          if (__any_sync(0xffffffffu, bits != ~0ull)) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if ((bits >> (32 * c + e) & 1) == 0) sc[c][e] = 0xff800000u;
+          }
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) mx[c] = fmax3(mx[c], __uint_as_float(sc[c][e]), __uint_as_float(sc[c][e + 1]));
+          const float top = fmaxf(mx[0], mx[1]) * a.scale_log2;
+          const bool grow = top > m_run + kRescaleThreshold;  // at first: from -inf
+          if (__any_sync(0xffffffffu, grow)) {
+            const float m_new = grow ? top : m_run;
+            const float alpha = grow ? exp2_approx(m_run - m_new) : 1.f;
+            if (done > 0) {
+              // P V of this group's step before is done before O is rescaled
+              if (!(ok = __all_sync(0xffffffffu, mbar_wait(&o_done[(s - 2) % kRing], ((s - 2) / kRing) & 1)))) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < kHS / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(lane_base + kTmemO + x * kHS + c * 32, o);
+                tmem_ld_wait_regs(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st_32x32b_x32(lane_base + kTmemO + x * kHS + c * 32, o);
+              }
+            }
+            l_run *= alpha;
+            m_run = m_new;
+          }
+          const float ref = m_run == -INFINITY ? 0.f : m_run;  // a row that has seen nothing yet
+          const float2 scale = make_float2(a.scale_log2, a.scale_log2), nm = make_float2(-ref, -ref);
+          float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[32];  // 16 columns of hi, 16 of lo
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 v =
+                  __ffma2_rn(make_float2(__uint_as_float(sc[c][2 * e]), __uint_as_float(sc[c][2 * e + 1])), scale, nm);
+              const float2 w = make_float2(exp2_approx(v.x), exp2_approx(v.y));
+              sum[e & 3] = __fadd2_rn(sum[e & 3], w);
+              split2<T16>(w.x, w.y, pk[e], pk[16 + e]);
+            }
+            tmem_st_32x32b_x32(lane_base + s_col + 64 * half + 32 * c, pk);
+          }
+          const float2 all = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+          l_run += all.x + all.y;
+        } else {
+          tmem_st_32x32b_x32(lane_base + s_col + 64 * half, zero);
+          tmem_st_32x32b_x32(lane_base + s_col + 64 * half + 32, zero);
+        }
+        // the other half of the keys is the other half of the rows'
+        tmem_st_32x32b_x32(lane_base + s_col + 64 * (1 - half), zero);
+        tmem_st_32x32b_x32(lane_base + s_col + 64 * (1 - half) + 32, zero);
+        tmem_st_wait();  // P written by this thread is in TMEM before the MMA reads it
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[r]);
+      }
+      // the four results of each node join in shared memory
+      if (ok && done > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&o_final[x], final_par));
+        final_par ^= 1;
+      }
+      // (also: the part before has been read)
+      if (bar_or(2, 64 * kSoftmaxWarps, !ok)) break;
+      const int sub = 2 * x + half;
+      join_ml[sub * kMaxNodes + row] = make_float2(m_run, l_run);
+      if (done > 0) {
+        tc_fence_after();
+        float* to = join + (sub * kMaxNodes + row) * kJoinRow;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(lane_base + kTmemO + x * kHS + 32 * c, o);
+          tmem_ld_wait_regs(o);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(to + 32 * c + 4 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[x]);
+      }
+      bar_or(3, 64 * kSoftmaxWarps, false);
+      const int ts = threadIdx.x - 64, node = ts >> 2, d = (ts & 3) * 16;  // 16 dimensions of a node
+      const bool from_start = p.t == 0;
+      Place end = p;
+      end.t += part.n - 1;
+      const Part mine = end_part(a, sh, end, part.i + part.n - 1, from_start, open, ts == 0);
+      if (node < a.N) {
+        float M = -INFINITY, l = 0.f, o[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) M = fmaxf(M, join_ml[u * kMaxNodes + node].x);
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 ml = join_ml[u * kMaxNodes + node];
+          if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing seen, or no step
+          const float w = exp2_approx(ml.x - ref);
+          l = fmaf(ml.y, w, l);
+          const float4* from = reinterpret_cast<const float4*>(join + (u * kMaxNodes + node) * kJoinRow + d);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 v = from[q];
+            o[4 * q] = fmaf(v.x, w, o[4 * q]);
+            o[4 * q + 1] = fmaf(v.y, w, o[4 * q + 1]);
+            o[4 * q + 2] = fmaf(v.z, w, o[4 * q + 2]);
+            o[4 * q + 3] = fmaf(v.w, w, o[4 * q + 3]);
+          }
+        }
+        const unsigned long long set = from_start ? sets[node] : 0;
+        const bool missing = from_start && set == 0;
+        if (from_start && odd[part.f & 1] != 0) {  // what was taken out of the nodes' values
+          for (unsigned long long left = set; left != 0; left &= left - 1) {
+            const int j = __ffsll(static_cast<long long>(left)) - 1;
+            const T16* v = static_cast<const T16*>(a.qkv) + (static_cast<size_t>(p.b) * a.N + j) * 3 * a.C + 2 * a.C +
+                           p.h * kHS + d;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float w = to_f32(v[e]);
+              if (!isfinite(w)) o[e] += w;
+            }
+          }
+        }
+        if (mine.whole) {
+          const float inv = 1.0f / l;
+          uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                               (static_cast<size_t>(p.b) * a.N + node) * a.C + p.h * kHS + d);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            to[q] = missing ? make_uint4(0u, 0u, 0u, 0u)
+                            : make_uint4(pack2<T16>(o[8 * q] * inv, o[8 * q + 1] * inv),
+                                         pack2<T16>(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                                         pack2<T16>(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
+                                         pack2<T16>(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+        } else {
+          const size_t to = mine.slot * a.N + node;
+          // a sum of -1 tells the join that the node is missing
+          if ((ts & 3) == 0) a.part.ml[to] = make_float2(M, missing ? -1.f : l);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4*>(a.part.o + to * kHS + d + 4 * q) =
+                make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
+      }
+    }
+    if (!split_by_pair(a) && threadIdx.x == 64) a.part.split[blockIdx.x] = open;
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <typename T16>
+int tc_typed(const TreeArgs& a, int* ctas, cudaStream_t s) {
+  static bool allowed[kMaxDevices] = {};
+  const CUtensorMapDataType dt =
+      std::is_same<T16, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap mk, mv, mq;
+  {
+    const uint64_t bs = 1ull << a.rows.lbs, row = kHS * 2;
+    const uint64_t dims[4] = {kHS, bs, static_cast<uint64_t>(a.NH), static_cast<uint64_t>(a.rows.num_blocks)};
+    const uint64_t strides[3] = {row, row * bs, row * bs * a.NH};
+    const uint32_t box[4] = {kHS, static_cast<uint32_t>(bs < kTK ? bs : kTK), 1, 1};
+    if (!encode_tensor_map(&mk, dt, 4, a.kcache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tensor_map(&mv, dt, 4, a.vcache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return GPT2_ERR_CUDA;
+  }
+  {
+    const uint64_t dims[2] = {3ull * a.C, static_cast<uint64_t>(a.B) * a.N}, strides[1] = {6ull * a.C};
+    const uint32_t box[2] = {kHS, kMaxNodes};
+    if (!encode_tensor_map(&mq, dt, 2, a.qkv, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return GPT2_ERR_CUDA;
+  }
+  *ctas = num_sms() < max_ctas(a.N) ? num_sms() : max_ctas(a.N);
+  cudaError_t e = allow_smem(allowed, tree_tc05_kernel<T16>, Smem::alloc);
+  if (e == cudaSuccess)
+    e = launch_pdl(tree_tc05_kernel<T16>, dim3(*ctas), dim3(kTcThreads), Smem::alloc, s, mk, mv, mq, a);
+  return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
+}
+
+}  // namespace
+
+namespace tree {
+
+int launch_tc05(const TreeArgs& a, int op, int* ctas, cudaStream_t s) {
+  return op == kOpF16 ? tc_typed<__half>(a, ctas, s) : tc_typed<__nv_bfloat16>(a, ctas, s);
+}
+
+}  // namespace tree
+}  // namespace gpt2
