@@ -1,15 +1,407 @@
 // attention_tree_f32.cu -- the part of attention_tree.cu for fp32 caches, on CUDA
-// cores.
-#include "tree_share.cuh"
-
+// cores (in the TF32 mode too).
+//   tree_f32_kernel    up to eight nodes
+//   tree_simt_kernel   more
 #include <algorithm>
+
+#include "tree_share.cuh"
 
 namespace gpt2 {
 namespace {
 
 using namespace tree;
 
-// fp32 caches, fp32 arithmetic (in the TF32 mode too).  128 threads: ty = thread
+// Up to eight nodes: a warp keeps their rows.  Scores: a lane has a key (two of a
+// tile of 64), reads it once and the queries as broadcasts, eight rows against it in
+// packed pairs of dimensions.  The probabilities go through shared memory; then a
+// lane has four dimensions and every (128 / HS)-th group of four keys, so that a
+// value is read once and a probability once for four dimensions.  Keys and values
+// come by TMA as in attention_tree_16.cuh, whose shares and groups these are.  (A
+// broadcast takes a wavefront for each four of its 16 bytes: with more rows, in more
+// warps, shared memory is what they wait for: 480 pairs of 64 dimensions, 1000-4000
+// cached, 30 nodes 463 us against 379 of tree_simt_kernel, 5 nodes 166 against 303.)
+constexpr int R = 8;           // rows of a warp
+constexpr float kGrow = 8.0f;  // log2 units by which a score may pass its row's maximum before that is raised
+
+template <int HS, int WM>
+struct RingF32 {
+  static constexpr int kKeys = HS == 64 && WM < 8 ? 32 : 64;  // of a tile
+  static constexpr int kRow = HS * 4;                         // bytes of a key
+  static constexpr int kStrips = HS == 64 ? 2 : 1;            // a TMA box is at most 128 bytes wide
+  static constexpr int kTileBytes = kKeys * kRow;
+  static constexpr int kNodeBytes = R * WM * kRow;  // of the nodes' queries, keys or values
+  static constexpr int kStage = 2 * kTileBytes > 3 * kNodeBytes ? 2 * kTileBytes : 3 * kNodeBytes;
+  static constexpr int kStages = HS == 16 ? 3 : 2;
+  static constexpr int kPRow = kKeys + 4;  // floats of a row of probabilities
+  static constexpr int kWarp = R * (HS + kPRow) * 4 + R * 8;  // a warp's queries, probabilities, sets
+  // the rings from a multiple of 1024 bytes on, the warps' own, the barriers
+  static constexpr int kGroup = kStages * kStage;
+  static constexpr int smem(int groups) { return 1024 + groups * (kGroup + WM * kWarp + kStages * 8); }
+};
+
+constexpr int f32_warps(int WM, int groups) { return WM * (groups > 0 ? groups : 1); }
+template <int HS, int WM, int kGroups>
+constexpr int f32_ctas() {  // CTAs an SM: twelve warps, as far as shared memory goes
+  const int fit = 228 * 1024 / (RingF32<HS, WM>::smem(kGroups > 0 ? kGroups : 1) + 1024);
+  const int most = 12 / f32_warps(WM, kGroups);
+  return fit < most ? fit : most;
+}
+
+template <int HS, int WM, int kGroups>
+__global__ void __launch_bounds__(32 * f32_warps(WM, kGroups), f32_ctas<HS, WM, kGroups>())
+    tree_f32_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                    const __grid_constant__ CUtensorMap map_qkv, TreeArgs a) {
+  using Ring = RingF32<HS, WM>;
+  constexpr int K = Ring::kKeys, kStages = Ring::kStages, kStrips = Ring::kStrips, kChunks = HS / 4;
+  constexpr int KG = 32 / kChunks;  // key groups of the lanes
+  constexpr bool kPairs = kGroups > 0;
+  constexpr int WK = kPairs ? kGroups : 1;
+  extern __shared__ uint8_t tree_f32_raw[];
+  uint8_t* rings = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tree_f32_raw) + 1023) & ~uintptr_t(1023));
+  const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / WM;
+  const int warp = (threadIdx.x >> 5) % WM;  // of the group: its nodes are R warp ..
+  uint8_t* ring = rings + group * Ring::kGroup;
+  uint8_t* own = rings + WK * Ring::kGroup + (threadIdx.x >> 5) * Ring::kWarp;
+  float* qb = reinterpret_cast<float*>(own);
+  float* pb = qb + R * HS;
+  unsigned long long* sets = reinterpret_cast<unsigned long long*>(pb + R * Ring::kPRow);
+  uint64_t* full = reinterpret_cast<uint64_t*>(rings + WK * (Ring::kGroup + WM * Ring::kWarp)) + group * kStages;
+  const int kg = lane / kChunks, dl = lane % kChunks;  // key group, dimensions 4 dl ..
+  float* kcache = static_cast<float*>(a.kcache);
+  float* vcache = static_cast<float*>(a.vcache);
+  if (warp == 0 && lane == 0) {
+    if (group == 0) {
+      tma_prefetch_desc(&map_k);
+      tma_prefetch_desc(&map_v);
+      tma_prefetch_desc(&map_qkv);
+    }
+    for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1);
+    fence_barrier_init();
+  }
+  pdl_wait();  // the QKV projection ahead has finished
+  pdl_trigger();
+  Share sh;
+  if constexpr (kPairs)
+    sh = pair_share<K, WK>(a, group);
+  else
+    sh = share_of<K>(a);
+  int4 open = make_int4(-1, 0, 0, 0);
+  group_or<WM>(group, false);  // the barriers
+
+  Feed<Ring, WM, WK> feed(a, sh, kPairs, map_k, map_v, map_qkv, ring, full);
+  const int lead = feed.lead, n_steps = feed.n_steps;
+  if (warp == 0) feed.begin();
+
+  Place at = sh.at;
+  bool from_start = false;
+  float m[R], l[R];  // the row's maximum (log2 units), the sum over this lane's keys
+  float4 o[R];
+  auto begin_pair = [&](const uint8_t* q) {
+    __syncwarp();  // (the pair before is done with the queries)
+#pragma unroll
+    for (int x = lane; x < R * kChunks; x += 32) {
+      const int r = x / kChunks, c = x % kChunks;
+      *reinterpret_cast<float4*>(qb + r * HS + 4 * c) =
+          *reinterpret_cast<const float4*>(q + tile_at_bytes<Ring::kRow, kStrips>(warp * R + r, c, R * WM));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+      o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  // rows [from, to) of a tile of `rows`, that hold no key: 0 times what stands there
+  // may not be 0
+  auto zero_rows = [&](uint8_t* v, int from, int to, int rows) {
+    for (int x = lane; x < (to - from) * kChunks; x += 32)
+      *reinterpret_cast<uint4*>(v + tile_at_bytes<Ring::kRow, kStrips>(from + x / kChunks, x % kChunks, rows)) =
+          make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();  // before the next copy into the stage
+    __syncwarp();
+  };
+  // The online softmax and O += P V over a tile of `rows` of which `keys` hold one.
+  // nodes: row r sees those of sets[r]; otherwise all.  odd: a node's value may not
+  // be finite, which only the rows that see it may take in.  (One instance for both
+  // kinds of step: code that is fetched once costs more than what it computes.)
+  auto attend = [&](const uint8_t* kt, const uint8_t* vt, int rows, int keys, bool nodes, bool odd) {
+    constexpr int KL = K / 32;
+    float2 s[R][KL];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int u = 0; u < KL; ++u) s[r][u] = make_float2(0.f, 0.f);
+#pragma unroll 2
+    for (int c = 0; c < kChunks; ++c) {
+      float4 k[KL];
+#pragma unroll
+      for (int u = 0; u < KL; ++u)
+        k[u] = *reinterpret_cast<const float4*>(kt + tile_at_bytes<Ring::kRow, kStrips>(lane + 32 * u, c, rows));
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float4 q = *reinterpret_cast<const float4*>(qb + r * HS + 4 * c);
+#pragma unroll
+        for (int u = 0; u < KL; ++u) {
+          s[r][u] = __ffma2_rn(make_float2(q.x, q.y), make_float2(k[u].x, k[u].y), s[r][u]);
+          s[r][u] = __ffma2_rn(make_float2(q.z, q.w), make_float2(k[u].z, k[u].w), s[r][u]);
+        }
+      }
+    }
+    bool up = false;
+    const unsigned long long all = keys >= 64 ? ~0ull : (1ull << keys) - 1;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const unsigned long long seen = nodes ? sets[r] : all;
+#pragma unroll
+      for (int u = 0; u < KL; ++u) {
+        const bool sees = (seen >> (lane + 32 * u) & 1) != 0;
+        s[r][u].x = sees ? s[r][u].x + s[r][u].y : -INFINITY;
+        up |= s[r][u].x * a.scale_log2 > m[r] + kGrow;  // at first: than -inf
+      }
+    }
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float mx = s[r][0].x;
+#pragma unroll
+        for (int u = 1; u < KL; ++u) mx = fmaxf(mx, s[r][u].x);
+        mx = warp_max(mx) * a.scale_log2;
+        if (mx > m[r] + kGrow) {
+          const float alpha = exp2_approx(m[r] - mx);
+          m[r] = mx;
+          l[r] *= alpha;
+          o[r].x *= alpha;
+          o[r].y *= alpha;
+          o[r].z *= alpha;
+          o[r].w *= alpha;
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float ref = m[r] == -INFINITY ? 0.f : m[r];  // a row that has seen nothing yet
+#pragma unroll
+      for (int u = 0; u < KL; ++u) {
+        const float p = exp2_approx(fmaf(s[r][u].x, a.scale_log2, -ref));
+        l[r] += p;
+        pb[r * Ring::kPRow + lane + 32 * u] = p;
+      }
+    }
+    __syncwarp();
+    const int blocks = (keys + 3) / 4;  // of four keys; the rows behind the keys are zero
+    if (!odd) {
+#pragma unroll 1
+      for (int b = kg; b < blocks; b += KG) {
+        float4 v[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          v[x] = *reinterpret_cast<const float4*>(vt + tile_at_bytes<Ring::kRow, kStrips>(4 * b + x, dl, rows));
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float4 p = *reinterpret_cast<const float4*>(pb + r * Ring::kPRow + 4 * b);
+          o[r].x = fmaf(p.x, v[0].x, fmaf(p.y, v[1].x, fmaf(p.z, v[2].x, fmaf(p.w, v[3].x, o[r].x))));
+          o[r].y = fmaf(p.x, v[0].y, fmaf(p.y, v[1].y, fmaf(p.z, v[2].y, fmaf(p.w, v[3].y, o[r].y))));
+          o[r].z = fmaf(p.x, v[0].z, fmaf(p.y, v[1].z, fmaf(p.z, v[2].z, fmaf(p.w, v[3].z, o[r].z))));
+          o[r].w = fmaf(p.x, v[0].w, fmaf(p.y, v[1].w, fmaf(p.z, v[2].w, fmaf(p.w, v[3].w, o[r].w))));
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int j = kg; j < keys; j += KG) {
+        const float4 v = *reinterpret_cast<const float4*>(vt + tile_at_bytes<Ring::kRow, kStrips>(j, dl, rows));
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if ((sets[r] >> j & 1) == 0) continue;
+          const float p = pb[r * Ring::kPRow + j];
+          o[r].x = fmaf(p, v.x, o[r].x);
+          o[r].y = fmaf(p, v.y, o[r].y);
+          o[r].z = fmaf(p, v.z, o[r].z);
+          o[r].w = fmaf(p, v.w, o[r].w);
+        }
+      }
+    }
+    __syncwarp();  // the probabilities are read
+  };
+  // the lanes' sums over their keys
+  auto reduce = [&]() {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      l[r] = warp_sum(l[r]);
+#pragma unroll
+      for (int x = 16; x >= kChunks; x >>= 1) {
+        o[r].x += __shfl_xor_sync(0xffffffffu, o[r].x, x);
+        o[r].y += __shfl_xor_sync(0xffffffffu, o[r].y, x);
+        o[r].z += __shfl_xor_sync(0xffffffffu, o[r].z, x);
+        o[r].w += __shfl_xor_sync(0xffffffffu, o[r].w, x);
+      }
+    }
+  };
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int n = 0; n < n_steps; ++n) {
+    const bool came = mbar_wait(full + stage, phase);
+    // the step's keys are there, and every warp is past the step whose stage is
+    // refilled now; a copy that did not come (flagged by the wait) ends the share
+    if (group_or<WM>(group, !came)) {
+      if (warp == 0) feed.drain(n);
+      break;
+    }
+    if (warp == 0) feed.copy((stage + kStages - 1) % kStages);
+    uint8_t* st = ring + stage * Ring::kStage;
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+    if (n < lead) {  // the queries of the pair inside which the share begins
+      begin_pair(st);
+      from_start = false;
+      continue;
+    }
+    const uint8_t *keys_at = st, *values_at = st + Ring::kTileBytes;
+    int rows = K, keys = min(K, at.seq.pos - (at.t - 1) * K);
+    bool odd = false;
+    if (at.t == 0) {
+      from_start = true;
+      begin_pair(st);
+      const int* row = a.parent != nullptr ? a.parent + static_cast<size_t>(at.b) * a.N : nullptr;
+      int par[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) par[u] = at.seq.live > 0 ? tree_parent(row, lane + 32 * u, a.N) : -2;
+      const bool report = at.h == 0 && warp == 0;
+      if (report && lane == 0) seq_of(a, at.b, true);
+      const TreeSets ts = tree_sets(par, a.N, at.seq.live, report);
+      const unsigned long long mine = tree_set_of(ts, warp * R + (lane & (R - 1))), live = tree_live(ts);
+      if (lane < R) sets[lane] = mine;
+      const uint8_t* kt = st + Ring::kNodeBytes;
+      uint8_t* vt = st + 2 * Ring::kNodeBytes;
+      // this warp's nodes are stored; every warp looks at all values
+      bool bad = false;
+      for (int x = lane; x < a.N * kChunks; x += 32) {
+        const int node = x / kChunks, c = x % kChunks;
+        const uint32_t in = tile_at_bytes<Ring::kRow, kStrips>(node, c, R * WM);
+        const float4 v = *reinterpret_cast<const float4*>(vt + in);
+        bad |= !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w));
+        if (node / R != warp || (live >> node & 1) == 0) continue;
+        const int j = at.seq.pos + node;
+        const int blk = __ldg(a.rows.table + static_cast<size_t>(at.b) * a.rows.max_blocks + (j >> a.rows.lbs));
+        if (blk < 0 || blk >= a.rows.num_blocks) {
+          if (at.h == 0) set_error(GPT2_DEVERR_BLOCK);
+          continue;
+        }
+        const size_t to = cache_row(a, blk, at.h, j) * HS + c * 4;
+        *reinterpret_cast<float4*>(kcache + to) = *reinterpret_cast<const float4*>(kt + in);
+        *reinterpret_cast<float4*>(vcache + to) = v;
+      }
+      zero_rows(vt, a.N, R * WM, R * WM);
+      keys_at = kt;
+      values_at = vt;
+      rows = keys = R * WM;
+      odd = __any_sync(0xffffffffu, bad);
+    } else if (keys < K) {
+      zero_rows(st + Ring::kTileBytes, keys, K, K);
+    }
+    attend(keys_at, values_at, rows, keys, at.t == 0, odd);
+    const long long i = sh.begin + n - lead;
+    if (!kPairs && (at.t + 1 == at.steps || i + 1 == sh.end)) {  // the pair's part in this share is done
+      const Part part = end_part(a, sh, at, i, from_start, open, threadIdx.x == 0);
+      reduce();
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int node = warp * R + r;
+        if (node >= a.N || r % KG != kg) continue;
+        const bool missing = from_start && sets[r] == 0;
+        if (part.whole) {
+          const float inv = 1.0f / l[r];
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (static_cast<size_t>(at.b) * a.N + node) * a.C +
+                                     at.h * HS + 4 * dl) =
+              missing ? make_float4(0.f, 0.f, 0.f, 0.f)
+                      : make_float4(o[r].x * inv, o[r].y * inv, o[r].z * inv, o[r].w * inv);
+        } else {
+          const size_t to = part.slot * a.N + node;
+          // a sum of -1 tells the join that the node is missing
+          if (dl == 0) a.part.ml[to] = make_float2(m[r], missing ? -1.f : l[r]);
+          *reinterpret_cast<float4*>(a.part.o + to * HS + 4 * dl) = o[r];
+        }
+      }
+    }
+    feed.forward(at);
+  }
+  if constexpr (!kPairs) {
+    if (!split_by_pair(a) && threadIdx.x == 0) a.part.split[blockIdx.x] = open;
+  } else {
+    // the groups' results join where their rings were; group 0, which has the
+    // nodes' own step, writes the rows
+    constexpr int kRowF = HS + 4;  // floats: the row, its maximum and sum
+    static_assert(R * WM * kRowF * 4 <= Ring::kGroup, "a group's results fit in its ring");
+    const bool some = sh.end > 0;
+    if (some) reduce();
+    if (WK > 1) {
+      __syncthreads();
+      if (group > 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float* row = reinterpret_cast<float*>(ring) + (warp * R + r) * kRowF;
+          if (r % KG != kg) continue;
+          if (some) *reinterpret_cast<float4*>(row + 4 * dl) = o[r];
+          if (dl == 0) *reinterpret_cast<float2*>(row + HS) = some ? make_float2(m[r], l[r]) : make_float2(-INFINITY, 0.f);
+        }
+      }
+      __syncthreads();
+      if (group > 0) return;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int node = warp * R + r;
+      if (node >= a.N || r % KG != kg) continue;
+      auto other = [&](int k) {
+        return reinterpret_cast<const float*>(rings + k * Ring::kGroup) + (warp * R + r) * kRowF;
+      };
+      float M = m[r];
+#pragma unroll
+      for (int k = 1; k < WK; ++k) M = fmaxf(M, other(k)[HS]);
+      const float ref = M == -INFINITY ? 0.f : M, f = exp2_approx(m[r] - ref);
+      float sum = l[r] * f;
+      float4 v = make_float4(o[r].x * f, o[r].y * f, o[r].z * f, o[r].w * f);
+#pragma unroll
+      for (int k = 1; k < WK; ++k) {
+        const float2 ml = *reinterpret_cast<const float2*>(other(k) + HS);
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // a group without a step leaves no row
+        const float w = exp2_approx(ml.x - ref);
+        sum = fmaf(ml.y, w, sum);
+        const float4 x = *reinterpret_cast<const float4*>(other(k) + 4 * dl);
+        v.x = fmaf(x.x, w, v.x);
+        v.y = fmaf(x.y, w, v.y);
+        v.z = fmaf(x.z, w, v.z);
+        v.w = fmaf(x.w, w, v.w);
+      }
+      const float inv = 1.0f / sum;
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (static_cast<size_t>(at.b) * a.N + node) * a.C + at.h * HS +
+                                 4 * dl) =
+          sets[r] != 0 ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+}
+
+template <int HS, int WM, int kGroups>
+int f32_typed(const TreeArgs& a, int* ctas, cudaStream_t s) {
+  static bool allowed[kMaxDevices] = {};
+  using Ring = RingF32<HS, WM>;
+  constexpr int kSmem = Ring::smem(kGroups > 0 ? kGroups : 1), kPerSm = f32_ctas<HS, WM, kGroups>();
+  static_assert(kPerSm > 0 && kSmem <= 227 * 1024, "shared memory");
+  CUtensorMap mk, mv, mq;
+  if (!tree_maps(&mk, &mv, &mq, a, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, HS, Ring::kKeys, R * WM)) return GPT2_ERR_CUDA;
+  cudaError_t e = allow_smem(allowed, tree_f32_kernel<HS, WM, kGroups>, kSmem);
+  // of shares as many as the SMs hold at once
+  const int grid = kGroups > 0 ? a.B * a.NH : std::min(max_ctas(a.N), kPerSm * num_sms());
+  if (e == cudaSuccess)
+    e = launch_pdl(tree_f32_kernel<HS, WM, kGroups>, dim3(grid), dim3(32 * f32_warps(WM, kGroups)), kSmem, s, mk, mv, mq,
+                   a);
+  *ctas = kGroups > 0 ? 0 : grid;
+  return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
+}
+
+// More than eight nodes.  128 threads: ty = thread
 // / 16 owns nodes R ty .., tx = thread % 16 keys tx + 16 i of a tile (S) and
 // dimensions tx * HS / 16 .. (O); tiles by cp.async into two buffers.
 constexpr int kSimtKeys = 64;  // of a tile, and at most as many nodes
@@ -255,7 +647,7 @@ template <int HS, int R>
 int simt_typed(const TreeArgs& a, int* grid, cudaStream_t s) {
   static bool allowed[kMaxDevices] = {};
   constexpr int kSmem = sizeof(TreeSimtSmem<HS, R>);
-  static_assert(kSmem <= 227 * 1024 / 2, "two CTAs an SM");
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
   const int ctas = ctas_of(a.N, 2);
   cudaError_t e = allow_smem(allowed, tree_simt_kernel<HS, R>, kSmem);
   if (e == cudaSuccess) e = launch_pdl(tree_simt_kernel<HS, R>, dim3(ctas), dim3(kThreads), kSmem, s, a);
@@ -264,8 +656,12 @@ int simt_typed(const TreeArgs& a, int* grid, cudaStream_t s) {
 }
 
 template <int HS>
-int simt(const TreeArgs& a, int* grid, cudaStream_t s) {
-  if (a.N <= 8) return simt_typed<HS, 1>(a, grid, s);
+int f32(const TreeArgs& a, int* grid, cudaStream_t s) {
+  // (Five nodes, 12 heads of 64, cache up to n, shares / pairs, us: 12 pairs, n 60
+  // 11.9 / 6.8, 250 11.5 / 8.8, 500 11.8 / 13.7; 96: 13.0 / 7.1, 13.2 / 11.5, 14.2 /
+  // 16.0; 192: 13.2 / 13.0, 15.0 / 19.4.)
+  const bool pairs = static_cast<long long>(a.B) * a.NH <= 152 && a.rows.capacity <= 384;
+  if (a.N <= 8) return pairs ? f32_typed<HS, 1, 4>(a, grid, s) : f32_typed<HS, 1, 0>(a, grid, s);
   if (a.N <= 16) return simt_typed<HS, 2>(a, grid, s);
   if (a.N <= 32) return simt_typed<HS, 4>(a, grid, s);
   return simt_typed<HS, 8>(a, grid, s);
@@ -275,11 +671,11 @@ int simt(const TreeArgs& a, int* grid, cudaStream_t s) {
 
 namespace tree {
 
-int launch_simt(const TreeArgs& a, int hs, int* ctas, cudaStream_t s) {
+int launch_f32(const TreeArgs& a, int hs, int* ctas, cudaStream_t s) {
   switch (hs) {
-    case 16: return simt<16>(a, ctas, s);
-    case 32: return simt<32>(a, ctas, s);
-    case 64: return simt<64>(a, ctas, s);
+    case 16: return f32<16>(a, ctas, s);
+    case 32: return f32<32>(a, ctas, s);
+    case 64: return f32<64>(a, ctas, s);
   }
   return GPT2_ERR_UNSUPPORTED;
 }

@@ -15,8 +15,9 @@
 // P is written over (16 columns of hi and 16 of lo for 32 keys: P enters the
 // product as the sum of two values of the operand type), one warp issuing S, one
 // issuing P V, a rescale only where a row's maximum grows by more than 2^8.
-//   warp 0      loads by TMA: the queries of a pair's part (two buffers), then its
-//               steps' keys and values through a ring of three stages;
+//   warps 0, 11  loads by TMA: the queries of a pair's part (two buffers) and its
+//               steps' keys, and their values, through rings of four and five
+//               stages (keys are free again after S, values only after P V);
 //   warp 1      TMEM and the S products; warp 10 the P V products;
 //   warps 2-5, 6-9  the softmax groups.  The one that has the nodes' step stores
 //               their keys and values in the cache, zeroes the rows of the tile
@@ -37,27 +38,30 @@ constexpr int kTK = 128;    // keys of a step
 constexpr int kHS = 64;
 constexpr int kTileBytes = 128 * kHS * 2;  // 128 rows of 128 bytes
 constexpr int kRing = 3;    // S accumulators (and P) in TMEM
-constexpr int kKV = 3;      // K/V stages
+constexpr int kK = 4;       // K stages
+constexpr int kV = 5;       // V stages
 constexpr int kSoftmaxWarps = 4;  // per group
 constexpr int kPvWarp = 2 + 2 * kSoftmaxWarps;
-constexpr int kTcThreads = 32 * (kPvWarp + 1);
+constexpr int kVWarp = kPvWarp + 1;
+constexpr int kTcThreads = 32 * (kVWarp + 1);
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0;           // S buffer r at 128 r
 constexpr uint32_t kTmemO = kRing * kTK;  // O of group x at 384 + 64 x
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kJoinRow = kHS + 4;          // floats: rows' float4s in distinct banks
+constexpr int kJoinCols = 32;              // dimensions that are joined at a time
+constexpr int kJoinRow = kJoinCols + 4;    // floats: rows' float4s in distinct banks
 
 struct Smem {
   static constexpr int q = 0;                       // two buffers
-  static constexpr int k = q + 2 * kTileBytes;      // kKV stages of K
-  static constexpr int v = k + kKV * kTileBytes;    // kKV stages of V
-  static constexpr int join = v + kKV * kTileBytes;  // [4][64][kJoinRow] floats
+  static constexpr int k = q + 2 * kTileBytes;
+  static constexpr int v = k + kK * kTileBytes;
+  static constexpr int join = v + kV * kTileBytes;  // [4][64][kJoinRow] floats
   static constexpr int ml = join + 4 * kMaxNodes * kJoinRow * 4;  // [4][64] float2
   static constexpr int sets = ml + 4 * kMaxNodes * 8;             // [2][64] 64-bit sets
   static constexpr int bars = sets + 2 * kMaxNodes * 8;
-  // q_full[2], q_empty[2], kv_full[kKV], kv_empty[kKV], s_full[2][kRing], p_full[kRing], o_done[kRing], o_final[2],
-  // o_free[2], drain
-  static constexpr int n_bars = 4 + 2 * kKV + 4 * kRing + 4 + 1;
+  // q_full[2], q_empty[2], k_full[kK], k_empty[kK], v_full[kV], v_empty[kV], s_full[2][kRing], p_full[kRing],
+  // o_done[kRing], o_final[2], o_free[2], drain
+  static constexpr int n_bars = 4 + 2 * kK + 2 * kV + 4 * kRing + 4 + 1;
   static constexpr int misc = bars + n_bars * 8;  // TMEM address, odd[2]
   static constexpr int total = misc + 16;
   static constexpr int alloc = total + 1024;
@@ -99,11 +103,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tree_tc_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::bars);
   uint64_t* q_empty = q_full + 2;
-  uint64_t* kv_full = q_empty + 2;
-  uint64_t* kv_empty = kv_full + kKV;
+  uint64_t* k_full = q_empty + 2;
+  uint64_t* k_empty = k_full + kK;
+  uint64_t* v_full = k_empty + kK;
+  uint64_t* v_empty = v_full + kV;
   // S is signalled per group and slot: a group walks only its own steps (see
   // attn_tc05_kernel on why a shared barrier's parity would be ambiguous)
-  uint64_t* s_full = kv_empty + kKV;
+  uint64_t* s_full = v_empty + kV;
   uint64_t* p_full = s_full + 2 * kRing;
   uint64_t* o_done = p_full + kRing;
   uint64_t* o_final = o_done + kRing;
@@ -124,9 +130,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&o_final[i], 1u);
       mbar_init(&o_free[i], kSoftmaxWarps);
     }
-    for (int i = 0; i < kKV; ++i) {
-      mbar_init(&kv_full[i], 1u);
-      mbar_init(&kv_empty[i], 1u);
+    for (int i = 0; i < kK; ++i) {
+      mbar_init(&k_full[i], 1u);
+      mbar_init(&k_empty[i], 1u);
+    }
+    for (int i = 0; i < kV; ++i) {
+      mbar_init(&v_full[i], 1u);
+      mbar_init(&v_empty[i], 1u);
     }
     for (int r = 0; r < 2 * kRing; ++r) mbar_init(&s_full[r], 1u);
     for (int r = 0; r < kRing; ++r) {
@@ -154,69 +164,80 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const Share sh = share_of<kTK>(a);
   Parts part(a, sh);
 
-  if (warp == 0) {
+  if (warp == 0 || warp == kVWarp) {
     // ------------------------------------------------------------ loads
-    const int box = min(kTK, 1 << a.rows.lbs), boxes = kTK / box;  // of a step
+    // A copy takes its warp some 50 cycles to issue, and blocks of 16 positions
+    // make eight of them a tile: keys and values have a warp each.
+    const bool keys = warp == 0;
+    const int stages = keys ? kK : kV;
+    uint64_t* full = keys ? k_full : v_full;
+    uint64_t* empty = keys ? k_empty : v_empty;
+    uint8_t* ring = smem + (keys ? L::k : L::v);
+    const CUtensorMap* map = keys ? &map_k : &map_v;
+    const int lbox = min(a.rows.lbs, 7), box = 1 << lbox, boxes = kTK >> lbox;  // of a step
     constexpr int kIds = kTK / 32;
+    int stage = 0, phase = 1;  // of the next fill, and the parity of the phase that frees it
     bool ok = true;
     for (; part.more() && ok; part.next()) {
       const int f = part.f, x = part.p.h * kHS, y = part.p.b * a.N;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[f & 1], ((f >> 1) & 1) ^ 1)))) break;
-      if (lane == 0) {
-        uint8_t* q = smem + L::q + (f & 1) * kTileBytes;
-        mbar_arrive_expect_tx(&q_full[f & 1], kTileBytes);
-        tma_load_2d(q, &map_qkv, &q_full[f & 1], x, y);
-        tma_load_2d(q + kTileBytes / 2, &map_qkv, &q_full[f & 1], x, y);
+      if (keys) {
+        // (a timeout seen by any lane stops all of them)
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[f & 1], ((f >> 1) & 1) ^ 1)))) break;
+        if (lane == 0) {
+          uint8_t* q = smem + L::q + (f & 1) * kTileBytes;
+          mbar_arrive_expect_tx(&q_full[f & 1], kTileBytes);
+          tma_load_2d(q, &map_qkv, &q_full[f & 1], x, y);
+          tma_load_2d(q + kTileBytes / 2, &map_qkv, &q_full[f & 1], x, y);
+        }
       }
       const int* table = a.rows.table + static_cast<size_t>(part.p.b) * a.rows.max_blocks;
+      const int pos = part.p.seq.pos, h = part.p.h;
       int ids[kIds];
       auto lookup = [&](int t) {  // lane i: the blocks of step t's boxes i, i + 32, ..
 #pragma unroll
         for (int u = 0; u < kIds; ++u) {
-          const int j = (t - 1) * kTK + (lane + 32 * u) * box;
-          ids[u] = t > 0 && lane + 32 * u < boxes && j < part.p.seq.pos ? __ldg(table + (j >> a.rows.lbs)) : 0;
+          if (32 * u >= boxes) break;
+          const int i = lane + 32 * u, j = (t - 1) * kTK + (i << lbox);
+          ids[u] = t > 0 && i < boxes && j < pos ? __ldg(table + (j >> a.rows.lbs)) : 0;
         }
       };
       lookup(part.p.t);
       for (int k = 0; k < part.n; ++k) {
-        const int s = part.s + k, t = part.p.t + k, stg = s % kKV;
-        // (a timeout seen by any lane stops all of them)
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[stg], ((s / kKV) & 1) ^ 1)))) break;
-        uint8_t* kd = smem + L::k + stg * kTileBytes;
-        uint8_t* vd = smem + L::v + stg * kTileBytes;
+        const int t = part.p.t + k, j0 = (t - 1) * kTK;
+        const int n = min(boxes, (pos - j0 + box - 1) >> lbox);  // boxes that hold a cached position
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(empty + stage, phase)))) break;
+        uint8_t* dst = ring + stage * kTileBytes;
+        uint64_t* bar = full + stage;
+        if (lane == 0) mbar_arrive_expect_tx(bar, t == 0 ? kTileBytes / 2 : n * box * 128);
+        __syncwarp();
         if (t == 0) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&kv_full[stg], kTileBytes);
-            tma_load_2d(kd, &map_qkv, &kv_full[stg], a.C + x, y);
-            tma_load_2d(vd, &map_qkv, &kv_full[stg], 2 * a.C + x, y);
-          }
+          if (lane == 0) tma_load_2d(dst, &map_qkv, bar, (keys ? a.C : 2 * a.C) + x, y);
         } else {
-          const int j0 = (t - 1) * kTK;
-          const int n = min(boxes, (part.p.seq.pos - j0 + box - 1) / box);  // boxes that hold a cached position
-          if (lane == 0) mbar_arrive_expect_tx(&kv_full[stg], 2 * n * box * 128);
-          __syncwarp();
 #pragma unroll
           for (int u = 0; u < kIds; ++u) {
+            if (32 * u >= n) break;
             const int i = lane + 32 * u;
-            if (i >= n) continue;
             int blk = ids[u];
-            if (blk < 0 || blk >= a.rows.num_blocks) {
-              if (part.p.h == 0) set_error(GPT2_DEVERR_BLOCK);
+            if (i < n && (blk < 0 || blk >= a.rows.num_blocks)) {
+              if (h == 0) set_error(GPT2_DEVERR_BLOCK);
               blk = 0;
             }
-            const int row = (j0 + i * box) & ((1 << a.rows.lbs) - 1);
-            tma_load_4d(kd + i * box * 128, &map_k, &kv_full[stg], 0, row, part.p.h, blk);
-            tma_load_4d(vd + i * box * 128, &map_v, &kv_full[stg], 0, row, part.p.h, blk);
+            if (i < n)
+              tma_load_4d(dst + i * box * 128, map, bar, 0, (j0 + i * box) & ((1 << a.rows.lbs) - 1), h, blk);
           }
+        }
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1;
         }
         if (k + 1 < part.n) lookup(t + 1);
       }
     }
-    // the copies issued here land before the CTA may exit: those of the last
-    // stages, waited for again (after a timeout with the same limit)
+    // the copies issued here land before the CTA may exit: after a timeout the
+    // last ones are waited for again, with the same limit
     if (!ok && lane == 0) {
-      for (int stg = 0; stg < kKV; ++stg) mbar_wait(&kv_full[stg], 0), mbar_wait(&kv_full[stg], 1);
-      for (int x = 0; x < 2; ++x) mbar_wait(&q_full[x], 0), mbar_wait(&q_full[x], 1);
+      for (int i = 0; i < stages; ++i) mbar_wait(full + i, 0), mbar_wait(full + i, 1);
+      for (int i = 0; keys && i < 2; ++i) mbar_wait(&q_full[i], 0), mbar_wait(&q_full[i], 1);
     }
     __syncwarp();
   } else if (warp == 1 || warp == kPvWarp) {
@@ -231,15 +252,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int k = 0; k < part.n && ok; ++k) {
           const int s = part.s + k;
           if (s >= kRing) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[s % kRing], ((s - kRing) / kRing) & 1));
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[s % kKV], (s / kKV) & 1));
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&k_full[s % kK], (s / kK) & 1));
           if (!ok) break;
           tc_fence_after();
           const uint64_t qd = smem_desc_sw128(smem_u32(smem + L::q + (part.f & 1) * kTileBytes));
-          const uint64_t kdsc = smem_desc_sw128(smem_u32(smem + L::k + (s % kKV) * kTileBytes));
+          const uint64_t kdsc = smem_desc_sw128(smem_u32(smem + L::k + (s % kK) * kTileBytes));
 #pragma unroll
           for (int kk = 0; kk < kHS / 16; ++kk)  // 16 dimensions = 32 bytes = 2 in the descriptor's address field
             tc_mma_warp<false>(tmem + kTmemS + (s % kRing) * kTK, qd + 2 * kk, kdsc + 2 * kk, kIdescS, kk > 0 ? 1u : 0u);
           tc_commit_warp(&s_full[(s & 1) * kRing + s % kRing]);
+          if (part.p.t + k > 0) tc_commit_warp(&k_empty[s % kK]);
         }
         if (ok) tc_commit_warp(&q_empty[part.f & 1]);
       } else {
@@ -249,10 +271,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool first = k < 2;
           if (first && used[x]++ > 0) ok = __all_sync(0xffffffffu, mbar_wait(&o_free[x], (used[x] - 2) & 1));
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&p_full[s % kRing], (s / kRing) & 1));
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&v_full[s % kV], (s / kV) & 1));
           if (!ok) break;
           tc_fence_after();
           const uint32_t p_tmem = tmem + kTmemS + (s % kRing) * kTK;
-          const uint64_t vdsc = smem_desc_sw128_mn(smem_u32(smem + L::v + (s % kKV) * kTileBytes), 1024);
+          const uint64_t vdsc = smem_desc_sw128_mn(smem_u32(smem + L::v + (s % kV) * kTileBytes), 1024);
           const int ksteps = part.p.t + k == 0 ? kMaxNodes / 16 : kTK / 16;  // the nodes are 64 keys
 #pragma unroll
           for (int kk = 0; kk < kTK / 16; ++kk) {  // P: 16 keys = 8 TMEM columns; V: 16 rows of 128 bytes
@@ -264,7 +287,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           tc_commit_warp(&o_done[s % kRing]);
           if (k + 2 >= part.n) tc_commit_warp(&o_final[x]);
-          tc_commit_warp(&kv_empty[s % kKV]);
+          tc_commit_warp(&v_empty[s % kV]);
+          // the nodes' keys are also read by the softmax group, before its P
+          if (part.p.t + k == 0) tc_commit_warp(&k_empty[s % kK]);
         }
       }
     }
@@ -307,9 +332,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           bits = half == 0 ? mine : 0;
           if (half == 0) sets[row] = mine;
           // (every thread reaches the group's barrier below, whatever its wait returned)
-          ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[s % kKV], (s / kKV) & 1));
-          const uint8_t* kd = smem + L::k + (s % kKV) * kTileBytes;
-          uint8_t* vd = smem + L::v + (s % kKV) * kTileBytes;
+          ok = __all_sync(0xffffffffu, mbar_wait(&k_full[s % kK], (s / kK) & 1) && mbar_wait(&v_full[s % kV], (s / kV) & 1));
+          const uint8_t* kd = smem + L::k + (s % kK) * kTileBytes;
+          uint8_t* vd = smem + L::v + (s % kV) * kTileBytes;
           bool bad = false;
           for (int c0 = tg; ok && c0 < kMaxNodes * 8; c0 += 32 * kSoftmaxWarps) {
             const int node = c0 >> 3, c = c0 & 7;
@@ -342,6 +367,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             *reinterpret_cast<uint4*>(vcache + to) = v;
           }
           fence_proxy_async_smem();
+          __syncwarp();
           bad = bar_or(4 + x, 32 * kSoftmaxWarps, bad);
           if (tg == 0) odd[part.f & 1] = bad;
           if (!ok) break;
@@ -350,8 +376,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int mine = valid - 64 * half;
           bits = mine >= 64 ? ~0ull : mine <= 0 ? 0ull : (1ull << mine) - 1;
           if (valid < kTK) {  // the rows of the last tile that hold no key
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[s % kKV], (s / kKV) & 1)))) break;
-            uint8_t* vd = smem + L::v + (s % kKV) * kTileBytes;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[s % kV], (s / kV) & 1)))) break;
+            uint8_t* vd = smem + L::v + (s % kV) * kTileBytes;
             for (int c = tg; c < (kTK - valid) * 8; c += 32 * kSoftmaxWarps)
               *reinterpret_cast<uint4*>(vd + valid * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
@@ -439,35 +465,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         final_par ^= 1;
       }
       // (also: the part before has been read)
+      __syncwarp();
       if (bar_or(2, 64 * kSoftmaxWarps, !ok)) break;
       const int sub = 2 * x + half;
       join_ml[sub * kMaxNodes + row] = make_float2(m_run, l_run);
-      if (done > 0) {
-        tc_fence_after();
-        float* to = join + (sub * kMaxNodes + row) * kJoinRow;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(lane_base + kTmemO + x * kHS + 32 * c, o);
-          tmem_ld_wait_regs(o);
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<uint4*>(to + 32 * c + 4 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&o_free[x]);
-      }
-      bar_or(3, 64 * kSoftmaxWarps, false);
-      const int ts = threadIdx.x - 64, node = ts >> 2, d = (ts & 3) * 16;  // 16 dimensions of a node
+      const int ts = threadIdx.x - 64, node = ts >> 2, d = (ts & 3) * 8;  // 8 of the 32 dimensions of a node
       const bool from_start = p.t == 0;
       Place end = p;
       end.t += part.n - 1;
       const Part mine = end_part(a, sh, end, part.i + part.n - 1, from_start, open, ts == 0);
-      if (node < a.N) {
-        float M = -INFINITY, l = 0.f, o[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = 0.f;
+      for (int c = 0; c < kHS / kJoinCols; ++c) {
+        __syncwarp();
+        if (c > 0) bar_or(2, 64 * kSoftmaxWarps, false);  // the columns before have been read
+        if (done > 0) {
+          tc_fence_after();
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(lane_base + kTmemO + x * kHS + kJoinCols * c, o);
+          tmem_ld_wait_regs(o);
+          float* to = join + (sub * kMaxNodes + row) * kJoinRow;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(to + 4 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          if (c + 1 == kHS / kJoinCols) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[x]);
+          }
+        }
+        bar_or(3, 64 * kSoftmaxWarps, false);
+        if (node >= a.N) continue;
+        const int dim = kJoinCols * c + d;
+        float M = -INFINITY, l = 0.f, o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = 0.f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) M = fmaxf(M, join_ml[u * kMaxNodes + node].x);
         const float ref = M == -INFINITY ? 0.f : M;
@@ -479,7 +510,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           l = fmaf(ml.y, w, l);
           const float4* from = reinterpret_cast<const float4*>(join + (u * kMaxNodes + node) * kJoinRow + d);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             const float4 v = from[q];
             o[4 * q] = fmaf(v.x, w, o[4 * q]);
             o[4 * q + 1] = fmaf(v.y, w, o[4 * q + 1]);
@@ -493,9 +524,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (unsigned long long left = set; left != 0; left &= left - 1) {
             const int j = __ffsll(static_cast<long long>(left)) - 1;
             const T16* v = static_cast<const T16*>(a.qkv) + (static_cast<size_t>(p.b) * a.N + j) * 3 * a.C + 2 * a.C +
-                           p.h * kHS + d;
+                           p.h * kHS + dim;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 8; ++e) {
               const float w = to_f32(v[e]);
               if (!isfinite(w)) o[e] += w;
             }
@@ -503,22 +534,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (mine.whole) {
           const float inv = 1.0f / l;
-          uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
-                                               (static_cast<size_t>(p.b) * a.N + node) * a.C + p.h * kHS + d);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            to[q] = missing ? make_uint4(0u, 0u, 0u, 0u)
-                            : make_uint4(pack2<T16>(o[8 * q] * inv, o[8 * q + 1] * inv),
-                                         pack2<T16>(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
-                                         pack2<T16>(o[8 * q + 4] * inv, o[8 * q + 5] * inv),
-                                         pack2<T16>(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (static_cast<size_t>(p.b) * a.N + node) * a.C +
+                                    p.h * kHS + dim) =
+              missing ? make_uint4(0u, 0u, 0u, 0u)
+                      : make_uint4(pack2<T16>(o[0] * inv, o[1] * inv), pack2<T16>(o[2] * inv, o[3] * inv),
+                                   pack2<T16>(o[4] * inv, o[5] * inv), pack2<T16>(o[6] * inv, o[7] * inv));
         } else {
           const size_t to = mine.slot * a.N + node;
           // a sum of -1 tells the join that the node is missing
-          if ((ts & 3) == 0) a.part.ml[to] = make_float2(M, missing ? -1.f : l);
+          if (c == 0 && (ts & 3) == 0) a.part.ml[to] = make_float2(M, missing ? -1.f : l);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<float4*>(a.part.o + to * kHS + d + 4 * q) =
+          for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<float4*>(a.part.o + to * kHS + dim + 4 * q) =
                 make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
       }
@@ -541,20 +568,7 @@ int tc_typed(const TreeArgs& a, int* ctas, cudaStream_t s) {
   const CUtensorMapDataType dt =
       std::is_same<T16, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap mk, mv, mq;
-  {
-    const uint64_t bs = 1ull << a.rows.lbs, row = kHS * 2;
-    const uint64_t dims[4] = {kHS, bs, static_cast<uint64_t>(a.NH), static_cast<uint64_t>(a.rows.num_blocks)};
-    const uint64_t strides[3] = {row, row * bs, row * bs * a.NH};
-    const uint32_t box[4] = {kHS, static_cast<uint32_t>(bs < kTK ? bs : kTK), 1, 1};
-    if (!encode_tensor_map(&mk, dt, 4, a.kcache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tensor_map(&mv, dt, 4, a.vcache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
-      return GPT2_ERR_CUDA;
-  }
-  {
-    const uint64_t dims[2] = {3ull * a.C, static_cast<uint64_t>(a.B) * a.N}, strides[1] = {6ull * a.C};
-    const uint32_t box[2] = {kHS, kMaxNodes};
-    if (!encode_tensor_map(&mq, dt, 2, a.qkv, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return GPT2_ERR_CUDA;
-  }
+  if (!tree_maps(&mk, &mv, &mq, a, dt, 2, kHS, kTK, kMaxNodes)) return GPT2_ERR_CUDA;
   *ctas = num_sms() < max_ctas(a.N) ? num_sms() : max_ctas(a.N);
   cudaError_t e = allow_smem(allowed, tree_tc05_kernel<T16>, Smem::alloc);
   if (e == cudaSuccess)

@@ -9,7 +9,7 @@
 namespace gpt2 {
 namespace tree {
 
-constexpr int kThreads = 128;  // of tree_simt_kernel and tree_join_kernel
+constexpr int kThreads = 128;  // of tree_join_kernel
 // Shares at most: twelve CTAs on each of 152 SMs.  The workspace holds their parts,
 // so the count goes by the number of nodes alone.
 constexpr int ctas_per_sm(int N) { return N <= 16 ? 12 : N <= 32 ? 6 : 3; }
@@ -159,17 +159,192 @@ __device__ __forceinline__ bool any_not_finite(const uint4& v) {
   return bad;
 }
 
-// Byte offset of 16-byte chunk c of row r in a tile that TMA wrote with that
-// swizzle: the chunk's number is combined with the 128-byte line's.
+// Byte offset of 16-byte chunk c of row r in a tile of `rows` rows of kRow bytes that
+// TMA wrote with the swizzle of its row length, in strips of up to 128 bytes: the
+// chunk's number is combined with the 128-byte line's.
+template <int kRow, int kStrips>
+__device__ __forceinline__ uint32_t tile_at_bytes(int r, int c, int rows) {
+  constexpr int kStrip = kRow / kStrips, kChunks = kStrip / 16;
+  const int cc = c % kChunks;
+  return static_cast<uint32_t>((c / kChunks) * rows * kStrip + r * kStrip +
+                               ((cc ^ (r / (8 / kChunks) & (kChunks - 1))) << 4));
+}
+// of 16-bit values
 template <int HS>
 __device__ __forceinline__ uint32_t tile_at(int r, int c) {
-  constexpr int kChunks = HS / 8;
-  return static_cast<uint32_t>(r * (HS * 2) + ((c ^ (r / (8 / kChunks) & (kChunks - 1))) << 4));
+  return tile_at_bytes<HS * 2, 1>(r, c, 0);
 }
 
-// attention_tree_f32.cu, attention_tree_tc.cu: the partial results of a grid of
-// *ctas CTAs are to be joined.
-int launch_simt(const TreeArgs& a, int hs, int* ctas, cudaStream_t s);
+// A barrier of a group's threads that also ORs a predicate over them.
+template <int WM>
+__device__ __forceinline__ bool group_or(int group, bool pred) {
+  if constexpr (WM == 1)
+    return __any_sync(0xffffffffu, pred);
+  else
+    return bar_or(1 + group, 32 * WM, pred);
+}
+
+// A pair of a CTA's own, of which group `group` of WK takes steps group, group + WK,
+// .. .
+template <int K, int WK>
+__device__ __forceinline__ Share pair_share(const TreeArgs& a, int group) {
+  Share s;
+  s.at = Place{static_cast<int>(blockIdx.x / a.NH), static_cast<int>(blockIdx.x % a.NH), group, 0, {0, 0}};
+  enter<K>(a, s.at);
+  s.begin = 0;
+  s.end = group < s.at.steps ? (s.at.steps - group + WK - 1) / WK : 0;
+  s.per = s.end;
+  return s;
+}
+
+// The copies of a group's share by TMA into its ring, in order, issued by its
+// first warp: a step's tile in a copy per block of the cache that it touches (one
+// where blocks are as long as tiles); the nodes' step is their queries, keys and
+// values.  A share that begins inside a pair has one step more at the start, for
+// the queries.  Block ids are looked up a step ahead.  R (the ring): kKeys of a
+// tile, bytes kRow of a key in kStrips columns of up to 128 bytes, which stand
+// one behind the other.
+template <class R, int WM, int WK>
+struct Feed {
+  static constexpr int K = R::kKeys, kIds = (K + 31) / 32, kStripRow = R::kRow / R::kStrips;
+  const TreeArgs& a;
+  const CUtensorMap &map_k, &map_v, &map_qkv;
+  uint8_t* ring;
+  uint64_t* full;
+  Place ld;
+  int lead, n_steps, i;  // i: of the next copy, among the share's steps
+  int ids[kIds];
+  int lbox, boxes;  // positions of a box (log2), boxes of a tile
+  bool pairs, tiled;
+
+  __device__ __forceinline__ Feed(const TreeArgs& args, const Share& sh, bool by_pairs, const CUtensorMap& mk,
+                                  const CUtensorMap& mv, const CUtensorMap& mq, uint8_t* r, uint64_t* f)
+      : a(args), map_k(mk), map_v(mv), map_qkv(mq), ring(r), full(f), ld(sh.at), pairs(by_pairs) {
+    lead = sh.begin < sh.end && sh.at.t > 0 ? 1 : 0;
+    n_steps = static_cast<int>(sh.end - sh.begin) + lead;  // (2^31 of them would take hours)
+    i = -lead;
+    constexpr int kLog = K == 32 ? 5 : 6;
+    lbox = min(kLog, a.rows.lbs);
+    boxes = K >> lbox;
+    // a tiled copy begins at a multiple of 128 bytes in shared memory; smaller
+    // boxes (one position of 64 bytes, one or two of 32) are copied by 16 bytes
+    tiled = (kStripRow << lbox) >= 128;
+  }
+  __device__ __forceinline__ void forward(Place& p) const {  // to the group's next step
+    if (pairs)
+      p.t += WK;
+    else
+      advance<K>(a, p);
+  }
+  __device__ __forceinline__ void lookup() {  // lane l: the blocks of the next tile's boxes l and l + 32
+    if (ld.t == 0) return;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int u = 0; u < kIds; ++u) {
+      const int x = lane + 32 * u, j = (ld.t - 1) * K + (x << lbox);
+      ids[u] = x < boxes && j < ld.seq.pos
+                   ? __ldg(a.rows.table + static_cast<size_t>(ld.b) * a.rows.max_blocks + (j >> a.rows.lbs))
+                   : 0;
+    }
+  }
+  __device__ __forceinline__ void begin() {
+    if (n_steps > 0 && lead == 0) lookup();
+#pragma unroll
+    for (int s = 0; s < R::kStages - 1; ++s) copy(s);
+  }
+  __device__ __forceinline__ void copy(int stage) {
+    if (i + lead >= n_steps) return;
+    const int lane = threadIdx.x & 31;
+    uint8_t* st = ring + stage * R::kStage;
+    uint64_t* bar = full + stage;
+    if (i < 0 || ld.t == 0) {
+      if (lane == 0) {
+        const int x = ld.h * (a.C / a.NH), y = ld.b * a.N, parts = i < 0 ? 1 : 3;
+        mbar_arrive_expect_tx(bar, parts * R::kNodeBytes);
+        for (int p = 0; p < parts; ++p)
+#pragma unroll
+          for (int c = 0; c < R::kStrips; ++c)
+            tma_load_2d(st + p * R::kNodeBytes + c * (R::kNodeBytes / R::kStrips), &map_qkv, bar,
+                        p * a.C + x + c * (a.C / a.NH / R::kStrips), y);
+      }
+    } else {
+      const int j0 = (ld.t - 1) * K, box = 1 << lbox;
+      const int n = min(boxes, (ld.seq.pos - j0 + box - 1) >> lbox);  // boxes that hold a cached position
+      if (lane == 0) mbar_arrive_expect_tx(bar, 2 * n * box * R::kRow);
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < kIds; ++u) {
+        const int x = lane + 32 * u;
+        if (x >= n) continue;
+        if (ids[u] < 0 || ids[u] >= a.rows.num_blocks) {
+          if (ld.h == 0) set_error(GPT2_DEVERR_BLOCK);
+          ids[u] = 0;
+        }
+        if (tiled) {
+          const int y = (j0 + x * box) & ((1 << a.rows.lbs) - 1), to = x * box * kStripRow;
+#pragma unroll
+          for (int c = 0; c < R::kStrips; ++c) {
+            uint8_t* dst = st + c * (R::kTileBytes / R::kStrips) + to;
+            tma_load_4d(dst, &map_k, bar, c * (a.C / a.NH / R::kStrips), y, ld.h, ids[u]);
+            tma_load_4d(dst + R::kTileBytes, &map_v, bar, c * (a.C / a.NH / R::kStrips), y, ld.h, ids[u]);
+          }
+        }
+      }
+      if (!tiled) {
+        __syncwarp();
+        constexpr int kChunks = R::kRow / 16;
+        for (int x0 = 0; x0 < n * box * kChunks; x0 += 32) {
+          const int x = x0 + lane, r = x / kChunks, c = x % kChunks, b = r >> lbox;
+          int blk = __shfl_sync(0xffffffffu, ids[0], b & 31);
+          if constexpr (kIds > 1) {
+            const int high = __shfl_sync(0xffffffffu, ids[kIds - 1], b & 31);
+            if (b >= 32) blk = high;
+          }
+          if (x < n * box * kChunks) {
+            const size_t from = cache_row(a, blk, ld.h, j0 + r) * R::kRow + c * 16;
+            const uint32_t to = tile_at_bytes<R::kRow, R::kStrips>(r, c, K);
+            bulk_load(st + to, static_cast<const uint8_t*>(a.kcache) + from, 16, bar);
+            bulk_load(st + R::kTileBytes + to, static_cast<const uint8_t*>(a.vcache) + from, 16, bar);
+          }
+        }
+      }
+    }
+    if (i >= 0) forward(ld);
+    ++i;
+    if (i + lead < n_steps) lookup();
+  }
+  // after a copy that did not come: the group's others since step n, with the same
+  // limit each
+  __device__ __forceinline__ void drain(int n) const {
+    for (int k = n; k < i + lead; ++k) mbar_wait(full + k % R::kStages, k / R::kStages & 1);
+  }
+};
+
+// The tensor maps of the cache halves ([blocks][heads][positions][HS], boxes of up
+// to `keys` positions) and of the QKV rows (boxes of `rows`), elements of `bytes`.
+inline bool tree_maps(CUtensorMap* mk, CUtensorMap* mv, CUtensorMap* mq, const TreeArgs& a, CUtensorMapDataType dt,
+                      int bytes, int hs, int keys, int rows) {
+  const uint64_t bs = 1ull << a.rows.lbs, row = static_cast<uint64_t>(hs) * bytes;
+  const uint32_t width = row > 128 ? 128 / bytes : hs;  // columns of a box
+  const CUtensorMapSwizzle swizzle = row >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                 : CU_TENSOR_MAP_SWIZZLE_32B;
+  const uint64_t dims[4] = {static_cast<uint64_t>(hs), bs, static_cast<uint64_t>(a.NH),
+                            static_cast<uint64_t>(a.rows.num_blocks)};
+  const uint64_t strides[3] = {row, row * bs, row * bs * a.NH};
+  const uint32_t box[4] = {width, static_cast<uint32_t>(bs < static_cast<uint64_t>(keys) ? bs : keys), 1, 1};
+  const uint64_t qdims[2] = {3ull * a.C, static_cast<uint64_t>(a.B) * a.N}, qstrides[1] = {3ull * a.C * bytes};
+  const uint32_t qbox[2] = {width, static_cast<uint32_t>(rows)};
+  return encode_tensor_map(mk, dt, 4, a.kcache, dims, strides, box, swizzle) &&
+         encode_tensor_map(mv, dt, 4, a.vcache, dims, strides, box, swizzle) &&
+         encode_tensor_map(mq, dt, 2, a.qkv, qdims, qstrides, qbox, swizzle);
+}
+
+// attention_tree_f16.cu, _bf16.cu, _f32.cu, _tc.cu: the parts of *ctas shares are to
+// be joined (0: none).
+int launch_mma_f16(const TreeArgs& a, int hs, int* ctas, cudaStream_t s);
+int launch_mma_bf16(const TreeArgs& a, int hs, int* ctas, cudaStream_t s);
+int launch_f32(const TreeArgs& a, int hs, int* ctas, cudaStream_t s);
 int launch_tc05(const TreeArgs& a, int op, int* ctas, cudaStream_t s);
 
 }  // namespace tree
