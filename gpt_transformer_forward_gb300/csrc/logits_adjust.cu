@@ -3,15 +3,15 @@
 //
 // A CTA takes a segment of the vocabulary for the rows of some nodes of one
 // sequence.  Few of its tokens stand in the history, the biases or the node's
-// path: it finds those of the history and the biases once for all of its rows,
-// and gives each a slot that holds
-//   bits 0..20 of one word   times in the output, counted by integer atomics,
-//   bit 21                   whether it stands in the prompt,
-//   another word             the last of its biases.
+// path: those of the history and the biases it puts into a hash table in shared
+// memory once for all of its rows, which holds for each a word:
+//   bits 0..20   times in the output, counted by integer atomics,
+//   bit 21       whether it stands in the prompt,
+//   bits 22..31  the place of the last of its biases, plus 1.
 // A row's segment then goes through shared memory by bulk copies, where only the
-// tokens with a slot, those of the node's path and, under a mask, what it rules
-// out are changed.  In place nothing goes through: the tokens that change are
-// read and written where they stand.
+// table's tokens, those of the node's path and, under a mask, what it rules out
+// are changed.  In place nothing goes through: the tokens that change are read and
+// written where they stand.
 #include "draft.cuh"
 
 #include <algorithm>
@@ -24,7 +24,8 @@ constexpr int kSegBytes = 16384;  // of a segment, at most
 constexpr int kStages = 3;        // rows in flight
 constexpr int kSegWords = kSegBytes / 2 / 32;  // mask words of a segment, at most
 constexpr uint32_t kPrompt = 1u << 21, kCountMask = kPrompt - 1;
-static_assert(GPT2_LOGIT_MAX_HISTORY + kMaxNodes < (1 << 21), "a count fits its bits");
+constexpr int kBiasShift = 22;
+static_assert(GPT2_LOGIT_MAX_HISTORY + kMaxNodes < (1 << 21) && GPT2_LOGIT_MAX_BIASES < (1 << 10), "bits of a word");
 
 struct AdjustArgs {
   void* out;
@@ -37,6 +38,8 @@ struct AdjustArgs {
   int nodes;   // rows of a CTA
   int stages;  // rows in flight, at most kStages
   int slots;   // tokens of a segment that a history and biases can name at most
+  int table;   // words of these: one for each token of a segment, or a hash table's, a power of
+               // two and at least 3 / 2 of the slots, where that takes less room
 };
 
 struct Penalty {
@@ -44,15 +47,19 @@ struct Penalty {
   bool repeats;  // a repetition penalty is given
   const float* some;  // the first kThreads biases, in shared memory
   const float* bias;
+  // the bias of a token's word; -0, which changes nothing, for none
+  __device__ __forceinline__ float bias_of(uint32_t w) const {
+    const uint32_t x = w >> kBiasShift;
+    return x == 0 ? -0.f : x <= kThreads ? some[x - 1] : __ldg(bias + x - 1);
+  }
 };
 template <typename E>
-__device__ __forceinline__ E adjust_one(E logit, uint32_t w, int bias, const Penalty& p) {
+__device__ __forceinline__ E adjust_one(E logit, uint32_t w, float bias, const Penalty& p) {
   float x = to_f32(logit);
   const uint32_t count = w & kCountMask;
-  if (p.repeats && w != 0) x = x > 0.f ? x / p.repetition : x * p.repetition;
+  if (p.repeats && (w & (kPrompt | kCountMask)) != 0) x = x > 0.f ? x / p.repetition : x * p.repetition;
   if (count != 0) x = x - p.frequency * static_cast<float>(count) - p.presence;
-  if (bias >= 0) x += bias < kThreads ? p.some[bias] : __ldg(p.bias + bias);
-  return from_f32<E>(x);
+  return from_f32<E>(x + bias);
 }
 
 // The value of the bits of word `m`'s bytes as masks: byte k of the result is 0xff
@@ -96,9 +103,36 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
                : "memory");
 }
 
+// The words of a segment's tokens: one for each token of it, or, with keys (a
+// token's number in the segment plus 1; 0: none), a hash table of them.  A word is 0
+// as long as nothing is known of its token.
+struct Table {
+  uint32_t *word, *key;  // key: null for one word a token
+  uint32_t last;         // number of entries - 1
+  __device__ __forceinline__ uint32_t first(int t) const { return static_cast<uint32_t>(t) * 0x9e3779b1u & last; }
+  // the entry of token t, its own from now on (a third of them stays free)
+  __device__ __forceinline__ uint32_t take(int t) const {
+    if (key == nullptr) return t;
+    uint32_t at = first(t);
+    for (uint32_t n = 0; n <= last; ++n) {
+      const uint32_t old = atomicCAS(key + at, 0u, static_cast<uint32_t>(t) + 1);
+      if (old == 0 || old == static_cast<uint32_t>(t) + 1) break;
+      at = (at + 1) & last;
+    }
+    return at;
+  }
+  // the entry of token t, or a free one
+  __device__ __forceinline__ uint32_t find(int t) const {
+    if (key == nullptr) return t;
+    uint32_t at = first(t);
+    for (uint32_t n = 0; n <= last && key[at] != 0 && key[at] != static_cast<uint32_t>(t) + 1; ++n) at = (at + 1) & last;
+    return at;
+  }
+  __device__ __forceinline__ int token(uint32_t at) const { return key == nullptr ? at : key[at] - 1; }
+};
+
 // Dynamic shared memory: [stages] segments of a row (not in place); where a
-// history or biases are given, per token of the segment whether it has a slot, a
-// bit each, and which; per slot its token and its two words.
+// history or biases are given, the table and a list of its entries.
 template <typename E, bool kInPlace>
 __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a) {
   constexpr int kN = 16 / static_cast<int>(sizeof(E));
@@ -119,11 +153,12 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
   const bool last = v0 + a.seg >= a.V;
   const int columns = (v1 - v0 + kN - 1) / kN * kN;  // whole vectors, of Vp >= V at most
   const size_t stage_bytes = kInPlace ? 0 : a.seg * sizeof(E);
-  uint32_t* has_slot = reinterpret_cast<uint32_t*>(shared_raw + a.stages * stage_bytes);
-  uint32_t* word = has_slot + a.seg / 32;
-  int* bias = reinterpret_cast<int*>(word + a.slots);
-  uint16_t* slot_of = reinterpret_cast<uint16_t*>(bias + a.slots);
-  uint16_t* token_of = slot_of + a.seg;
+  Table tab;
+  tab.word = reinterpret_cast<uint32_t*>(shared_raw + a.stages * stage_bytes);
+  tab.key = a.table < a.seg ? tab.word + a.table : nullptr;
+  tab.last = a.table - 1;
+  const int table_words = a.table < a.seg ? 2 * a.table : a.table;
+  uint16_t* list = reinterpret_cast<uint16_t*>(tab.word + table_words);
   const size_t row0 = static_cast<size_t>(b) * a.N;
   const GPT2LogitRules& r = a.r;
   auto src = [&](int i) { return static_cast<const E*>(a.logits) + (row0 + i) * a.Vp + v0; };
@@ -170,7 +205,8 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
       early_id = __ldg(ids + tid);
       early_bias = __ldg(r.bias_values + static_cast<size_t>(b) * r.num_bias + tid);
     }
-    for (int x = tid; x < a.seg / 32; x += kThreads) has_slot[x] = 0;
+    for (int x = tid; x < table_words / 4; x += kThreads)
+      reinterpret_cast<uint4*>(tab.word)[x] = make_uint4(0u, 0u, 0u, 0u);
   }
   const Penalty pen{r.repetition != nullptr ? __ldg(r.repetition + b) : 1.f,
                     r.presence != nullptr ? __ldg(r.presence + b) : 0.f,
@@ -239,26 +275,21 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
   __syncthreads();
   if (a.slots > 0) {
     // a token of a list that lies in the segment; -1 otherwise
-    auto token = [&](int t, bool say) {
+    auto token = [&](int t) {
       if (t < -1 || t >= a.V) {
-        if (say && report) set_error(GPT2_DEVERR_TOKEN);
+        if (report) set_error(GPT2_DEVERR_TOKEN);
         return -1;
       }
       return t >= v0 && t < v1 ? t - v0 : -1;
     };
-    auto id_at = [&](int x) { return x < kThreads ? early_id : __ldg(ids + x); };
-    // a slot for each of up to kAhead tokens of a thread that has none yet (whole
+    // lists the entries of up to kAhead tokens of a thread that are new (whole
     // warps call)
-    auto take = [&](const int (&t)[kAhead]) {
-      bool first[kAhead];
+    auto enlist = [&](const bool (&fresh)[kAhead], const uint32_t (&entry)[kAhead]) {
       unsigned who[kAhead];
       int n = 0;
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        first[k] = t[k] >= 0 && (atomicOr(&has_slot[t[k] >> 5], 1u << (t[k] & 31)) >> (t[k] & 31) & 1) == 0;
-#pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        who[k] = __ballot_sync(0xffffffffu, first[k]);
+        who[k] = __ballot_sync(0xffffffffu, fresh[k]);
         n += __popc(who[k]);
       }
       if (n == 0) return;
@@ -267,25 +298,26 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
       at = __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        if (first[k]) {
-          const int slot = at + __popc(who[k] & ((1u << lane) - 1));
-          slot_of[t[k]] = static_cast<uint16_t>(slot);
-          token_of[slot] = static_cast<uint16_t>(t[k]);
-          word[slot] = 0;
-          bias[slot] = -1;
-        }
+        if (fresh[k]) list[at + __popc(who[k] & ((1u << lane) - 1))] = static_cast<uint16_t>(entry[k]);
         at += __popc(who[k]);
       }
     };
-    int t[kAhead];
+    bool fresh[kAhead];
+    uint32_t entry[kAhead];
     for (int x0 = 0; x0 < r.num_bias; x0 += kAhead * kThreads) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int x = x0 + tid + k * kThreads;
-        t[k] = x < r.num_bias ? token(id_at(x), true) : -1;
+        const int t = x < r.num_bias ? token(x < kThreads ? early_id : __ldg(ids + x)) : -1;
+        fresh[k] = false;
+        if (t >= 0) {
+          entry[k] = tab.take(t);
+          fresh[k] = atomicMax(tab.word + entry[k], static_cast<uint32_t>(x + 1) << kBiasShift) == 0;
+        }
       }
-      take(t);
+      enlist(fresh, entry);
     }
+    if (r.num_bias > 0) __syncthreads();  // nothing is counted in a word before its bias is known
     for (int x0 = 0; x0 < len; x0 += kAhead * kThreads) {
       int raw[kAhead];
 #pragma unroll
@@ -294,32 +326,38 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
         raw[k] = x0 == 0 ? early[k] : x < len ? __ldg(hist + x) : -1;
       }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) t[k] = x0 + tid + k * kThreads < len ? token(raw[k], true) : -1;
-      take(t);
+      for (int k = 0; k < kAhead; ++k) {
+        const int x = x0 + tid + k * kThreads, t = x < len ? token(raw[k]) : -1;
+        fresh[k] = false;
+        if (t >= 0) {
+          entry[k] = tab.take(t);
+          uint32_t* w = tab.word + entry[k];
+          fresh[k] = (x < prompt ? atomicOr(w, kPrompt) : atomicAdd(w, 1u)) == 0;
+        }
+      }
+      enlist(fresh, entry);
     }
-    __syncthreads();
-    for (int x = tid; x < r.num_bias; x += kThreads) {
-      const int t = token(id_at(x), false);
-      if (t >= 0) atomicMax(&bias[slot_of[t]], x);
-    }
-    auto count = [&](int x, int t) {
-      if (t < 0) return;
-      if (x < prompt)
-        atomicOr(&word[slot_of[t]], kPrompt);
-      else
-        atomicAdd(&word[slot_of[t]], 1u);
-    };
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int x = tid + k * kThreads;
-      if (x < len) count(x, token(early[k], false));
-    }
-#pragma unroll 4
-    for (int x = tid + kAhead * kThreads; x < len; x += kThreads) count(x, token(__ldg(hist + x), false));
     __syncthreads();
   }
   const unsigned long long in_segment = here;
   const int slots = a.slots > 0 ? n_slots : 0, vecs = columns / kN;
+  // a thread's first tokens stay in its registers over the rows
+  constexpr int kOwn = 2;
+  int own[kOwn];
+  uint32_t own_word[kOwn];
+  float own_bias[kOwn];
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    own[k] = -1;
+    own_word[k] = 0;
+    own_bias[k] = -0.f;
+    if (tid + k * kThreads < slots) {
+      const int e = list[tid + k * kThreads];
+      own[k] = tab.token(e);
+      own_word[k] = tab.word[e];
+      own_bias[k] = pen.bias_of(tab.word[e]);
+    }
+  }
   const uint4 lowest = ruled_out<E>(make_uint4(0u, 0u, 0u, 0u), 0u);
   uint32_t phases = 0, pending = kInPlace ? 0 : (1u << min(a.stages, n1 - n0)) - 1;  // a bit a stage
   bool alive = true;  // every copy came
@@ -357,17 +395,19 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
         }
         __syncthreads();
       }
-      for (int e = tid; e < slots; e += kThreads) {
-        const int t = token_of[e];
-        x[t] = adjust_one(x[t], word[e], bias[e], pen);
+#pragma unroll
+      for (int k = 0; k < kOwn; ++k)
+        if (own[k] >= 0) x[own[k]] = adjust_one(x[own[k]], own_word[k], own_bias[k], pen);
+      for (int at = tid + kOwn * kThreads; at < slots; at += kThreads) {
+        const int e = list[at], t = tab.token(e);
+        x[t] = adjust_one(x[t], tab.word[e], pen.bias_of(tab.word[e]), pen);
       }
       if (path != 0) {
         __syncthreads();
         if (mine) {
           const int t = toks[tid];
-          const bool known = slots > 0 && (has_slot[t >> 5] >> (t & 31) & 1) != 0;
-          const int e = known ? slot_of[t] : 0;
-          x[t] = adjust_one(was, (known ? word[e] : 0u) + __popcll(same[tid] & path), known ? bias[e] : -1, pen);
+          const uint32_t w = slots > 0 ? tab.word[tab.find(t)] : 0;  // 0 in a free entry
+          x[t] = adjust_one(was, w + __popcll(same[tid] & path), pen.bias_of(w), pen);
         }
       }
       if (masked || last) {
@@ -418,11 +458,11 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
 template <typename E, bool kInPlace>
 int adjust_launch(const AdjustArgs& a, cudaStream_t s) {
   static bool allowed[kMaxDevices] = {};
-  auto bytes = [](size_t stages, size_t seg, size_t slots) {
-    return stages * seg * sizeof(E) + (slots > 0 ? seg / 8 + seg * 2 + slots * 10 : 0);
+  auto bytes = [](size_t stages, size_t seg, size_t table, size_t slots) {
+    return stages * seg * sizeof(E) + table * (table < seg ? 8 : 4) + slots * 2;
   };
   constexpr size_t kMaxSeg = kSegBytes / sizeof(E);
-  const size_t most = bytes(kInPlace ? 0 : kStages, kMaxSeg, kMaxSeg);
+  const size_t most = bytes(kInPlace ? 0 : kStages, kMaxSeg, kMaxSeg, kMaxSeg);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && dev < kMaxDevices && !allowed[dev]) {
@@ -432,8 +472,8 @@ int adjust_launch(const AdjustArgs& a, cudaStream_t s) {
   }
   const dim3 grid((a.V + a.seg - 1) / a.seg, (a.N + a.nodes - 1) / a.nodes, a.B);
   if (e == cudaSuccess)
-    e = launch_pdl(logits_adjust_kernel<E, kInPlace>, grid, dim3(kThreads), bytes(kInPlace ? 0 : a.stages, a.seg, a.slots),
-                   s, a);
+    e = launch_pdl(logits_adjust_kernel<E, kInPlace>, grid, dim3(kThreads),
+                   bytes(kInPlace ? 0 : a.stages, a.seg, a.table, a.slots), s, a);
   return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
 }
 
@@ -450,6 +490,9 @@ int adjust_typed(AdjustArgs a, cudaStream_t s) {
   while (a.nodes > 1 && segments() * ((a.N + a.nodes - 1) / a.nodes) < want) a.nodes = (a.nodes + 1) / 2;
   a.stages = std::min(kStages, a.nodes);
   a.slots = std::min(a.seg, (a.r.history_stride + a.r.num_bias + 7) / 8 * 8);
+  a.table = a.slots > 0 ? 128 : 0;
+  while (2 * a.table < 3 * a.slots) a.table *= 2;
+  if (2 * a.table >= a.seg) a.table = a.seg;
   return a.out == a.logits ? adjust_launch<E, true>(a, s) : adjust_launch<E, false>(a, s);
 }
 
@@ -457,7 +500,7 @@ int adjust_typed(AdjustArgs a, cudaStream_t s) {
 
 int launch_logits_adjust(void* out, const void* logits, int logits_type, const GPT2LogitRules& r, const int* tok,
                          const int* parent, int B, int N, int V, int Vp, cudaStream_t s) {
-  const AdjustArgs a{out, logits, r, tok, parent, B, N, V, Vp, 0, 0, 0, 0};
+  const AdjustArgs a{out, logits, r, tok, parent, B, N, V, Vp, 0, 0, 0, 0, 0};
   if (logits_type == GPT2_PROBS_F32) return adjust_typed<float>(a, s);
   if (logits_type == GPT2_PROBS_F16) return adjust_typed<__half>(a, s);
   return adjust_typed<__nv_bfloat16>(a, s);
