@@ -481,10 +481,15 @@ template <typename E>
 int adjust_typed(AdjustArgs a, cudaStream_t s) {
   // segments and groups of rows as large as still leave some CTAs to each SM, and
   // no more than 16 rows, which makes the last CTAs end together (64 sequences of
-  // 64 nodes, 50257 fp32: 64 rows 317 us, 32 293, 16 284, 8 311)
+  // 64 nodes, 50257 fp32: 64 rows 317 us, 32 293, 16 284, 8 311).  A CTA of many
+  // rows does better with half a segment, as more of them share an SM, and one of
+  // few rows not, as each has its table to make (50257 tokens; us with 16 and 8 KB:
+  // 512 sequences of 1 node fp32 40 and 59, 256 of 2 fp32 38 and 43, 256 of 4 bf16
+  // 39.1 and 40.6, 128 of 4 fp32 33.1 and 32.1, 128 of 8 bf16 44.1 and 41.9, 128 of
+  // 8 fp32 72 and 67, 64 of 64 fp32 257 and 244).
   const long long want = 4LL * num_sms();
   a.nodes = std::min(a.N, 16);
-  a.seg = kSegBytes / static_cast<int>(sizeof(E));
+  a.seg = (a.N >= 8 ? kSegBytes / 2 : kSegBytes) / static_cast<int>(sizeof(E));
   auto segments = [&]() { return static_cast<long long>((a.V + a.seg - 1) / a.seg) * a.B; };
   while (a.seg > 1024 && segments() < want) a.seg /= 2;
   while (a.nodes > 1 && segments() * ((a.N + a.nodes - 1) / a.nodes) < want) a.nodes = (a.nodes + 1) / 2;
