@@ -131,8 +131,8 @@ struct Table {
   __device__ __forceinline__ int token(uint32_t at) const { return key == nullptr ? at : key[at] - 1; }
 };
 
-// Dynamic shared memory: [stages] segments of a row (not in place); where a
-// history or biases are given, the table and a list of its entries.
+// Dynamic shared memory: [stages] segments of a row (not in place); a row's mask;
+// where a history or biases are given, the table and a list of its entries.
 template <typename E, bool kInPlace>
 __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a) {
   constexpr int kN = 16 / static_cast<int>(sizeof(E));
@@ -140,7 +140,6 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
   __shared__ __align__(8) uint64_t full[kStages];
   __shared__ unsigned long long sets[kMaxNodes], same[kMaxNodes];
   __shared__ int toks[kMaxNodes], mask_rows[kMaxNodes];
-  __shared__ uint32_t mask[kSegWords];
   __shared__ float some_biases[kThreads];
   __shared__ unsigned long long here;  // nodes whose token lies in the segment
   __shared__ int n_slots;
@@ -154,7 +153,8 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
   const int columns = (v1 - v0 + kN - 1) / kN * kN;  // whole vectors, of Vp >= V at most
   const size_t stage_bytes = kInPlace ? 0 : a.seg * sizeof(E);
   Table tab;
-  tab.word = reinterpret_cast<uint32_t*>(shared_raw + a.stages * stage_bytes);
+  uint32_t* mask = reinterpret_cast<uint32_t*>(shared_raw + a.stages * stage_bytes);
+  tab.word = mask + a.seg / 32;
   tab.key = a.table < a.seg ? tab.word + a.table : nullptr;
   tab.last = a.table - 1;
   const int table_words = a.table < a.seg ? 2 * a.table : a.table;
@@ -459,7 +459,7 @@ template <typename E, bool kInPlace>
 int adjust_launch(const AdjustArgs& a, cudaStream_t s) {
   static bool allowed[kMaxDevices] = {};
   auto bytes = [](size_t stages, size_t seg, size_t table, size_t slots) {
-    return stages * seg * sizeof(E) + table * (table < seg ? 8 : 4) + slots * 2;
+    return stages * seg * sizeof(E) + seg / 8 + table * (table < seg ? 8 : 4) + slots * 2;
   };
   constexpr size_t kMaxSeg = kSegBytes / sizeof(E);
   const size_t most = bytes(kInPlace ? 0 : kStages, kMaxSeg, kMaxSeg, kMaxSeg);
