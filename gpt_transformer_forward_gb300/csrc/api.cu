@@ -1054,6 +1054,10 @@ int logprobs_backward(void* dlogits, const void* logits, int logits_type, const 
 
 // --------------------------------------------------- gpt2fwd_draft.h
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + b_bytes && y < x + a_bytes;
+}
 
 size_t attention_tree_workspace_size(int B, int N, int C, int NH, int precision) {
   if (B <= 0 || B > kMaxSharedBatch || N <= 0 || N > kMaxNodes || C <= 0 || NH <= 0 || NH > kMaxSharedBatch ||
@@ -1079,6 +1083,8 @@ int attention_tree(void* out, const void* qkv, const GPT2PagedKVCache* kvc, cons
   RETURN_IF(!aligned16(out) || !aligned16(qkv) || !aligned16(kvc->pool) || !aligned16(workspace) ||
                 !aligned4(kvc->block_table) || !aligned4(pos) || !aligned4(parent),
             GPT2_ERR_ALIGN);
+  const size_t out_bytes = static_cast<size_t>(B) * N * C * kv_elem_bytes(precision);
+  RETURN_IF(overlap(out, out_bytes, qkv, 3 * out_bytes), GPT2_ERR_ARG);
   const long long cap =
       std::min<long long>(kMaxSharedPositions, static_cast<long long>(kvc->max_blocks_per_seq) << lbs);
   const size_t e = kv_elem_bytes(precision);
@@ -1142,6 +1148,8 @@ int logits_adjust(void* out, const void* logits, int logits_type, const GPT2Logi
                         static_cast<const void*>(tok), static_cast<const void*>(parent)})
     RETURN_IF(!aligned4(p), GPT2_ERR_ALIGN);
   if (B == 0) return GPT2_OK;
+  const size_t bytes = static_cast<size_t>(B) * N * Vp * (logits_type == GPT2_PROBS_F32 ? 4 : 2);
+  RETURN_IF(out != logits && overlap(out, bytes, logits, bytes), GPT2_ERR_ARG);
   PdlScope pdl(true);
   TRY(launch_logits_adjust(out, logits, logits_type, *r, tok, parent, B, N, V, Vp, as_stream(stream)));
   return check_launch();
@@ -1152,14 +1160,12 @@ int gpt2_accept_tree(int* path, int* count, int* emitted, int* next_tok, int* ne
                      int B, int N, int precision, void* stream) {
   RETURN_IF(!tok || !next || !pos || B < 0 || N <= 0, GPT2_ERR_ARG);
   RETURN_IF(N > kMaxNodes || B > kMaxSharedBatch, GPT2_ERR_SHAPE);
-  int* const outputs[] = {path, count, emitted, next_tok, next_pos};
-  const int* const inputs[] = {tok, parent, next, pos};
-  for (int i = 0; i < 5; ++i) {
-    RETURN_IF(!aligned4(outputs[i]), GPT2_ERR_ALIGN);
-    for (const int* p : inputs) RETURN_IF(outputs[i] != nullptr && outputs[i] == p, GPT2_ERR_ARG);
-    for (int j = 0; j < i; ++j) RETURN_IF(outputs[i] != nullptr && outputs[i] == outputs[j], GPT2_ERR_ARG);
-  }
-  for (const int* p : inputs) RETURN_IF(!aligned4(p), GPT2_ERR_ALIGN);
+  const int* const arrays[] = {path, emitted, count, next_tok, next_pos, tok, parent, next, pos};
+  const size_t row = static_cast<size_t>(B) * 4, all = row * N;
+  const size_t bytes[] = {all, all, row, row, row, all, all, all, row};
+  for (int i = 0; i < 9; ++i) RETURN_IF(!aligned4(arrays[i]), GPT2_ERR_ALIGN);
+  for (int i = 0; i < 5; ++i)  // the outputs
+    for (int j = i + 1; j < 9; ++j) RETURN_IF(overlap(arrays[i], bytes[i], arrays[j], bytes[j]), GPT2_ERR_ARG);
   AcceptArgs a{path, count, emitted, next_tok, next_pos, tok, parent, next, pos, N, 0, 0, 0, nullptr, 0,
                KVRows{nullptr, 0, 0, 0, kMaxSharedPositions, kMaxSharedPositions}};
   if (kvc != nullptr) {

@@ -64,7 +64,8 @@ GPT2_API size_t attention_tree_workspace_size(int B, int N, int C, int NH, int p
  *   out[b * N + i, head h] = sum_j softmax_j(q . k_j / sqrt(hs)) v_j
  * over the cached positions j < pos[b], read through row b of the block table,
  * and the nodes j of node i's path, from qkv; nothing else, whatever its
- * values, reaches a row.  Node i's key and value are stored at position pos[b]
+ * values, reaches a row (an infinity or a NaN among the values that a row does
+ * see makes that dimension of it infinite or NaN).  Node i's key and value are stored at position pos[b]
  * + i of the cache (by its number, not its depth: gpt2_accept_tree moves the
  * accepted ones).  A missing node has a zero row and is not stored.
  *   kv: one layer's slab [2][num_blocks][NH][block_size][hs], and the table
@@ -81,7 +82,8 @@ GPT2_API size_t attention_tree_workspace_size(int B, int N, int C, int NH, int p
  * outside it, which is then missing.  A reached table entry outside [0,
  * num_blocks) sets GPT2_DEVERR_BLOCK_BIT: block 0 is read in its place, and no
  * node is stored through it.  Positions from pos[b] on lie in blocks that no
- * other sequence reads.  out must not alias qkv.
+ * other sequence, and no other position of this one, has.  out must not overlap
+ * qkv.
  * Workspace: 16-byte aligned, attention_tree_workspace_size bytes. */
 GPT2_API int attention_tree(void* out, const void* qkv, const GPT2PagedKVCache* kv, const int* pos, const int* parent,
                             int B, int N, int C, int NH, int precision, void* workspace, size_t ws_bytes,

@@ -53,6 +53,8 @@ def attention_args(**kw):
     (dict(out=FAKE + 8), AL), (dict(qkv=FAKE + 8), AL), (dict(workspace=FAKE + 8), AL), (dict(pos=FAKE + 2), AL),
     (dict(parent=FAKE + 1), AL), (dict(kv=ab.paged_kv(FAKE + 8, FAKE, 64, 16, 32)), AL),
     (dict(kv=ab.paged_kv(FAKE, FAKE + 2, 64, 16, 32)), AL),
+    # 32 rows of 256 values: the output's last bytes are the first queries', or the other way round
+    (dict(qkv=FAKE + 32 * 256 * 2 - 16), A), (dict(qkv=FAKE - 3 * 32 * 256 * 2 + 16), A),
 ])
 def test_tree_attention_refuses(change, code):
     refused(code, ab.attention_tree, **attention_args(**change))
@@ -111,6 +113,7 @@ def adjust_args(rules=(), **kw):
     (dict(N=65), S), (dict(B=65536), S), (dict(Vp=14), S), (dict(logits_type=ab.GPT2_PROBS_F16), S),
     (dict(logits_type=ab.GPT2_PROBS_BF16), S), (dict(V=(1 << 30) + 1, Vp=(1 << 30) + 8), S),
     (dict(logits=FAKE + 8), AL), (dict(out=FAKE + 8), AL), (dict(tok=FAKE + 2), AL), (dict(parent=FAKE + 1), AL),
+    (dict(out=FAKE + 2 * 3 * 48 - 16), A), (dict(logits=FAKE + 48), A),  # they share a row
 ])
 def test_adjust_refuses(change, code):
     refused(code, ab.logits_adjust, **{**adjust_args(), **change})
@@ -143,6 +146,7 @@ def accept_args(**kw):
     # outputs that another CTA's inputs, or another output, would share
     (dict(next_pos=FAKE + 512), A), (dict(next_tok=FAKE + 320), A), (dict(emitted=FAKE + 448), A),
     (dict(path=FAKE + 384), A), (dict(count=FAKE + 256), A), (dict(path=FAKE + 128), A),
+    (dict(path=FAKE + 384 - 20), A), (dict(next_tok=FAKE + 320 + 20), A), (dict(count=FAKE + 4), A),
     (dict(N=65), S), (dict(B=65536), S), (dict(kv=ab.paged_kv(FAKE, FAKE, 64, 16, 1025)), S),
     (dict(path=FAKE + 2), AL), (dict(next_pos=FAKE + 257), AL), (dict(tok=FAKE + 322), AL), (dict(pos=FAKE + 513), AL),
     (dict(parent=FAKE + 386), AL), (dict(kv=ab.paged_kv(FAKE + 8, FAKE, 64, 16, 4)), AL),
