@@ -23,53 +23,52 @@ using namespace tree;
 constexpr int R = 8;           // rows of a warp
 constexpr float kGrow = 8.0f;  // log2 units by which a score may pass its row's maximum before that is raised
 
-template <int HS, int WM>
+template <int HS>
 struct RingF32 {
-  static constexpr int kKeys = HS == 64 && WM < 8 ? 32 : 64;  // of a tile
-  static constexpr int kRow = HS * 4;                         // bytes of a key
-  static constexpr int kStrips = HS == 64 ? 2 : 1;            // a TMA box is at most 128 bytes wide
+  static constexpr int kKeys = HS == 64 ? 32 : 64;          // of a tile
+  static constexpr int kRow = HS * 4;                      // bytes of a key
+  static constexpr int kStrips = HS == 64 ? 2 : 1;         // a TMA box is at most 128 bytes wide
   static constexpr int kTileBytes = kKeys * kRow;
-  static constexpr int kNodeBytes = R * WM * kRow;  // of the nodes' queries, keys or values
+  static constexpr int kNodeBytes = R * kRow;  // of the nodes' queries, keys or values
   static constexpr int kStage = 2 * kTileBytes > 3 * kNodeBytes ? 2 * kTileBytes : 3 * kNodeBytes;
   static constexpr int kStages = HS == 16 ? 3 : 2;
   static constexpr int kPRow = kKeys + 4;  // floats of a row of probabilities
   static constexpr int kWarp = R * (HS + kPRow) * 4 + R * 8;  // a warp's queries, probabilities, sets
   // the rings from a multiple of 1024 bytes on, the warps' own, the barriers
   static constexpr int kGroup = kStages * kStage;
-  static constexpr int smem(int groups) { return 1024 + groups * (kGroup + WM * kWarp + kStages * 8); }
+  static constexpr int smem(int groups) { return 1024 + groups * (kGroup + kWarp + kStages * 8); }
 };
 
-constexpr int f32_warps(int WM, int groups) { return WM * (groups > 0 ? groups : 1); }
-template <int HS, int WM, int kGroups>
+constexpr int f32_warps(int groups) { return groups > 0 ? groups : 1; }
+template <int HS, int kGroups>
 constexpr int f32_ctas() {  // CTAs an SM: twelve warps, as far as shared memory goes
-  const int fit = 228 * 1024 / (RingF32<HS, WM>::smem(kGroups > 0 ? kGroups : 1) + 1024);
-  const int most = 12 / f32_warps(WM, kGroups);
+  const int fit = 228 * 1024 / (RingF32<HS>::smem(f32_warps(kGroups)) + 1024);
+  const int most = 12 / f32_warps(kGroups);
   return fit < most ? fit : most;
 }
 
-template <int HS, int WM, int kGroups>
-__global__ void __launch_bounds__(32 * f32_warps(WM, kGroups), f32_ctas<HS, WM, kGroups>())
+template <int HS, int kGroups>
+__global__ void __launch_bounds__(32 * f32_warps(kGroups), f32_ctas<HS, kGroups>())
     tree_f32_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                     const __grid_constant__ CUtensorMap map_qkv, TreeArgs a) {
-  using Ring = RingF32<HS, WM>;
+  using Ring = RingF32<HS>;
   constexpr int K = Ring::kKeys, kStages = Ring::kStages, kStrips = Ring::kStrips, kChunks = HS / 4;
   constexpr int KG = 32 / kChunks;  // key groups of the lanes
   constexpr bool kPairs = kGroups > 0;
   constexpr int WK = kPairs ? kGroups : 1;
   extern __shared__ uint8_t tree_f32_raw[];
   uint8_t* rings = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tree_f32_raw) + 1023) & ~uintptr_t(1023));
-  const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / WM;
-  const int warp = (threadIdx.x >> 5) % WM;  // of the group: its nodes are R warp ..
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
   uint8_t* ring = rings + group * Ring::kGroup;
-  uint8_t* own = rings + WK * Ring::kGroup + (threadIdx.x >> 5) * Ring::kWarp;
+  uint8_t* own = rings + WK * Ring::kGroup + group * Ring::kWarp;
   float* qb = reinterpret_cast<float*>(own);
   float* pb = qb + R * HS;
   unsigned long long* sets = reinterpret_cast<unsigned long long*>(pb + R * Ring::kPRow);
-  uint64_t* full = reinterpret_cast<uint64_t*>(rings + WK * (Ring::kGroup + WM * Ring::kWarp)) + group * kStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(rings + WK * (Ring::kGroup + Ring::kWarp)) + group * kStages;
   const int kg = lane / kChunks, dl = lane % kChunks;  // key group, dimensions 4 dl ..
   float* kcache = static_cast<float*>(a.kcache);
   float* vcache = static_cast<float*>(a.vcache);
-  if (warp == 0 && lane == 0) {
+  if (lane == 0) {
     if (group == 0) {
       tma_prefetch_desc(&map_k);
       tma_prefetch_desc(&map_v);
@@ -86,11 +85,11 @@ __global__ void __launch_bounds__(32 * f32_warps(WM, kGroups), f32_ctas<HS, WM, 
   else
     sh = share_of<K>(a);
   int4 open = make_int4(-1, 0, 0, 0);
-  group_or<WM>(group, false);  // the barriers
+  __syncwarp();  // the barriers
 
-  Feed<Ring, WM, WK> feed(a, sh, kPairs, map_k, map_v, map_qkv, ring, full);
+  Feed<Ring, 1, WK> feed(a, sh, kPairs, map_k, map_v, map_qkv, ring, full);
   const int lead = feed.lead, n_steps = feed.n_steps;
-  if (warp == 0) feed.begin();
+  feed.begin();
 
   Place at = sh.at;
   bool from_start = false;
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(32 * f32_warps(WM, kGroups), f32_ctas<HS, WM, 
     for (int x = lane; x < R * kChunks; x += 32) {
       const int r = x / kChunks, c = x % kChunks;
       *reinterpret_cast<float4*>(qb + r * HS + 4 * c) =
-          *reinterpret_cast<const float4*>(q + tile_at_bytes<Ring::kRow, kStrips>(warp * R + r, c, R * WM));
+          *reinterpret_cast<const float4*>(q + tile_at_bytes<Ring::kRow, kStrips>(r, c, R));
     }
     __syncwarp();
 #pragma unroll
@@ -241,13 +240,13 @@ __global__ void __launch_bounds__(32 * f32_warps(WM, kGroups), f32_ctas<HS, WM, 
   uint32_t phase = 0;
   for (int n = 0; n < n_steps; ++n) {
     const bool came = mbar_wait(full + stage, phase);
-    // the step's keys are there, and every warp is past the step whose stage is
+    // the step's keys are there, and every lane is past the step whose stage is
     // refilled now; a copy that did not come (flagged by the wait) ends the share
-    if (group_or<WM>(group, !came)) {
-      if (warp == 0) feed.drain(n);
+    if (__any_sync(0xffffffffu, !came)) {
+      feed.drain(n);
       break;
     }
-    if (warp == 0) feed.copy((stage + kStages - 1) % kStages);
+    feed.copy((stage + kStages - 1) % kStages);
     uint8_t* st = ring + stage * Ring::kStage;
     if (++stage == kStages) {
       stage = 0;
@@ -268,21 +267,20 @@ __global__ void __launch_bounds__(32 * f32_warps(WM, kGroups), f32_ctas<HS, WM, 
       int par[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) par[u] = at.seq.live > 0 ? tree_parent(row, lane + 32 * u, a.N) : -2;
-      const bool report = at.h == 0 && warp == 0;
+      const bool report = at.h == 0;
       if (report && lane == 0) seq_of(a, at.b, true);
       const TreeSets ts = tree_sets(par, a.N, at.seq.live, report);
-      const unsigned long long mine = tree_set_of(ts, warp * R + (lane & (R - 1))), live = tree_live(ts);
+      const unsigned long long mine = tree_set_of(ts, lane & (R - 1)), live = tree_live(ts);
       if (lane < R) sets[lane] = mine;
       const uint8_t* kt = st + Ring::kNodeBytes;
       uint8_t* vt = st + 2 * Ring::kNodeBytes;
-      // this warp's nodes are stored; every warp looks at all values
       bool bad = false;
       for (int x = lane; x < a.N * kChunks; x += 32) {
         const int node = x / kChunks, c = x % kChunks;
-        const uint32_t in = tile_at_bytes<Ring::kRow, kStrips>(node, c, R * WM);
+        const uint32_t in = tile_at_bytes<Ring::kRow, kStrips>(node, c, R);
         const float4 v = *reinterpret_cast<const float4*>(vt + in);
         bad |= !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w));
-        if (node / R != warp || (live >> node & 1) == 0) continue;
+        if ((live >> node & 1) == 0) continue;
         const int j = at.seq.pos + node;
         const int blk = __ldg(a.rows.table + static_cast<size_t>(at.b) * a.rows.max_blocks + (j >> a.rows.lbs));
         if (blk < 0 || blk >= a.rows.num_blocks) {
@@ -293,10 +291,10 @@ __global__ void __launch_bounds__(32 * f32_warps(WM, kGroups), f32_ctas<HS, WM, 
         *reinterpret_cast<float4*>(kcache + to) = *reinterpret_cast<const float4*>(kt + in);
         *reinterpret_cast<float4*>(vcache + to) = v;
       }
-      zero_rows(vt, a.N, R * WM, R * WM);
+      zero_rows(vt, a.N, R, R);
       keys_at = kt;
       values_at = vt;
-      rows = keys = R * WM;
+      rows = keys = R;
       odd = __any_sync(0xffffffffu, bad);
     } else if (keys < K) {
       zero_rows(st + Ring::kTileBytes, keys, K, K);
@@ -308,17 +306,16 @@ __global__ void __launch_bounds__(32 * f32_warps(WM, kGroups), f32_ctas<HS, WM, 
       reduce();
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int node = warp * R + r;
-        if (node >= a.N || r % KG != kg) continue;
+        if (r >= a.N || r % KG != kg) continue;
         const bool missing = from_start && sets[r] == 0;
         if (part.whole) {
           const float inv = 1.0f / l[r];
-          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (static_cast<size_t>(at.b) * a.N + node) * a.C +
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (static_cast<size_t>(at.b) * a.N + r) * a.C +
                                      at.h * HS + 4 * dl) =
               missing ? make_float4(0.f, 0.f, 0.f, 0.f)
                       : make_float4(o[r].x * inv, o[r].y * inv, o[r].z * inv, o[r].w * inv);
         } else {
-          const size_t to = part.slot * a.N + node;
+          const size_t to = part.slot * a.N + r;
           // a sum of -1 tells the join that the node is missing
           if (dl == 0) a.part.ml[to] = make_float2(m[r], missing ? -1.f : l[r]);
           *reinterpret_cast<float4*>(a.part.o + to * HS + 4 * dl) = o[r];
@@ -333,7 +330,7 @@ __global__ void __launch_bounds__(32 * f32_warps(WM, kGroups), f32_ctas<HS, WM, 
     // the groups' results join where their rings were; group 0, which has the
     // nodes' own step, writes the rows
     constexpr int kRowF = HS + 4;  // floats: the row, its maximum and sum
-    static_assert(R * WM * kRowF * 4 <= Ring::kGroup, "a group's results fit in its ring");
+    static_assert(R * kRowF * 4 <= Ring::kGroup, "a group's results fit in its ring");
     const bool some = sh.end > 0;
     if (some) reduce();
     if (WK > 1) {
@@ -341,7 +338,7 @@ __global__ void __launch_bounds__(32 * f32_warps(WM, kGroups), f32_ctas<HS, WM, 
       if (group > 0) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          float* row = reinterpret_cast<float*>(ring) + (warp * R + r) * kRowF;
+          float* row = reinterpret_cast<float*>(ring) + r * kRowF;
           if (r % KG != kg) continue;
           if (some) *reinterpret_cast<float4*>(row + 4 * dl) = o[r];
           if (dl == 0) *reinterpret_cast<float2*>(row + HS) = some ? make_float2(m[r], l[r]) : make_float2(-INFINITY, 0.f);
@@ -352,11 +349,8 @@ __global__ void __launch_bounds__(32 * f32_warps(WM, kGroups), f32_ctas<HS, WM, 
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int node = warp * R + r;
-      if (node >= a.N || r % KG != kg) continue;
-      auto other = [&](int k) {
-        return reinterpret_cast<const float*>(rings + k * Ring::kGroup) + (warp * R + r) * kRowF;
-      };
+      if (r >= a.N || r % KG != kg) continue;
+      auto other = [&](int k) { return reinterpret_cast<const float*>(rings + k * Ring::kGroup) + r * kRowF; };
       float M = m[r];
 #pragma unroll
       for (int k = 1; k < WK; ++k) M = fmaxf(M, other(k)[HS]);
@@ -376,34 +370,34 @@ __global__ void __launch_bounds__(32 * f32_warps(WM, kGroups), f32_ctas<HS, WM, 
         v.w = fmaf(x.w, w, v.w);
       }
       const float inv = 1.0f / sum;
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (static_cast<size_t>(at.b) * a.N + node) * a.C + at.h * HS +
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (static_cast<size_t>(at.b) * a.N + r) * a.C + at.h * HS +
                                  4 * dl) =
           sets[r] != 0 ? make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
 }
 
-template <int HS, int WM, int kGroups>
+template <int HS, int kGroups>
 int f32_typed(const TreeArgs& a, int* ctas, cudaStream_t s) {
   static bool allowed[kMaxDevices] = {};
-  using Ring = RingF32<HS, WM>;
-  constexpr int kSmem = Ring::smem(kGroups > 0 ? kGroups : 1), kPerSm = f32_ctas<HS, WM, kGroups>();
+  using Ring = RingF32<HS>;
+  constexpr int kSmem = Ring::smem(f32_warps(kGroups)), kPerSm = f32_ctas<HS, kGroups>();
   static_assert(kPerSm > 0 && kSmem <= 227 * 1024, "shared memory");
   CUtensorMap mk, mv, mq;
-  if (!tree_maps(&mk, &mv, &mq, a, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, HS, Ring::kKeys, R * WM)) return GPT2_ERR_CUDA;
-  cudaError_t e = allow_smem(allowed, tree_f32_kernel<HS, WM, kGroups>, kSmem);
+  if (!tree_maps(&mk, &mv, &mq, a, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, HS, Ring::kKeys, R)) return GPT2_ERR_CUDA;
+  cudaError_t e = allow_smem(allowed, tree_f32_kernel<HS, kGroups>, kSmem);
   // of shares as many as the SMs hold at once
   const int grid = kGroups > 0 ? a.B * a.NH : std::min(max_ctas(a.N), kPerSm * num_sms());
   if (e == cudaSuccess)
-    e = launch_pdl(tree_f32_kernel<HS, WM, kGroups>, dim3(grid), dim3(32 * f32_warps(WM, kGroups)), kSmem, s, mk, mv, mq,
+    e = launch_pdl(tree_f32_kernel<HS, kGroups>, dim3(grid), dim3(32 * f32_warps(kGroups)), kSmem, s, mk, mv, mq,
                    a);
   *ctas = kGroups > 0 ? 0 : grid;
   return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
 }
 
-// More than eight nodes.  128 threads: ty = thread
-// / 16 owns nodes R ty .., tx = thread % 16 keys tx + 16 i of a tile (S) and
-// dimensions tx * HS / 16 .. (O); tiles by cp.async into two buffers.
+// More than eight nodes.  128 threads: ty = thread / 16 owns nodes R ty .., tx =
+// thread % 16 keys tx + 16 i of a tile (S) and dimensions tx * HS / 16 .. (O); tiles
+// by cp.async into two buffers.
 constexpr int kSimtKeys = 64;  // of a tile, and at most as many nodes
 static_assert(kSimtKeys >= kMaxNodes, "the nodes' keys are one step");
 template <int HS, int R>
@@ -661,7 +655,7 @@ int f32(const TreeArgs& a, int* grid, cudaStream_t s) {
   // 11.9 / 6.8, 250 11.5 / 8.8, 500 11.8 / 13.7; 96: 13.0 / 7.1, 13.2 / 11.5, 14.2 /
   // 16.0; 192: 13.2 / 13.0, 15.0 / 19.4.)
   const bool pairs = static_cast<long long>(a.B) * a.NH <= 152 && a.rows.capacity <= 384;
-  if (a.N <= 8) return pairs ? f32_typed<HS, 1, 4>(a, grid, s) : f32_typed<HS, 1, 0>(a, grid, s);
+  if (a.N <= 8) return pairs ? f32_typed<HS, 4>(a, grid, s) : f32_typed<HS, 0>(a, grid, s);
   if (a.N <= 16) return simt_typed<HS, 2>(a, grid, s);
   if (a.N <= 32) return simt_typed<HS, 4>(a, grid, s);
   return simt_typed<HS, 8>(a, grid, s);
