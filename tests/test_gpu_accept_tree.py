@@ -178,3 +178,40 @@ def test_offsets_past_32_bits():
     assert np.array_equal(pool[:, :, far:].cpu().numpy(), moved(c["pool"], c["table"], want[0], c["pos"], c["bs"]))
     assert not pool[:, :, :far].any()
     no_device_error()
+
+
+@pytest.mark.parametrize("precision", [ab.GPT2_FP32, ab.GPT2_FP16], ids=["fp32", "fp16"])
+def test_graph_and_streams(precision):
+    """Captured once and replayed on other trees; two on two streams."""
+    cs = [make(precision, 6, 21, 2, 3, 16, 4, seed=s) for s in (1, 2)]
+    want = [run(c) for c in cs]
+    names = ("pool", "table", "tok", "parent", "chosen", "pos")
+    state = []
+    for _ in range(2):
+        t = {k: dev(cs[0][k].copy()) for k in names}
+        o = [torch.empty(x, dtype=torch.int32, device="cuda") for x in ((6, 21), (6,), (6, 21), (6,), (6,))]
+        kv = ab.paged_kv(t["pool"], t["table"], cs[0]["pool"].shape[2], 4, cs[0]["table"].shape[1])
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            ab.gpt2_accept_tree(*o, config(cs[0]), kv, t["tok"], t["parent"], t["chosen"], t["pos"], 6, 21, precision, s)
+        state.append((t, o, s, g))
+    for round in range(4):
+        for k, (t, o, s, g) in enumerate(state):
+            with torch.cuda.stream(s):
+                for n in names:
+                    t[n].copy_(torch.from_numpy(cs[(round + k) % 2][n]))
+                g.replay()
+        torch.cuda.synchronize()
+        for k, (t, o, s, g) in enumerate(state):
+            (path, emitted, count, tok, pos), pool = want[(round + k) % 2]
+            for a, b in zip(o, (path, count, emitted, tok, pos)):
+                assert np.array_equal(a.cpu().numpy(), b)
+            assert np.array_equal(t["pool"].cpu().numpy(), pool)
+    no_device_error()
+
+
+def test_one_node_and_full_trees_of_many_sequences():
+    for B, N in ((1, 1), (700, 1), (400, 64)):
+        check(make(ab.GPT2_BF16, B, N, 1, 1, 16, 16, seed=B))
+    no_device_error()

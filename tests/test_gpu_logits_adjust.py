@@ -122,6 +122,56 @@ def test_large_rows_of_many_nodes(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("B,N,H,M", [(160, 1, 80, 5), (160, 1, 300, 0), (90, 3, 0, 85), (60, 9, 85, 0), (60, 9, 900, 40)])
+def test_tokens_that_share_their_low_bits(dtype, B, N, H, M):
+    """Multiples of 128 and of 512: where few tokens of a segment can be named they
+    stand in a table of a power of two entries."""
+    V = 32003
+    c = make(dtype, B, N, V, H, M, 2, seed=H + M, pad=5)
+    rng = np.random.default_rng(H)
+    pick = lambda shape: (rng.integers(0, V // 512, shape) * 512 + rng.choice([0, 128, 7], shape)).astype(np.int32)  # noqa: E731
+    c["tok"] = pick((B, N))
+    if H:
+        c["rules"]["history"] = pick((B, H))
+        c["rules"]["history_len"][:] = H
+    if M:
+        c["rules"]["bias_ids"] = pick((B, M))
+    check(c)
+    no_device_error()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_histories_of_distinct_tokens(dtype):
+    """As many tokens of a segment as a history has, and every token of it."""
+    for V, H, B in ((1024, 1024, 3), (8192, 1365, 200), (5000, 4990, 2)):
+        c = make(dtype, B, 2, V, H, 3, 0, seed=H, pad=0)
+        rng = np.random.default_rng(V)
+        c["rules"]["history"] = np.stack([rng.permutation(min(V, 8192 if V != 8192 else 1400))[:H] for _ in range(B)]).astype(np.int32)
+        c["rules"]["history_len"][:] = H
+        c["rules"]["prompt_len"][:] = H // 3
+        check(c)
+    no_device_error()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_calls_behind_each_other_in_place(dtype):
+    """Twice in place, the second on what the first wrote, no wait between them."""
+    c = make(dtype, 7, 5, 3000, 60, 5, 3, seed=3, pad=8)
+    once = run(c)
+    twice = run(dict(c, x=torch.where((once == 7).all(1, keepdim=True), c["x"], once)))
+    x = c["x"].cuda()
+    rules, tok, parent = rules_of(c), gpu(c["tok"]), gpu(c["parent"])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(2):
+        ab.logits_adjust(x, x, ab.element_type(x), rules, tok, parent, 7, 5, 3000, c["Vp"], s)
+    s.synchronize()
+    there = ~(once == 7).all(1)
+    assert torch.equal(x.cpu()[there], twice[there])
+    no_device_error()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("left", [
     dict(repetition=None), dict(presence=None), dict(frequency=None), dict(bias_ids=None, bias_values=None),
     dict(masks=None, mask_rows=None), dict(history=None, history_len=None, prompt_len=None), dict(history_len=None),

@@ -168,6 +168,60 @@ def test_shares(precision, B, N, NH, most):
     no_device_error()
 
 
+# Tables that could hold more positions than a CTA takes by itself: pairs are cut
+# into shares, of which a few hold many pairs and many hold none.
+@pytest.mark.parametrize("precision", TYPES, ids=IDS)
+@pytest.mark.parametrize("hs", [16, 32, 64])
+@pytest.mark.parametrize("B,N,NH,most,bs", [
+    (1, 1, 1, 0, 16), (1, 5, 3, 33, 8), (3, 8, 2, 700, 16), (6, 16, 4, 300, 32), (4, 17, 3, 65, 4), (3, 32, 2, 900, 64),
+    (2, 33, 2, 130, 4), (3, 64, 3, 640, 16),
+])
+def test_short_pairs_in_long_tables(precision, hs, B, N, NH, most, bs):
+    c = make(precision, N, NH, hs, ragged(B, most, N), bs, trees(B, N, seed=B + N, roots=True), seed=B, spare=2100 // bs)
+    check(c)
+    no_device_error()
+
+
+@pytest.mark.parametrize("precision", TYPES, ids=IDS)
+@pytest.mark.parametrize("B,N,NH,hs,most,spare", [
+    (500, 3, 4, 16, 90, 40), (300, 12, 8, 16, 40, 40), (330, 20, 3, 32, 70, 40), (160, 40, 3, 16, 70, 40),
+    (40, 64, 12, 64, 100, 40), (90, 40, 2, 32, 70, 2), (90, 20, 2, 64, 200, 2),
+])
+def test_more_pairs_than_shares(precision, B, N, NH, hs, most, spare):
+    """Every share holds the ends of several pairs; and as many CTAs as pairs."""
+    check(make(precision, N, NH, hs, ragged(B, most, B), 64, trees(B, N, seed=B), seed=B, spare=spare))
+    no_device_error()
+
+
+@pytest.mark.parametrize("precision", TYPES, ids=IDS)
+@pytest.mark.parametrize("bs", [1, 2, 4, 8, 128])
+def test_wide_trees_over_small_blocks(precision, bs):
+    check(make(precision, 50, 2, 64, [300, 0, -1, 127, 128, 1], bs, trees(6, 50, seed=bs, roots=True), seed=bs))
+    no_device_error()
+
+
+@pytest.mark.parametrize("precision", TYPES, ids=IDS)
+def test_calls_behind_each_other_in_one_workspace(precision):
+    """Larger and smaller trees, without a wait between them: each finds what the
+    others left."""
+    cs = [make(precision, N, 4, 64, ragged(B, most, N), 16, trees(B, N, seed=N), seed=N, spare=spare)
+          for B, N, most, spare in [(5, 64, 500, 2), (9, 5, 900, 140), (3, 20, 300, 140), (7, 8, 200, 2), (4, 40, 700, 2)]]
+    want = [run(c) for c in cs]
+    ws = torch.full((max(ab.attention_tree_workspace_size(1, c["N"], 256, 4, precision) for c in cs),), 255,
+                    dtype=torch.uint8, device="cuda")
+    ts = [on_gpu(c) for c in cs]
+    outs = [torch.empty(o.shape[0] * o.shape[1], 256, dtype=o.dtype, device="cuda") for o, _ in want]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for c, t, out in zip(cs, ts, outs):
+            call(c, t, out, ws, stream=s)
+    s.synchronize()
+    for (o, p), out, t in zip(want, outs, ts):
+        assert same(out.cpu().view(o.shape), o) and same(t["pool"].cpu(), p)
+    no_device_error()
+
+
 @pytest.mark.parametrize("precision", TYPES, ids=IDS)
 def test_same_bits_again(precision):
     c = make(precision, 24, 4, 64, ragged(9, 900, 1), 16, trees(9, 24, seed=1), seed=1)
@@ -191,17 +245,18 @@ def test_peaked_and_rising_scores(precision):
 
 @pytest.mark.parametrize("precision", TYPES, ids=IDS)
 @pytest.mark.parametrize("N", [6, 30, 64])
+@pytest.mark.parametrize("hs,spare", [(32, 2), (32, 140), (64, 2), (64, 140)])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
-def test_unseen_values_stay_out(precision, N, value):
+def test_unseen_values_stay_out(precision, N, hs, spare, value):
     """NaN and infinities in cache slots that no position reaches, in the rows of
     missing nodes, and in one node's key and value: only the rows behind it may
     change."""
     for pos in ([70, 0, 200], [61, 3, 128]):
         parent = trees(3, N, seed=N, missing=False)
         parent[0, N // 2] = -2
-        c = make(precision, N, 2, 32, pos, 16, parent, seed=N)
+        c = make(precision, N, 2, hs, pos, 16, parent, seed=N, spare=spare)
         good = check(c)
-        kv = c["qkv"].view(3, N, 3, 2, 32)
+        kv = c["qkv"].view(3, N, 3, 2, hs)
         used = torch.zeros(c["pool"].shape[1], 16, dtype=torch.bool)
         for b in range(3):
             for j in range(pos[b]):
