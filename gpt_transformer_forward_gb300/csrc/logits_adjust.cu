@@ -22,7 +22,8 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kSegBytes = 16384;  // of a segment, at most
 constexpr int kStages = 3;        // rows in flight
-constexpr int kSegWords = kSegBytes / 2 / 32;  // mask words of a segment, at most
+constexpr int kVecs = kSegBytes / 16 / kThreads;  // vectors of a segment for a thread, at most
+constexpr int kSegWords = kSegBytes / 2 / 32;     // mask words of a segment, at most
 constexpr uint32_t kPrompt = 1u << 21, kCountMask = kPrompt - 1;
 constexpr int kBiasShift = 22;
 static_assert(GPT2_LOGIT_MAX_HISTORY + kMaxNodes < (1 << 21) && GPT2_LOGIT_MAX_BIASES < (1 << 10), "bits of a word");
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
   constexpr int kAhead = 4;
   const int* hist = r.history + static_cast<size_t>(b) * r.history_stride;
   const int* ids = r.bias_ids + static_cast<size_t>(b) * r.num_bias;
+  const int bias_at = tid ^ 96;  // the biases begin with the last warp: the first has the tree
   int early[kAhead], early_id = -1, len = 0, prompt = 0;
   float early_bias = 0.f;
 #pragma unroll
@@ -201,9 +203,9 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
       for (int k = 0; k < kAhead; ++k)
         if (tid + k * kThreads < r.history_stride) early[k] = __ldg(hist + tid + k * kThreads);
     }
-    if (tid < r.num_bias) {
-      early_id = __ldg(ids + tid);
-      early_bias = __ldg(r.bias_values + static_cast<size_t>(b) * r.num_bias + tid);
+    if (bias_at < r.num_bias) {
+      early_id = __ldg(ids + bias_at);
+      early_bias = __ldg(r.bias_values + static_cast<size_t>(b) * r.num_bias + bias_at);
     }
     for (int x = tid; x < table_words / 4; x += kThreads)
       reinterpret_cast<uint4*>(tab.word)[x] = make_uint4(0u, 0u, 0u, 0u);
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
     mask_rows[i] = my_mask;
   }
   if (r.num_masks > 0) fetch_mask(first_mask);
-  some_biases[tid] = early_bias;
+  some_biases[bias_at] = early_bias;
   if (len < 0 || len > r.history_stride || prompt < 0 || prompt > len) {
     if (report && tid == 0) set_error(GPT2_DEVERR_POSITION);
     len = min(max(len, 0), r.history_stride);
@@ -282,13 +284,13 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
       }
       return t >= v0 && t < v1 ? t - v0 : -1;
     };
-    // lists the entries of up to kAhead tokens of a thread that are new (whole
-    // warps call)
-    auto enlist = [&](const bool (&fresh)[kAhead], const uint32_t (&entry)[kAhead]) {
-      unsigned who[kAhead];
+    // puts the entries that a lane took with a word of 0 in the list (whole warps call)
+    auto enlist = [&](const auto& fresh, const auto& entry) {
+      constexpr int kTokens = sizeof(entry) / sizeof(entry[0]);
+      unsigned who[kTokens];
       int n = 0;
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
+      for (int k = 0; k < kTokens; ++k) {
         who[k] = __ballot_sync(0xffffffffu, fresh[k]);
         n += __popc(who[k]);
       }
@@ -297,38 +299,41 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
       if (lane == 0) at = atomicAdd(&n_slots, n);
       at = __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
+      for (int k = 0; k < kTokens; ++k) {
         if (fresh[k]) list[at + __popc(who[k] & ((1u << lane) - 1))] = static_cast<uint16_t>(entry[k]);
         at += __popc(who[k]);
       }
     };
-    bool fresh[kAhead];
-    uint32_t entry[kAhead];
-    for (int x0 = 0; x0 < r.num_bias; x0 += kAhead * kThreads) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int x = x0 + tid + k * kThreads;
-        const int t = x < r.num_bias ? token(x < kThreads ? early_id : __ldg(ids + x)) : -1;
-        fresh[k] = false;
-        if (t >= 0) {
-          entry[k] = tab.take(t);
-          fresh[k] = atomicMax(tab.word + entry[k], static_cast<uint32_t>(x + 1) << kBiasShift) == 0;
-        }
+    // what is added to a word commutes but for the place of a token's last bias: that
+    // is known in a warp; of more biases nothing is counted before they are done
+    const bool one_warp = r.num_bias <= 32;
+    for (int x = bias_at; x - lane < r.num_bias; x += kThreads) {
+      const int t = x < r.num_bias ? token(x < kThreads ? early_id : __ldg(ids + x)) : -1;
+      const bool later = (__match_any_sync(0xffffffffu, t) >> lane) > 1;  // a higher lane has the token too
+      uint32_t entry[1] = {0};
+      bool fresh[1] = {false};
+      if (t >= 0 && !later) {
+        entry[0] = tab.take(t);
+        const uint32_t place = static_cast<uint32_t>(x + 1) << kBiasShift;
+        fresh[0] = (one_warp ? atomicAdd(tab.word + entry[0], place) : atomicMax(tab.word + entry[0], place)) == 0;
       }
       enlist(fresh, entry);
     }
-    if (r.num_bias > 0) __syncthreads();  // nothing is counted in a word before its bias is known
-    for (int x0 = 0; x0 < len; x0 += kAhead * kThreads) {
+    if (!one_warp) __syncthreads();
+    for (int x0 = tid; x0 - lane < len; x0 += kAhead * kThreads) {
       int raw[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int x = x0 + tid + k * kThreads;
-        raw[k] = x0 == 0 ? early[k] : x < len ? __ldg(hist + x) : -1;
+        const int x = x0 + k * kThreads;
+        raw[k] = x0 == tid ? early[k] : x < len ? __ldg(hist + x) : -1;
       }
+      bool fresh[kAhead];
+      uint32_t entry[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int x = x0 + tid + k * kThreads, t = x < len ? token(raw[k]) : -1;
+        const int x = x0 + k * kThreads, t = x < len ? token(raw[k]) : -1;
         fresh[k] = false;
+        entry[k] = 0;
         if (t >= 0) {
           entry[k] = tab.take(t);
           uint32_t* w = tab.word + entry[k];
@@ -414,10 +419,12 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
         __syncthreads();
         if (masked) {
           uint4* x4 = reinterpret_cast<uint4*>(x);
-#pragma unroll 4
-          for (int at = tid; at < vecs; at += kThreads) {
-            const uint32_t bits = mask[at * kN / 32] >> (at * kN % 32) & ((1u << kN) - 1);
-            if (bits != (1u << kN) - 1) x4[at] = ruled_out<E>(x4[at], bits);
+          const uint32_t* words = mask + tid * kN / 32;
+          const int shift = tid * kN % 32;
+#pragma unroll
+          for (int y = 0; y < kVecs; ++y) {
+            const int at = tid + y * kThreads;
+            if (at < vecs) x4[at] = ruled_out<E>(x4[at], words[y * (kThreads * kN / 32)] >> shift);
           }
         }
         if (last) {  // the padding, the rest of the last vector first
