@@ -410,8 +410,16 @@ struct TreeSimtSmem {
   float p[8 * R][kPPad];
 };
 
+// CTAs an SM: three as far as registers and shared memory go (320 pairs, 500-2000
+// cached, two / three an SM: 12 nodes of 32 dimensions 81 / 60 us, of 64 133 / 96, 31
+// of 32 102 / 85).
 template <int HS, int R>
-__global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeArgs a) {
+constexpr int simt_ctas() {
+  return (HS <= 32 && R <= 4) || R <= 2 ? 3 : 2;
+}
+
+template <int HS, int R>
+__global__ void __launch_bounds__(kThreads, simt_ctas<HS, R>()) tree_simt_kernel(TreeArgs a) {
   extern __shared__ __align__(128) uint8_t shared_raw[];
   auto& sm = *reinterpret_cast<TreeSimtSmem<HS, R>*>(shared_raw);
   constexpr int kD = HS / 16, kChunks = HS / 4;
@@ -641,8 +649,8 @@ template <int HS, int R>
 int simt_typed(const TreeArgs& a, int* grid, cudaStream_t s) {
   static bool allowed[kMaxDevices] = {};
   constexpr int kSmem = sizeof(TreeSimtSmem<HS, R>);
-  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
-  const int ctas = ctas_of(a.N, 2);
+  static_assert(simt_ctas<HS, R>() * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+  const int ctas = ctas_of(a.N, simt_ctas<HS, R>());
   cudaError_t e = allow_smem(allowed, tree_simt_kernel<HS, R>, kSmem);
   if (e == cudaSuccess) e = launch_pdl(tree_simt_kernel<HS, R>, dim3(ctas), dim3(kThreads), kSmem, s, a);
   *grid = ctas;
@@ -656,8 +664,13 @@ int f32(const TreeArgs& a, int* grid, cudaStream_t s) {
   // 16.0; 192: 13.2 / 13.0, 15.0 / 19.4.)
   const bool pairs = static_cast<long long>(a.B) * a.NH <= 152 && a.rows.capacity <= 384;
   if (a.N <= 8) return pairs ? f32_typed<HS, 4>(a, grid, s) : f32_typed<HS, 0>(a, grid, s);
+  // rows in steps of eight, as their products are what takes the time (48 pairs of 32
+  // dimensions, 500-2000 cached, 23 nodes in 24 rows / 32: 19.3 / 20.9 us, 40 in 48 / 64
+  // 25 / 31)
   if (a.N <= 16) return simt_typed<HS, 2>(a, grid, s);
+  if (a.N <= 24) return simt_typed<HS, 3>(a, grid, s);
   if (a.N <= 32) return simt_typed<HS, 4>(a, grid, s);
+  if (a.N <= 48) return simt_typed<HS, 6>(a, grid, s);
   return simt_typed<HS, 8>(a, grid, s);
 }
 
