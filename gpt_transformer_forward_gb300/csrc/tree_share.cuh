@@ -178,6 +178,7 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
 // A barrier of a group's threads that also ORs a predicate over them.
 template <int WM>
 __device__ __forceinline__ bool group_or(int group, bool pred) {
+  __syncwarp();
   if constexpr (WM == 1)
     return __any_sync(0xffffffffu, pred);
   else

@@ -70,18 +70,27 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_tree_kernel(AcceptArgs 
   if (threadIdx.x < 32) {
     const size_t row = static_cast<size_t>(b) * a.N;
     const int pos = __ldg(a.pos + b);
-    const bool ok = pos >= 0 && pos < a.rows.capacity, report = blockIdx.x == 0;
-    if (!ok && pos != -1 && report && lane == 0) set_error(GPT2_DEVERR_POSITION);
     int p[2], tok[2] = {0, 0}, chosen[2] = {0, 0};
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int i = lane + 32 * u;
-      p[u] = ok ? tree_parent(a.parent != nullptr ? a.parent + row : nullptr, i, a.N) : -2;
+      p[u] = tree_parent(a.parent != nullptr ? a.parent + row : nullptr, i, a.N);
       if (i < a.N) {
         tok[u] = __ldg(a.tok + row + i);
         chosen[u] = __ldg(a.next + row + i);
       }
       first[i] = kMaxNodes;
+    }
+    const bool ok = pos >= 0 && pos < a.rows.capacity, report = blockIdx.x == 0;
+    if (!ok && pos != -1 && report && lane == 0) set_error(GPT2_DEVERR_POSITION);
+    // the blocks of the nodes' places, before it is known which of them are needed
+    int blk[2] = {-1, -1};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int i = lane + 32 * u;
+      if (!ok) p[u] = -2;
+      if (a.pool != nullptr && ok && i < a.N && i < a.rows.capacity - pos)
+        blk[u] = __ldg(a.rows.table + static_cast<size_t>(b) * a.rows.max_blocks + ((pos + i) >> a.rows.lbs));
     }
     const TreeSets ts = tree_sets(p, a.N, ok ? min(a.N, a.rows.capacity - pos) : 0, report);
     __syncwarp();
@@ -134,17 +143,18 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_tree_kernel(AcceptArgs 
       }
     }
     if (a.pool != nullptr) {  // the rows that have to move
-      const int* table = a.rows.table + static_cast<size_t>(b) * a.rows.max_blocks;
       const int bs1 = (1 << a.rows.lbs) - 1;
       int moves = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int k = lane + 32 * u;
-        bool move = k < n && path[k] != k;
+        const int node = k < n ? path[k] : 0, db = blk[u];
+        const int b0 = __shfl_sync(0xffffffffu, blk[0], node & 31), b1 = __shfl_sync(0xffffffffu, blk[1], node & 31);
+        const int sb = node < 32 ? b0 : b1;
+        bool move = k < n && node != k;
         long long src = 0, dst = 0;
         if (move) {
-          const int sp = pos + path[k], dp = pos + k;
-          const int sb = __ldg(table + (sp >> a.rows.lbs)), db = __ldg(table + (dp >> a.rows.lbs));
+          const int sp = pos + node, dp = pos + k;
           if (sb < 0 || sb >= a.rows.num_blocks || db < 0 || db >= a.rows.num_blocks) {
             if (report) set_error(GPT2_DEVERR_BLOCK);
             move = false;
