@@ -164,10 +164,9 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
   const GPT2LogitRules& r = a.r;
   auto src = [&](int i) { return static_cast<const E*>(a.logits) + (row0 + i) * a.Vp + v0; };
   auto dst = [&](int i) { return static_cast<E*>(a.out) + (row0 + i) * a.Vp + v0; };
-  auto load = [&](int i) {  // one thread; rows of missing nodes are read for nothing at the start
-    uint64_t* bar = full + (i - n0) % a.stages;
-    mbar_arrive_expect_tx(bar, columns * sizeof(E));
-    bulk_load(shared_raw + (i - n0) % a.stages * stage_bytes, src(i), columns * sizeof(E), bar);
+  auto load = [&](int i, int stage) {  // one thread; rows of missing nodes are read for nothing at the start
+    mbar_arrive_expect_tx(full + stage, columns * sizeof(E));
+    bulk_load(shared_raw + stage * stage_bytes, src(i), columns * sizeof(E), full + stage);
   };
   pdl_wait();
   pdl_trigger();
@@ -218,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
   if (!kInPlace && tid == 0) {
     for (int s = 0; s < a.stages; ++s) mbar_init(full + s, 1);
     fence_barrier_init();
-    for (int i = n0; i < min(n1, n0 + a.stages); ++i) load(i);
+    for (int i = n0; i < min(n1, n0 + a.stages); ++i) load(i, i - n0);
   }
   // the mask words of the segment that this thread holds for the next row
   constexpr int kMaskWords = kSegWords / kThreads;
@@ -366,8 +365,7 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
   const uint4 lowest = ruled_out<E>(make_uint4(0u, 0u, 0u, 0u), 0u);
   uint32_t phases = 0, pending = kInPlace ? 0 : (1u << min(a.stages, n1 - n0)) - 1;  // a bit a stage
   bool alive = true;  // every copy came
-  for (int i = n0; i < n1; ++i) {
-    const int stage = (i - n0) % a.stages;
+  for (int i = n0, stage = 0; i < n1; ++i, stage = stage + 1 < a.stages ? stage + 1 : 0) {
     const unsigned long long set = sets[i];
     const int g = mask_rows[i];
     const bool none = g < -1 || g >= r.num_masks;  // a bad mask row: everything is ruled out
@@ -419,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
         __syncthreads();
         if (masked) {
           uint4* x4 = reinterpret_cast<uint4*>(x);
-          const uint32_t* words = mask + tid * kN / 32;
-          const int shift = tid * kN % 32;
+          const uint32_t* words = mask + tid / (32 / kN);
+          const int shift = (tid & (32 / kN - 1)) * kN;
 #pragma unroll
           for (int y = 0; y < kVecs; ++y) {
             const int at = tid + y * kThreads;
@@ -446,13 +444,14 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
       alive = __syncthreads_and(there) && alive;
       const int next = i + a.stages - 1;
       const bool more = alive && i > n0 && next < n1 && sets[next] != 0;
-      if (more) pending |= 1u << (next - n0) % a.stages;
+      const int before = stage > 0 ? stage - 1 : a.stages - 1;
+      if (more) pending |= 1u << before;
       if (tid == 0) {
         if (alive && set != 0) bulk_store(dst(i), shared_raw + stage * stage_bytes, columns * sizeof(E));
         bulk_commit_group();
         if (more) {  // into the stage of the row before, once that is read out
           bulk_wait_group_read<1>();
-          load(next);
+          load(next, before);
         }
       }
     } else if (masked) {
