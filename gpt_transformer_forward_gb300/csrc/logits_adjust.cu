@@ -20,9 +20,8 @@ namespace gpt2 {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kSegBytes = 16384;  // of a segment, at most
+constexpr int kSegBytes = 32768;  // of a segment, at most
 constexpr int kStages = 3;        // rows in flight
-constexpr int kVecs = kSegBytes / 16 / kThreads;  // vectors of a segment for a thread, at most
 constexpr int kSegWords = kSegBytes / 2 / 32;     // mask words of a segment, at most
 constexpr uint32_t kPrompt = 1u << 21, kCountMask = kPrompt - 1;
 constexpr int kBiasShift = 22;
@@ -419,11 +418,9 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
           uint4* x4 = reinterpret_cast<uint4*>(x);
           const uint32_t* words = mask + tid / (32 / kN);
           const int shift = (tid & (32 / kN - 1)) * kN;
-#pragma unroll
-          for (int y = 0; y < kVecs; ++y) {
-            const int at = tid + y * kThreads;
-            if (at < vecs) x4[at] = ruled_out<E>(x4[at], words[y * (kThreads * kN / 32)] >> shift);
-          }
+#pragma unroll 4
+          for (int at = tid; at < vecs; at += kThreads, words += kThreads * kN / 32)
+            x4[at] = ruled_out<E>(x4[at], *words >> shift);
         }
         if (last) {  // the padding, the rest of the last vector first
           __syncthreads();
@@ -488,14 +485,19 @@ int adjust_typed(AdjustArgs a, cudaStream_t s) {
   // segments and groups of rows as large as still leave some CTAs to each SM, and
   // no more than 16 rows, which makes the last CTAs end together (64 sequences of
   // 64 nodes, 50257 fp32: 64 rows 317 us, 32 293, 16 284, 8 311).  A CTA of many
-  // rows does better with half a segment, as more of them share an SM, and one of
-  // few rows not, as each has its table to make (50257 tokens; us with 16 and 8 KB:
-  // 512 sequences of 1 node fp32 40 and 59, 256 of 2 fp32 38 and 43, 256 of 4 bf16
-  // 39.1 and 40.6, 128 of 4 fp32 33.1 and 32.1, 128 of 8 bf16 44.1 and 41.9, 128 of
-  // 8 fp32 72 and 67, 64 of 64 fp32 257 and 244).
+  // rows does better with smaller segments, as more of them share an SM, and one of
+  // few rows with larger ones, as each has its table to make (50257 tokens; us with 16
+  // and 8 KB: 512 sequences of 1 node fp32 40 and 59, 256 of 2 fp32 38 and 43, 256 of
+  // 4 bf16 39.1 and 40.6, 128 of 4 fp32 33.1 and 32.1, 128 of 8 bf16 44.1 and 41.9,
+  // 128 of 8 fp32 72 and 67, 64 of 64 fp32 257 and 244; with 16 and 32 KB, histories
+  // and biases of 500 / 1000 / 2000: 512 sequences of 1 node bf16 23.6 and 24.3 / 30.9
+  // and 29.6 / 45.7 and 47.3, fp32 38.6 and 35.4 / 47.9 and 45.8 / 66.1 and 63.8, 256 of
+  // 1 bf16 - / 19.0 and 16.6 / -, 2048 of 1 bf16 - / 122 and 97 / -, 128 of 4 fp32 32.2
+  // and 31.1 / 36.4 and 52.4 / 44.2 and 61.2).
   const long long want = 4LL * num_sms();
   a.nodes = std::min(a.N, 16);
-  a.seg = (a.N >= 8 ? kSegBytes / 2 : kSegBytes) / static_cast<int>(sizeof(E));
+  const bool long_lists = a.r.history_stride + a.r.num_bias > 512;
+  a.seg = (a.N >= 8 ? kSegBytes / 4 : a.N == 1 && long_lists ? kSegBytes : kSegBytes / 2) / static_cast<int>(sizeof(E));
   auto segments = [&]() { return static_cast<long long>((a.V + a.seg - 1) / a.seg) * a.B; };
   while (a.seg > 1024 && segments() < want) a.seg /= 2;
   while (a.nodes > 1 && segments() * ((a.N + a.nodes - 1) / a.nodes) < want) a.nodes = (a.nodes + 1) / 2;
