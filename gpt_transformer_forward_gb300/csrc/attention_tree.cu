@@ -21,8 +21,9 @@
 //
 // Measured (captured): 16 sequences of 16 nodes, 16 heads of 64, cache 4000-16000,
 // bf16 (653 MB, floor 97 us): 108 us, 6.1 TB/s.  32 of 16, 12 heads, 240-960, fp16
-// (64 MB, floor 9.4): 16.0 us, of which about 4 us are the launch and the first
-// loads' chain (positions, table, keys).  16 of 64, 16 heads, 4096-16384, bf16 (684
+// (64 MB, floor 9.4): 15.9 us, of which about 4 us are the launch and the first
+// loads' chain (positions, table, keys); the longest pair's steps are most of the
+// rest (pairs in the order of their lengths, there and back over the SMs, took 17.2).  16 of 64, 16 heads, 4096-16384, bf16 (684
 // MB, floor 101): 150 us on tcgen05, 233 on mma.sync.
 #include "tree_share.cuh"
 

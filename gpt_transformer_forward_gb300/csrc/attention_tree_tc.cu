@@ -26,6 +26,12 @@
 //               to the rows that see them.
 // Every wait is bounded; after a timeout the CTA drains its copies and MMAs, frees
 // TMEM and returns.
+//
+// Measured: 16 sequences of 64 nodes, 16 heads, cache 4096-16384, bf16 (684 MB, floor
+// 101 us) 150 us, 4.6 TB/s; on mma.sync 233.  A step takes some 2080 cycles where its
+// 32 KB take 1400: P V's issue is 810 of them (twice 8 products, for P's two values)
+// and the S products, which wait for a slot, come between.  With one loading warp for
+// keys and values it was 188 us, with as many stages as before the rings 161.
 #include "tree_share.cuh"
 
 namespace gpt2 {
