@@ -66,10 +66,12 @@ __global__ void __launch_bounds__(32 * tree_warps(WM, kGroups), tree_ctas(WM, kG
   pdl_wait();  // the QKV projection ahead has finished
   pdl_trigger();
   Share sh;
-  if constexpr (kPairs)
+  if constexpr (kPairs) {
     sh = pair_share<K, WK>(a, group);
-  else
+  } else {
     sh = share_of<K>(a);
+    zero_absent<T16>(a);
+  }
   int4 open = make_int4(-1, 0, 0, 0);
   group_or<WM>(group, false);  // the barriers
 
@@ -242,9 +244,8 @@ __global__ void __launch_bounds__(32 * tree_warps(WM, kGroups), tree_ctas(WM, kG
       const int* row = a.parent != nullptr ? a.parent + static_cast<size_t>(at.b) * a.N : nullptr;
       int par[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) par[u] = at.seq.live > 0 ? tree_parent(row, lane + 32 * u, a.N) : -2;
+      for (int u = 0; u < 2; ++u) par[u] = tree_parent(row, lane + 32 * u, a.N);
       const bool report = at.h == 0 && warp == 0;
-      if (report && lane == 0) seq_of(a, at.b, true);
       const TreeSets ts = tree_sets(par, a.N, at.seq.live, report);
       set[0] = tree_set_of(ts, warp * 16 + g);
       set[1] = tree_set_of(ts, warp * 16 + g + 8);

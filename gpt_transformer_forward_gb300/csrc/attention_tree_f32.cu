@@ -80,10 +80,13 @@ __global__ void __launch_bounds__(32 * f32_warps(kGroups), f32_ctas<HS, kGroups>
   pdl_wait();  // the QKV projection ahead has finished
   pdl_trigger();
   Share sh;
-  if constexpr (kPairs)
+  if constexpr (kPairs) {
     sh = pair_share<K, WK>(a, group);
-  else
+    if (lane < R) sets[lane] = 0;  // of a sequence without a tree
+  } else {
     sh = share_of<K>(a);
+    zero_absent<float>(a);
+  }
   int4 open = make_int4(-1, 0, 0, 0);
   __syncwarp();  // the barriers
 
@@ -266,9 +269,8 @@ __global__ void __launch_bounds__(32 * f32_warps(kGroups), f32_ctas<HS, kGroups>
       const int* row = a.parent != nullptr ? a.parent + static_cast<size_t>(at.b) * a.N : nullptr;
       int par[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) par[u] = at.seq.live > 0 ? tree_parent(row, lane + 32 * u, a.N) : -2;
+      for (int u = 0; u < 2; ++u) par[u] = tree_parent(row, lane + 32 * u, a.N);
       const bool report = at.h == 0;
-      if (report && lane == 0) seq_of(a, at.b, true);
       const TreeSets ts = tree_sets(par, a.N, at.seq.live, report);
       const unsigned long long mine = tree_set_of(ts, lane & (R - 1)), live = tree_live(ts);
       if (lane < R) sets[lane] = mine;
@@ -433,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas<HS, R>()) tree_simt_kernel
   pdl_trigger();
   constexpr int K = kSimtKeys;
   const Share sh = share_of<K>(a);
+  zero_absent<float>(a);
   int4 open = make_int4(-1, 0, 0, 0);
 
   Place ld = sh.at;
@@ -477,7 +480,6 @@ __global__ void __launch_bounds__(kThreads, simt_ctas<HS, R>()) tree_simt_kernel
     copy(buf ^ 1);
     if (i == sh.begin || at.t == 0) {
       from_start = at.t == 0;
-      if (from_start && at.h == 0 && threadIdx.x == 0) seq_of(a, at.b, true);
       for (int x = threadIdx.x; x < 8 * R * kChunks; x += kThreads) {
         const int r = x / kChunks, c = x % kChunks * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, simt_ctas<HS, R>()) tree_simt_kernel
       const int* row = a.parent != nullptr ? a.parent + static_cast<size_t>(at.b) * a.N : nullptr;
       int par[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) par[u] = at.seq.live > 0 ? tree_parent(row, lane + 32 * u, a.N) : -2;
+      for (int u = 0; u < 2; ++u) par[u] = tree_parent(row, lane + 32 * u, a.N);
       ts = tree_sets(par, a.N, at.seq.live, at.h == 0 && warp == 0);
       const unsigned long long live = tree_live(ts);
       bool bad = false;

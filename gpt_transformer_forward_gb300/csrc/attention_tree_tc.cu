@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   pdl_wait();  // the QKV projection ahead has finished
   pdl_trigger();
   const Share sh = share_of<kTK>(a);
+  zero_absent<T16>(a);
   Parts part(a, sh);
 
   if (warp == 0 || warp == kVWarp) {
@@ -330,9 +331,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int* parents = a.parent != nullptr ? a.parent + static_cast<size_t>(p.b) * a.N : nullptr;
           int par[2];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) par[u] = p.seq.live > 0 ? tree_parent(parents, lane + 32 * u, a.N) : -2;
+          for (int u = 0; u < 2; ++u) par[u] = tree_parent(parents, lane + 32 * u, a.N);
           const bool report = p.h == 0 && tg < 32;
-          if (report && lane == 0) seq_of(a, p.b, true);
           const TreeSets ts = tree_sets(par, a.N, p.seq.live, report);
           const unsigned long long mine = tree_set_of(ts, row), live = tree_live(ts);
           bits = half == 0 ? mine : 0;

@@ -30,7 +30,8 @@ struct TreeArgs {
 };
 
 // A sequence's cached positions and the nodes that have a place behind them;
-// none of either where it has no tree in this step.
+// none of either where it has no tree in this step (a position that is not -1 is
+// reported).
 struct Seq {
   int pos, live;
 };
@@ -40,10 +41,10 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs& a, int b, bool report) {
   if (!ok && p != -1 && report) set_error(GPT2_DEVERR_POSITION);
   return {ok ? p : 0, ok ? min(a.N, a.rows.capacity - p) : 0};
 }
-// Steps of a pair with tiles of K cached keys.
+// Steps of a pair with tiles of K cached keys; none without a tree.
 template <int K>
 __device__ __forceinline__ int steps_of(const Seq& q) {
-  return 1 + (q.pos + K - 1) / K;
+  return q.live == 0 ? 0 : 1 + (q.pos + K - 1) / K;
 }
 
 // A place in the row of all pairs' steps: step t of a pair, 0 the nodes' own keys,
@@ -64,7 +65,10 @@ __device__ __forceinline__ void advance(const TreeArgs& a, Place& p) {
   p.t = 0;
   if (++p.h < a.NH) return;
   p.h = 0;
-  if (++p.b < a.B) enter<K>(a, p);
+  while (++p.b < a.B) {
+    enter<K>(a, p);
+    if (p.steps > 0) break;
+  }
 }
 
 // This CTA's share [begin, end) of the steps and where it begins (the whole warp
@@ -123,6 +127,23 @@ __device__ __forceinline__ size_t cache_row(const TreeArgs& a, int blk, int h, i
 // begins in a share and goes on in the next.
 __device__ __forceinline__ bool split_by_pair(const TreeArgs& a) {
   return static_cast<long long>(a.B) * a.NH <= gridDim.x;
+}
+
+// The rows of the sequences that have no tree, and so no step in a share, are this
+// CTA's where their number meets its own.  (As steps of their own, one a head, they
+// made the share that held them the last by far: 16 sequences of 64 nodes, 16 heads,
+// 4096-16384, one of them without a tree, 146 us for it and 105 for the others.)
+template <typename E>
+__device__ __forceinline__ void zero_absent(const TreeArgs& a) {
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    if (seq_of(a, b, threadIdx.x == 0).live > 0) continue;
+    const size_t vecs = static_cast<size_t>(a.N) * a.C * sizeof(E) / 16;
+    uint4* row = static_cast<uint4*>(a.out) + b * vecs;
+    for (size_t x = threadIdx.x; x < vecs; x += blockDim.x) row[x] = make_uint4(0u, 0u, 0u, 0u);
+    if (split_by_pair(a))
+      for (int h = threadIdx.x; h < a.NH; h += blockDim.x)
+        a.part.split[static_cast<size_t>(b) * a.NH + h] = make_int4(-1, 0, 0, 0);
+  }
 }
 
 // A pair's part in this share, at the end of it.
@@ -191,7 +212,8 @@ template <int K, int WK>
 __device__ __forceinline__ Share pair_share(const TreeArgs& a, int group) {
   Share s;
   s.at = Place{static_cast<int>(blockIdx.x / a.NH), static_cast<int>(blockIdx.x % a.NH), group, 0, {0, 0}};
-  enter<K>(a, s.at);
+  s.at.seq = seq_of(a, s.at.b, s.at.h == 0 && threadIdx.x == 0);
+  s.at.steps = steps_of<K>(s.at.seq);
   s.begin = 0;
   s.end = group < s.at.steps ? (s.at.steps - group + WK - 1) / WK : 0;
   s.per = s.end;
