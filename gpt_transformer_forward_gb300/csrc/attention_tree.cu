@@ -24,7 +24,8 @@
 // (64 MB, floor 9.4): 15.9 us, of which about 4 us are the launch and the first
 // loads' chain (positions, table, keys); the longest pair's steps are most of the
 // rest (pairs in the order of their lengths, there and back over the SMs, took 17.2).  16 of 64, 16 heads, 4096-16384, bf16 (684
-// MB, floor 101): 150 us on tcgen05, 233 on mma.sync.
+// MB, floor 101): 120 us on tcgen05; on mma.sync, before sequences without a tree left
+// the shares, 233 where tcgen05 took 161.
 #include "tree_share.cuh"
 
 #include <algorithm>

@@ -28,10 +28,10 @@
 // TMEM and returns.
 //
 // Measured: 16 sequences of 64 nodes, 16 heads, cache 4096-16384, bf16 (684 MB, floor
-// 101 us) 150 us, 4.6 TB/s; on mma.sync 233.  A step takes some 2080 cycles where its
-// 32 KB take 1400: P V's issue is 810 of them (twice 8 products, for P's two values)
-// and the S products, which wait for a slot, come between.  With one loading warp for
-// keys and values it was 188 us, with as many stages as before the rings 161.
+// 101 us) 120 us, 5.7 TB/s.  A step takes some 1600 cycles where its 32 KB take 1400
+// at the rate of a copy; a further pair in a share some 10000, as the groups' outputs
+// have to be joined before the next ones are added up.  With one loading warp for keys
+// and values the kernel took 1.25 times as long.
 #include "tree_share.cuh"
 
 namespace gpt2 {
@@ -43,6 +43,12 @@ constexpr int kRows = 128;  // TMEM lanes: the queries, twice
 constexpr int kTK = 128;    // keys of a step
 constexpr int kHS = 64;
 constexpr int kTileBytes = 128 * kHS * 2;  // 128 rows of 128 bytes
+// What a pair's begin and end take beside its steps, in steps (the nodes' step, the
+// wait for the last products, the join of its results): 16 sequences of 64 nodes, 16
+// heads, 4096-16384 cached, counted as 0 / 3 / 6 / 10: 127.7 / 122.5 / 119.9 / 122.7
+// us; 16, 12 heads, 240-960: 26.2 / 22.4 / 22.3 / 21.7; one, 16 heads, 16000: 21.8 /
+// 19.2 / 18.7 / 18.9.
+constexpr int kPairCost = 6;
 constexpr int kRing = 3;    // S accumulators (and P) in TMEM
 constexpr int kK = 4;       // K stages
 constexpr int kV = 5;       // V stages
@@ -95,6 +101,7 @@ struct Parts {
     s += n;
     ++f;
     p.t += n - 1;
+    if (p.t + 1 == p.steps) i += kPairCost;
     advance<kTK>(a, p);
     count();
   }
@@ -167,7 +174,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();  // the QKV projection ahead has finished
   pdl_trigger();
-  const Share sh = share_of<kTK>(a);
+  const Share sh = share_of<kTK, kPairCost>(a);
   zero_absent<T16>(a);
   Parts part(a, sh);
 
@@ -316,6 +323,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint32_t s_par = 0;  // bit r: parity of this group's next phase of s_full[x][r]
     uint32_t final_par = 0;
     int4 open = make_int4(-1, 0, 0, 0);
+    // What a pair's first step needs from memory is loaded before the part ahead of it
+    // is joined: the nodes' parents and the blocks of the rows that this thread stores.
+    constexpr int kStores = kMaxNodes * 8 / (32 * kSoftmaxWarps);
+    int par[2], blks[kStores];
+    auto fetch = [&](const Parts& of) {
+      if (!of.more() || of.p.t > 0) return;
+      const int* parents = a.parent != nullptr ? a.parent + static_cast<size_t>(of.p.b) * a.N : nullptr;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) par[u] = tree_parent(parents, lane + 32 * u, a.N);
+      const int* table = a.rows.table + static_cast<size_t>(of.p.b) * a.rows.max_blocks;
+#pragma unroll
+      for (int u = 0; u < kStores; ++u) {
+        const int node = (tg >> 3) + u * (4 * kSoftmaxWarps);
+        blks[u] = node < of.p.seq.live ? __ldg(table + ((of.p.seq.pos + node) >> a.rows.lbs)) : -1;
+      }
+    };
+    fetch(part);
     for (; part.more(); part.next()) {
       const Place& p = part.p;
       unsigned long long* sets = reinterpret_cast<unsigned long long*>(smem + L::sets) + (part.f & 1) * kMaxNodes;
@@ -328,10 +352,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         unsigned long long bits;  // the keys of this row's half that it sees
         int valid = kTK;          // keys of the step
         if (t == 0) {
-          const int* parents = a.parent != nullptr ? a.parent + static_cast<size_t>(p.b) * a.N : nullptr;
-          int par[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) par[u] = tree_parent(parents, lane + 32 * u, a.N);
           const bool report = p.h == 0 && tg < 32;
           const TreeSets ts = tree_sets(par, a.N, p.seq.live, report);
           const unsigned long long mine = tree_set_of(ts, row), live = tree_live(ts);
@@ -342,8 +362,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint8_t* kd = smem + L::k + (s % kK) * kTileBytes;
           uint8_t* vd = smem + L::v + (s % kV) * kTileBytes;
           bool bad = false;
-          for (int c0 = tg; ok && c0 < kMaxNodes * 8; c0 += 32 * kSoftmaxWarps) {
-            const int node = c0 >> 3, c = c0 & 7;
+#pragma unroll
+          for (int u = 0; u < kStores; ++u) {
+            if (!ok) break;
+            const int node = (tg >> 3) + u * (4 * kSoftmaxWarps), c = tg & 7;
             uint4* vp = reinterpret_cast<uint4*>(vd + tile_at<kHS>(node, c));
             if (node >= a.N) {
               *vp = make_uint4(0u, 0u, 0u, 0u);
@@ -362,8 +384,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               *vp = make_uint4(w[0], w[1], w[2], w[3]);
             }
             if ((live >> node & 1) == 0) continue;
-            const int j = p.seq.pos + node;
-            const int blk = __ldg(a.rows.table + static_cast<size_t>(p.b) * a.rows.max_blocks + (j >> a.rows.lbs));
+            const int j = p.seq.pos + node, blk = blks[u];
             if (blk < 0 || blk >= a.rows.num_blocks) {
               if (p.h == 0) set_error(GPT2_DEVERR_BLOCK);
               continue;
@@ -464,6 +485,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[r]);
+      }
+      {
+        Parts ahead = part;
+        ahead.next();
+        fetch(ahead);
       }
       // the four results of each node join in shared memory
       if (ok && done > 0) {

@@ -72,15 +72,19 @@ __device__ __forceinline__ void advance(const TreeArgs& a, Place& p) {
 }
 
 // This CTA's share [begin, end) of the steps and where it begins (the whole warp
-// calls, every warp for itself).  `per`: the steps of a share.
+// calls, every warp for itself).  `per`: the steps of a share.  Where a pair's begin and
+// end cost as much as W steps, W numbers that no step has stand ahead of its steps'.
 struct Share {
   long long begin, end, per;
   Place at;
 };
-template <int K>
+template <int K, int W = 0>
 __device__ __forceinline__ Share share_of(const TreeArgs& a) {
   const int lane = threadIdx.x & 31;
-  auto steps_at = [&](int b) { return b < a.B ? steps_of<K>(seq_of(a, b, false)) : 0; };
+  auto steps_at = [&](int b) {
+    const int steps = b < a.B ? steps_of<K>(seq_of(a, b, false)) : 0;
+    return steps > 0 ? steps + W : 0;
+  };
   long long total = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, steps_at(b0 + lane));
   total *= a.NH;
@@ -107,7 +111,9 @@ __device__ __forceinline__ Share share_of(const TreeArgs& a) {
       const long long rest = s.begin - (before + __shfl_sync(0xffffffffu, incl - mine, l)) * a.NH;
       s.at.b = b0 + l;
       s.at.h = static_cast<int>(rest / steps);
-      s.at.t = static_cast<int>(rest % steps);
+      const int t = static_cast<int>(rest % steps) - W;
+      s.at.t = max(t, 0);
+      s.begin += s.at.t - t;
       enter<K>(a, s.at);
       return s;
     }
