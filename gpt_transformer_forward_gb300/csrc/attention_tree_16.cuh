@@ -20,6 +20,11 @@ struct TreeRing {
   static constexpr int kKeys = WM == 1 ? 32 : 64;   // of a tile
   static constexpr int kRow = HS * 2;               // bytes of a key
   static constexpr int kStrips = 1;                 // a TMA box is at most 128 bytes wide
+  // What a pair's begin and end take in a share beside its steps, in steps; counted as
+  // 0 / 2 / 4: 16 sequences of 16 nodes, 16 heads, 4000-16000 cached 107 / 97 / 98 us, 40
+  // of 16, 12 heads, 1000-4000 60.3 / 55.2 / 55.2, 8 of 32, 16 heads, 4000-16000 61.3 / 59.2
+  // / 59.8.
+  static constexpr int kPairCost = 2;
   static constexpr int kTileBytes = kKeys * kRow;
   static constexpr int kNodeBytes = 16 * WM * kRow;  // of the nodes' queries, keys or values
   static constexpr int kStage = 2 * kTileBytes > 3 * kNodeBytes ? 2 * kTileBytes : 3 * kNodeBytes;
@@ -69,14 +74,14 @@ __global__ void __launch_bounds__(32 * tree_warps(WM, kGroups), tree_ctas(WM, kG
   if constexpr (kPairs) {
     sh = pair_share<K, WK>(a, group);
   } else {
-    sh = share_of<K>(a);
+    sh = share_of<K, Ring::kPairCost>(a);
     zero_absent<T16>(a);
   }
   int4 open = make_int4(-1, 0, 0, 0);
   group_or<WM>(group, false);  // the barriers
 
   Feed<Ring, WM, WK> feed(a, sh, kPairs, map_k, map_v, map_qkv, ring, full);
-  const int lead = feed.lead, n_steps = feed.n_steps;
+  const int lead = feed.lead;
   if (warp == 0) feed.begin();
 
   Place at = sh.at;
@@ -209,7 +214,8 @@ __global__ void __launch_bounds__(32 * tree_warps(WM, kGroups), tree_ctas(WM, kG
     }
   };
   uint32_t stage = 0, phase = 0;
-  for (int n = 0; n < n_steps; ++n) {
+  long long i = sh.begin;  // the step, of all shares'
+  for (int n = 0; n < lead || i < sh.end; ++n) {
     // The stage of the step before is refilled.  A warp with a pair does so before it
     // waits for this step's keys (256 sequences of 8 nodes, 12 heads, 225-900 cached:
     // 76.1 us, behind the wait 78.2; one with a share behind it: 16 of 16, 1000-4000,
@@ -278,7 +284,6 @@ __global__ void __launch_bounds__(32 * tree_warps(WM, kGroups), tree_ctas(WM, kG
       if (valid < K) zero_rows(st + Ring::kTileBytes, valid, K);
       attend(std::integral_constant<int, K / 8>{}, st, st + Ring::kTileBytes, valid < K, seen, false);
     }
-    const long long i = sh.begin + n - lead;
     if (!kPairs && (at.t + 1 == at.steps || i + 1 == sh.end)) {  // the pair's part in this share is done
       const Part part = end_part(a, sh, at, i, from_start, open, threadIdx.x == 0);
 #pragma unroll
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(32 * tree_warps(WM, kGroups), tree_ctas(WM, kG
         }
       }
     }
-    feed.forward(at);
+    feed.forward(at, i);
   }
   if constexpr (!kPairs) {
     if (!split_by_pair(a) && threadIdx.x == 0) a.part.split[blockIdx.x] = open;

@@ -32,6 +32,9 @@ struct RingF32 {
   static constexpr int kNodeBytes = R * kRow;  // of the nodes' queries, keys or values
   static constexpr int kStage = 2 * kTileBytes > 3 * kNodeBytes ? 2 * kTileBytes : 3 * kNodeBytes;
   static constexpr int kStages = HS == 16 ? 3 : 2;
+  // (40 sequences of 5 nodes, 12 heads, 1000-4000 cached, counted as 0 / 2 / 4: 152.0 /
+  // 151.4 / 155.6 us; 6: 25.6 / 24.2 / 24.2)
+  static constexpr int kPairCost = 2;  // of a share, as in attention_tree_16.cuh
   static constexpr int kPRow = kKeys + 4;  // floats of a row of probabilities
   static constexpr int kWarp = R * (HS + kPRow) * 4 + R * 8;  // a warp's queries, probabilities, sets
   // the rings from a multiple of 1024 bytes on, the warps' own, the barriers
@@ -84,14 +87,14 @@ __global__ void __launch_bounds__(32 * f32_warps(kGroups), f32_ctas<HS, kGroups>
     sh = pair_share<K, WK>(a, group);
     if (lane < R) sets[lane] = 0;  // of a sequence without a tree
   } else {
-    sh = share_of<K>(a);
+    sh = share_of<K, Ring::kPairCost>(a);
     zero_absent<float>(a);
   }
   int4 open = make_int4(-1, 0, 0, 0);
   __syncwarp();  // the barriers
 
   Feed<Ring, 1, WK> feed(a, sh, kPairs, map_k, map_v, map_qkv, ring, full);
-  const int lead = feed.lead, n_steps = feed.n_steps;
+  const int lead = feed.lead;
   feed.begin();
 
   Place at = sh.at;
@@ -241,7 +244,8 @@ __global__ void __launch_bounds__(32 * f32_warps(kGroups), f32_ctas<HS, kGroups>
   };
   int stage = 0;
   uint32_t phase = 0;
-  for (int n = 0; n < n_steps; ++n) {
+  long long i = sh.begin;  // the step, of all shares'
+  for (int n = 0; n < lead || i < sh.end; ++n) {
     const bool came = mbar_wait(full + stage, phase);
     // the step's keys are there, and every lane is past the step whose stage is
     // refilled now; a copy that did not come (flagged by the wait) ends the share
@@ -302,7 +306,6 @@ __global__ void __launch_bounds__(32 * f32_warps(kGroups), f32_ctas<HS, kGroups>
       zero_rows(st + Ring::kTileBytes, keys, K, K);
     }
     attend(keys_at, values_at, rows, keys, at.t == 0, odd);
-    const long long i = sh.begin + n - lead;
     if (!kPairs && (at.t + 1 == at.steps || i + 1 == sh.end)) {  // the pair's part in this share is done
       const Part part = end_part(a, sh, at, i, from_start, open, threadIdx.x == 0);
       reduce();
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(32 * f32_warps(kGroups), f32_ctas<HS, kGroups>
         }
       }
     }
-    feed.forward(at);
+    feed.forward(at, i);
   }
   if constexpr (!kPairs) {
     if (!split_by_pair(a) && threadIdx.x == 0) a.part.split[blockIdx.x] = open;

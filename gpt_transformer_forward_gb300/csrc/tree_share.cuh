@@ -241,7 +241,8 @@ struct Feed {
   uint8_t* ring;
   uint64_t* full;
   Place ld;
-  int lead, n_steps, i;  // i: of the next copy, among the share's steps
+  long long at, end;  // the next copy's step and the share's end
+  int lead, i;        // i: the next copy's number, -1 for the queries ahead of the first step
   int ids[kIds];
   int lbox, boxes;  // positions of a box (log2), boxes of a tile
   bool pairs, tiled;
@@ -249,8 +250,9 @@ struct Feed {
   __device__ __forceinline__ Feed(const TreeArgs& args, const Share& sh, bool by_pairs, const CUtensorMap& mk,
                                   const CUtensorMap& mv, const CUtensorMap& mq, uint8_t* r, uint64_t* f)
       : a(args), map_k(mk), map_v(mv), map_qkv(mq), ring(r), full(f), ld(sh.at), pairs(by_pairs) {
-    lead = sh.begin < sh.end && sh.at.t > 0 ? 1 : 0;
-    n_steps = static_cast<int>(sh.end - sh.begin) + lead;  // (2^31 of them would take hours)
+    at = sh.begin;
+    end = sh.end;
+    lead = at < end && sh.at.t > 0 ? 1 : 0;
     i = -lead;
     constexpr int kLog = K == 32 ? 5 : 6;
     lbox = min(kLog, a.rows.lbs);
@@ -259,11 +261,15 @@ struct Feed {
     // boxes (one position of 64 bytes, one or two of 32) are copied by 16 bytes
     tiled = (kStripRow << lbox) >= 128;
   }
-  __device__ __forceinline__ void forward(Place& p) const {  // to the group's next step
-    if (pairs)
+  // to the group's next step, `n` of the steps
+  __device__ __forceinline__ void forward(Place& p, long long& n) const {
+    ++n;
+    if (pairs) {
       p.t += WK;
-    else
+    } else {
+      if (p.t + 1 == p.steps) n += R::kPairCost;
       advance<K>(a, p);
+    }
   }
   __device__ __forceinline__ void lookup() {  // lane l: the blocks of the next tile's boxes l and l + 32
     if (ld.t == 0) return;
@@ -277,12 +283,12 @@ struct Feed {
     }
   }
   __device__ __forceinline__ void begin() {
-    if (n_steps > 0 && lead == 0) lookup();
+    if (at < end && lead == 0) lookup();
 #pragma unroll
     for (int s = 0; s < R::kStages - 1; ++s) copy(s);
   }
   __device__ __forceinline__ void copy(int stage) {
-    if (i + lead >= n_steps) return;
+    if (at >= end) return;
     const int lane = threadIdx.x & 31;
     uint8_t* st = ring + stage * R::kStage;
     uint64_t* bar = full + stage;
@@ -338,9 +344,9 @@ struct Feed {
         }
       }
     }
-    if (i >= 0) forward(ld);
+    if (i >= 0) forward(ld, at);
     ++i;
-    if (i + lead < n_steps) lookup();
+    if (at < end) lookup();
   }
   // after a copy that did not come: the group's others since step n, with the same
   // limit each
