@@ -411,13 +411,13 @@ int mma_typed(const TreeArgs& a, int* ctas, cudaStream_t s) {
 // The warps that take a pair; 0: the pairs are cut into shares.  The lengths are
 // not known here, but the longest that the tables can hold.  16 nodes, 12 heads of
 // 64, bf16, cache up to n; shares / four warps / eight warps, us:
-//   pairs   n 60            500               1000              2000
-//   12      7.7 / 3.8 / 4.1   7.9 /  6.7 /  5.7   8.4 /  8.6 /  7.1  10.2 / 14.7 / 10.5
-//   144     8.7 / 4.1 / 4.5  10.8 /  8.5 /  7.4  13.2 / 12.2 /  9.4  19.7 / 22.2 / 16.1
-//   192     8.9 / 4.3 / 7.9  10.3 /  8.9 / 11.6  15.5 / 13.3 / 14.9  21.1 / 23.7 / 21.5
-//   384                      15.6 / 11.3         20.3 / 17.3         30.3 / 28.7
-//   576                      18.4 / 17.8         25.4 / 25.4         40.0 / 42.5
-// and with n 4000 13.3 / 32.1 / 20.7 for 12 pairs, 30.3 / 43.6 / 36.2 for 192.
+//   pairs   n 60             500                1000               2000
+//   12      7.0 / 3.9 / 4.2   7.7 /  6.4 /  5.7   8.2 /  8.1 /  6.9   9.2 / 13.3 /  9.8
+//   144     8.3 / 4.1 / 4.4   9.9 /  7.9 /  7.0  13.0 / 11.1 /  8.7  18.1 / 19.6 / 14.8
+//   192     8.4 / 4.3 / 7.9   9.8 /  8.5 / 11.3  14.1 / 12.2 / 13.8  19.4 / 21.2 / 19.8
+//   384     9.5 / 4.9 / 11.8 14.5 / 10.6 / 18.2  18.7 / 16.5 / 23.6  28.4 / 26.7 / 32.7
+//   576    10.2 / 8.0 / 15.7 17.5 / 16.6 / 26.3  25.8 / 23.8 / 31.7  38.4 / 40.6 / 45.5
+// and with n 4000 12.9 / 28.5 / 18.7 for 12 pairs, 29.0 / 38.3 / 33.0 for 192.
 int pair_warps(const TreeArgs& a) {
   if (static_cast<long long>(a.B) * a.NH <= 152) return a.rows.capacity <= 2048 ? 8 : 0;
   return a.rows.capacity <= 1536 ? 4 : 0;
