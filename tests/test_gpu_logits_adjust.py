@@ -306,3 +306,29 @@ def test_graph_and_stream():
         torch.cuda.synchronize()
         assert torch.equal(out.cpu(), want[round % 2])
     no_device_error()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_two_calls_at_once(dtype):
+    """On two streams, over the same logits and rules, into outputs of their own."""
+    c = make(dtype, 9, 7, 20000, 700, 30, 5, seed=9, pad=16)
+    want = run(c)
+    x, rules, tok, parent = c["x"].cuda(), rules_of(c), gpu(c["tok"]), gpu(c["parent"])
+    outs = [torch.full_like(x, 7.0) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for out, s in zip(outs, streams):
+            ab.logits_adjust(out, x, ab.element_type(x), rules, tok, parent, 9, 7, 20000, c["Vp"], s)
+    torch.cuda.synchronize()
+    for out in outs:
+        assert torch.equal(out.cpu(), want)
+    no_device_error()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("B,H", [(300, 600), (2, 5000)])
+def test_single_rows_with_long_histories(dtype, B, H):
+    """One token a sequence and as long lists as make segments of the largest size."""
+    check(make(dtype, B, 1, 40000, H, 40, 2, seed=H, pad=3))
+    no_device_error()

@@ -194,6 +194,35 @@ def test_more_pairs_than_shares(precision, B, N, NH, hs, most, spare):
 
 
 @pytest.mark.parametrize("precision", TYPES, ids=IDS)
+@pytest.mark.parametrize("spare", [2, 140])
+@pytest.mark.parametrize("N", [3, 12, 20, 40, 64])
+def test_sequences_without_a_tree(precision, N, spare):
+    """At the ends, between others, most of them, all of them; some at positions
+    that are none."""
+    def take(pos):
+        c = make(precision, N, 3, 64, [min(max(p, -1), 700) for p in pos], 16, trees(len(pos), N, seed=N), seed=N, spare=spare)
+        c["pos"] = torch.tensor(pos, dtype=torch.int32)
+        return check(c)
+    take([-1, 300, -1, -1, 0, 64, -1, 700, -1])
+    take([5, -1, -1, -1, -1, -1, -1, -1, 130])
+    assert not take([-1] * 70).any()
+    no_device_error()
+    out = take([-1, 300, -2, 2**31 - 1, 40, -2**31])
+    assert ab.gpt2_get_error() == ab.DEVERR_POSITION
+    some = (trees(6, N, seed=N) != -2).any(1)  # (a drawn tree may have no node at all)
+    assert [bool(o.any()) for o in out] == [False, some[1], False, False, some[4], False]
+
+
+@pytest.mark.parametrize("precision", TYPES, ids=IDS)
+def test_many_sequences_without_a_tree(precision):
+    """More pairs than shares, most of them without a step."""
+    for N, hs in ((4, 16), (20, 32), (64, 64)):
+        pos = np.where(np.random.default_rng(N).random(400) < 0.7, -1, ragged(400, 90, N))
+        check(make(precision, N, 5, hs, pos, 64, trees(400, N, seed=N), seed=N, spare=40))
+    no_device_error()
+
+
+@pytest.mark.parametrize("precision", TYPES, ids=IDS)
 @pytest.mark.parametrize("bs", [1, 2, 4, 8, 128])
 def test_wide_trees_over_small_blocks(precision, bs):
     check(make(precision, 50, 2, 64, [300, 0, -1, 127, 128, 1], bs, trees(6, 50, seed=bs, roots=True), seed=bs))
