@@ -19,7 +19,8 @@ using namespace tree;
 // come by TMA as in attention_tree_16.cuh, whose shares and groups these are.  (A
 // broadcast takes a wavefront for each four of its 16 bytes: with more rows, in more
 // warps, shared memory is what they wait for: 480 pairs of 64 dimensions, 1000-4000
-// cached, 30 nodes 463 us against 379 of tree_simt_kernel, 5 nodes 166 against 303.)
+// cached, 30 nodes 463 us against 379 of tree_simt_kernel, 5 nodes 166 against 303; 152
+// since shares leave out sequences without a tree and count what a pair costs.)
 constexpr int R = 8;           // rows of a warp
 constexpr float kGrow = 8.0f;  // log2 units by which a score may pass its row's maximum before that is raised
 
