@@ -331,9 +331,10 @@ __global__ void __launch_bounds__(kThreads, 7) logits_adjust_kernel(AdjustArgs a
     for (int x0 = tid; x0 - lane < len; x0 += kAhead * kThreads) {
       int raw[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int x = x0 + k * kThreads;
-        raw[k] = x0 == tid ? early[k] : x < len ? __ldg(hist + x) : -1;
+      for (int k = 0; k < kAhead; ++k) {  // the next ones are on their way meanwhile
+        const int x = x0 + (k + kAhead) * kThreads;
+        raw[k] = early[k];
+        early[k] = x < len ? __ldg(hist + x) : -1;
       }
       bool fresh[kAhead];
       uint32_t entry[kAhead];
