@@ -16,7 +16,8 @@
 // unnormalised output O of each part in the workspace, which tree_join_kernel joins
 // in order.
 //   attention_tree_16.cuh   16-bit caches, mma.sync (a file for each type)
-//   attention_tree_tc.cu    16-bit caches, more than 32 nodes, heads of 64: tcgen05
+//   attention_tree_tc.cu    16-bit caches that can be long, more than 32 nodes, heads
+//                           of 64: tcgen05
 //   attention_tree_f32.cu   fp32 caches, CUDA cores
 //
 // Measured (captured): 16 sequences of 16 nodes, 16 heads of 64, cache 4000-16000,
@@ -112,6 +113,13 @@ int join_heads(const TreeArgs& a, int hs, int ctas, cudaStream_t s) {
   return hs == 16 ? join<E, 16>(a, ctas, s) : hs == 32 ? join<E, 32>(a, ctas, s) : join<E, 64>(a, ctas, s);
 }
 
+// Positions of a table from which on trees of more than 32 nodes, of 64 dimensions,
+// are tcgen05's, whose pairs take long to begin and end; up to there they are a CTA's
+// each on mma.sync.  64 nodes, 12 heads, bf16, cache up to n, tcgen05 / mma.sync, us: 12
+// pairs, n 60 9.0 / 6.4, 250 9.6 / 8.1, 500 10.7 / 10.8, 1000 10.9 / 13.6; 384: 22.9 / 11.0,
+// 25.1 / 17.4, 30.0 / 25.8, 36.0 / 38.9; 1200: 52 / 31, 65 / 43, 76 / 59, 95 / 90.
+constexpr int kLong = 768;
+
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
@@ -144,7 +152,7 @@ int launch_attention_tree(void* out, const void* qkv, void* kcache, void* vcache
   int ctas = 0, rc = 0;
   if (op == kOpTF32)
     rc = launch_f32(a, hs, &ctas, s);
-  else if (hs == 64 && N > 32)
+  else if (hs == 64 && N > 32 && rows.capacity > kLong)
     rc = launch_tc05(a, op, &ctas, s);
   else
     rc = op == kOpF16 ? launch_mma_f16(a, hs, &ctas, s) : launch_mma_bf16(a, hs, &ctas, s);

@@ -436,8 +436,12 @@ int mma_rows(const TreeArgs& a, int* ctas, cudaStream_t s) {
 template <int HS, typename T16>
 int mma(const TreeArgs& a, int* ctas, cudaStream_t s) {
   if (a.N <= 16) return mma_rows<HS, T16, 1>(a, ctas, s);
-  if constexpr (HS < 64) {  // (of 64 dimensions larger trees are attention_tree_tc.cu's)
-    if (a.N > 32) return mma_rows<HS, T16, 4>(a, ctas, s);
+  if (a.N > 32) {
+    if constexpr (HS < 64)
+      return mma_rows<HS, T16, 4>(a, ctas, s);
+    else  // (in tables that can be long they are attention_tree_tc.cu's)
+      return static_cast<long long>(a.B) * a.NH <= 152 ? mma_typed<HS, T16, 4, 2>(a, ctas, s)
+                                                       : mma_typed<HS, T16, 4, 1>(a, ctas, s);
   }
   return mma_rows<HS, T16, 2>(a, ctas, s);
 }

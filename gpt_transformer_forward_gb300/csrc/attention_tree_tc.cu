@@ -1,5 +1,6 @@
 // attention_tree_tc.cu -- attention of trees of more than 32 nodes over 16-bit
-// caches (attention_tree.cu) on the tcgen05 tensor cores, head size 64.
+// caches that can be long (attention_tree.cu) on the tcgen05 tensor cores, head size
+// 64.
 //
 // A step is 128 keys (the nodes' own: 64).  The up to 64 queries stand twice in
 // the 128 rows of the A operand, so S = Q K^T has every score twice: rows 0-63

@@ -185,7 +185,7 @@ def test_short_pairs_in_long_tables(precision, hs, B, N, NH, most, bs):
 @pytest.mark.parametrize("precision", TYPES, ids=IDS)
 @pytest.mark.parametrize("B,N,NH,hs,most,spare", [
     (500, 3, 4, 16, 90, 40), (300, 12, 8, 16, 40, 40), (330, 20, 3, 32, 70, 40), (160, 40, 3, 16, 70, 40),
-    (40, 64, 12, 64, 100, 40), (90, 40, 2, 32, 70, 2), (90, 20, 2, 64, 200, 2),
+    (40, 64, 12, 64, 100, 40), (90, 40, 2, 32, 70, 2), (90, 20, 2, 64, 200, 2), (90, 50, 2, 64, 200, 2),
 ])
 def test_more_pairs_than_shares(precision, B, N, NH, hs, most, spare):
     """Every share holds the ends of several pairs; and as many CTAs as pairs."""
@@ -224,8 +224,10 @@ def test_many_sequences_without_a_tree(precision):
 
 @pytest.mark.parametrize("precision", TYPES, ids=IDS)
 @pytest.mark.parametrize("bs", [1, 2, 4, 8, 128])
-def test_wide_trees_over_small_blocks(precision, bs):
-    check(make(precision, 50, 2, 64, [300, 0, -1, 127, 128, 1], bs, trees(6, 50, seed=bs, roots=True), seed=bs))
+@pytest.mark.parametrize("long", [False, True])
+def test_wide_trees_over_small_blocks(precision, bs, long):
+    spare = 900 // bs - 349 // bs - 1 if long else 2  # tables of 900 positions
+    check(make(precision, 50, 2, 64, [300, 0, -1, 127, 128, 1], bs, trees(6, 50, seed=bs, roots=True), seed=bs, spare=spare))
     no_device_error()
 
 
