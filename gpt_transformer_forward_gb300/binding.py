@@ -123,6 +123,7 @@ _DRAFT_SIGNATURES = {
     "gpt2_decode_step_tree": (_I, [_CFG, _P, _P, _PKV, _P, _P, _P, _I, _I, _P, _P, _P, _Z, _I, _P]),
     "logits_adjust": (_I, [_P, _P, _I, _RULES, _P, _P, _I, _I, _I, _I, _P]),
     "gpt2_accept_tree": (_I, [_P, _P, _P, _P, _P, _CFG, _PKV, _P, _P, _P, _P, _I, _I, _I, _P]),
+    "gpt2_diag_tree_join": (_I, [_P, _I, _I, _I, _I, _I, _I, _P, _Z, _P]),
 }
 
 _handle = None
@@ -469,6 +470,13 @@ def gpt2_accept_tree(path, count, emitted, next_tok, next_pos, cfg, kv, tok, par
         _ptr(path), _ptr(count), _ptr(emitted), _ptr(next_tok), _ptr(next_pos), _cfg(cfg) if cfg is not None else None,
         ctypes.byref(kv) if kv is not None else None, _ptr(tok), _ptr(parent), _ptr(next), _ptr(pos), B, N, precision,
         _stream(stream)))
+
+
+def gpt2_diag_tree_join(out, B, N, C, NH, shares, precision, workspace, ws_bytes, stream=None):
+    """The last launch of an attention_tree over long tables, by itself (see the
+    header)."""
+    _check("gpt2_diag_tree_join", _lib().gpt2_diag_tree_join(
+        _ptr(out), B, N, C, NH, shares, precision, _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def gpt2_forward_profile(cfg, params, packed, tok, B, T, logits, probs, workspace, ws_bytes, precision,

@@ -1096,6 +1096,23 @@ int attention_tree(void* out, const void* qkv, const GPT2PagedKVCache* kvc, cons
   return tree_attention(out, qkv, kc, kc + half * e, precision, B, C, NH, pos, rows, t, as_stream(stream));
 }
 
+int gpt2_diag_tree_join(void* out, int B, int N, int C, int NH, int shares, int precision, void* workspace,
+                        size_t ws_bytes, void* stream) {
+  RETURN_IF(!out || B <= 0 || N <= 0 || C <= 0 || NH <= 0 || !valid_precision(precision), GPT2_ERR_ARG);
+  RETURN_IF(C % NH != 0 || N > kMaxNodes || B > kMaxSharedBatch || NH > kMaxSharedBatch ||
+                static_cast<long long>(B) * NH > 0x7fffffffLL || C > 0x7fffffff / 3,
+            GPT2_ERR_SHAPE);
+  TRY(check_attention_shape(C, NH));
+  RETURN_IF(shares <= 0 || shares > tree_max_shares(N), GPT2_ERR_SHAPE);
+  RETURN_IF(workspace == nullptr || ws_bytes < attention_tree_workspace_size(B, N, C, NH, precision),
+            GPT2_ERR_WORKSPACE);
+  RETURN_IF(!aligned16(out) || !aligned16(workspace), GPT2_ERR_ALIGN);
+  PdlScope pdl(true);
+  TRY(launch_tree_join(out, is16(precision) ? op_of(precision) : kOpTF32, B, N, C, NH, shares,
+                       tree_partial_layout(workspace, N, C / NH), as_stream(stream)));
+  return check_launch();
+}
+
 size_t gpt2_tree_workspace_size(const GPT2Config* cfg, int B, int N, int precision) {
   if (check_config(cfg) != GPT2_OK || N <= 0 || N > kMaxNodes || B <= 0 || B > kMaxSharedBatch) return 0;
   const size_t base = gpt2_workspace_size(cfg, B, N, precision);

@@ -39,16 +39,19 @@ using namespace tree;
 
 // ------------------------------------------------------------------- join
 // The parts of a pair that lies in several shares, weighed by 2^(m - max m), in
-// the order of the shares: HS / 4 threads a node.
+// the order of the shares: HS / 4 threads a node.  A CTA whose copies do not come
+// (GPT2_DEVERR_TIMEOUT) leaves without its entries, so that what stands in their
+// place is whatever the workspace held before: an entry that names no pair, or parts
+// outside the workspace, is passed over.
 template <typename E, int HS>
-__global__ void __launch_bounds__(kThreads) tree_join_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(kThreads) tree_join_kernel(TreeArgs a, int ctas) {
   constexpr int kLanes = HS / 4, kRows = kThreads / kLanes;
   const int node = static_cast<int>(blockIdx.y) * kRows + static_cast<int>(threadIdx.x) / kLanes;
   const int d = threadIdx.x % kLanes * 4;
   pdl_wait();  // the parts
   pdl_trigger();
   const int4 e = a.part.split[blockIdx.x];
-  if (e.x < 0 || node >= a.N) return;
+  if (e.x < 0 || e.x >= a.B * a.NH || e.y < 0 || e.z < e.y || e.z >= ctas || node >= a.N) return;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   bool missing = false;
@@ -104,13 +107,19 @@ int join(const TreeArgs& a, int ctas, cudaStream_t s) {
   constexpr int kRows = kThreads / (HS / 4);
   const unsigned splits = static_cast<unsigned>(std::min<long long>(ctas, static_cast<long long>(a.B) * a.NH));
   const cudaError_t e =
-      launch_pdl(tree_join_kernel<E, HS>, dim3(splits, (a.N + kRows - 1) / kRows), dim3(kThreads), 0, s, a);
+      launch_pdl(tree_join_kernel<E, HS>, dim3(splits, (a.N + kRows - 1) / kRows), dim3(kThreads), 0, s, a, ctas);
   return e == cudaSuccess ? GPT2_OK : note_cuda_error(e);
 }
 
 template <typename E>
 int join_heads(const TreeArgs& a, int hs, int ctas, cudaStream_t s) {
   return hs == 16 ? join<E, 16>(a, ctas, s) : hs == 32 ? join<E, 32>(a, ctas, s) : join<E, 64>(a, ctas, s);
+}
+
+int join_typed(const TreeArgs& a, int op, int ctas, cudaStream_t s) {
+  const int hs = a.C / a.NH;
+  if (op == kOpTF32) return join_heads<float>(a, hs, ctas, s);
+  return op == kOpF16 ? join_heads<__half>(a, hs, ctas, s) : join_heads<__nv_bfloat16>(a, hs, ctas, s);
 }
 
 // Positions of a table from which on trees of more than 32 nodes, of 64 dimensions,
@@ -156,9 +165,19 @@ int launch_attention_tree(void* out, const void* qkv, void* kcache, void* vcache
     rc = launch_tc05(a, op, &ctas, s);
   else
     rc = op == kOpF16 ? launch_mma_f16(a, hs, &ctas, s) : launch_mma_bf16(a, hs, &ctas, s);
-  if (rc != GPT2_OK || ctas == 0) return rc;
-  if (op == kOpTF32) return join_heads<float>(a, hs, ctas, s);
-  return op == kOpF16 ? join_heads<__half>(a, hs, ctas, s) : join_heads<__nv_bfloat16>(a, hs, ctas, s);
+  return rc != GPT2_OK || ctas == 0 ? rc : join_typed(a, op, ctas, s);
 }
+
+int launch_tree_join(void* out, int op, int B, int N, int C, int NH, int ctas, const TreePartials& p, cudaStream_t s) {
+  TreeArgs a{};
+  a.out = out;
+  a.B = B;
+  a.N = N;
+  a.C = C;
+  a.NH = NH;
+  a.part = p;
+  return join_typed(a, op, ctas, s);
+}
+int tree_max_shares(int N) { return max_ctas(N); }
 
 }  // namespace gpt2

@@ -24,6 +24,9 @@ TreePartials tree_partial_layout(void* workspace, int N, int hs);
 int launch_attention_tree(void* out, const void* qkv, void* kcache, void* vcache, int op, const int* pos,
                           const int* parent, int B, int N, int C, int NH, const KVRows& rows, const TreePartials& p,
                           cudaStream_t s);
+// its last launch alone, over parts of `ctas` shares, tree_max_shares(N) at most
+int launch_tree_join(void* out, int op, int B, int N, int C, int NH, int ctas, const TreePartials& p, cudaStream_t s);
+int tree_max_shares(int N);
 
 // tree_step.cu
 // x[b * N + i] = wte[tok] + wpe[pos[b] + depth of node i]; a zero row for a

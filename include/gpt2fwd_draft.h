@@ -193,6 +193,18 @@ GPT2_API int gpt2_accept_tree(int* path, int* count, int* emitted, int* next_tok
                               const GPT2PagedKVCache* kv, const int* tok, const int* parent, const int* next,
                               const int* pos, int B, int N, int precision, void* stream);
 
+/* ---------------------------------------------------------- diagnostics */
+
+/* The launch that ends an attention_tree whose work is cut into shares (long
+ * tables), by itself, so that it can be tested: it joins what the workspace says
+ * is to be joined, from the parts of `shares` CTAs.  An attention whose waits gave
+ * up (GPT2_DEVERR_TIMEOUT_BIT) leaves entries unwritten; whatever they hold, the
+ * launch reads and writes nothing outside the workspace and the B * N rows of out.
+ * GPT2_ERR_SHAPE for shares outside 1 .. the most that N nodes have.  Arguments as
+ * in attention_tree. */
+GPT2_API int gpt2_diag_tree_join(void* out, int B, int N, int C, int NH, int shares, int precision, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
