@@ -179,83 +179,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   zero_absent<T16>(a);
   Parts part(a, sh);
 
-  if (warp == 0 || warp == kVWarp) {
-    // ------------------------------------------------------------ loads
-    // A copy takes its warp some 50 cycles to issue, and blocks of 16 positions
-    // make eight of them a tile: keys and values have a warp each.
-    const bool keys = warp == 0;
-    const int stages = keys ? kK : kV;
-    uint64_t* full = keys ? k_full : v_full;
-    uint64_t* empty = keys ? k_empty : v_empty;
-    uint8_t* ring = smem + (keys ? L::k : L::v);
-    const CUtensorMap* map = keys ? &map_k : &map_v;
-    const int lbox = min(a.rows.lbs, 7), box = 1 << lbox, boxes = kTK >> lbox;  // of a step
-    constexpr int kIds = kTK / 32;
-    int stage = 0, phase = 1;  // of the next fill, and the parity of the phase that frees it
-    bool ok = true;
-    for (; part.more() && ok; part.next()) {
-      const int f = part.f, x = part.p.h * kHS, y = part.p.b * a.N;
-      if (keys) {
-        // (a timeout seen by any lane stops all of them)
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[f & 1], ((f >> 1) & 1) ^ 1)))) break;
-        if (lane == 0) {
-          uint8_t* q = smem + L::q + (f & 1) * kTileBytes;
-          mbar_arrive_expect_tx(&q_full[f & 1], kTileBytes);
-          tma_load_2d(q, &map_qkv, &q_full[f & 1], x, y);
-          tma_load_2d(q + kTileBytes / 2, &map_qkv, &q_full[f & 1], x, y);
-        }
-      }
-      const int* table = a.rows.table + static_cast<size_t>(part.p.b) * a.rows.max_blocks;
-      const int pos = part.p.seq.pos, h = part.p.h;
-      int ids[kIds];
-      auto lookup = [&](int t) {  // lane i: the blocks of step t's boxes i, i + 32, ..
-#pragma unroll
-        for (int u = 0; u < kIds; ++u) {
-          if (32 * u >= boxes) break;
-          const int i = lane + 32 * u, j = (t - 1) * kTK + (i << lbox);
-          ids[u] = t > 0 && i < boxes && j < pos ? __ldg(table + (j >> a.rows.lbs)) : 0;
-        }
-      };
-      lookup(part.p.t);
-      for (int k = 0; k < part.n; ++k) {
-        const int t = part.p.t + k, j0 = (t - 1) * kTK;
-        const int n = min(boxes, (pos - j0 + box - 1) >> lbox);  // boxes that hold a cached position
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(empty + stage, phase)))) break;
-        uint8_t* dst = ring + stage * kTileBytes;
-        uint64_t* bar = full + stage;
-        if (lane == 0) mbar_arrive_expect_tx(bar, t == 0 ? kTileBytes / 2 : n * box * 128);
-        __syncwarp();
-        if (t == 0) {
-          if (lane == 0) tma_load_2d(dst, &map_qkv, bar, (keys ? a.C : 2 * a.C) + x, y);
-        } else {
-#pragma unroll
-          for (int u = 0; u < kIds; ++u) {
-            if (32 * u >= n) break;
-            const int i = lane + 32 * u;
-            int blk = ids[u];
-            if (i < n && (blk < 0 || blk >= a.rows.num_blocks)) {
-              if (h == 0) set_error(GPT2_DEVERR_BLOCK);
-              blk = 0;
-            }
-            if (i < n)
-              tma_load_4d(dst + i * box * 128, map, bar, 0, (j0 + i * box) & ((1 << a.rows.lbs) - 1), h, blk);
-          }
-        }
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1;
-        }
-        if (k + 1 < part.n) lookup(t + 1);
-      }
-    }
-    // the copies issued here land before the CTA may exit: after a timeout the
-    // last ones are waited for again, with the same limit
-    if (!ok && lane == 0) {
-      for (int i = 0; i < stages; ++i) mbar_wait(full + i, 0), mbar_wait(full + i, 1);
-      for (int i = 0; keys && i < 2; ++i) mbar_wait(&q_full[i], 0), mbar_wait(&q_full[i], 1);
-    }
-    __syncwarp();
-  } else if (warp == 1 || warp == kPvWarp) {
+  // (The order of the branches is that of the code: with the loads first the last
+  // waits there took 3 us of tree-long's 120, behind the others none, 117.)
+  if (warp == 1 || warp == kPvWarp) {
     // ------------------------------------------------------------- MMAs
     // the whole warp runs the loop, one lane issues
     bool ok = true;
@@ -310,7 +236,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     tc_commit_warp(drain);
     mbar_wait(drain, 0);
-  } else {
+  } else if (warp >= 2 && warp < kPvWarp) {
     // ---------------------------------------------------------- softmax (warps 2-9)
     const int x = (warp - 2) / kSoftmaxWarps;
     const int tg = ((warp - 2) % kSoftmaxWarps) * 32 + lane;  // of the group's threads
@@ -584,6 +510,89 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     if (!split_by_pair(a) && threadIdx.x == 64) a.part.split[blockIdx.x] = open;
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ loads
+    // A copy takes its warp some 50 cycles to issue, and blocks of 16 positions
+    // make eight of them a tile: keys and values have a warp each.
+    const bool keys = warp == 0;
+    const int stages = keys ? kK : kV;
+    uint64_t* full = keys ? k_full : v_full;
+    uint64_t* empty = keys ? k_empty : v_empty;
+    uint8_t* ring = smem + (keys ? L::k : L::v);
+    const CUtensorMap* map = keys ? &map_k : &map_v;
+    const int lbox = min(a.rows.lbs, 7), box = 1 << lbox, boxes = kTK >> lbox;  // of a step
+    constexpr int kIds = kTK / 32;
+    int stage = 0, phase = 1;  // of the next fill, and the parity of the phase that frees it
+    bool ok = true;
+    for (; part.more() && ok; part.next()) {
+      const int f = part.f, x = part.p.h * kHS, y = part.p.b * a.N;
+      if (keys) {
+        // (a timeout seen by any lane stops all of them)
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[f & 1], ((f >> 1) & 1) ^ 1)))) break;
+        if (lane == 0) {
+          uint8_t* q = smem + L::q + (f & 1) * kTileBytes;
+          mbar_arrive_expect_tx(&q_full[f & 1], kTileBytes);
+          tma_load_2d(q, &map_qkv, &q_full[f & 1], x, y);
+          tma_load_2d(q + kTileBytes / 2, &map_qkv, &q_full[f & 1], x, y);
+        }
+      }
+      const int* table = a.rows.table + static_cast<size_t>(part.p.b) * a.rows.max_blocks;
+      const int pos = part.p.seq.pos, h = part.p.h;
+      int ids[kIds];
+      auto lookup = [&](int t) {  // lane i: the blocks of step t's boxes i, i + 32, ..
+#pragma unroll
+        for (int u = 0; u < kIds; ++u) {
+          if (32 * u >= boxes) break;
+          const int i = lane + 32 * u, j = (t - 1) * kTK + (i << lbox);
+          ids[u] = t > 0 && i < boxes && j < pos ? __ldg(table + (j >> a.rows.lbs)) : 0;
+        }
+      };
+      lookup(part.p.t);
+      for (int k = 0; k < part.n; ++k) {
+        const int t = part.p.t + k, j0 = (t - 1) * kTK;
+        const int n = min(boxes, (pos - j0 + box - 1) >> lbox);  // boxes that hold a cached position
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(empty + stage, phase)))) break;
+        uint8_t* dst = ring + stage * kTileBytes;
+        uint64_t* bar = full + stage;
+        if (lane == 0) mbar_arrive_expect_tx(bar, t == 0 ? kTileBytes / 2 : n * box * 128);
+        __syncwarp();
+        if (t == 0) {
+          if (lane == 0) tma_load_2d(dst, &map_qkv, bar, (keys ? a.C : 2 * a.C) + x, y);
+        } else {
+#pragma unroll
+          for (int u = 0; u < kIds; ++u) {
+            if (32 * u >= n) break;
+            const int i = lane + 32 * u;
+            int blk = ids[u];
+            if (i < n && (blk < 0 || blk >= a.rows.num_blocks)) {
+              if (h == 0) set_error(GPT2_DEVERR_BLOCK);
+              blk = 0;
+            }
+            if (i < n)
+              tma_load_4d(dst + i * box * 128, map, bar, 0, (j0 + i * box) & ((1 << a.rows.lbs) - 1), h, blk);
+          }
+        }
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+        if (k + 1 < part.n) lookup(t + 1);
+      }
+    }
+    // The copies issued here land before the CTA may exit, whichever warp gave up on a
+    // wait.  Of each stage, from the next one on, the phase of its last fill has the
+    // parity that would free it for one more; a barrier that no copy used lets that of
+    // the phase ahead of its first through.
+    for (int i = 0; i < stages; ++i) {
+      mbar_wait(full + stage, phase);
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    // part.f parts had a copy of their queries, in turn into two buffers
+    for (int i = 0; keys && i < 2; ++i) mbar_wait(q_full + i, ((part.f + 1 - i) / 2 - 1) & 1);
     __syncwarp();
   }
 
