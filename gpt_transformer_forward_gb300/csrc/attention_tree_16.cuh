@@ -419,7 +419,7 @@ int mma_typed(const TreeArgs& a, int* ctas, cudaStream_t s) {
 //   576    10.2 / 8.0 / 15.7 17.5 / 16.6 / 26.3  25.8 / 23.8 / 31.7  38.4 / 40.6 / 45.5
 // and with n 4000 12.9 / 28.5 / 18.7 for 12 pairs, 29.0 / 38.3 / 33.0 for 192.
 int pair_warps(const TreeArgs& a) {
-  if (static_cast<long long>(a.B) * a.NH <= 152) return a.rows.capacity <= 2048 ? 8 : 0;
+  if (few_pairs(a)) return a.rows.capacity <= 2048 ? 8 : 0;
   return a.rows.capacity <= 1536 ? 4 : 0;
 }
 
@@ -440,8 +440,7 @@ int mma(const TreeArgs& a, int* ctas, cudaStream_t s) {
     if constexpr (HS < 64)
       return mma_rows<HS, T16, 4>(a, ctas, s);
     else  // (in tables that can be long they are attention_tree_tc.cu's)
-      return static_cast<long long>(a.B) * a.NH <= 152 ? mma_typed<HS, T16, 4, 2>(a, ctas, s)
-                                                       : mma_typed<HS, T16, 4, 1>(a, ctas, s);
+      return few_pairs(a) ? mma_typed<HS, T16, 4, 2>(a, ctas, s) : mma_typed<HS, T16, 4, 1>(a, ctas, s);
   }
   return mma_rows<HS, T16, 2>(a, ctas, s);
 }

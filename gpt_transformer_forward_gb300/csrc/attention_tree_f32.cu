@@ -668,7 +668,7 @@ int f32(const TreeArgs& a, int* grid, cudaStream_t s) {
   // (Five nodes, 12 heads of 64, cache up to n, shares / pairs, us: 12 pairs, n 60
   // 11.4 / 6.7, 250 11.5 / 8.7, 500 12.0 / 13.6; 96: 12.0 / 6.9, 12.0 / 11.5, 13.9 /
   // 16.0; 192: 12.1 / 12.9, 14.0 / 19.3.)
-  const bool pairs = static_cast<long long>(a.B) * a.NH <= 152 && a.rows.capacity <= 384;
+  const bool pairs = few_pairs(a) && a.rows.capacity <= 384;
   if (a.N <= 8) return pairs ? f32_typed<HS, 4>(a, grid, s) : f32_typed<HS, 0>(a, grid, s);
   // rows in steps of eight, as their products are what takes the time (48 pairs of 32
   // dimensions, 500-2000 cached, 23 nodes in 24 rows / 32: 19.3 / 20.9 us, 40 in 48 / 64

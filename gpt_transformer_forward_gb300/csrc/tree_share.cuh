@@ -375,6 +375,9 @@ inline bool tree_maps(CUtensorMap* mk, CUtensorMap* mv, CUtensorMap* mq, const T
          encode_tensor_map(mq, dt, 2, a.qkv, qdims, qstrides, qbox, swizzle);
 }
 
+// Whether pairs of a CTA each are one to an SM at most (of 152 on a GB300).
+inline bool few_pairs(const TreeArgs& a) { return static_cast<long long>(a.B) * a.NH <= num_sms(); }
+
 // attention_tree_f16.cu, _bf16.cu, _f32.cu, _tc.cu: the parts of *ctas shares are to
 // be joined (0: none).
 int launch_mma_f16(const TreeArgs& a, int hs, int* ctas, cudaStream_t s);

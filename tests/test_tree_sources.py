@@ -36,3 +36,13 @@ def test_the_parity_of_a_rings_last_fills(stages):
                 stage, phase = 0, phase ^ 1
         for i in range(2):
             assert ((n + 1 - i) // 2 - 1) & 1 == (len(range(i, n, 2)) - 1) % 2
+
+
+def test_the_rules_for_pairs_go_by_the_devices_sms():
+    """As the grids do: a pair to an SM is as many pairs as the device has SMs.  The
+    one literal is the bound on shares, which the workspace's size goes by."""
+    srcs = {f: t for f, t in _sources().items() if f.startswith(("attention_tree", "tree_share"))}
+    code = {f: re.sub(r"//[^\n]*", "", t) for f, t in srcs.items()}
+    assert {f: len(re.findall(r"\b15[0-9]\b", t)) for f, t in code.items() if re.search(r"\b15[0-9]\b", t)} == {"tree_share.cuh": 1}
+    assert "return 152 * ctas_per_sm(N);" in code["tree_share.cuh"]
+    assert sum(t.count("few_pairs(a)") for t in code.values()) == 3
