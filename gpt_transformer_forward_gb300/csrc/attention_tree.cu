@@ -122,12 +122,26 @@ int join_typed(const TreeArgs& a, int op, int ctas, cudaStream_t s) {
   return op == kOpF16 ? join_heads<__half>(a, hs, ctas, s) : join_heads<__nv_bfloat16>(a, hs, ctas, s);
 }
 
-// Positions of a table from which on trees of more than 32 nodes, of 64 dimensions,
-// are tcgen05's, whose pairs take long to begin and end; up to there they are a CTA's
-// each on mma.sync.  64 nodes, 12 heads, bf16, cache up to n, tcgen05 / mma.sync, us: 12
-// pairs, n 60 9.0 / 6.4, 250 9.6 / 8.1, 500 10.7 / 10.8, 1000 10.9 / 13.6; 384: 22.9 / 11.0,
-// 25.1 / 17.4, 30.0 / 25.8, 36.0 / 38.9; 1200: 52 / 31, 65 / 43, 76 / 59, 95 / 90.
-constexpr int kLong = 768;
+// Whether trees of more than 32 nodes, of 64 dimensions, are tcgen05's, whose pairs take
+// long to begin and end, or a CTA's each on mma.sync.  The lengths are not known here,
+// but the longest that the table can hold; a program's tables are as wide as its model's
+// context whatever its texts.  64 nodes, bf16, in a table of 1024 positions, cache up to
+// n, tcgen05 / mma.sync, us:
+//   pairs   n 60          250          500          700          960
+//   12       9.2 /  6.6  10.6 /  8.3  10.7 / 12.1  10.8 / 13.4  10.8 / 12.8
+//   96      11.2 /  7.0  11.6 /  9.4  13.8 / 12.9  15.2 / 15.2  16.3 / 18.2
+//   192     17.0 /  9.0  17.7 / 13.3  19.3 / 19.4  20.0 / 23.2  22.3 / 30.4
+//   312     21.4 / 11.0  21.9 / 16.9  26.0 / 24.8  28.7 / 30.3  30.7 / 36.5
+//   384     22.7 / 11.1  25.3 / 17.6  30.4 / 25.3  33.3 / 31.1  34.0 / 38.0
+//   600     28.8 / 20.0  36.1 / 28.8  41.8 / 38.0  47.1 / 46.5  51.2 / 56.9
+//   1200    52.2 / 32.4  64.4 / 45.3  75.9 / 58.8  83.2 / 72.4  90.2 / 88.8
+// and of 2048, up to 2000, 46.9 / 65.2 for 384 pairs, 123 / 154 for 1200.  With two pairs
+// an SM or more, mma.sync in tables of up to 1024: ahead up to 500 to 700 positions, by a
+// tenth to a fifth behind at the longest.  With fewer, up to 768.
+bool on_tcgen05(const TreeArgs& a, int hs) {
+  const bool many = static_cast<long long>(a.B) * a.NH >= 2LL * num_sms();
+  return hs == 64 && a.N > 32 && a.rows.capacity > (many ? 1024 : 768);
+}
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -161,7 +175,7 @@ int launch_attention_tree(void* out, const void* qkv, void* kcache, void* vcache
   int ctas = 0, rc = 0;
   if (op == kOpTF32)
     rc = launch_f32(a, hs, &ctas, s);
-  else if (hs == 64 && N > 32 && rows.capacity > kLong)
+  else if (on_tcgen05(a, hs))
     rc = launch_tc05(a, op, &ctas, s);
   else
     rc = op == kOpF16 ? launch_mma_f16(a, hs, &ctas, s) : launch_mma_bf16(a, hs, &ctas, s);
