@@ -20,14 +20,14 @@
 //                           of 64: tcgen05
 //   attention_tree_f32.cu   fp32 caches, CUDA cores
 //
-// Measured (captured): 16 sequences of 16 nodes, 16 heads of 64, cache 4000-16000,
-// bf16 (653 MB, floor 97 us): 97 us, 6.7 TB/s.  32 of 16, 12 heads, 240-960, fp16
-// (64 MB, floor 9.4): 15.9 us, of which about 4 us are the launch and the first
-// loads' chain (positions, table, keys); the longest pair's steps are most of the
-// rest (pairs in the order of their lengths, there and back over the SMs, took 17.2).
-// 16 of 64, 16 heads, 4096-16384, bf16 (684 MB, floor 101): 120 us on tcgen05; on
-// mma.sync, before sequences without a tree left the shares, 233 where tcgen05 took
-// 161.
+// Measured (captured; bytes of the lengths drawn, without sequences that wait): 16
+// sequences of 16 nodes, 16 heads of 64, cache 4000-16000, bf16 (598 MB, floor 88 us):
+// 98 us, 6.1 TB/s.  32 of 16, 12 heads, 240-960, fp16 (59 MB, floor 8.7): 15.8 us, of
+// which about 4 us are the launch and the first loads' chain (positions, table, keys);
+// the longest pair's steps are most of the rest (pairs in the order of their lengths,
+// there and back over the SMs, took 17.2).  16 of 64, 16 heads, 4096-16384, bf16 (668
+// MB, floor 99): 117 us on tcgen05; on mma.sync, before sequences without a tree left
+// the shares, 233 where tcgen05 took 161.
 #include "tree_share.cuh"
 
 #include <algorithm>

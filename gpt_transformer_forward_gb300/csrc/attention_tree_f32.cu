@@ -655,7 +655,7 @@ template <int HS, int R>
 int simt_typed(const TreeArgs& a, int* grid, cudaStream_t s) {
   static bool allowed[kMaxDevices] = {};
   constexpr int kSmem = sizeof(TreeSimtSmem<HS, R>);
-  static_assert(simt_ctas<HS, R>() * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+  static_assert(simt_ctas<HS, R>() * (kSmem + 1024) <= 228 * 1024, "the CTAs of an SM");
   const int ctas = ctas_of(a.N, simt_ctas<HS, R>());
   cudaError_t e = allow_smem(allowed, tree_simt_kernel<HS, R>, kSmem);
   if (e == cudaSuccess) e = launch_pdl(tree_simt_kernel<HS, R>, dim3(ctas), dim3(kThreads), kSmem, s, a);

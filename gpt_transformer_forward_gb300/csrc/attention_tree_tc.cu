@@ -28,8 +28,8 @@
 // Every wait is bounded; after a timeout the CTA drains its copies and MMAs, frees
 // TMEM and returns.
 //
-// Measured: 16 sequences of 64 nodes, 16 heads, cache 4096-16384, bf16 (684 MB, floor
-// 101 us) 120 us, 5.7 TB/s.  A step takes some 1600 cycles where its 32 KB take 1400
+// Measured: 16 sequences of 64 nodes, 16 heads, cache 4096-16384, bf16 (668 MB, floor
+// 99 us) 117 us, 5.7 TB/s.  A step takes some 1600 cycles where its 32 KB take 1400
 // at the rate of a copy; a further pair in a share some 10000, as the groups' outputs
 // have to be joined before the next ones are added up.  With one loading warp for keys
 // and values the kernel took 1.25 times as long.
@@ -46,9 +46,9 @@ constexpr int kHS = 64;
 constexpr int kTileBytes = 128 * kHS * 2;  // 128 rows of 128 bytes
 // What a pair's begin and end take beside its steps, in steps (the nodes' step, the
 // wait for the last products, the join of its results): 16 sequences of 64 nodes, 16
-// heads, 4096-16384 cached, counted as 0 / 3 / 6 / 10: 127.7 / 122.5 / 119.9 / 122.7
-// us; 16, 12 heads, 240-960: 26.2 / 22.4 / 22.3 / 21.7; one, 16 heads, 16000: 21.8 /
-// 19.2 / 18.7 / 18.9.
+// heads, 4096-16384 cached, counted as 0 / 3 / 6 / 10: 125.2 / 119.2 / 117.1 / 118.9
+// us; 12 heads, 1000-4000: 39.2 / 36.1 / 35.0 / 35.6, 240-960: 25.8 / 22.3 / 22.3 /
+// 22.0; one, 16 heads, 16000: 21.9 / 19.3 / 18.7 / 19.0.
 constexpr int kPairCost = 6;
 constexpr int kRing = 3;    // S accumulators (and P) in TMEM
 constexpr int kK = 4;       // K stages

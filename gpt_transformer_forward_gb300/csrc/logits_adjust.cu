@@ -11,15 +11,22 @@
 // A row's segment then goes through shared memory by bulk copies, where only the
 // table's tokens, those of the node's path and, under a mask, what it rules out
 // are changed.  In place nothing goes through: the tokens that change are read and
-// written where they stand.
+// written where they stand, one row behind the other, and a row under a mask is read
+// and written as a whole.
 //
-// Measured (captured): 64 sequences of 64 nodes, 50257 fp32, histories of 1024, 50
-// biases, 64 masks (1.40 GB from and to memory, as missing nodes' rows are left out)
-// 229 us, 6.1 TB/s; 32 of 16, penalties alone (206 MB) 34.8 us, 5.9 TB/s: the copies
+// Measured (captured; bytes without the rows of missing nodes, which are left out): 64
+// sequences of 64 nodes, 50257 fp32, histories of 1024, 50 biases, 64 masks (1.45 GB)
+// 228 us, 6.4 TB/s; 32 of 16, penalties alone (179 MB) 34.8 us, 5.1 TB/s: the copies
 // bound them.  777 single rows of 32003 bf16, histories of 333, 7 biases, 40 masks (100
-// MB) 22.8 us, 4.4 TB/s: 17 without rules; the history costs 2.5 and the masks the same,
+// MB) 23.1 us, 4.3 TB/s: 17 without rules; the history costs 2.5 and the masks the same,
 // latencies that follow each other in a CTA (issue slots 58 % busy, four of ten stalls
-// are barriers and fixed latencies).  One row 3.7 us: the launch and that chain.
+// are barriers and fixed latencies).  One row 3.6 us: the launch and that chain.
+// In place, us, beside those into a second buffer: these four 332 / 228, 39.2 / 34.8,
+// 29.0 / 23.1, 3.7 / 3.6; 32 of 16 under 8 masks too 67.5 / 38.1; penalties alone, 512
+// single rows of 50257 bf16, histories of 1000, 19.0 / 25.6, of 3000 60 / 51; 128 of 8,
+// of 300, 23.5 / 31.9; 256 of 4, of 300, 17.7 / 31.5.  What is not moved is saved where
+// few tokens change and a CTA has few rows; elsewhere the rows' latencies, two or three
+// each with nothing ahead, cost more.
 // CTAs that go on to the next sequences' rows, with copies ahead, were slower (777
 // rows 35 us): fewer of them share an SM, and their chains stand one behind the other.
 #include "draft.cuh"

@@ -59,10 +59,10 @@ __global__ void __launch_bounds__(256) encoder_tree_kernel(float4* __restrict__ 
 // the order of the path.  Row k goes to k <= path[k] < path[k + 1]: no row is
 // written before it is read.
 //
-// 64 sequences of 64 nodes, 12 layers of 12 heads of 64, fp16 (19 MB): 7.1 us (floor
-// 2.8), one sequence 2.1: the launch, then positions, trees and blocks, the path, and
+// 64 sequences of 64 nodes, 24 layers of 16 heads of 64, bf16 (19 MB): 7.2 us (floor
+// 2.8), one sequence 2.0: the launch, then positions, trees and blocks, the path, and
 // rows out and in, each a latency behind the other; the other warps of a CTA wait for
-// the first.
+// the first, and these 1536 CTAs are two waves of the 760 that fit.
 constexpr int kAcceptThreads = 256;
 __global__ void __launch_bounds__(kAcceptThreads) accept_tree_kernel(AcceptArgs a) {
   __shared__ int first[kMaxNodes];  // a node's lowest agreeing child

@@ -84,6 +84,10 @@ GPT2_API size_t attention_tree_workspace_size(int B, int N, int C, int NH, int p
  * node is stored through it.  Positions from pos[b] on lie in blocks that no
  * other sequence, and no other position of this one, has.  out must not overlap
  * qkv.
+ * The lengths stand on the device, so the kernel is chosen by what a row of the table
+ * can hold: a program whose sequences are short does well to give a table hardly wider
+ * than the longest (384 pairs of sequence and head, 16 nodes, 60 positions, bf16: 5.0
+ * us in a table of 1024 positions, 9.5 in one of 4096; 500: 10.8 and 14.4).
  * Workspace: 16-byte aligned, attention_tree_workspace_size bytes. */
 GPT2_API int attention_tree(void* out, const void* qkv, const GPT2PagedKVCache* kv, const int* pos, const int* parent,
                             int B, int N, int C, int NH, int precision, void* workspace, size_t ws_bytes,
@@ -150,8 +154,13 @@ typedef struct {
  * that nothing names keeps its logit bit for bit.  Rows of missing nodes are
  * left as they are.
  * logits, out [B*N,Vp] of logits_type (a GPT2ProbsType), each row a whole number
- * of 16 bytes, 16-byte aligned, Vp <= 2^30.  out may be logits itself (then only
- * what changes is read and written); otherwise they must not overlap.
+ * of 16 bytes, 16-byte aligned, Vp <= 2^30.  out may be logits itself (then of a
+ * row without a mask only the tokens that the rules name are read and written, and the
+ * columns from V on written; a row under a mask is read and written whole.  That is
+ * faster than another buffer without masks for few nodes and short histories, 128
+ * sequences of 8 nodes, 50257 bf16, 300 tokens 23.5 us against 31.9, and slower
+ * otherwise, 32 of 16, fp32, 1000 tokens 39.2 against 34.8, under masks 67.5 against
+ * 38.1); otherwise they must not overlap.
  * parent: the trees, NULL for chains.  A token of the history, the path or the
  * biases outside [-1, V) sets GPT2_DEVERR_TOKEN_BIT and is left out; one of the
  * missing nodes is not read.  A history_len outside [0, history_stride], or a
